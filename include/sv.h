@@ -16,6 +16,16 @@
  *   sv_kv_commit       copy of the accepted path's K/V into the paged cache
  *                      for every layer.
  *
+ * and what fills and keeps the cache those trees are verified against:
+ *
+ *   sv_kv_append       copy of a chunk's K/V (a prompt, or one token) into
+ *                      its cache slots;
+ *   sv_chunk_attention causal attention of each sequence's chunk of new
+ *                      tokens over its paged cache, one layer per call;
+ *   sv_pages_*         which sequence holds which page: fork, reserve (with
+ *                      copy on write), release, compact, and the page copy
+ *                      they ask for.
+ *
  * Conventions shared by every entry point
  *   - All pointers not marked "host" are device pointers.  The caller owns
  *     all memory; the library allocates nothing.
@@ -68,7 +78,10 @@ enum {
   SV_DEVERR_BAD_PAGE = 3,    /* page id outside [0, num_pages) or table     */
   SV_DEVERR_BAD_PATH = 4,    /* accepted path node outside its tree         */
   SV_DEVERR_DEPTH = 5,       /* accepted depth exceeds max_depth            */
-  SV_DEVERR_BAD_TREE = 6     /* a tree has no nodes or more than max_nodes  */
+  SV_DEVERR_BAD_TREE = 6,    /* a tree has no nodes or more than max_nodes  */
+  SV_DEVERR_BAD_LENGTH = 7,  /* a token or page count outside its range     */
+  SV_DEVERR_NO_PAGES = 8,    /* the pool has fewer free pages than asked for */
+  SV_DEVERR_BAD_ROW = 9      /* a table row outside the table, or in use    */
 };
 
 /* Library ABI version (incremented on incompatible changes). */
@@ -491,6 +504,165 @@ sv_status sv_specpv_full_trees(const int* cand_parents, const int* cand_tokens, 
                                const int* buffer_tokens, const int* buffer_cu, int batch,
                                int* parents, int* tokens, int* cu_nodes, void* workspace,
                                size_t workspace_bytes, sv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Append of a chunk's K/V to the paged cache, any number of layers.
+ *
+ * Sequence b brings N_b = cu_tokens[b+1] - cu_tokens[b] new tokens (0
+ * allowed): token i's K and V go to cache slot ctx_lens[b] + i for every KV
+ * head and layer, a bit copy of 16-bit elements.  new_ctx_lens[b] (optional,
+ * must not alias ctx_lens) receives ctx_lens[b] + N_b.  The caller holds
+ * pages for those slots (sv_pages_reserve).  Nothing else changes: rows
+ * behind cu_tokens[B] are not read.
+ *
+ * k/v: [num_layers][total_tokens, Hkv, D], token_stride elements from a token
+ * to the next (>= Hkv * D; slices of a fused projection's rows are fine),
+ * layer_stride from a layer to the next.  k_cache/v_cache as for
+ * sv_kv_commit.  All strides are multiples of 8.  head_dim is a multiple of
+ * 8; num_layers <= 65535.  A sequence whose lengths do not fit its block
+ * table or the token rows is left out (SV_DEVERR_BAD_LENGTH, its length
+ * stays); a slot whose page id is out of range is skipped
+ * (SV_DEVERR_BAD_PAGE).  workspace optional (error word).
+ * ---------------------------------------------------------------------- */
+sv_status sv_kv_append(const void* k, const void* v, long long token_stride, long long layer_stride,
+                       void* k_cache, void* v_cache, long long cache_layer_stride, int num_layers,
+                       int num_pages, const int* block_table, int max_pages_per_seq, const int* ctx_lens,
+                       const int* cu_tokens, int batch, int total_tokens, int num_kv_heads, int head_dim,
+                       int page_size, int* new_ctx_lens, void* workspace, size_t workspace_bytes,
+                       sv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Attention of a chunk of new tokens over the paged cache (one layer).
+ *
+ * The forward that precedes tree verification: a prompt processed in chunks,
+ * or one token without a draft.  Sequence b holds ctx_lens[b] = L_b tokens
+ * from before and brings N_b new ones, whose K/V already lie in slots
+ * L_b .. L_b + N_b - 1 (sv_kv_append).  Token i (position L_b + i), query
+ * head h (KV head h / G, G = Hq / Hkv) computes
+ *     out[i,h] = sum_j softmax_j(scale * q[i,h] . k_j) v_j,
+ *     lse[i,h] = ln sum_j exp(scale * q[i,h] . k_j)
+ * over the positions j <= L_b + i and, with window_tokens = W > 0, of those
+ * only j > L_b + i - W or j < sink_tokens (a token always sees itself).
+ * Batches mix sequences of one token, of long chunks and of none (N_b = 0:
+ * nothing is written).  Rows of q/out behind cu_tokens[B] are left as they
+ * are.  K and V of the positions some row sees are finite; cache slots
+ * behind L_b + N_b may hold anything, and pages a window has left behind
+ * are not read.
+ * ---------------------------------------------------------------------- */
+typedef enum sv_dtype { SV_BF16 = 0, SV_FP16 = 1 } sv_dtype;
+
+typedef struct sv_chunk_params {
+  int batch;              /* B, 1..65535                                     */
+  int num_q_heads;        /* Hq                                              */
+  int num_kv_heads;       /* Hkv; G = Hq / Hkv is an integer, 1..128         */
+  int head_dim;           /* D: 64 or 128                                    */
+  int page_size;          /* 16                                              */
+  int num_pages;          /* pages in this layer's pool (cache dim 0)        */
+  int total_tokens;       /* T = cu_tokens[B] (host copy), or rows of q      */
+  int max_tokens;         /* >= max_b N_b (host copy)                        */
+  int max_pages_per_seq;  /* row length of block_table                       */
+  int dtype;              /* sv_dtype of q, the cache and out                */
+  int window_tokens;      /* W; 0 = every earlier token is visible           */
+  int sink_tokens;        /* tokens visible whatever the window              */
+  float sm_scale;         /* softmax scale; <= 0 selects 1/sqrt(D)           */
+  int flags;              /* 0                                               */
+  long long q_stride;     /* elements from a token of q to the next; 0: Hq*D */
+  long long out_stride;   /* the same for out                                */
+
+  const void* q;          /* [T, Hq, D], heads contiguous                    */
+  const void* k_cache;    /* [num_pages, Hkv, 16, D]                         */
+  const void* v_cache;    /* [num_pages, Hkv, 16, D]                         */
+  const int* block_table; /* int32 [B, max_pages_per_seq]                    */
+  const int* ctx_lens;    /* int32 [B] L_b >= 0                              */
+  const int* cu_tokens;   /* int32 [B+1] prefix sums of N_b, cu_tokens[0] = 0 */
+  void* out;              /* [T, Hq, D] (written)                            */
+  float* lse;             /* optional fp32 [T, Hq]                           */
+  void* workspace;
+  size_t workspace_bytes;
+} sv_chunk_params;
+
+/* Bytes of workspace for these parameters on the current device. */
+sv_status sv_chunk_attention_workspace_size(const sv_chunk_params* params, size_t* bytes);
+
+/* Device errors: SV_DEVERR_BAD_LENGTH for a sequence whose lengths do not fit
+ * its block table, max_tokens or the token rows (its rows are not written);
+ * SV_DEVERR_BAD_PAGE for a page id out of range (its keys read as zero). */
+sv_status sv_chunk_attention(const sv_chunk_params* params, sv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Pages of the cache: which sequence holds which.
+ *
+ * State, all int32 in device memory and the caller's: block_table [rows,
+ * max_pages_per_seq] as everywhere; held_pages [rows], how many leading
+ * entries of a row name pages; page_refs [num_pages], how many entries name
+ * each page (0 = free).  A page named by several rows is shared (the common
+ * prefix of forked sequences) and must not be written; sv_pages_reserve
+ * replaces it first.  All results are the same on every run: no atomic's
+ * order shows.  page_size >= 1; num_pages <= 2097152; rows <= 65535.
+ * workspace: sv_pages_workspace_size bytes, zero-filled once (error word and
+ * scratch); release, fork and copy use its error word only.
+ * ---------------------------------------------------------------------- */
+sv_status sv_pages_workspace_size(int rows, int num_pages, size_t* bytes);
+
+/* Gives back what lies behind keep_lens[b] tokens (a rollback; 0 ends the
+ * sequence): the entries from ceil(keep_lens[b] / page_size) to held_pages[b]
+ * become -1, their pages lose a reference, held_pages[b] shrinks to match.
+ * Rows with nothing behind keep_lens[b] stay as they are. */
+sv_status sv_pages_release(const int* keep_lens, int rows, int* block_table, int max_pages_per_seq,
+                           int* held_pages, int* page_refs, int num_pages, int page_size, void* workspace,
+                           size_t workspace_bytes, sv_stream_t stream);
+
+/* Row children[i] becomes a copy of row parents[i] (i < count): its entries
+ * name the parent's first ceil(ctx_lens[parent] / page_size) pages, which
+ * gain a reference; held_pages and ctx_lens follow.  No K/V moves.  A pair
+ * is left out (SV_DEVERR_BAD_ROW) when a row is outside the table, the child
+ * holds pages, an earlier pair has the same child, or the parent is some
+ * pair's child. */
+sv_status sv_pages_fork(const int* parents, const int* children, int count, int* block_table, int rows,
+                        int max_pages_per_seq, int* ctx_lens, int* held_pages, int* page_refs, int num_pages,
+                        int page_size, void* workspace, size_t workspace_bytes, sv_stream_t stream);
+
+/* Makes the slots ctx_lens[b] .. new_lens[b] - 1 of every row writable (rows
+ * with new_lens[b] <= ctx_lens[b] stay as they are).  Pages the row lacks up
+ * to ceil(new_lens[b] / page_size) are taken from the pool.  A held page of
+ * that range that other entries name too is replaced by a page of its own;
+ * only when every entry naming it lies in such a range of this call, the
+ * lowest row keeps it.  Taken pages are the lowest-numbered free ones, in
+ * (row, logical page) order.  Where a replaced page holds tokens before
+ * ctx_lens[b], the pair (old, new) is appended to copy_src / copy_dst (room
+ * for `rows` entries, written in row order) and *copy_count is their number:
+ * sv_pages_copy moves them.  If the pool has too few free pages nothing
+ * changes, *copy_count is 0 and SV_DEVERR_NO_PAGES is recorded; a row whose
+ * new length exceeds its table (SV_DEVERR_BAD_LENGTH), or whose held entries
+ * in that range name no page (SV_DEVERR_BAD_PAGE), takes no part. */
+sv_status sv_pages_reserve(const int* ctx_lens, const int* new_lens, int rows, int* block_table,
+                           int max_pages_per_seq, int* held_pages, int* page_refs, int num_pages, int page_size,
+                           int* copy_src, int* copy_dst, int* copy_count, void* workspace,
+                           size_t workspace_bytes, sv_stream_t stream);
+
+/* Closes the pool's holes: with n = the number of pages in use, the k-th used
+ * page from n on moves to the k-th free page below n.  Writes the moves to
+ * copy_src / copy_dst (room for num_pages / 2 entries) and *copy_count, n to
+ * *num_live, and the tables and references after the moves to
+ * block_table_out / page_refs_out, which may be block_table / page_refs
+ * themselves.  Until sv_pages_copy and later writes reuse them, the old
+ * pages still hold their contents, so the old tables stay readable. */
+sv_status sv_pages_compact(const int* block_table, const int* held_pages, int rows, int max_pages_per_seq,
+                           const int* page_refs, int num_pages, int* block_table_out, int* page_refs_out,
+                           int* copy_src, int* copy_dst, int* copy_count, int* num_live, void* workspace,
+                           size_t workspace_bytes, sv_stream_t stream);
+
+/* Copies page copy_src[i] to page copy_dst[i], i < min(*copy_count,
+ * max_copies), in every layer of k_cache and v_cache (v_cache may be NULL;
+ * page summaries are such a pool too).  A page is page_elems 16-bit elements,
+ * contiguous (a multiple of 8), pages follow one another, layers are
+ * cache_layer_stride elements apart (a multiple of 8).  No page is a source
+ * and a destination, or twice a destination: lists of sv_pages_reserve and
+ * sv_pages_compact are so.  num_layers <= 65535. */
+sv_status sv_pages_copy(void* k_cache, void* v_cache, long long cache_layer_stride, int num_layers,
+                        int num_pages, int page_elems, const int* copy_src, const int* copy_dst,
+                        const int* copy_count, int max_copies, void* workspace, size_t workspace_bytes,
+                        sv_stream_t stream);
 
 /* Diagnostics: per-CTA phase tracing of sv_tree_attention.
  *

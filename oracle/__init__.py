@@ -14,6 +14,10 @@ verification hot path computes, written from the method descriptions:
   pages, block importance against the tree's queries, the partial page list;
   the full/partial schedule and the tree of a full verification that
   re-verifies the buffer of partially verified tokens.
+* ``chunk``      — causal attention of a chunk of new tokens over the paged
+  cache (window and sink tokens included), and the append of its K/V.
+* ``pages``      — the page bookkeeping: fork, reserve with copy on write,
+  release, compact, as a pool in plain Python.
 * ``sampling``   — stochastic (temperature > 0) acceptance: speculative
   sampling node by node over the tree, residual draws for the bonus token.
 
@@ -35,7 +39,9 @@ from .attention import (  # noqa: F401
     visibility_mask,
 )
 from .accept import greedy_accept  # noqa: F401
+from .chunk import chunk_attention, chunk_visible, kv_append  # noqa: F401
 from .commit import kv_commit  # noqa: F401
+from .pages import Pool, copy_pages  # noqa: F401
 from .sampling import inverse_cdf, node_verify, speculative_tree_accept, target_probs  # noqa: F401
 from .retrieval import (  # noqa: F401
     extend_partial_lists,

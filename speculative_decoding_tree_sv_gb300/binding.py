@@ -23,12 +23,14 @@ STATUS_NAMES = {0: "SV_OK", 1: "SV_ERR_INVALID_ARG", 2: "SV_ERR_UNSUPPORTED", 3:
 # device error codes (sv_deverr in include/sv.h)
 SV_DEVERR_NONE, SV_DEVERR_TIMEOUT, SV_DEVERR_BAD_PARENT, SV_DEVERR_BAD_PAGE = 0, 1, 2, 3
 SV_DEVERR_BAD_PATH, SV_DEVERR_DEPTH, SV_DEVERR_BAD_TREE = 4, 5, 6
+SV_DEVERR_BAD_LENGTH, SV_DEVERR_NO_PAGES, SV_DEVERR_BAD_ROW = 7, 8, 9
+SV_BF16, SV_FP16 = 0, 1
 SV_ATTN_EARLY_CONTEXT = 1
 SV_ATTN_KERNEL_PAIRED = 2
 SV_ATTN_KERNEL_WIDE = 4
 SV_ATTN_KERNEL_DEALT = 8
 DEVICE_ERRORS = {0: "none", 1: "timeout", 2: "bad parent", 3: "bad page", 4: "bad path", 5: "depth",
-                 6: "bad tree"}
+                 6: "bad tree", 7: "bad length", 8: "no pages", 9: "bad row"}
 
 
 class SvError(RuntimeError):
@@ -60,6 +62,18 @@ class sv_retrieve_params(ctypes.Structure):
         ("q", c_void_p), ("summaries", c_void_p), ("block_table", c_void_p), ("ctx_lens", c_void_p),
         ("cu_nodes", c_void_p), ("kv_pages", c_void_p), ("cu_kv_pages", c_void_p), ("scores", c_void_p),
         ("kv_pages_capacity", c_size_t), ("workspace", c_void_p), ("workspace_bytes", c_size_t),
+    ]
+
+
+class sv_chunk_params(ctypes.Structure):
+    _fields_ = [
+        ("batch", c_int), ("num_q_heads", c_int), ("num_kv_heads", c_int), ("head_dim", c_int),
+        ("page_size", c_int), ("num_pages", c_int), ("total_tokens", c_int), ("max_tokens", c_int),
+        ("max_pages_per_seq", c_int), ("dtype", c_int), ("window_tokens", c_int), ("sink_tokens", c_int),
+        ("sm_scale", c_float), ("flags", c_int), ("q_stride", c_longlong), ("out_stride", c_longlong),
+        ("q", c_void_p), ("k_cache", c_void_p), ("v_cache", c_void_p), ("block_table", c_void_p),
+        ("ctx_lens", c_void_p), ("cu_tokens", c_void_p), ("out", c_void_p), ("lse", c_void_p),
+        ("workspace", c_void_p), ("workspace_bytes", c_size_t),
     ]
 
 
@@ -131,6 +145,19 @@ def load(path: Optional[str] = None):
     lib.sv_specpv_next.argtypes = [P(sv_specpv_seq), c_int, c_int]
     lib.sv_specpv_after.restype = c_int
     lib.sv_specpv_after.argtypes = [P(sv_specpv_seq), c_int, c_int]
+    V, I, L, Z = c_void_p, c_int, c_longlong, c_size_t
+    for name, args in (
+            ("sv_kv_append", [V, V, L, L, V, V, L, I, I, V, I, V, V, I, I, I, I, I, V, V, Z, V]),
+            ("sv_chunk_attention_workspace_size", [P(sv_chunk_params), P(Z)]),
+            ("sv_chunk_attention", [P(sv_chunk_params), V]),
+            ("sv_pages_workspace_size", [I, I, P(Z)]),
+            ("sv_pages_release", [V, I, V, I, V, V, I, I, V, Z, V]),
+            ("sv_pages_fork", [V, V, I, V, I, I, V, V, V, I, I, V, Z, V]),
+            ("sv_pages_reserve", [V, V, I, V, I, V, V, I, I, V, V, V, V, Z, V]),
+            ("sv_pages_compact", [V, V, I, I, V, I, V, V, V, V, V, V, V, Z, V]),
+            ("sv_pages_copy", [V, V, L, I, I, I, V, V, V, I, V, Z, V])):
+        getattr(lib, name).restype = c_int
+        getattr(lib, name).argtypes = args
     lib.sv_set_trace_buffer.restype = c_int
     lib.sv_set_trace_buffer.argtypes = [c_void_p, c_size_t]
     lib.sv_get_device_error.restype = c_int
@@ -377,6 +404,245 @@ def sv_specpv_next(seq: sv_specpv_seq, step_tokens: int, buffer_limit: int) -> i
 
 def sv_specpv_after(seq: sv_specpv_seq, kind: int, ctx_len_after: int) -> None:
     _check(load().sv_specpv_after(ctypes.byref(seq), kind, ctx_len_after), "sv_specpv_after")
+
+
+def _device_tensors(**tensors):
+    """Checks of the cache operators' tensors: all on the current CUDA device
+    (the launch goes there).  Names map to tensors; None is left out."""
+    import torch
+    current = torch.cuda.current_device() if torch.cuda.is_available() else None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name}: the library takes device memory; got a tensor on {t.device}")
+        if t.device.index != current:
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{current}")
+
+
+def _ints(shapes, **tensors):
+    """int32, contiguous, of the given shape (None: any); None is left out."""
+    import torch
+    for (name, t), shape in zip(tensors.items(), shapes):
+        if t is None:
+            continue
+        if t.dtype != torch.int32 or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int32 tensor")
+        if shape is not None and tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _space(workspace):
+    """(address, bytes) of an optional workspace tensor."""
+    if workspace is None:
+        return None, 0
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _pool(k_cache, v_cache):
+    """Layers, pages, heads, page size, head dim and layer stride of a cache
+    [layers, pages, Hkv, page, D] (or one layer of it, without the first)."""
+    if k_cache.dim() not in (4, 5) or k_cache.element_size() != 2:
+        raise ValueError("a cache is [layers, pages, Hkv, page_size, D] or [pages, Hkv, page_size, D] of 16-bit elements")
+    one = k_cache if k_cache.dim() == 4 else k_cache[0]
+    layers = 1 if k_cache.dim() == 4 else k_cache.shape[0]
+    stride = k_cache.stride(0) if layers > 1 else 0
+    if not one.is_contiguous():
+        raise ValueError("a layer of the cache must be contiguous")
+    if v_cache is not None and (v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype or
+                                v_cache.stride() != k_cache.stride()):
+        raise ValueError("k_cache and v_cache must have the same shape, type and strides")
+    return (layers, *one.shape, stride)
+
+
+def make_chunk_params(*, q, k_cache, v_cache, block_table, ctx_lens, cu_tokens, out, max_tokens: int, lse=None,
+                      workspace=None, window_tokens: int = 0, sink_tokens: int = 0,
+                      sm_scale: float = 0.0) -> sv_chunk_params:
+    """Fill an ``sv_chunk_params`` from torch tensors: q/out [T, Hq, D] (heads
+    contiguous, any token stride), caches [pages, Hkv, 16, D], all bf16 or all
+    fp16; lse fp32 [T, Hq] if wanted.  The result keeps the tensors alive."""
+    import torch
+    if q.dim() != 3 or out.shape != q.shape:
+        raise ValueError("q and out must both be [tokens, heads, head_dim]")
+    if q.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"q must be bfloat16 or float16, got {q.dtype}")
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache), ("out", out)):
+        if t.dtype != q.dtype:
+            raise ValueError(f"{name} is {t.dtype}, q is {q.dtype}")
+    T, Hq, D = q.shape
+    layers, pages, Hkv, page, Dk, _ = _pool(k_cache, v_cache)
+    if layers != 1 or k_cache.dim() != 4 or Dk != D:
+        raise ValueError("the caches must be one layer, [pages, Hkv, page_size, head_dim], of q's head_dim")
+    for name, t in (("q", q), ("out", out)):
+        if D > 1 and t.stride(2) != 1 or Hq > 1 and t.stride(1) != D:
+            raise ValueError(f"the heads of {name} must be contiguous")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [batch, max_pages]")
+    B = block_table.shape[0]
+    _ints([None, (B,), (B + 1,)], block_table=block_table, ctx_lens=ctx_lens, cu_tokens=cu_tokens)
+    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (T, Hq) or not lse.is_contiguous()):
+        raise ValueError(f"lse must be a contiguous float32 tensor of shape {(T, Hq)}")
+    _device_tensors(q=q, k_cache=k_cache, v_cache=v_cache, block_table=block_table, ctx_lens=ctx_lens,
+                    cu_tokens=cu_tokens, out=out, lse=lse, workspace=workspace)
+    p = sv_chunk_params()
+    p.batch, p.num_q_heads, p.num_kv_heads, p.head_dim = B, Hq, Hkv, D
+    p.page_size, p.num_pages, p.total_tokens, p.max_tokens = page, pages, T, int(max_tokens)
+    p.max_pages_per_seq = block_table.shape[1]
+    p.dtype = SV_BF16 if q.dtype == torch.bfloat16 else SV_FP16
+    p.window_tokens, p.sink_tokens, p.sm_scale, p.flags = int(window_tokens), int(sink_tokens), float(sm_scale), 0
+    p.q_stride = q.stride(0) if T > 1 else 0
+    p.out_stride = out.stride(0) if T > 1 else 0
+    p.q, p.k_cache, p.v_cache, p.out = q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr()
+    p.block_table, p.ctx_lens, p.cu_tokens = block_table.data_ptr(), ctx_lens.data_ptr(), cu_tokens.data_ptr()
+    p.lse = None if lse is None else lse.data_ptr()
+    p.workspace, p.workspace_bytes = _space(workspace)
+    p.tensors = (q, k_cache, v_cache, block_table, ctx_lens, cu_tokens, out, lse, workspace)
+    return p
+
+
+def sv_chunk_attention_workspace_size(params: sv_chunk_params) -> int:
+    n = c_size_t(0)
+    _check(load().sv_chunk_attention_workspace_size(ctypes.byref(params), ctypes.byref(n)),
+           "sv_chunk_attention_workspace_size")
+    return int(n.value)
+
+
+def sv_chunk_attention(params: sv_chunk_params, stream=None) -> None:
+    """Causal attention of every sequence's new tokens over its paged cache,
+    which already holds their K/V (see include/sv.h)."""
+    _check(load().sv_chunk_attention(ctypes.byref(params), _stream(stream)), "sv_chunk_attention")
+
+
+def sv_kv_append(k, v, k_cache, v_cache, block_table, ctx_lens, cu_tokens, new_ctx_lens=None, workspace=None,
+                 stream=None) -> None:
+    """Copies a chunk's K/V to its cache slots.  k/v: [layers, T, Hkv, D], or
+    [T, Hkv, D] with caches of one layer [pages, Hkv, page_size, D]; heads
+    contiguous, any token and layer stride."""
+    layers, pages, Hkv, page, D, cache_stride = _pool(k_cache, v_cache)
+    want = 3 if k_cache.dim() == 4 else 4
+    if k.dim() != want or v.shape != k.shape or v.stride() != k.stride():
+        raise ValueError("k and v must have the cache's layers and the same shape and strides")
+    if k.dtype != k_cache.dtype or v.dtype != k_cache.dtype:
+        raise ValueError(f"k and v must have the cache's type {k_cache.dtype}")
+    T = k.shape[-3]
+    if tuple(k.shape[-2:]) != (Hkv, D) or (want == 4 and k.shape[0] != layers):
+        raise ValueError(f"k must be [{layers} layers, tokens, {Hkv}, {D}], got {tuple(k.shape)}")
+    if D > 1 and k.stride(-1) != 1 or Hkv > 1 and k.stride(-2) != D:
+        raise ValueError("the heads of k and v must be contiguous")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [batch, max_pages]")
+    B = block_table.shape[0]
+    _ints([None, (B,), (B + 1,), (B,)], block_table=block_table, ctx_lens=ctx_lens, cu_tokens=cu_tokens,
+          new_ctx_lens=new_ctx_lens)
+    _device_tensors(k=k, v=v, k_cache=k_cache, v_cache=v_cache, block_table=block_table, ctx_lens=ctx_lens,
+                    cu_tokens=cu_tokens, new_ctx_lens=new_ctx_lens, workspace=workspace)
+    ws, ws_bytes = _space(workspace)
+    _check(load().sv_kv_append(k.data_ptr(), v.data_ptr(), k.stride(-3) if T > 1 else Hkv * D,
+                               k.stride(0) if layers > 1 else 0, k_cache.data_ptr(), v_cache.data_ptr(),
+                               cache_stride, layers, pages, block_table.data_ptr(), block_table.shape[1],
+                               ctx_lens.data_ptr(), cu_tokens.data_ptr(), B, T, Hkv, D, page,
+                               None if new_ctx_lens is None else new_ctx_lens.data_ptr(), ws, ws_bytes,
+                               _stream(stream)), "sv_kv_append")
+
+
+def sv_pages_workspace_size(rows: int, num_pages: int) -> int:
+    n = c_size_t(0)
+    _check(load().sv_pages_workspace_size(rows, num_pages, ctypes.byref(n)), "sv_pages_workspace_size")
+    return int(n.value)
+
+
+def _state(block_table, held_pages, page_refs):
+    """(rows, max pages per row, pages of the pool) of the bookkeeping state."""
+    if block_table.dim() != 2 or page_refs.dim() != 1:
+        raise ValueError("block_table must be [rows, max_pages], page_refs [num_pages]")
+    rows = block_table.shape[0]
+    _ints([None, (rows,), None], block_table=block_table, held_pages=held_pages, page_refs=page_refs)
+    return rows, block_table.shape[1], page_refs.shape[0]
+
+
+def sv_pages_release(keep_lens, block_table, held_pages, page_refs, page_size: int = 16, workspace=None,
+                     stream=None) -> None:
+    """Gives back the pages behind keep_lens[b] tokens of every row."""
+    rows, width, pages = _state(block_table, held_pages, page_refs)
+    _ints([(rows,)], keep_lens=keep_lens)
+    _device_tensors(keep_lens=keep_lens, block_table=block_table, held_pages=held_pages, page_refs=page_refs,
+                    workspace=workspace)
+    ws, ws_bytes = _space(workspace)
+    _check(load().sv_pages_release(keep_lens.data_ptr(), rows, block_table.data_ptr(), width, held_pages.data_ptr(),
+                                   page_refs.data_ptr(), pages, page_size, ws, ws_bytes, _stream(stream)),
+           "sv_pages_release")
+
+
+def sv_pages_fork(parents, children, block_table, ctx_lens, held_pages, page_refs, page_size: int = 16,
+                  workspace=None, stream=None) -> None:
+    """Row children[i] becomes a copy of row parents[i] that shares its pages."""
+    rows, width, pages = _state(block_table, held_pages, page_refs)
+    n = parents.numel()
+    _ints([(n,), (n,), (rows,)], parents=parents, children=children, ctx_lens=ctx_lens)
+    _device_tensors(parents=parents, children=children, block_table=block_table, ctx_lens=ctx_lens,
+                    held_pages=held_pages, page_refs=page_refs, workspace=workspace)
+    if n == 0:
+        return
+    ws, ws_bytes = _space(workspace)
+    _check(load().sv_pages_fork(parents.data_ptr(), children.data_ptr(), n, block_table.data_ptr(), rows, width,
+                                ctx_lens.data_ptr(), held_pages.data_ptr(), page_refs.data_ptr(), pages, page_size,
+                                ws, ws_bytes, _stream(stream)), "sv_pages_fork")
+
+
+def sv_pages_reserve(ctx_lens, new_lens, block_table, held_pages, page_refs, copy_src, copy_dst, copy_count,
+                     page_size: int = 16, workspace=None, stream=None) -> None:
+    """Makes the slots ctx_lens[b] .. new_lens[b] - 1 of every row writable and
+    lists the pages to copy (sv_pages_copy) for those it had to replace."""
+    rows, width, pages = _state(block_table, held_pages, page_refs)
+    _ints([(rows,), (rows,), None, None, (1,)], ctx_lens=ctx_lens, new_lens=new_lens, copy_src=copy_src,
+          copy_dst=copy_dst, copy_count=copy_count)
+    if min(copy_src.numel(), copy_dst.numel()) < rows:
+        raise ValueError(f"copy_src and copy_dst need room for {rows} entries")
+    _device_tensors(ctx_lens=ctx_lens, new_lens=new_lens, block_table=block_table, held_pages=held_pages,
+                    page_refs=page_refs, copy_src=copy_src, copy_dst=copy_dst, copy_count=copy_count,
+                    workspace=workspace)
+    ws, ws_bytes = _space(workspace)
+    _check(load().sv_pages_reserve(ctx_lens.data_ptr(), new_lens.data_ptr(), rows, block_table.data_ptr(), width,
+                                   held_pages.data_ptr(), page_refs.data_ptr(), pages, page_size,
+                                   copy_src.data_ptr(), copy_dst.data_ptr(), copy_count.data_ptr(), ws, ws_bytes,
+                                   _stream(stream)), "sv_pages_reserve")
+
+
+def sv_pages_compact(block_table, held_pages, page_refs, block_table_out, page_refs_out, copy_src, copy_dst,
+                     copy_count, num_live, workspace=None, stream=None) -> None:
+    """Moves the used pages to the front of the pool: lists the copies and
+    writes the tables and references after them (the outputs may be the
+    inputs themselves)."""
+    rows, width, pages = _state(block_table, held_pages, page_refs)
+    _ints([(rows, width), (pages,), None, None, (1,), (1,)], block_table_out=block_table_out,
+          page_refs_out=page_refs_out, copy_src=copy_src, copy_dst=copy_dst, copy_count=copy_count, num_live=num_live)
+    if min(copy_src.numel(), copy_dst.numel()) < pages // 2:
+        raise ValueError(f"copy_src and copy_dst need room for {pages // 2} entries")
+    _device_tensors(block_table=block_table, held_pages=held_pages, page_refs=page_refs,
+                    block_table_out=block_table_out, page_refs_out=page_refs_out, copy_src=copy_src,
+                    copy_dst=copy_dst, copy_count=copy_count, num_live=num_live, workspace=workspace)
+    ws, ws_bytes = _space(workspace)
+    _check(load().sv_pages_compact(block_table.data_ptr(), held_pages.data_ptr(), rows, width, page_refs.data_ptr(),
+                                   pages, block_table_out.data_ptr(), page_refs_out.data_ptr(), copy_src.data_ptr(),
+                                   copy_dst.data_ptr(), copy_count.data_ptr(), num_live.data_ptr(), ws, ws_bytes,
+                                   _stream(stream)), "sv_pages_compact")
+
+
+def sv_pages_copy(k_cache, v_cache, copy_src, copy_dst, copy_count, workspace=None, stream=None) -> None:
+    """Copies the listed pages in every layer.  Caches [layers, pages, ...] of
+    five dimensions, or one layer [pages, ...] of four; v_cache may be None.
+    Page summaries [pages, Hkv, 2, D] are such a pool too."""
+    layers, pages, Hkv, page, D, stride = _pool(k_cache, v_cache)
+    _ints([None, None, (1,)], copy_src=copy_src, copy_dst=copy_dst, copy_count=copy_count)
+    if copy_src.numel() != copy_dst.numel():
+        raise ValueError("copy_src and copy_dst must have the same size")
+    _device_tensors(k_cache=k_cache, v_cache=v_cache, copy_src=copy_src, copy_dst=copy_dst, copy_count=copy_count,
+                    workspace=workspace)
+    ws, ws_bytes = _space(workspace)
+    _check(load().sv_pages_copy(k_cache.data_ptr(), None if v_cache is None else v_cache.data_ptr(), stride, layers,
+                                pages, Hkv * page * D, copy_src.data_ptr(), copy_dst.data_ptr(),
+                                copy_count.data_ptr(), copy_src.numel(), ws, ws_bytes, _stream(stream)),
+           "sv_pages_copy")
 
 
 TRACE_SLOTS = 16

@@ -1,0 +1,329 @@
+// Chunk attention: argument checks, workspace, launches, and the combine of
+// units that several workers shared.
+//
+// The combine reads each cut unit's pieces: O / l in fp32 and the log2 of the
+// softmax sum, weighs them with 2^(lse_i - max) and divides by the weights'
+// sum.  It is launched as a programmatic dependent of the last attention
+// kernel; a block whose unit was not cut leaves at once.
+#include <math.h>
+
+#include "chunk_attention.cuh"
+
+namespace sv {
+namespace chunk {
+
+constexpr int kCombineThreads = 256;
+constexpr int kCombineWarps = kCombineThreads / 32;
+constexpr int kTileBlocks = 8;  // blocks per cut tile unit: two M tiles x four runs of 32 rows
+
+// A row unit: warps split its rows and, when there are few, its pieces.
+template <int D, bool FP16>
+__device__ void combine_rows(const Params& p, int unit) {
+  constexpr int E = D / 32;  // columns per lane
+  __shared__ float part_o[kCombineWarps][D];
+  __shared__ float part_w[kCombineWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int b = unit / p.num_kv_heads, kh = unit - b * p.num_kv_heads;
+  const Seq s = load_seq(p, b, false);
+  if (s.n == 0 || !in_rows(p, s.n)) return;
+  const int4 u = p.row_units[unit];
+  const int first = u.x, pieces = u.y - u.x + 1;
+  if (first < 0 || u.y >= p.row_workers || pieces <= 1) return;  // (a kernel that timed out left no record)
+  const int rows = s.n * p.group;
+  const int parts = rows <= 1 ? 8 : rows <= 2 ? 4 : rows <= 4 ? 2 : 1;
+  const int part = warp % parts;
+  for (int r0 = 0; r0 < rows; r0 += kCombineWarps / parts) {
+    const int r = r0 + warp / parts;
+    float acc[E], wsum = 0.f, mx = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    if (r < rows) {
+      auto at = [&](int i) {  // row of piece i: the unit's head sits in slot 1 of its worker, the rest in slot 0
+        return (static_cast<size_t>(first + i) * 2 + (i == 0 ? 1 : 0)) * kRowUnit + r;
+      };
+      for (int i = lane; i < pieces; i += 32) mx = fmaxf(mx, __ldcg(p.row_lse + at(i)));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      const int per = (pieces + parts - 1) / parts;
+      const int i1 = min(pieces, (part + 1) * per);
+      constexpr int kBatch = 8;
+      for (int i0 = part * per; i0 < i1; i0 += kBatch) {
+        float w[kBatch], v[kBatch][E];
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x) {
+          const int i = min(i0 + x, i1 - 1);
+          w[x] = __ldcg(p.row_lse + at(i));
+          const float* src = p.row_o + at(i) * D + lane * E;
+          if constexpr (E == 4) {
+            const float4 f = __ldcg(reinterpret_cast<const float4*>(src));
+            v[x][0] = f.x, v[x][1] = f.y, v[x][2] = f.z, v[x][3] = f.w;
+          } else {
+            const float2 f = __ldcg(reinterpret_cast<const float2*>(src));
+            v[x][0] = f.x, v[x][1] = f.y;
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x) {
+          const float f = (i0 + x < i1 && w[x] != -INFINITY) ? ex2(w[x] - mx) : 0.f;
+          wsum += f;
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] = fmaf(f, v[x][e], acc[e]);
+        }
+      }
+    }
+    if (parts > 1) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) part_o[warp][lane * E + e] = acc[e];
+      if (lane == 0) part_w[warp] = wsum;
+      __syncthreads();
+      if (part == 0)
+        for (int x = 1; x < parts; ++x) {
+          wsum += part_w[warp + x];
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] += part_o[warp + x][lane * E + e];
+        }
+      __syncthreads();
+    }
+    if (r < rows && part == 0) {
+      const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+      const int tok = r / p.group, head = kh * p.group + r - tok * p.group;
+      const long long token = s.n0 + tok;
+      uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + token * p.out_stride +
+                                                  static_cast<long long>(head) * D) + lane * (E / 2);
+#pragma unroll
+      for (int e = 0; e < E; e += 2) dst[e / 2] = pack2<FP16>(acc[e] * inv, acc[e + 1] * inv);
+      if (lane == 0 && p.lse != nullptr)
+        p.lse[token * p.num_q_heads + head] = wsum > 0.f ? (mx + log2f(wsum)) * kLn2 : -INFINITY;
+    }
+  }
+}
+
+// 32 rows of one M tile of a tile unit: a lane per row, the columns in fours
+// over the warps.
+template <int D, bool FP16>
+__device__ void combine_tiles(const Params& p, int block) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int first = block / kTileBlocks, t = (block / 4) & 1;
+  const int r = (block & 3) * 32 + lane;
+  const int4 u = p.tile_units[2 * first];
+  const int b = u.x, kh = u.y, last = u.w;
+  // not cut, or no record of a kernel that timed out
+  if (b < 0 || b >= p.batch || kh < 0 || kh >= p.num_kv_heads || u.z < 0 || last >= p.tile_ctas) return;
+  const Seq s = load_seq(p, b, false);
+  const int tok = u.z + t * p.tile_tokens + r / p.group;
+  if (r >= p.tile_tokens * p.group || tok >= s.n) return;
+  auto at = [&](int c) {  // (cta, slot, M tile); the unit's head sits in slot 1
+    return (static_cast<size_t>(c) * 2 + (c == first ? 1 : 0)) * 2 + t;
+  };
+  auto holds = [&](int c) { return c == first || p.tile_units[2 * c + 1].x != 0; };
+  float mx = -INFINITY;
+#pragma unroll 4
+  for (int c = first; c <= last; ++c)
+    if (holds(c)) mx = fmaxf(mx, __ldcg(p.tile_lse + at(c) * kTileRows + r));
+  constexpr int kCols = D / 4 / kCombineWarps;  // float4 columns per thread
+  float4 acc[kCols];
+#pragma unroll
+  for (int i = 0; i < kCols; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  float wsum = 0.f;
+#pragma unroll 4
+  for (int c = first; c <= last; ++c) {
+    if (!holds(c)) continue;
+    const float l2 = __ldcg(p.tile_lse + at(c) * kTileRows + r);
+    const float f = l2 == -INFINITY ? 0.f : ex2(l2 - mx);
+    wsum += f;
+    const float4* src = reinterpret_cast<const float4*>(p.tile_o) + at(c) * (D / 4) * kTileRows + r;
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) {
+      const float4 v = __ldcg(src + (warp * kCols + i) * kTileRows);
+      acc[i].x = fmaf(f, v.x, acc[i].x);
+      acc[i].y = fmaf(f, v.y, acc[i].y);
+      acc[i].z = fmaf(f, v.z, acc[i].z);
+      acc[i].w = fmaf(f, v.w, acc[i].w);
+    }
+  }
+  const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+  const int head = kh * p.group + r % p.group;
+  const long long token = s.n0 + tok;
+  uint2* dst = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + token * p.out_stride +
+                                        static_cast<long long>(head) * D) + warp * kCols;
+#pragma unroll
+  for (int i = 0; i < kCols; ++i)
+    dst[i] = make_uint2(pack2<FP16>(acc[i].x * inv, acc[i].y * inv), pack2<FP16>(acc[i].z * inv, acc[i].w * inv));
+  if (warp == 0 && p.lse != nullptr)
+    p.lse[token * p.num_q_heads + head] = wsum > 0.f ? (mx + log2f(wsum)) * kLn2 : -INFINITY;
+}
+
+template <int D, bool FP16>
+__global__ void __launch_bounds__(kCombineThreads) chunk_combine_kernel(const __grid_constant__ Params p,
+                                                                         int tile_blocks) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int block = blockIdx.x;
+  if (block < tile_blocks) combine_tiles<D, FP16>(p, block);
+  else combine_rows<D, FP16>(p, block - tile_blocks);
+}
+
+bool encode_pool(CUtensorMap* map, const void* base, const Launch& l) {
+  const cuuint64_t D = static_cast<cuuint64_t>(l.head_dim), H = static_cast<cuuint64_t>(l.p.num_kv_heads);
+  const cuuint64_t dims[4] = {D, kPage, H, static_cast<cuuint64_t>(l.p.num_pages)};
+  const cuuint64_t strides[3] = {D * 2, kPage * D * 2, H * kPage * D * 2};
+  const cuuint32_t box[4] = {64, kPage, 1, 1};
+  return encode_tiled(map, l.fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                      const_cast<void*>(base), dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B) == CUDA_SUCCESS;
+}
+
+// Where the parts of a call lie in its workspace, and which kernels it needs.
+struct Plan {
+  int row_workers, tile_ctas;
+  size_t row_o, row_lse, row_units, tile_o, tile_lse, tile_units, bytes;
+};
+
+Plan make_plan(const sv_chunk_params* c, int sms) {
+  const int G = c->num_q_heads / c->num_kv_heads;
+  Plan w{};
+  // a sequence of one token has G rows, the longest max_tokens * G; with one
+  // sequence its length is the call's
+  const bool some_small = G <= kRowUnit && !(c->batch == 1 && static_cast<long long>(c->total_tokens) * G > kRowUnit);
+  const bool some_large = static_cast<long long>(c->max_tokens) * G > kRowUnit;
+  w.row_workers = some_small ? sms * kRowWarps : 0;
+  w.tile_ctas = some_large ? sms : 0;
+  size_t at = kWorkspaceHeader;
+  auto take = [&](size_t bytes) {
+    const size_t o = at;
+    at += align_up(bytes, 256);
+    return o;
+  };
+  const size_t D = static_cast<size_t>(c->head_dim);
+  w.row_o = take(static_cast<size_t>(w.row_workers) * 2 * kRowUnit * D * sizeof(float));
+  w.row_lse = take(static_cast<size_t>(w.row_workers) * 2 * kRowUnit * sizeof(float));
+  w.row_units = take(w.row_workers ? static_cast<size_t>(c->batch) * c->num_kv_heads * sizeof(int4) : 0);
+  w.tile_o = take(static_cast<size_t>(w.tile_ctas) * 2 * kGroupRows * D * sizeof(float));
+  w.tile_lse = take(static_cast<size_t>(w.tile_ctas) * 2 * kGroupRows * sizeof(float));
+  w.tile_units = take(static_cast<size_t>(w.tile_ctas) * 2 * sizeof(int4));
+  w.bytes = at;
+  return w;
+}
+
+sv_status check(const sv_chunk_params* c) {
+  if (c == nullptr) return SV_ERR_INVALID_ARG;
+  if (!c->q || !c->k_cache || !c->v_cache || !c->block_table || !c->ctx_lens || !c->cu_tokens || !c->out)
+    return SV_ERR_INVALID_ARG;
+  if (c->batch < 1 || c->num_q_heads < 1 || c->num_kv_heads < 1 || c->num_pages < 1 || c->max_pages_per_seq < 1 ||
+      c->total_tokens < 0 || c->max_tokens < 0 || c->window_tokens < 0 || c->sink_tokens < 0)
+    return SV_ERR_INVALID_ARG;
+  if (c->num_q_heads % c->num_kv_heads != 0 || c->flags != 0 || !(c->sm_scale <= 3.0e38f)) return SV_ERR_INVALID_ARG;
+  if (c->dtype != SV_BF16 && c->dtype != SV_FP16) return SV_ERR_UNSUPPORTED;
+  if (c->head_dim != 64 && c->head_dim != 128) return SV_ERR_UNSUPPORTED;
+  if (c->page_size != kPage || c->batch > 65535) return SV_ERR_UNSUPPORTED;
+  if (c->num_q_heads / c->num_kv_heads > kTileRows) return SV_ERR_UNSUPPORTED;
+  if (c->num_q_heads > 65535 || c->num_pages == 0x7fffffff ||
+      static_cast<long long>(c->batch) * c->num_kv_heads > (1 << 30))
+    return SV_ERR_UNSUPPORTED;
+  // positions are 32-bit
+  if (c->max_pages_per_seq > 0x7fffffff / kPage - 16 || c->window_tokens > (1 << 30) || c->sink_tokens > (1 << 30))
+    return SV_ERR_UNSUPPORTED;
+  const long long dense = static_cast<long long>(c->num_q_heads) * c->head_dim;
+  for (const long long stride : {c->q_stride, c->out_stride})
+    if (stride != 0 && (stride < dense || stride % 8 != 0 || stride > (1ll << 38))) return SV_ERR_INVALID_ARG;
+  if (!aligned16(c->q) || !aligned16(c->k_cache) || !aligned16(c->v_cache) || !aligned16(c->out))
+    return SV_ERR_INVALID_ARG;
+  return SV_OK;
+}
+
+template <int D, bool FP16>
+sv_status launch_combine(const Launch& l) {
+  const int tile_blocks = l.p.tile_ctas * kTileBlocks;
+  const int row_blocks = l.p.row_workers > 0 ? l.p.batch * l.p.num_kv_heads : 0;
+  cudaLaunchConfig_t cfg = cudaLaunchConfig_t{};
+  cfg.gridDim = dim3(static_cast<unsigned>(tile_blocks + row_blocks), 1, 1);
+  cfg.blockDim = dim3(kCombineThreads, 1, 1);
+  cfg.stream = l.stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, chunk_combine_kernel<D, FP16>, l.p, tile_blocks) == cudaSuccess ? SV_OK
+                                                                                                  : SV_ERR_CUDA;
+}
+
+}  // namespace chunk
+}  // namespace sv
+
+extern "C" {
+
+sv_status sv_chunk_attention_workspace_size(const sv_chunk_params* params, size_t* bytes) {
+  using namespace sv;
+  if (params == nullptr || bytes == nullptr) return SV_ERR_INVALID_ARG;
+  const sv_status st = chunk::check(params);
+  if (st != SV_OK) return st;
+  int sms = device_sm_count();
+  if (sms < 1) sms = 152;  // no device to ask: a GB300's
+  *bytes = chunk::make_plan(params, sms).bytes;
+  return SV_OK;
+}
+
+sv_status sv_chunk_attention(const sv_chunk_params* params, sv_stream_t stream) {
+  using namespace sv;
+  const sv_status st = chunk::check(params);
+  if (st != SV_OK) return st;
+  if (params->workspace == nullptr) return SV_ERR_WORKSPACE;
+  if (!aligned16(params->workspace)) return SV_ERR_INVALID_ARG;
+  if (params->total_tokens == 0 || params->max_tokens == 0) return SV_OK;
+  int sms = device_sm_count();
+  const chunk::Plan w = chunk::make_plan(params, sms < 1 ? 152 : sms);
+  if (params->workspace_bytes < w.bytes) return SV_ERR_WORKSPACE;
+  if (sms < 1) return SV_ERR_CUDA;
+  chunk::Launch l;
+  chunk::Params& p = l.p;
+  char* base = static_cast<char*>(params->workspace);
+  const long long dense = static_cast<long long>(params->num_q_heads) * params->head_dim;
+  p.q = params->q;
+  p.block_table = params->block_table;
+  p.ctx_lens = params->ctx_lens;
+  p.cu_tokens = params->cu_tokens;
+  p.out = params->out;
+  p.lse = params->lse;
+  p.err = static_cast<int*>(params->workspace);
+  p.q_stride = params->q_stride ? params->q_stride : dense;
+  p.out_stride = params->out_stride ? params->out_stride : dense;
+  p.batch = params->batch;
+  p.num_q_heads = params->num_q_heads;
+  p.num_kv_heads = params->num_kv_heads;
+  p.group = params->num_q_heads / params->num_kv_heads;
+  p.num_pages = params->num_pages;
+  p.max_pages_per_seq = params->max_pages_per_seq;
+  p.total_tokens = params->total_tokens;
+  p.max_tokens = params->max_tokens;
+  p.window = params->window_tokens;
+  p.sink = params->sink_tokens;
+  p.tile_tokens = chunk::kTileRows / p.group;
+  const float scale = params->sm_scale > 0.f ? params->sm_scale : 1.0f / sqrtf(static_cast<float>(params->head_dim));
+  p.scale_log2 = scale * chunk::kLog2e;
+  p.row_o = reinterpret_cast<float*>(base + w.row_o);
+  p.row_lse = reinterpret_cast<float*>(base + w.row_lse);
+  p.row_units = reinterpret_cast<int4*>(base + w.row_units);
+  p.tile_o = reinterpret_cast<float*>(base + w.tile_o);
+  p.tile_lse = reinterpret_cast<float*>(base + w.tile_lse);
+  p.tile_units = reinterpret_cast<int4*>(base + w.tile_units);
+  p.row_workers = w.row_workers;
+  p.tile_ctas = w.tile_ctas;
+  l.k_cache = params->k_cache;
+  l.v_cache = params->v_cache;
+  l.head_dim = params->head_dim;
+  l.fp16 = params->dtype == SV_FP16;
+  l.stream = reinterpret_cast<cudaStream_t>(stream);
+  if (p.row_workers > 0) {
+    const sv_status r = chunk::launch_rows(l);
+    if (r != SV_OK) return r;
+  }
+  if (p.tile_ctas > 0) {
+    const sv_status r = chunk::launch_tiles(l);
+    if (r != SV_OK) return r;
+  }
+  if (l.head_dim == 128) return l.fp16 ? chunk::launch_combine<128, true>(l) : chunk::launch_combine<128, false>(l);
+  return l.fp16 ? chunk::launch_combine<64, true>(l) : chunk::launch_combine<64, false>(l);
+}
+
+}  // extern "C"

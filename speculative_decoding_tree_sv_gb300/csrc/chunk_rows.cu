@@ -1,0 +1,471 @@
+// Chunk attention for sequences of at most 16 query rows per KV head (one
+// decoded token, or a few): the row kernel.
+//
+// Mathematics: for the 16 rows (token x query head of the group) of a unit and
+// its keys, O = softmax(scale * Q K^T + mask) V with a running maximum m and
+// sum l per row: m' = max(m, max s), p = 2^(s - m'), l' = l 2^(m - m') +
+// sum p, O' = O 2^(m - m') + p V.
+//
+// Bound by HBM: a page of K and V (2 * 16 * D * 2 bytes) is read once and
+// takes 2 * 2 * 16 * 16 * D operations, 16 per byte.  What the memory system
+// needs is bytes in flight, so a worker is a single warp with a ring of its
+// own (24 KB, TMA boxes of 16 rows x 128 bytes, 128-byte swizzle), 8 warps
+// per SM hold 192 KB in flight, and no barrier joins them: a warp waits only
+// for its own pages.  At 16 rows the products are mma.sync m16n8k16 (the
+// rows fill one such tile; a 128-row tcgen05 tile would be 7/8 empty).
+//
+// The pages of all units form one list (sequence, KV head, page); worker w
+// takes an equal contiguous range.  Page ids are fetched 32 at a time.  The
+// last page of a sequence may hold anything behind its last token: its box
+// starts at a negative row, so the missing rows in front arrive as zeros and
+// its tokens end at row 15.
+#include <math.h>
+
+#include <mutex>
+
+#include "chunk_attention.cuh"
+
+namespace sv {
+namespace chunk {
+
+template <int D>
+struct RowCfg {
+  static constexpr int kHalves = D / 64;
+  static constexpr int kHalfBytes = kPage * 128;
+  static constexpr int kPageBytes = kPage * D * 2;  // K or V of one page and head
+  static constexpr int kStages = (D == 128) ? 3 : 6;
+  static constexpr int kRingBytes = kStages * 2 * kPageBytes;  // 24 KB
+  static constexpr int kSmemBytes = kRowWarps * kRingBytes + 1024;
+};
+
+constexpr float kRescale = 8.0f;  // log2 units: O is rescaled only when a maximum grows by more than 2^8
+// A worker's least share in pages: below it more workers only add pieces to merge.
+constexpr int kMinPages = 2;
+
+// What the worker's range holds of a sequence.
+struct RowSeq {
+  Seq s;
+  Keys keys;
+  int pages;
+};
+
+__device__ __forceinline__ RowSeq row_seq(const Params& p, int b, bool report) {
+  RowSeq r;
+  r.s = load_seq(p, b, report);
+  r.pages = 0;
+  if (r.s.n > 0 && in_rows(p, r.s.n)) {
+    r.keys = unit_keys(p, r.s, 0, r.s.n);
+    r.pages = r.keys.sink_pages + (r.keys.end + kPage - 1) / kPage - r.keys.first_page;
+  }
+  return r;
+}
+
+// Walks the units of a range in order: sequence b, KV head kh.
+struct RowCursor {
+  long long pos;  // first page position of the current unit
+  int b, kh;
+  RowSeq seq;
+};
+
+struct RowPiece {
+  int b, kh, j0, j1;  // pages [j0, j1) of the unit's seq.pages
+  long long pos;
+  RowSeq seq;
+};
+
+__device__ __forceinline__ bool next_piece(const Params& p, RowCursor& c, long long lo, long long hi, RowPiece& out) {
+  while (c.b < p.batch && c.pos < hi) {
+    if (c.seq.pages == 0 || c.kh == p.num_kv_heads) {
+      ++c.b;
+      c.kh = 0;
+      if (c.b < p.batch) c.seq = row_seq(p, c.b, false);
+      continue;
+    }
+    const long long a = lo > c.pos ? lo - c.pos : 0;
+    const long long e = hi - c.pos;
+    out.b = c.b;
+    out.kh = c.kh;
+    out.pos = c.pos;
+    out.seq = c.seq;
+    out.j0 = a < c.seq.pages ? static_cast<int>(a) : c.seq.pages;
+    out.j1 = e < c.seq.pages ? static_cast<int>(e) : c.seq.pages;
+    c.pos += c.seq.pages;
+    ++c.kh;
+    if (out.j0 < out.j1) return true;
+  }
+  return false;
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+template <bool FP16>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (FP16) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  } else {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  }
+}
+
+template <int D, bool FP16>
+__global__ void __launch_bounds__(kRowWarps * 32, 1)
+    chunk_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                      const __grid_constant__ Params p) {
+  using C = RowCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bars[kRowWarps * C::kStages];
+  __shared__ int abort_word;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* ring = smem + warp * C::kRingBytes;
+  uint64_t* full = bars + warp * C::kStages;
+  volatile int* abort_flag = &abort_word;
+  if (lane == 0) {
+    for (int i = 0; i < C::kStages; ++i) mbar_init(full + i, 1);
+    if (warp == 0) abort_word = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  __syncthreads();
+  griddep_wait();
+
+  // ---- this worker's range of the page list
+  // consecutive ranges go to different CTAs, so few workers spread over the SMs
+  const int worker = warp * gridDim.x + blockIdx.x;
+  RowCursor start;
+  long long lo, hi, total = 0;
+  int workers;
+  {
+    for (int b0 = 0; b0 < p.batch; b0 += 32) {
+      const int b = b0 + lane;
+      long long w = b < p.batch ? row_seq(p, b, worker == 0).pages : 0;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+      total += w;
+    }
+    total *= p.num_kv_heads;
+    const long long most = (total + kMinPages - 1) / kMinPages;
+    workers = static_cast<int>(most < p.row_workers ? (most > 0 ? most : 1) : p.row_workers);
+    lo = worker < workers ? total * worker / workers : 0;
+    hi = worker < workers ? total * (worker + 1) / workers : 0;
+    long long base = 0;
+    int bsel = p.batch;
+    for (int b0 = 0; b0 < p.batch && bsel == p.batch; b0 += 32) {
+      const int b = b0 + lane;
+      const long long w = (b < p.batch ? row_seq(p, b, false).pages : 0) * static_cast<long long>(p.num_kv_heads);
+      long long incl = w;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, b < p.batch && base + incl > lo);
+      if (hit) {
+        const int l = __ffs(hit) - 1;
+        bsel = b0 + l;
+        base += __shfl_sync(0xffffffffu, incl - w, l);
+      } else {
+        base += __shfl_sync(0xffffffffu, incl, 31);
+      }
+    }
+    start.b = bsel;
+    start.kh = 0;
+    start.pos = base;
+    if (bsel < p.batch) {
+      start.seq = row_seq(p, bsel, false);
+      start.kh = static_cast<int>((lo - base) / start.seq.pages);
+      start.pos = base + static_cast<long long>(start.kh) * start.seq.pages;
+    }
+  }
+  if (hi <= lo) {
+    griddep_launch_dependents();
+    return;
+  }
+
+  // ---- the loads, a ring ahead of the products, running on across pieces
+  RowCursor load_cur = start;
+  RowPiece lp;
+  lp.j0 = lp.j1 = 0;
+  int load_j = 0, id_base = 0, ids = 0, issued = 0;
+  bool more = true;
+  auto issue = [&]() {
+    if (!more) return;
+    if (load_j >= lp.j1) {
+      if (!next_piece(p, load_cur, lo, hi, lp)) {
+        more = false;
+        return;
+      }
+      load_j = lp.j0;
+      id_base = load_j - 32;
+    }
+    const Keys& k = lp.seq.keys;
+    if (load_j - id_base >= 32) {
+      id_base = load_j;
+      const int j = load_j + lane;
+      if (j < lp.j1) {
+        const int page = j < k.sink_pages ? j : k.first_page + (j - k.sink_pages);
+        ids = p.block_table[static_cast<size_t>(lp.b) * p.max_pages_per_seq + page];
+        if (ids < 0 || ids >= p.num_pages) {
+          report_error(p.err, SV_DEVERR_BAD_PAGE);
+          ids = p.num_pages;  // outside the pool: the box arrives as zeros
+        }
+      }
+    }
+    const int phys = __shfl_sync(0xffffffffu, ids, load_j - id_base);
+    const int page = load_j < k.sink_pages ? load_j : k.first_page + (load_j - k.sink_pages);
+    const int tail = k.end - page * kPage;  // tokens from this page on
+    if (lane == 0) {
+      const int row = tail < kPage ? tail - kPage : 0;
+      const int st = issued % C::kStages;
+      uint8_t* dst = ring + st * 2 * C::kPageBytes;
+      mbar_arrive_expect_tx(full + st, 2 * C::kPageBytes);
+#pragma unroll
+      for (int h = 0; h < C::kHalves; ++h)
+        tma_load_4d(dst + h * C::kHalfBytes, &tm_k, full + st, h * 64, row, lp.kh, phys);
+#pragma unroll
+      for (int h = 0; h < C::kHalves; ++h)
+        tma_load_4d(dst + C::kPageBytes + h * C::kHalfBytes, &tm_v, full + st, h * 64, row, lp.kh, phys);
+    }
+    ++issued;
+    ++load_j;
+    __syncwarp();
+  };
+  for (int i = 0; i < C::kStages; ++i) issue();
+
+  const int g = lane >> 2, tq = lane & 3;  // fragment rows g, g + 8; columns 2 tq, 2 tq + 1
+  const int mi = lane >> 3, mr = lane & 7;
+  RowCursor cur = start;
+  RowPiece pc;
+  int done = 0;
+  bool ok = true;
+  while (ok && next_piece(p, cur, lo, hi, pc)) {
+    const Seq& s = pc.seq.s;
+    const Keys& keys = pc.seq.keys;
+    const int rows = s.n * p.group;
+    int tok[2];
+    uint32_t qf[D / 16][4];
+    {
+      const uint32_t* src[2];
+      bool live[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = g + 8 * i;
+        live[i] = r < rows;
+        tok[i] = live[i] ? r / p.group : s.n - 1;
+        const int head = pc.kh * p.group + (live[i] ? r - tok[i] * p.group : 0);
+        src[i] = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.q) +
+                                                   (s.n0 + tok[i]) * p.q_stride + static_cast<long long>(head) * D) + tq;
+      }
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) qf[kk][i] = live[i & 1] ? src[i & 1][kk * 8 + (i >> 1) * 4] : 0u;
+      }
+    }
+    float o[D / 8][4];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+
+    for (int j = pc.j0; j < pc.j1; ++j) {
+      const int st = done % C::kStages;
+      if (!__all_sync(0xffffffffu, mbar_wait(full + st, (done / C::kStages) & 1, abort_flag))) {
+        ok = false;
+        break;
+      }
+      const uint32_t kb = smem_u32(ring + st * 2 * C::kPageBytes);
+      const uint32_t vb = kb + C::kPageBytes;
+      float sc[2][4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sc[0][e] = sc[1][e] = 0.f;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        uint32_t bf[4];
+        const int key = (mi >> 1) * 8 + mr;
+        const int ch = kk * 2 + (mi & 1);
+        ldsm4(bf, kb + (ch >> 3) * C::kHalfBytes + key * 128 + (((ch & 7) ^ (key & 7)) << 4));
+        mma16816<FP16>(sc[0], qf[kk], bf[0], bf[1]);
+        mma16816<FP16>(sc[1], qf[kk], bf[2], bf[3]);
+      }
+      const int page = j < keys.sink_pages ? j : keys.first_page + (j - keys.sink_pages);
+      const int tail = keys.end - page * kPage;
+      const int shift = tail < kPage ? kPage - tail : 0;
+      // a page that every row sees whole needs no mask
+      if (page * kPage + kPage > s.ctx + 1 || (p.window > 0 && page * kPage <= s.ctx + s.n - 1 - p.window)) {
+#pragma unroll
+        for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int col = nb * 8 + tq * 2 + (e & 1);
+            const int key = page * kPage + col - shift;
+            const int at = s.ctx + tok[e >> 1];
+            const bool seen = col >= shift && key <= at && (p.window == 0 || key > at - p.window || key < p.sink);
+            if (!seen) sc[nb][e] = -INFINITY;
+          }
+      }
+      float mx[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        mx[i] = fmaxf(fmaxf(sc[0][2 * i], sc[0][2 * i + 1]), fmaxf(sc[1][2 * i], sc[1][2 * i + 1]));
+        mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
+        mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2)) * p.scale_log2;
+      }
+      const bool grow = mx[0] > m[0] + kRescale || mx[1] > m[1] + kRescale;
+      if (__any_sync(0xffffffffu, grow)) {
+        float f[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float mn = fmaxf(m[i], mx[i]);
+          f[i] = m[i] == mn ? 1.f : ex2(m[i] - mn);  // m = -inf: 0
+          m[i] = mn;
+          l[i] *= f[i];
+        }
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          o[i][0] *= f[0];
+          o[i][1] *= f[0];
+          o[i][2] *= f[1];
+          o[i][3] *= f[1];
+        }
+      }
+      uint32_t pf[4];
+      float pr[2][4];
+#pragma unroll
+      for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float mu = m[e >> 1] == -INFINITY ? 0.f : m[e >> 1];
+          pr[nb][e] = ex2(fmaf(sc[nb][e], p.scale_log2, -mu));
+          l[e >> 1] += pr[nb][e];
+        }
+      // P in 16 bits for the second product: an error of half a step per weight
+      // against its row's sum, below the output's own rounding
+      pf[0] = pack2<FP16>(pr[0][0], pr[0][1]);
+      pf[1] = pack2<FP16>(pr[0][2], pr[0][3]);
+      pf[2] = pack2<FP16>(pr[1][0], pr[1][1]);
+      pf[3] = pack2<FP16>(pr[1][2], pr[1][3]);
+#pragma unroll
+      for (int dd = 0; dd < D / 16; ++dd) {
+        uint32_t bf[4];
+        const int key = (mi & 1) * 8 + mr;
+        const int ch = dd * 2 + (mi >> 1);
+        ldsm4t(bf, vb + (ch >> 3) * C::kHalfBytes + key * 128 + (((ch & 7) ^ (key & 7)) << 4));
+        mma16816<FP16>(o[2 * dd], pf, bf[0], bf[1]);
+        mma16816<FP16>(o[2 * dd + 1], pf, bf[2], bf[3]);
+      }
+      ++done;
+      __syncwarp();  // every lane has read the stage
+      issue();
+    }
+    if (!ok) break;
+    // ---- the piece's rows
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+    }
+    const bool whole = pc.j0 == 0 && pc.j1 == pc.seq.pages;
+    const int slot = pc.j0 == 0 ? 1 : 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = g + 8 * i;
+      if (r >= rows) continue;
+      const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
+      const float lse2 = l[i] > 0.f ? m[i] + log2f(l[i]) : -INFINITY;
+      if (whole) {
+        const int head = pc.kh * p.group + (r - tok[i] * p.group);
+        const long long token = s.n0 + tok[i];
+        uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + token * p.out_stride +
+                                                    static_cast<long long>(head) * D) + tq;
+#pragma unroll
+        for (int nb = 0; nb < D / 8; ++nb) dst[nb * 4] = pack2<FP16>(o[nb][2 * i] * inv, o[nb][2 * i + 1] * inv);
+        if (tq == 0 && p.lse != nullptr) p.lse[token * p.num_q_heads + head] = lse2 * kLn2;
+      } else {
+        const size_t at = (static_cast<size_t>(worker) * 2 + slot) * kRowUnit + r;
+        float2* dst = reinterpret_cast<float2*>(p.row_o + at * D) + tq;
+#pragma unroll
+        for (int nb = 0; nb < D / 8; ++nb) dst[nb * 4] = make_float2(o[nb][2 * i] * inv, o[nb][2 * i + 1] * inv);
+        if (tq == 0) p.row_lse[at] = lse2;
+      }
+    }
+    if (pc.j0 == 0 && lane == 0) {
+      // workers of the unit's first and last page: w holds [total w / n, total (w + 1) / n)
+      int last = worker;
+      if (!whole) last = static_cast<int>(((pc.pos + pc.seq.pages) * workers - 1) / total);
+      p.row_units[static_cast<size_t>(pc.b) * p.num_kv_heads + pc.kh] = make_int4(worker, last, 0, 0);
+    }
+  }
+  if (!ok) {
+    if (lane == 0) {
+      report_error(p.err, SV_DEVERR_TIMEOUT);
+      *abort_flag = 1;
+      // let this warp's own copies land before the memory is given back
+      int never = 0;
+      for (int i = done; i < issued; ++i) mbar_wait(full + i % C::kStages, (i / C::kStages) & 1, &never);
+    }
+    __syncwarp();
+  }
+  griddep_launch_dependents();
+}
+
+template <int D, bool FP16>
+static sv_status launch(const Launch& l) {
+  static std::mutex mu;
+  static bool done[64] = {false};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return SV_ERR_CUDA;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev >= 64 || !done[dev]) {
+      if (cudaFuncSetAttribute(chunk_rows_kernel<D, FP16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               RowCfg<D>::kSmemBytes) != cudaSuccess)
+        return SV_ERR_CUDA;
+      if (dev < 64) done[dev] = true;
+    }
+  }
+  CUtensorMap tm_k, tm_v;
+  if (!encode_pool(&tm_k, l.k_cache, l) || !encode_pool(&tm_v, l.v_cache, l)) return SV_ERR_CUDA;
+  cudaLaunchConfig_t cfg = cudaLaunchConfig_t{};
+  cfg.gridDim = dim3(static_cast<unsigned>(l.p.row_workers / kRowWarps), 1, 1);
+  cfg.blockDim = dim3(kRowWarps * 32, 1, 1);
+  cfg.dynamicSmemBytes = RowCfg<D>::kSmemBytes;
+  cfg.stream = l.stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, chunk_rows_kernel<D, FP16>, tm_k, tm_v, l.p) != cudaSuccess) return SV_ERR_CUDA;
+  return SV_OK;
+}
+
+sv_status launch_rows(const Launch& l) {
+  if (l.head_dim == 128) return l.fp16 ? launch<128, true>(l) : launch<128, false>(l);
+  return l.fp16 ? launch<64, true>(l) : launch<64, false>(l);
+}
+
+}  // namespace chunk
+}  // namespace sv
