@@ -182,8 +182,10 @@ def _ptr(x) -> Optional[int]:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
+        # the handle alone: building torch's Stream object costs 3 us a call,
+        # as much as the launch
         import torch
-        return int(torch.cuda.current_stream().cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return int(stream.cuda_stream)
@@ -406,53 +408,52 @@ def sv_specpv_after(seq: sv_specpv_seq, kind: int, ctx_len_after: int) -> None:
     _check(load().sv_specpv_after(ctypes.byref(seq), kind, ctx_len_after), "sv_specpv_after")
 
 
-def _device_tensors(**tensors):
-    """Checks of the cache operators' tensors: all on the current CUDA device
-    (the launch goes there).  Names map to tensors; None is left out."""
+def _on_device(*tensors) -> None:
+    """Every tensor (None is left out) lies on the current CUDA device, where
+    the launch goes."""
     import torch
-    current = torch.cuda.current_device() if torch.cuda.is_available() else None
-    for name, t in tensors.items():
+    current = -1
+    for t in tensors:
         if t is None:
             continue
         if not t.is_cuda:
-            raise ValueError(f"{name}: the library takes device memory; got a tensor on {t.device}")
-        if t.device.index != current:
-            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{current}")
+            raise ValueError(f"the library takes device memory; got a tensor on {t.device}")
+        if current < 0:
+            current = torch.cuda.current_device()
+        if t.get_device() != current:
+            raise ValueError(f"got a tensor on {t.device}, the current device is cuda:{current}")
 
 
-def _ints(shapes, **tensors):
-    """int32, contiguous, of the given shape (None: any); None is left out."""
+def _ints(name: str, t, count: Optional[int] = None) -> None:
+    """int32, contiguous, of `count` elements."""
     import torch
-    for (name, t), shape in zip(tensors.items(), shapes):
-        if t is None:
-            continue
-        if t.dtype != torch.int32 or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous int32 tensor")
-        if shape is not None and tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype is not torch.int32 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor")
+    if count is not None and t.numel() != count:
+        raise ValueError(f"{name} must have {count} elements, got {t.numel()}")
 
 
 def _space(workspace):
     """(address, bytes) of an optional workspace tensor."""
     if workspace is None:
         return None, 0
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return workspace.data_ptr(), workspace.nbytes
 
 
 def _pool(k_cache, v_cache):
     """Layers, pages, heads, page size, head dim and layer stride of a cache
     [layers, pages, Hkv, page, D] (or one layer of it, without the first)."""
-    if k_cache.dim() not in (4, 5) or k_cache.element_size() != 2:
+    shape = k_cache.shape
+    if len(shape) not in (4, 5) or k_cache.element_size() != 2:
         raise ValueError("a cache is [layers, pages, Hkv, page_size, D] or [pages, Hkv, page_size, D] of 16-bit elements")
-    one = k_cache if k_cache.dim() == 4 else k_cache[0]
-    layers = 1 if k_cache.dim() == 4 else k_cache.shape[0]
-    stride = k_cache.stride(0) if layers > 1 else 0
-    if not one.is_contiguous():
+    if len(shape) == 4:
+        shape = (1, *shape)
+    if not k_cache.is_contiguous() and not (k_cache.dim() == 5 and k_cache[0].is_contiguous()):
         raise ValueError("a layer of the cache must be contiguous")
-    if v_cache is not None and (v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype or
+    if v_cache is not None and (v_cache.shape != k_cache.shape or v_cache.dtype is not k_cache.dtype or
                                 v_cache.stride() != k_cache.stride()):
         raise ValueError("k_cache and v_cache must have the same shape, type and strides")
-    return (layers, *one.shape, stride)
+    return (*shape, k_cache.stride(0) if shape[0] > 1 else 0)
 
 
 def make_chunk_params(*, q, k_cache, v_cache, block_table, ctx_lens, cu_tokens, out, max_tokens: int, lse=None,
@@ -478,16 +479,17 @@ def make_chunk_params(*, q, k_cache, v_cache, block_table, ctx_lens, cu_tokens, 
             raise ValueError(f"the heads of {name} must be contiguous")
     if block_table.dim() != 2:
         raise ValueError("block_table must be [batch, max_pages]")
-    B = block_table.shape[0]
-    _ints([None, (B,), (B + 1,)], block_table=block_table, ctx_lens=ctx_lens, cu_tokens=cu_tokens)
+    B, width = block_table.shape
+    _ints("block_table", block_table)
+    _ints("ctx_lens", ctx_lens, B)
+    _ints("cu_tokens", cu_tokens, B + 1)
     if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (T, Hq) or not lse.is_contiguous()):
         raise ValueError(f"lse must be a contiguous float32 tensor of shape {(T, Hq)}")
-    _device_tensors(q=q, k_cache=k_cache, v_cache=v_cache, block_table=block_table, ctx_lens=ctx_lens,
-                    cu_tokens=cu_tokens, out=out, lse=lse, workspace=workspace)
+    _on_device(q, k_cache, v_cache, block_table, ctx_lens, cu_tokens, out, lse, workspace)
     p = sv_chunk_params()
     p.batch, p.num_q_heads, p.num_kv_heads, p.head_dim = B, Hq, Hkv, D
     p.page_size, p.num_pages, p.total_tokens, p.max_tokens = page, pages, T, int(max_tokens)
-    p.max_pages_per_seq = block_table.shape[1]
+    p.max_pages_per_seq = width
     p.dtype = SV_BF16 if q.dtype == torch.bfloat16 else SV_FP16
     p.window_tokens, p.sink_tokens, p.sm_scale, p.flags = int(window_tokens), int(sink_tokens), float(sm_scale), 0
     p.q_stride = q.stride(0) if T > 1 else 0
@@ -519,27 +521,29 @@ def sv_kv_append(k, v, k_cache, v_cache, block_table, ctx_lens, cu_tokens, new_c
     [T, Hkv, D] with caches of one layer [pages, Hkv, page_size, D]; heads
     contiguous, any token and layer stride."""
     layers, pages, Hkv, page, D, cache_stride = _pool(k_cache, v_cache)
-    want = 3 if k_cache.dim() == 4 else 4
-    if k.dim() != want or v.shape != k.shape or v.stride() != k.stride():
+    shape, stride = k.shape, k.stride()
+    if len(shape) != k_cache.dim() - 1 or v.shape != shape or v.stride() != stride:
         raise ValueError("k and v must have the cache's layers and the same shape and strides")
-    if k.dtype != k_cache.dtype or v.dtype != k_cache.dtype:
+    if k.dtype is not k_cache.dtype or v.dtype is not k_cache.dtype:
         raise ValueError(f"k and v must have the cache's type {k_cache.dtype}")
-    T = k.shape[-3]
-    if tuple(k.shape[-2:]) != (Hkv, D) or (want == 4 and k.shape[0] != layers):
-        raise ValueError(f"k must be [{layers} layers, tokens, {Hkv}, {D}], got {tuple(k.shape)}")
-    if D > 1 and k.stride(-1) != 1 or Hkv > 1 and k.stride(-2) != D:
+    T = shape[-3]
+    if shape[-2] != Hkv or shape[-1] != D or (len(shape) == 4 and shape[0] != layers):
+        raise ValueError(f"k must be [{layers} layers, tokens, {Hkv}, {D}], got {tuple(shape)}")
+    if D > 1 and stride[-1] != 1 or Hkv > 1 and stride[-2] != D:
         raise ValueError("the heads of k and v must be contiguous")
     if block_table.dim() != 2:
         raise ValueError("block_table must be [batch, max_pages]")
-    B = block_table.shape[0]
-    _ints([None, (B,), (B + 1,), (B,)], block_table=block_table, ctx_lens=ctx_lens, cu_tokens=cu_tokens,
-          new_ctx_lens=new_ctx_lens)
-    _device_tensors(k=k, v=v, k_cache=k_cache, v_cache=v_cache, block_table=block_table, ctx_lens=ctx_lens,
-                    cu_tokens=cu_tokens, new_ctx_lens=new_ctx_lens, workspace=workspace)
+    B, width = block_table.shape
+    _ints("block_table", block_table)
+    _ints("ctx_lens", ctx_lens, B)
+    _ints("cu_tokens", cu_tokens, B + 1)
+    if new_ctx_lens is not None:
+        _ints("new_ctx_lens", new_ctx_lens, B)
+    _on_device(k, v, k_cache, v_cache, block_table, ctx_lens, cu_tokens, new_ctx_lens, workspace)
     ws, ws_bytes = _space(workspace)
-    _check(load().sv_kv_append(k.data_ptr(), v.data_ptr(), k.stride(-3) if T > 1 else Hkv * D,
-                               k.stride(0) if layers > 1 else 0, k_cache.data_ptr(), v_cache.data_ptr(),
-                               cache_stride, layers, pages, block_table.data_ptr(), block_table.shape[1],
+    _check(load().sv_kv_append(k.data_ptr(), v.data_ptr(), stride[-3] if T > 1 else Hkv * D,
+                               stride[0] if layers > 1 else 0, k_cache.data_ptr(), v_cache.data_ptr(),
+                               cache_stride, layers, pages, block_table.data_ptr(), width,
                                ctx_lens.data_ptr(), cu_tokens.data_ptr(), B, T, Hkv, D, page,
                                None if new_ctx_lens is None else new_ctx_lens.data_ptr(), ws, ws_bytes,
                                _stream(stream)), "sv_kv_append")
@@ -555,18 +559,27 @@ def _state(block_table, held_pages, page_refs):
     """(rows, max pages per row, pages of the pool) of the bookkeeping state."""
     if block_table.dim() != 2 or page_refs.dim() != 1:
         raise ValueError("block_table must be [rows, max_pages], page_refs [num_pages]")
-    rows = block_table.shape[0]
-    _ints([None, (rows,), None], block_table=block_table, held_pages=held_pages, page_refs=page_refs)
-    return rows, block_table.shape[1], page_refs.shape[0]
+    rows, width = block_table.shape
+    _ints("block_table", block_table)
+    _ints("held_pages", held_pages, rows)
+    _ints("page_refs", page_refs)
+    return rows, width, page_refs.numel()
+
+
+def _pairs(copy_src, copy_dst, copy_count) -> int:
+    """Entries that both lists have room for."""
+    _ints("copy_src", copy_src)
+    _ints("copy_dst", copy_dst)
+    _ints("copy_count", copy_count, 1)
+    return min(copy_src.numel(), copy_dst.numel())
 
 
 def sv_pages_release(keep_lens, block_table, held_pages, page_refs, page_size: int = 16, workspace=None,
                      stream=None) -> None:
     """Gives back the pages behind keep_lens[b] tokens of every row."""
     rows, width, pages = _state(block_table, held_pages, page_refs)
-    _ints([(rows,)], keep_lens=keep_lens)
-    _device_tensors(keep_lens=keep_lens, block_table=block_table, held_pages=held_pages, page_refs=page_refs,
-                    workspace=workspace)
+    _ints("keep_lens", keep_lens, rows)
+    _on_device(keep_lens, block_table, held_pages, page_refs, workspace)
     ws, ws_bytes = _space(workspace)
     _check(load().sv_pages_release(keep_lens.data_ptr(), rows, block_table.data_ptr(), width, held_pages.data_ptr(),
                                    page_refs.data_ptr(), pages, page_size, ws, ws_bytes, _stream(stream)),
@@ -578,9 +591,10 @@ def sv_pages_fork(parents, children, block_table, ctx_lens, held_pages, page_ref
     """Row children[i] becomes a copy of row parents[i] that shares its pages."""
     rows, width, pages = _state(block_table, held_pages, page_refs)
     n = parents.numel()
-    _ints([(n,), (n,), (rows,)], parents=parents, children=children, ctx_lens=ctx_lens)
-    _device_tensors(parents=parents, children=children, block_table=block_table, ctx_lens=ctx_lens,
-                    held_pages=held_pages, page_refs=page_refs, workspace=workspace)
+    _ints("parents", parents)
+    _ints("children", children, n)
+    _ints("ctx_lens", ctx_lens, rows)
+    _on_device(parents, children, block_table, ctx_lens, held_pages, page_refs, workspace)
     if n == 0:
         return
     ws, ws_bytes = _space(workspace)
@@ -594,13 +608,11 @@ def sv_pages_reserve(ctx_lens, new_lens, block_table, held_pages, page_refs, cop
     """Makes the slots ctx_lens[b] .. new_lens[b] - 1 of every row writable and
     lists the pages to copy (sv_pages_copy) for those it had to replace."""
     rows, width, pages = _state(block_table, held_pages, page_refs)
-    _ints([(rows,), (rows,), None, None, (1,)], ctx_lens=ctx_lens, new_lens=new_lens, copy_src=copy_src,
-          copy_dst=copy_dst, copy_count=copy_count)
-    if min(copy_src.numel(), copy_dst.numel()) < rows:
+    _ints("ctx_lens", ctx_lens, rows)
+    _ints("new_lens", new_lens, rows)
+    if _pairs(copy_src, copy_dst, copy_count) < rows:
         raise ValueError(f"copy_src and copy_dst need room for {rows} entries")
-    _device_tensors(ctx_lens=ctx_lens, new_lens=new_lens, block_table=block_table, held_pages=held_pages,
-                    page_refs=page_refs, copy_src=copy_src, copy_dst=copy_dst, copy_count=copy_count,
-                    workspace=workspace)
+    _on_device(ctx_lens, new_lens, block_table, held_pages, page_refs, copy_src, copy_dst, copy_count, workspace)
     ws, ws_bytes = _space(workspace)
     _check(load().sv_pages_reserve(ctx_lens.data_ptr(), new_lens.data_ptr(), rows, block_table.data_ptr(), width,
                                    held_pages.data_ptr(), page_refs.data_ptr(), pages, page_size,
@@ -614,13 +626,13 @@ def sv_pages_compact(block_table, held_pages, page_refs, block_table_out, page_r
     writes the tables and references after them (the outputs may be the
     inputs themselves)."""
     rows, width, pages = _state(block_table, held_pages, page_refs)
-    _ints([(rows, width), (pages,), None, None, (1,), (1,)], block_table_out=block_table_out,
-          page_refs_out=page_refs_out, copy_src=copy_src, copy_dst=copy_dst, copy_count=copy_count, num_live=num_live)
-    if min(copy_src.numel(), copy_dst.numel()) < pages // 2:
+    _ints("block_table_out", block_table_out, rows * width)
+    _ints("page_refs_out", page_refs_out, pages)
+    _ints("num_live", num_live, 1)
+    if _pairs(copy_src, copy_dst, copy_count) < pages // 2:
         raise ValueError(f"copy_src and copy_dst need room for {pages // 2} entries")
-    _device_tensors(block_table=block_table, held_pages=held_pages, page_refs=page_refs,
-                    block_table_out=block_table_out, page_refs_out=page_refs_out, copy_src=copy_src,
-                    copy_dst=copy_dst, copy_count=copy_count, num_live=num_live, workspace=workspace)
+    _on_device(block_table, held_pages, page_refs, block_table_out, page_refs_out, copy_src, copy_dst, copy_count,
+               num_live, workspace)
     ws, ws_bytes = _space(workspace)
     _check(load().sv_pages_compact(block_table.data_ptr(), held_pages.data_ptr(), rows, width, page_refs.data_ptr(),
                                    pages, block_table_out.data_ptr(), page_refs_out.data_ptr(), copy_src.data_ptr(),
@@ -633,15 +645,12 @@ def sv_pages_copy(k_cache, v_cache, copy_src, copy_dst, copy_count, workspace=No
     five dimensions, or one layer [pages, ...] of four; v_cache may be None.
     Page summaries [pages, Hkv, 2, D] are such a pool too."""
     layers, pages, Hkv, page, D, stride = _pool(k_cache, v_cache)
-    _ints([None, None, (1,)], copy_src=copy_src, copy_dst=copy_dst, copy_count=copy_count)
-    if copy_src.numel() != copy_dst.numel():
-        raise ValueError("copy_src and copy_dst must have the same size")
-    _device_tensors(k_cache=k_cache, v_cache=v_cache, copy_src=copy_src, copy_dst=copy_dst, copy_count=copy_count,
-                    workspace=workspace)
+    most = _pairs(copy_src, copy_dst, copy_count)
+    _on_device(k_cache, v_cache, copy_src, copy_dst, copy_count, workspace)
     ws, ws_bytes = _space(workspace)
     _check(load().sv_pages_copy(k_cache.data_ptr(), None if v_cache is None else v_cache.data_ptr(), stride, layers,
                                 pages, Hkv * page * D, copy_src.data_ptr(), copy_dst.data_ptr(),
-                                copy_count.data_ptr(), copy_src.numel(), ws, ws_bytes, _stream(stream)),
+                                copy_count.data_ptr(), most, ws, ws_bytes, _stream(stream)),
            "sv_pages_copy")
 
 
