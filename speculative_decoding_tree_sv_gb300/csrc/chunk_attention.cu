@@ -14,7 +14,7 @@ namespace chunk {
 
 constexpr int kCombineThreads = 256;
 constexpr int kCombineWarps = kCombineThreads / 32;
-constexpr int kTileBlocks = 8;  // blocks per cut tile unit: two M tiles x four runs of 32 rows
+constexpr int kTileBlocks = 16;  // blocks per cut tile unit: two M tiles x eight runs of 16 rows
 
 // A row unit: warps split its rows and, when there are few, its pieces.
 template <int D, bool FP16>
@@ -98,58 +98,70 @@ __device__ void combine_rows(const Params& p, int unit) {
   }
 }
 
-// 32 rows of one M tile of a tile unit: a lane per row, the columns in fours
-// over the warps.
+// 16 rows of one M tile of a tile unit: half a warp per 16 rows, two groups of
+// four columns per thread.  The record, then every piece's sum and columns are
+// requested in one round each (two pieces at a time: most cut units have two).
 template <int D, bool FP16>
 __device__ void combine_tiles(const Params& p, int block) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int first = block / kTileBlocks, t = (block / 4) & 1;
-  const int r = (block & 3) * 32 + lane;
-  const int4 u = p.tile_units[2 * first];
-  const int b = u.x, kh = u.y, last = u.w;
+  const int first = block / kTileBlocks, t = (block / 8) & 1;
+  const int r = (block & 7) * 16 + (lane & 15);
+  const int4 u = p.tile_units[first];
+  const int last = u.w;
   // not cut, or no record of a kernel that timed out
-  if (b < 0 || b >= p.batch || kh < 0 || kh >= p.num_kv_heads || u.z < 0 || last >= p.tile_ctas) return;
-  const Seq s = load_seq(p, b, false);
-  const int tok = u.z + t * p.tile_tokens + r / p.group;
-  if (r >= p.tile_tokens * p.group || tok >= s.n) return;
+  if (u.y <= 0 || u.x < 0 || u.x > p.total_tokens - u.y || u.z < 0 || u.z >= p.num_kv_heads || last >= p.tile_ctas)
+    return;
+  const int tok = t * p.tile_tokens + r / p.group;
+  if (r >= p.tile_tokens * p.group || tok >= u.y) return;
   auto at = [&](int c) {  // (cta, slot, M tile); the unit's head sits in slot 1
     return (static_cast<size_t>(c) * 2 + (c == first ? 1 : 0)) * 2 + t;
   };
-  auto holds = [&](int c) { return c == first || p.tile_units[2 * c + 1].x != 0; };
-  float mx = -INFINITY;
-#pragma unroll 4
-  for (int c = first; c <= last; ++c)
-    if (holds(c)) mx = fmaxf(mx, __ldcg(p.tile_lse + at(c) * kTileRows + r));
-  constexpr int kCols = D / 4 / kCombineWarps;  // float4 columns per thread
-  float4 acc[kCols];
+  constexpr int kCols = D / 4 / (2 * kCombineWarps);  // float4 columns per thread
+  const int col = (warp * 2 + (lane >> 4)) * kCols;
+  float acc[kCols][4];
 #pragma unroll
-  for (int i = 0; i < kCols; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  float wsum = 0.f;
-#pragma unroll 4
-  for (int c = first; c <= last; ++c) {
-    if (!holds(c)) continue;
-    const float l2 = __ldcg(p.tile_lse + at(c) * kTileRows + r);
-    const float f = l2 == -INFINITY ? 0.f : ex2(l2 - mx);
-    wsum += f;
-    const float4* src = reinterpret_cast<const float4*>(p.tile_o) + at(c) * (D / 4) * kTileRows + r;
+  for (int i = 0; i < kCols; ++i)
 #pragma unroll
-    for (int i = 0; i < kCols; ++i) {
-      const float4 v = __ldcg(src + (warp * kCols + i) * kTileRows);
-      acc[i].x = fmaf(f, v.x, acc[i].x);
-      acc[i].y = fmaf(f, v.y, acc[i].y);
-      acc[i].z = fmaf(f, v.z, acc[i].z);
-      acc[i].w = fmaf(f, v.w, acc[i].w);
+    for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
+  float mx = -INFINITY, wsum = 0.f;
+  constexpr int kBatch = 2;
+  for (int c0 = first; c0 <= last; c0 += kBatch) {
+    float l2[kBatch];
+    float4 v[kBatch][kCols];
+#pragma unroll
+    for (int x = 0; x < kBatch; ++x) {
+      const size_t row = at(min(c0 + x, last));
+      l2[x] = __ldcg(p.tile_lse + row * kTileRows + r);
+      const float4* src = reinterpret_cast<const float4*>(p.tile_o) + row * (D / 4) * kTileRows + r;
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) v[x][i] = __ldcg(src + (col + i) * kTileRows);
+    }
+#pragma unroll
+    for (int x = 0; x < kBatch; ++x) {
+      // a piece without a visible key (or without a tile) has no sum, and its columns say nothing
+      if (c0 + x > last || l2[x] == -INFINITY) continue;
+      const float m = fmaxf(mx, l2[x]);
+      const float keep = mx == m ? 1.f : ex2(mx - m), f = ex2(l2[x] - m);
+      mx = m;
+      wsum = wsum * keep + f;
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) {
+        acc[i][0] = fmaf(f, v[x][i].x, acc[i][0] * keep);
+        acc[i][1] = fmaf(f, v[x][i].y, acc[i][1] * keep);
+        acc[i][2] = fmaf(f, v[x][i].z, acc[i][2] * keep);
+        acc[i][3] = fmaf(f, v[x][i].w, acc[i][3] * keep);
+      }
     }
   }
   const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
-  const int head = kh * p.group + r % p.group;
-  const long long token = s.n0 + tok;
+  const int head = u.z * p.group + r % p.group;
+  const long long token = u.x + tok;
   uint2* dst = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + token * p.out_stride +
-                                        static_cast<long long>(head) * D) + warp * kCols;
+                                        static_cast<long long>(head) * D) + col;
 #pragma unroll
   for (int i = 0; i < kCols; ++i)
-    dst[i] = make_uint2(pack2<FP16>(acc[i].x * inv, acc[i].y * inv), pack2<FP16>(acc[i].z * inv, acc[i].w * inv));
-  if (warp == 0 && p.lse != nullptr)
+    dst[i] = make_uint2(pack2<FP16>(acc[i][0] * inv, acc[i][1] * inv), pack2<FP16>(acc[i][2] * inv, acc[i][3] * inv));
+  if (col == 0 && p.lse != nullptr)
     p.lse[token * p.num_q_heads + head] = wsum > 0.f ? (mx + log2f(wsum)) * kLn2 : -INFINITY;
 }
 
@@ -182,10 +194,13 @@ struct Plan {
 Plan make_plan(const sv_chunk_params* c, int sms) {
   const int G = c->num_q_heads / c->num_kv_heads;
   Plan w{};
-  // a sequence of one token has G rows, the longest max_tokens * G; with one
-  // sequence its length is the call's
-  const bool some_small = G <= kRowUnit && !(c->batch == 1 && static_cast<long long>(c->total_tokens) * G > kRowUnit);
+  // a sequence of one token has G rows, the longest max_tokens * G; when the
+  // others at their longest leave every one more than the row kernel takes, it
+  // stays out (4.4 us of finding nothing beside a 220 us window chunk; should
+  // the token rows exceed cu_tokens[B], the tile kernel takes the short ones too)
+  const long long least = c->total_tokens - (c->batch - 1ll) * c->max_tokens;
   const bool some_large = static_cast<long long>(c->max_tokens) * G > kRowUnit;
+  const bool some_small = G <= kRowUnit && !(some_large && least * G > kRowUnit);
   w.row_workers = some_small ? sms * kRowWarps : 0;
   w.tile_ctas = some_large ? sms : 0;
   size_t at = kWorkspaceHeader;
@@ -200,7 +215,7 @@ Plan make_plan(const sv_chunk_params* c, int sms) {
   w.row_units = take(w.row_workers ? static_cast<size_t>(c->batch) * c->num_kv_heads * sizeof(int4) : 0);
   w.tile_o = take(static_cast<size_t>(w.tile_ctas) * 2 * kGroupRows * D * sizeof(float));
   w.tile_lse = take(static_cast<size_t>(w.tile_ctas) * 2 * kGroupRows * sizeof(float));
-  w.tile_units = take(static_cast<size_t>(w.tile_ctas) * 2 * sizeof(int4));
+  w.tile_units = take(static_cast<size_t>(w.tile_ctas) * sizeof(int4));
   w.bytes = at;
   return w;
 }
@@ -221,7 +236,7 @@ sv_status check(const sv_chunk_params* c) {
       static_cast<long long>(c->batch) * c->num_kv_heads > (1 << 30))
     return SV_ERR_UNSUPPORTED;
   // positions are 32-bit
-  if (c->max_pages_per_seq > 0x7fffffff / kPage - 16 || c->window_tokens > (1 << 30) || c->sink_tokens > (1 << 30))
+  if (c->max_pages_per_seq > 0x7fffffff / kPage - 16 || c->window_tokens > (1 << 28) || c->sink_tokens > (1 << 28))
     return SV_ERR_UNSUPPORTED;
   const long long dense = static_cast<long long>(c->num_q_heads) * c->head_dim;
   for (const long long stride : {c->q_stride, c->out_stride})

@@ -46,7 +46,7 @@ struct Params {
   int4* row_units;       // [B * Hkv]: x = first worker, y = last worker (x: none to merge if x == y)
   float* tile_o;         // [ctas][2][256][D]
   float* tile_lse;       // [ctas][2][256]
-  int4* tile_units;      // [ctas]: the cut unit that starts in this CTA: {b, kh * ..., ...}, see chunk_tiles.cu
+  int4* tile_units;      // [ctas]: the cut unit that starts in this CTA: first token row, tokens (0: none), KV head, last CTA
   int row_workers;       // 0: no row kernel in this call
   int tile_ctas;         // 0: no tile kernel in this call
 };
@@ -72,9 +72,10 @@ __device__ __forceinline__ Seq load_seq(const Params& p, int b, bool report) {
   return s;
 }
 
-// Whether the row kernel takes a sequence of n new tokens.
+// Whether the row kernel takes a sequence of n new tokens (a call without it
+// leaves every sequence to the tile kernel).
 __device__ __forceinline__ bool in_rows(const Params& p, int n) {
-  return static_cast<long long>(n) * p.group <= kRowUnit;
+  return p.row_workers > 0 && static_cast<long long>(n) * p.group <= kRowUnit;
 }
 
 // The key pages of a run of tokens [t0, t1) of a sequence: the sink pages
@@ -96,6 +97,31 @@ __device__ __forceinline__ Keys unit_keys(const Params& p, const Seq& s, int t0,
     k.sink_pages = min((min(p.sink, k.end) + kPage - 1) / kPage, k.first_page);
   }
   return k;
+}
+
+// Equal shares of `total` positions: worker c holds [start(c), start(c + 1)),
+// `each` positions and one more for the first `more` workers.
+struct Share {
+  long long each;
+  int more;
+  __device__ __forceinline__ long long start(int c) const { return each * c + min(c, more); }
+  // The worker whose range holds position x.
+  __device__ __forceinline__ int holder(long long x) const {
+    const long long wide = (each + 1) * more;
+    return static_cast<int>(x < wide ? divide(x, each + 1) : more + divide(x - wide, each));
+  }
+  // 64-bit division costs hundreds of cycles; most calls need 32 bits.
+  static __device__ __forceinline__ long long divide(long long a, long long b) {
+    if (((a | b) >> 32) == 0) return static_cast<unsigned>(a) / static_cast<unsigned>(b);
+    return a / b;
+  }
+};
+
+__device__ __forceinline__ Share share_of(long long total, int workers) {
+  Share s;
+  s.each = Share::divide(total, workers);
+  s.more = static_cast<int>(total - s.each * workers);
+  return s;
 }
 
 template <bool FP16>

@@ -156,6 +156,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
   RowCursor start;
   long long lo, hi, total = 0;
   int workers;
+  Share share;
   {
     for (int b0 = 0; b0 < p.batch; b0 += 32) {
       const int b = b0 + lane;
@@ -167,8 +168,9 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
     total *= p.num_kv_heads;
     const long long most = (total + kMinPages - 1) / kMinPages;
     workers = static_cast<int>(most < p.row_workers ? (most > 0 ? most : 1) : p.row_workers);
-    lo = worker < workers ? total * worker / workers : 0;
-    hi = worker < workers ? total * (worker + 1) / workers : 0;
+    share = share_of(total, workers);
+    lo = worker < workers ? share.start(worker) : 0;
+    hi = worker < workers ? share.start(worker + 1) : 0;
     long long base = 0;
     int bsel = p.batch;
     for (int b0 = 0; b0 < p.batch && bsel == p.batch; b0 += 32) {
@@ -194,7 +196,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
     start.pos = base;
     if (bsel < p.batch) {
       start.seq = row_seq(p, bsel, false);
-      start.kh = static_cast<int>((lo - base) / start.seq.pages);
+      start.kh = static_cast<int>(Share::divide(lo - base, start.seq.pages));
       start.pos = base + static_cast<long long>(start.kh) * start.seq.pages;
     }
   }
@@ -412,9 +414,8 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
       }
     }
     if (pc.j0 == 0 && lane == 0) {
-      // workers of the unit's first and last page: w holds [total w / n, total (w + 1) / n)
-      int last = worker;
-      if (!whole) last = static_cast<int>(((pc.pos + pc.seq.pages) * workers - 1) / total);
+      int last = worker;  // the workers of the unit's first and last page
+      if (!whole) last = share.holder(pc.pos + pc.seq.pages - 1);
       p.row_units[static_cast<size_t>(pc.b) * p.num_kv_heads + pc.kh] = make_int4(worker, last, 0, 0);
     }
   }

@@ -47,6 +47,9 @@ constexpr int kPieceRing = 4;
 constexpr int kUnitKeys = 192;
 constexpr int kHalfUnit = 5;
 constexpr long long kMinWeight = 8 * kBlockN;  // a CTA's least share
+// What cutting units costs a call, as weight: the partial rows a CTA writes and
+// the combine, about ten tiles of two M tiles.
+constexpr long long kCutWeight = 10 * 8 * kBlockN;
 
 template <int D>
 struct Cfg {
@@ -74,24 +77,29 @@ struct TileSeq {
   long long weight;  // of one KV head
 };
 
-__device__ __forceinline__ long long weight_cap(const Params& p) {
-  return p.window > 0 ? static_cast<long long>(p.window) + 2 * p.tile_tokens + p.sink + kPage : (1ll << 40);
+// What a row group under a window costs at most, in keys (window and sink are
+// at most 2^28, so sums stay in 32 bits).
+__device__ __forceinline__ int weight_cap(const Params& p) {
+  return p.window > 0 ? p.window + 2 * p.tile_tokens + p.sink + kPage : 0x7fffffff - kUnitKeys;
 }
 
 // Weight of the first m row groups, all of them taken as full (m <= units).
 __device__ __forceinline__ long long full_weight(const Params& p, const Seq& s, int m) {
-  const long long gt = 2 * p.tile_tokens;
-  const long long cap = weight_cap(p);
-  long long below = cap > s.ctx ? (cap - s.ctx) / gt : 0;  // groups whose keys do not reach the cap
-  if (below > m) below = m;
-  return 8 * (below * (s.ctx + kUnitKeys) + gt * below * (below + 1) / 2 + (m - below) * (cap + kUnitKeys));
+  const int gt = 2 * p.tile_tokens;
+  int below = m;  // groups whose keys do not reach the cap
+  long long capped = 0;
+  if (p.window > 0) {
+    const int cap = weight_cap(p);
+    below = min(m, cap > s.ctx ? (cap - s.ctx) / gt : 0);
+    capped = static_cast<long long>(m - below) * (cap + kUnitKeys);
+  }
+  const long long n = below;
+  return 8 * (n * (s.ctx + kUnitKeys) + gt * n * (n + 1) / 2 + capped);
 }
 
 __device__ __forceinline__ long long last_weight(const Params& p, const Seq& s, int units) {
-  const long long cap = weight_cap(p);
-  const long long end = s.ctx + s.n;
   const bool half = s.n - (units - 1) * 2 * p.tile_tokens <= p.tile_tokens;
-  return (half ? kHalfUnit : 8) * ((end < cap ? end : cap) + kUnitKeys);
+  return static_cast<long long>(half ? kHalfUnit : 8) * (min(s.ctx + s.n, weight_cap(p)) + kUnitKeys);
 }
 
 __device__ __forceinline__ TileSeq tile_seq(const Params& p, int b, bool report) {
@@ -131,28 +139,60 @@ __device__ __forceinline__ int tile_page(const Piece& pc, int j, int i) {
 template <class Publish>
 __device__ void deal_pieces(const Params& p, int cta, Publish&& publish) {
   const int lane = threadIdx.x & 31;
-  long long total = 0;
+  // the call's weight, its units and its heaviest unit (one KV head's)
+  long long total = 0, heaviest = 0;
+  int units = 0;
+  TileSeq mine{};  // of sequence `lane`: the only round when there are at most 32
   for (int b0 = 0; b0 < p.batch; b0 += 32) {
     const int b = b0 + lane;
-    long long w = b < p.batch ? tile_seq(p, b, cta == 0 && p.row_workers == 0).weight : 0;
+    TileSeq t{};
+    if (b < p.batch) t = tile_seq(p, b, cta == 0 && p.row_workers == 0);
+    if (b0 == 0) mine = t;
+    long long w = t.weight, h = t.units > 0 ? last_weight(p, t.s, t.units) : 0;
+    if (t.units > 1) {
+      const long long h2 = full_weight(p, t.s, t.units - 1) - full_weight(p, t.s, t.units - 2);
+      h = h2 > h ? h2 : h;
+    }
+    int u = t.units;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+    for (int o = 16; o > 0; o >>= 1) {
+      w += __shfl_xor_sync(0xffffffffu, w, o);
+      u += __shfl_xor_sync(0xffffffffu, u, o);
+      const long long x = __shfl_xor_sync(0xffffffffu, h, o);
+      h = x > h ? x : h;
+    }
     total += w;
+    units += u;
+    heaviest = h > heaviest ? h : heaviest;
   }
   total *= p.num_kv_heads;
-  const long long most = total / kMinWeight;
+  const long long all = static_cast<long long>(units) * p.num_kv_heads;
+  // Whole units, a count each per CTA, when even the heaviest on every CTA costs
+  // no more than equal shares with their partials and the combine.
+  const long long rounds = share_of(all + p.tile_ctas - 1, p.tile_ctas).each;
+  const Share even = share_of(total, p.tile_ctas);
+  const bool whole_units = rounds * heaviest <= even.each + kCutWeight;
+  if (whole_units) total = all;
+  auto weight_of = [&](const TileSeq& t) { return whole_units ? static_cast<long long>(t.units) : t.weight; };
+  auto prefix = [&](const TileSeq& t, int m) { return whole_units ? static_cast<long long>(m) : full_weight(p, t.s, m); };
+  const long long most = whole_units ? p.tile_ctas : total / kMinWeight;
   const int ctas = static_cast<int>(most < p.tile_ctas ? (most > 0 ? most : 1) : p.tile_ctas);
-  const long long lo = cta < ctas ? total * cta / ctas : 0;
-  const long long hi = cta < ctas ? total * (cta + 1) / ctas : 0;
-  int4 record = make_int4(-1, 0, 0, -1);  // cut unit that starts here: b, kh, tok0, last CTA
-  int tail = 0;
+  const Share share = !whole_units && ctas == p.tile_ctas ? even : share_of(total, ctas);
+  const long long lo = cta < ctas ? share.start(cta) : 0;
+  const long long hi = cta < ctas ? share.start(cta + 1) : 0;
+  int4 record = make_int4(0, 0, 0, 0);  // the cut unit that starts here
   bool open = hi > lo;
   if (open) {
     long long base = 0;
     int bsel = p.batch;
     for (int b0 = 0; b0 < p.batch && bsel == p.batch; b0 += 32) {
       const int b = b0 + lane;
-      const long long w = b < p.batch ? tile_seq(p, b, false).weight * p.num_kv_heads : 0;
+      TileSeq t = mine;
+      if (b0 > 0 || p.batch > 32) {
+        t = TileSeq{};
+        if (b < p.batch) t = tile_seq(p, b, false);
+      }
+      const long long w = weight_of(t) * p.num_kv_heads;
       long long incl = w;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -164,29 +204,35 @@ __device__ void deal_pieces(const Params& p, int cta, Publish&& publish) {
         const int l = __ffs(hit) - 1;
         bsel = b0 + l;
         base += __shfl_sync(0xffffffffu, incl - w, l);
+        mine.s.n0 = __shfl_sync(0xffffffffu, t.s.n0, l);
+        mine.s.n = __shfl_sync(0xffffffffu, t.s.n, l);
+        mine.s.ctx = __shfl_sync(0xffffffffu, t.s.ctx, l);
+        mine.units = __shfl_sync(0xffffffffu, t.units, l);
+        mine.weight = __shfl_sync(0xffffffffu, t.weight, l);
       } else {
         base += __shfl_sync(0xffffffffu, incl, 31);
       }
     }
     // (all lanes walk the same units from here)
-    TileSeq t = tile_seq(p, bsel, false);
+    TileSeq t = mine;
     int b = bsel;
-    int kh = static_cast<int>((lo - base) / t.weight);
-    long long pos = base + kh * t.weight;
+    int kh = 0;
+    long long pos = base;
+    for (const long long w = weight_of(t); lo - pos >= w; pos += w) ++kh;
     int m = 0;
     {
       int a = 0, e = t.units;  // the row group holding lo: prefix(m) <= lo - pos < prefix(m + 1)
       while (e - a > 1) {
         const int mid = (a + e) / 2;
-        if (full_weight(p, t.s, mid) <= lo - pos) a = mid;
+        if (prefix(t, mid) <= lo - pos) a = mid;
         else e = mid;
       }
       m = a;
-      pos += full_weight(p, t.s, m);
+      pos += prefix(t, m);
     }
     while (pos < hi) {
-      const long long w = m + 1 < t.units ? full_weight(p, t.s, m + 1) - full_weight(p, t.s, m)
-                                          : last_weight(p, t.s, t.units);
+      const long long w = m + 1 < t.units ? prefix(t, m + 1) - prefix(t, m)
+                                          : (whole_units ? 1 : last_weight(p, t.s, t.units));
       Piece pc;
       pc.b = b;
       pc.kh = kh;
@@ -202,16 +248,23 @@ __device__ void deal_pieces(const Params& p, int cta, Publish&& publish) {
       pc.end = keys.end;
       const int tiles = pc.sink_tiles +
                         ((keys.end + kPage - 1) / kPage - keys.first_page + kPagesPerTile - 1) / kPagesPerTile;
-      pc.ja = lo > pos ? static_cast<int>((lo - pos) * tiles / w) : 0;
-      pc.je = hi < pos + w ? static_cast<int>((hi - pos) * tiles / w) : tiles;
+      // (a boundary's tile in 32-bit floating point: the same from both sides)
+      auto tile_at = [&](long long x) {
+        return min(tiles, static_cast<int>(static_cast<float>(x) * __fdividef(static_cast<float>(tiles), static_cast<float>(w))));
+      };
+      pc.ja = lo > pos ? tile_at(lo - pos) : 0;
+      pc.je = hi < pos + w ? tile_at(hi - pos) : tiles;
       pc.nt = t.s.n - pc.tok0 > p.tile_tokens ? 2 : 1;
       const bool whole = pc.ja == 0 && pc.je == tiles;
       pc.slot = whole ? -1 : (pc.ja == 0 ? 1 : 0);
       if (pc.ja < pc.je) {
         if (pc.slot == 1)
-          record = make_int4(b, kh, pc.tok0, static_cast<int>(((pos + w) * ctas - 1) / total));
-        if (pc.slot == 0) tail = 1;
+          record = make_int4(pc.n0 + pc.tok0, t1 - pc.tok0, kh, share.holder(pos + w - 1));
         if (!publish(pc)) return;
+      } else if (pc.ja > 0) {
+        // less than a tile of a unit that others share: this CTA's piece is empty
+        for (int r = lane; r < kGroupRows; r += 32)
+          p.tile_lse[static_cast<size_t>(cta) * 2 * kGroupRows + r] = -INFINITY;
       }
       pos += w;
       if (++m == t.units) {
@@ -228,8 +281,7 @@ __device__ void deal_pieces(const Params& p, int cta, Publish&& publish) {
     }
   }
   if (lane == 0) {
-    p.tile_units[2 * cta] = record;
-    p.tile_units[2 * cta + 1] = make_int4(tail, 0, 0, 0);
+    p.tile_units[cta] = record;
   }
   Piece end;
   end.je = 0;
@@ -480,33 +532,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         commit(k_empty + kst);
         if (n == 1) commit(q_empty);  // the piece's last QK^T is issued
         if (++kst == KS) { kst = 0; kph ^= 1u; }
-        for (int it = 0; ok && it < n; ++it) {
-          const int nx = it + 1;
-          if (!wait_all(v_full + vst, vph)) { ok = false; break; }
-          for (int t = 0; t < nt; ++t) {
-            if (!wait_all(p_full + t, (tiles_t[t] + it) & 1)) { ok = false; break; }
+        // All but the last tile: PV of one M tile and its next QK^T are issued
+        // back to back (a wait or a branch between two groups of MMAs lets the
+        // tensor pipe run dry), so the tile's K and V are waited for first.
+        int it = 0;
+        for (; it + 1 < n; ++it) {
+          if (!wait_all(v_full + vst, vph) || !wait_all(k_full + kst, kph)) { ok = false; break; }
+          if (!wait_all(p_full, (tiles_t[0] + it) & 1)) { ok = false; break; }
+          tc_fence_after();
+          issue_pv(0, vst, it > 0);
+          issue_qk(0, kst);
+          commit(s_full);
+          if (nt == 2) {
+            if (!wait_all(p_full + 1, (tiles_t[1] + it) & 1)) { ok = false; break; }
             tc_fence_after();
-            issue_pv(t, vst, it > 0);
-            if (nx < n) {
-              if (t == 0) {
-                if (!wait_all(k_full + kst, kph)) { ok = false; break; }
-                tc_fence_after();
-              }
-              issue_qk(t, kst);
-              commit(s_full + t);
-            }
+            issue_pv(1, vst, it > 0);
+            issue_qk(1, kst);
+            commit(s_full + 1);
           }
-          if (!ok) break;
           commit(v_empty + vst);
+          commit(k_empty + kst);
+          if (it + 2 == n) commit(q_empty);
           if (++vst == VS) { vst = 0; vph ^= 1u; }
-          if (nx < n) {
-            commit(k_empty + kst);
-            if (nx == n - 1) commit(q_empty);
-            if (++kst == KS) { kst = 0; kph ^= 1u; }
-          }
+          if (++kst == KS) { kst = 0; kph ^= 1u; }
+        }
+        if (!ok || !wait_all(v_full + vst, vph)) { ok = false; break; }
+        for (int t = 0; t < nt; ++t) {
+          if (!wait_all(p_full + t, (tiles_t[t] + it) & 1)) { ok = false; break; }
+          tc_fence_after();
+          issue_pv(t, vst, it > 0);
+          commit(o_final + t);
         }
         if (!ok) break;
-        for (int t = 0; t < nt; ++t) commit(o_final + t);
+        commit(v_empty + vst);
+        if (++vst == VS) { vst = 0; vph ^= 1u; }
         for (int t = 0; t < nt; ++t) tiles_t[t] += n;
       }
       if (!ok) {
@@ -526,12 +585,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t col_o = t ? C::kColO1 : C::kColO0;
     int tiles_done = 0, pieces_done = 0;
     bool ok = true;
-    for (int k = 0; ok; ++k) {
-      if (!piece_ready(k)) { ok = false; break; }
-      const Piece pc = pieces[k % kPieceRing];
-      piece_done(k);
-      if (pc.je == 0) break;
-      if (t >= pc.nt) continue;  // this M tile has no rows in the unit
+    // Piece -1 is a rehearsal while the first loads are on their way: one tile
+    // of whatever the score columns hold, with nothing stored, handed over or
+    // waited for.  It brings the loop into the instruction cache, which cold
+    // cost the first tile 6000 cycles.
+    for (int k = -1; ok; ++k) {
+      const bool rehearsal = k < 0;
+      Piece pc{};
+      if (rehearsal) {
+        pc.je = 1;
+        pc.nt = 2;
+        pc.slot = -1;
+      } else {
+        if (!piece_ready(k)) { ok = false; break; }
+        pc = pieces[k % kPieceRing];
+        piece_done(k);
+        if (pc.je == 0) break;
+        if (t >= pc.nt) continue;  // this M tile has no rows in the unit
+      }
       const int tok_a = pc.tok0 + t * p.tile_tokens;                  // the M tile's first and last token
       const int tok_b = min(pc.n, tok_a + p.tile_tokens) - 1;
       const int tok_r = tok_a + r / G;
@@ -546,18 +617,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int j = pc.ja + it;
         const bool sink_tile = j < pc.sink_tiles;
         const int base = sink_tile ? j * kBlockN : pc.first_page * kPage + (j - pc.sink_tiles) * kBlockN;
-        const bool masked = sink_tile || base + kBlockN > pc.ctx + tok_a + 1 ||
-                            (p.window > 0 && base <= pc.ctx + tok_b - p.window);
-        if (!wait_all(s_full + t, (tiles_done + it) & 1)) { ok = false; break; }
+        const bool masked = !rehearsal && (sink_tile || base + kBlockN > pc.ctx + tok_a + 1 ||
+                            (p.window > 0 && base <= pc.ctx + tok_b - p.window));
+        if (!rehearsal && !wait_all(s_full + t, (tiles_done + it) & 1)) { ok = false; break; }
         tc_fence_after();
-        uint32_t sr[kBlockN];
-#pragma unroll
-        for (int c = 0; c < kBlockN / 32; ++c)
-          tmem_ld32(lane_base + col_s + c * 32, *reinterpret_cast<uint32_t(*)[32]>(sr + c * 32));
-        tmem_ld_wait();
         if (masked) {
-          // columns up to `whole` hold positions base + c; the sequence's ragged
-          // last page ends at its column 15, `shift` columns of zeros before it
+          // Invisible columns become -inf in the score columns themselves, 32 at
+          // a time: rare tiles, so short code rather than fast code (the loop's
+          // instructions stay in the cache that way).
+          // Columns up to `whole` hold positions base + c; the sequence's ragged
+          // last page ends at its column 15, `shift` columns of zeros before it.
           int whole = sink_tile ? pc.sink_pages * kPage - base : kBlockN;
           int shift = 0, page_col = kBlockN;
           const int seq_end = pc.ctx + pc.n;
@@ -569,23 +638,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           const int sink_end = min(p.sink, hi + 1);
-          constexpr uint32_t kNegInf = 0xFF800000u;
-#pragma unroll
+          const int at = shift - base;  // column of position x in the ragged page: x + at
+          const int c0 = page_col + shift, c1 = min(page_col + kPage, kBlockN);
+#pragma unroll 1
           for (int w = 0; w < kBlockN / 32; ++w) {
-            uint32_t bits = column_bits(max(lo - base, 0), min(hi + 1 - base, whole), w);
-            if (p.window > 0) bits |= column_bits(0, min(sink_end - base, whole), w);
-            if (page_col < kBlockN) {
-              const int at = page_col + shift - (base + page_col);  // column of position x: x + at
-              const int c0 = page_col + shift, c1 = page_col + kPage;
-              bits |= column_bits(max(lo + at, c0), min(hi + 1 + at, c1), w);
-              if (p.window > 0) bits |= column_bits(c0, min(sink_end + at, c1), w);
-            }
-            if (sink_tile) bits &= column_bits(0, min(sink_end - base, whole), w);
+            uint32_t bits = column_bits(c0, min(hi + 1 + at, c1), w);
+            if (p.window > 0)
+              bits = column_bits(max(lo + at, c0), min(hi + 1 + at, c1), w) | column_bits(c0, min(sink_end + at, c1), w) |
+                     column_bits(0, min(sink_end - base, whole), w);
+            bits |= column_bits(max(lo - base, 0), min(hi + 1 - base, whole), w);
+            if (sink_tile) bits = column_bits(0, min(sink_end - base, whole), w);
+            uint32_t x[32];
+            tmem_ld32(lane_base + col_s + w * 32, x);
+            tmem_ld_wait();
+            constexpr uint32_t kNegInf = 0xFF800000u;
 #pragma unroll
             for (int c = 0; c < 32; ++c)
-              if (!((bits >> c) & 1u)) sr[w * 32 + c] = kNegInf;
+              if (!((bits >> c) & 1u)) x[c] = kNegInf;
+            tmem_st32(lane_base + col_s + w * 32, x);
           }
+          tmem_st_wait();
         }
+        uint32_t sr[kBlockN];
+#pragma unroll
+        for (int c = 0; c < kBlockN / 32; ++c)
+          tmem_ld32(lane_base + col_s + c * 32, *reinterpret_cast<uint32_t(*)[32]>(sr + c * 32));
+        tmem_ld_wait();
         // row maximum of the raw scores (scale > 0 commutes with max)
         float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
 #pragma unroll
@@ -605,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           l_run *= f;
           const uint64_t f2 = f2_pack(f, f);
           uint32_t o[32];
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             tmem_ld32(lane_base + col_o + c * 32, o);
             tmem_ld_wait();
@@ -641,13 +719,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const uint64_t acc = f2_add(acc0, acc1);
         l_run += f2_lo(acc) + f2_hi(acc);
+        if (!rehearsal) {
 #pragma unroll
-        for (int c = 0; c < kBlockN / 64; ++c)
-          tmem_st32(lane_base + col_s + c * 32, *reinterpret_cast<uint32_t(*)[32]>(pk + c * 32));
-        tmem_st_wait();
-        tc_fence_before();
-        mbar_arrive(p_full + t);
+          for (int c = 0; c < kBlockN / 64; ++c)
+            tmem_st32(lane_base + col_s + c * 32, *reinterpret_cast<uint32_t(*)[32]>(pk + c * 32));
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(p_full + t);
+        }
       }
+      if (rehearsal) continue;
       if (ok) ok = wait_all(o_final + t, pieces_done & 1);
       if (!ok) break;
       // ------------------------------------------------------------ epilogue
@@ -659,23 +740,44 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (pc.slot < 0) {
         const int head = pc.kh * G + r % G;
         const long long token = pc.n0 + tok;
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + token * p.out_stride +
-                                              static_cast<long long>(head) * D);
+        const unsigned long long my_row = reinterpret_cast<unsigned long long>(
+            static_cast<uint16_t*>(p.out) + token * p.out_stride + static_cast<long long>(head) * D);
+        // A thread holds a row, a store wants a line: eight lanes exchange eight
+        // 16-byte chunks of eight rows, so that they write 128 bytes of one row.
+        const int l8 = lane & 7;
+#pragma unroll 1
+        for (int part = 0; part < D / 64; ++part) {
+          uint32_t x[8][4];
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          tmem_ld32(lane_base + col_o + c * 32, o);
-          tmem_ld_wait();
-          if (row_exists) {
+          for (int c = 0; c < 2; ++c) {
+            uint32_t o[32];
+            tmem_ld32(lane_base + col_o + part * 64 + c * 32, o);
+            tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t v[4];
+            for (int e = 0; e < 4; ++e)
 #pragma unroll
-              for (int x = 0; x < 4; ++x)
-                v[x] = pack2<FP16>(__uint_as_float(o[8 * e + 2 * x]) * inv_l,
-                                   __uint_as_float(o[8 * e + 2 * x + 1]) * inv_l);
-              dst[c * 4 + e] = make_uint4(v[0], v[1], v[2], v[3]);
+              for (int y = 0; y < 4; ++y)
+                x[c * 4 + e][y] = pack2<FP16>(__uint_as_float(o[8 * e + 2 * y]) * inv_l,
+                                              __uint_as_float(o[8 * e + 2 * y + 1]) * inv_l);
+          }
+#pragma unroll
+          for (int s = 1; s < 8; s *= 2)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              if (i & s) continue;
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const bool up = l8 & s;
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? x[i][y] : x[i | s][y], s);
+                if (up) x[i][y] = got;
+                else x[i | s][y] = got;
+              }
             }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {  // chunk l8 of the row that lane (lane & 24) + i holds
+            const unsigned long long to = __shfl_sync(0xffffffffu, my_row, (lane & 24) + i);
+            const int there = __shfl_sync(0xffffffffu, row_exists ? 1 : 0, (lane & 24) + i);
+            if (there) reinterpret_cast<uint4*>(to)[part * 8 + l8] = make_uint4(x[i][0], x[i][1], x[i][2], x[i][3]);
           }
         }
         if (row_exists && p.lse != nullptr) p.lse[token * p.num_q_heads + head] = lse2 * kLn2;
@@ -684,7 +786,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // 16-byte stores are contiguous: [cta][slot][M tile][D / 4][128] float4
         const size_t part = (static_cast<size_t>(cta) * 2 + pc.slot) * 2 + t;
         float4* dst = reinterpret_cast<float4*>(p.tile_o) + part * (D / 4) * kTileRows + r;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
           tmem_ld32(lane_base + col_o + c * 32, o);
