@@ -1,10 +1,14 @@
 // Chunk attention: argument checks, workspace, launches, and the combine of
-// units that several workers shared.
+// cut units.
 //
 // The combine reads each cut unit's pieces: O / l in fp32 and the log2 of the
 // softmax sum, weighs them with 2^(lse_i - max) and divides by the weights'
 // sum.  It is launched as a programmatic dependent of the last attention
-// kernel; a block whose unit was not cut leaves at once.
+// kernel; a block whose unit was not cut leaves at once.  It is short code on
+// purpose: its instructions come cold on every call, and for a few tokens that
+// is most of its time.  (Merging in the row kernel instead, by the CTA that
+// finishes a unit last, measured slower: 39.5 us against 37.7 for 32 sequences
+// of 1300 tokens, 158 against 148 for four of 50000.)
 #include <math.h>
 
 #include "chunk_attention.cuh"
@@ -16,44 +20,49 @@ constexpr int kCombineThreads = 256;
 constexpr int kCombineWarps = kCombineThreads / 32;
 constexpr int kTileBlocks = 16;  // blocks per cut tile unit: two M tiles x eight runs of 16 rows
 
-// A row unit: warps split its rows and, when there are few, its pieces.
+// A row unit: its rows, and parts of its pieces where warps are left over, go
+// to the warps, a lane per D / 32 columns, four partial rows in flight.
 template <int D, bool FP16>
-__device__ void combine_rows(const Params& p, int unit) {
-  constexpr int E = D / 32;  // columns per lane
+__device__ __forceinline__ void combine_rows(const Params& p, int unit) {
+  constexpr int E = D / 32;
   __shared__ float part_o[kCombineWarps][D];
-  __shared__ float part_w[kCombineWarps];
+  __shared__ float part_m[kCombineWarps], part_w[kCombineWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int2 u = p.row_units[unit];
   const int b = unit / p.num_kv_heads, kh = unit - b * p.num_kv_heads;
   const Seq s = load_seq(p, b, false);
-  if (s.n == 0 || !in_rows(p, s.n)) return;
-  const int4 u = p.row_units[unit];
   const int first = u.x, pieces = u.y - u.x + 1;
-  if (first < 0 || u.y >= p.row_workers || pieces <= 1) return;  // (a kernel that timed out left no record)
+  if (s.n == 0 || !in_rows(p, s.n) || first < 0 || u.y >= p.row_workers || pieces <= 1)
+    return;  // (a kernel that timed out left no record)
   const int rows = s.n * p.group;
-  const int parts = rows <= 1 ? 8 : rows <= 2 ? 4 : rows <= 4 ? 2 : 1;
-  const int part = warp % parts;
+  const int parts = pieces <= 4 ? 1 : rows <= 1 ? 8 : rows <= 2 ? 4 : rows <= 4 ? 2 : 1;
+  const int part = warp % parts, per = (pieces + parts - 1) / parts;
+  const int end = min((part + 1) * per, pieces);
   for (int r0 = 0; r0 < rows; r0 += kCombineWarps / parts) {
     const int r = r0 + warp / parts;
-    float acc[E], wsum = 0.f, mx = -INFINITY;
+    float acc[E], mx = -INFINITY, wsum = 0.f;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    auto add = [&](float l2, float weight, const float* v) {
+      if (l2 == -INFINITY) return;
+      const float m = fmaxf(mx, l2);
+      const float keep = ex2(mx - m), f = ex2(l2 - m);  // keep is 0 at the first, as mx = -inf
+      mx = m;
+      wsum = fmaf(wsum, keep, weight * f);
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(f, v[e], acc[e] * keep);
+    };
     if (r < rows) {
-      auto at = [&](int i) {  // row of piece i: the unit's head sits in slot 1 of its worker, the rest in slot 0
-        return (static_cast<size_t>(first + i) * 2 + (i == 0 ? 1 : 0)) * kRowUnit + r;
-      };
-      for (int i = lane; i < pieces; i += 32) mx = fmaxf(mx, __ldcg(p.row_lse + at(i)));
+#pragma unroll 1
+      for (int i = part * per; i < end; i += 4) {
+        float l2[4], v[4][E];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      const int per = (pieces + parts - 1) / parts;
-      const int i1 = min(pieces, (part + 1) * per);
-      constexpr int kBatch = 8;
-      for (int i0 = part * per; i0 < i1; i0 += kBatch) {
-        float w[kBatch], v[kBatch][E];
-#pragma unroll
-        for (int x = 0; x < kBatch; ++x) {
-          const int i = min(i0 + x, i1 - 1);
-          w[x] = __ldcg(p.row_lse + at(i));
-          const float* src = p.row_o + at(i) * D + lane * E;
+        for (int x = 0; x < 4; ++x) {
+          const int piece = min(i + x, end - 1);
+          // the unit's head sits in slot 1 of its worker, the rest in slot 0
+          const size_t row = (static_cast<size_t>(first + piece) * 2 + (piece == 0 ? 1 : 0)) * kRowUnit + r;
+          l2[x] = i + x < end ? __ldcg(p.row_lse + row) : -INFINITY;
+          const float* src = p.row_o + row * D + lane * E;
           if constexpr (E == 4) {
             const float4 f = __ldcg(reinterpret_cast<const float4*>(src));
             v[x][0] = f.x, v[x][1] = f.y, v[x][2] = f.z, v[x][3] = f.w;
@@ -63,25 +72,26 @@ __device__ void combine_rows(const Params& p, int unit) {
           }
         }
 #pragma unroll
-        for (int x = 0; x < kBatch; ++x) {
-          const float f = (i0 + x < i1 && w[x] != -INFINITY) ? ex2(w[x] - mx) : 0.f;
-          wsum += f;
-#pragma unroll
-          for (int e = 0; e < E; ++e) acc[e] = fmaf(f, v[x][e], acc[e]);
-        }
+        for (int x = 0; x < 4; ++x) add(l2[x], 1.f, v[x]);
       }
     }
     if (parts > 1) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) part_o[warp][lane * E + e] = acc[e];
-      if (lane == 0) part_w[warp] = wsum;
+      for (int e = 0; e < E; ++e) part_o[warp][e * 32 + lane] = acc[e];
+      if (lane == 0) {
+        part_m[warp] = mx;
+        part_w[warp] = wsum;
+      }
       __syncthreads();
-      if (part == 0)
+      if (part == 0) {
+#pragma unroll 1
         for (int x = 1; x < parts; ++x) {
-          wsum += part_w[warp + x];
+          float v[E];
 #pragma unroll
-          for (int e = 0; e < E; ++e) acc[e] += part_o[warp + x][lane * E + e];
+          for (int e = 0; e < E; ++e) v[e] = part_o[warp + x][e * 32 + lane];
+          add(part_m[warp + x], part_w[warp + x], v);
         }
+      }
       __syncthreads();
     }
     if (r < rows && part == 0) {
@@ -102,7 +112,7 @@ __device__ void combine_rows(const Params& p, int unit) {
 // four columns per thread.  The record, then every piece's sum and columns are
 // requested in one round each (two pieces at a time: most cut units have two).
 template <int D, bool FP16>
-__device__ void combine_tiles(const Params& p, int block) {
+__device__ __forceinline__ void combine_tiles(const Params& p, int block) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int first = block / kTileBlocks, t = (block / 8) & 1;
   const int r = (block & 7) * 16 + (lane & 15);
@@ -165,14 +175,13 @@ __device__ void combine_tiles(const Params& p, int block) {
     p.lse[token * p.num_q_heads + head] = wsum > 0.f ? (mx + log2f(wsum)) * kLn2 : -INFINITY;
 }
 
-template <int D, bool FP16>
-__global__ void __launch_bounds__(kCombineThreads) chunk_combine_kernel(const __grid_constant__ Params p,
-                                                                         int tile_blocks) {
+template <int D, bool FP16, bool ROWS, bool TILES>
+__global__ void __launch_bounds__(kCombineThreads, 6) chunk_combine_kernel(const __grid_constant__ Params p) {
   griddep_wait();
   griddep_launch_dependents();
-  const int block = blockIdx.x;
-  if (block < tile_blocks) combine_tiles<D, FP16>(p, block);
-  else combine_rows<D, FP16>(p, block - tile_blocks);
+  const int block = blockIdx.x, tile_blocks = TILES ? p.tile_ctas * kTileBlocks : 0;
+  if (TILES && block < tile_blocks) combine_tiles<D, FP16>(p, block);
+  if (ROWS && block >= tile_blocks) combine_rows<D, FP16>(p, block - tile_blocks);
 }
 
 bool encode_pool(CUtensorMap* map, const void* base, const Launch& l) {
@@ -212,7 +221,7 @@ Plan make_plan(const sv_chunk_params* c, int sms) {
   const size_t D = static_cast<size_t>(c->head_dim);
   w.row_o = take(static_cast<size_t>(w.row_workers) * 2 * kRowUnit * D * sizeof(float));
   w.row_lse = take(static_cast<size_t>(w.row_workers) * 2 * kRowUnit * sizeof(float));
-  w.row_units = take(w.row_workers ? static_cast<size_t>(c->batch) * c->num_kv_heads * sizeof(int4) : 0);
+  w.row_units = take(w.row_workers ? static_cast<size_t>(c->batch) * c->num_kv_heads * sizeof(int2) : 0);
   w.tile_o = take(static_cast<size_t>(w.tile_ctas) * 2 * kGroupRows * D * sizeof(float));
   w.tile_lse = take(static_cast<size_t>(w.tile_ctas) * 2 * kGroupRows * sizeof(float));
   w.tile_units = take(static_cast<size_t>(w.tile_ctas) * sizeof(int4));
@@ -250,6 +259,9 @@ template <int D, bool FP16>
 sv_status launch_combine(const Launch& l) {
   const int tile_blocks = l.p.tile_ctas * kTileBlocks;
   const int row_blocks = l.p.row_workers > 0 ? l.p.batch * l.p.num_kv_heads : 0;
+  auto* kernel = tile_blocks == 0  ? chunk_combine_kernel<D, FP16, true, false>
+                 : row_blocks == 0 ? chunk_combine_kernel<D, FP16, false, true>
+                                   : chunk_combine_kernel<D, FP16, true, true>;
   cudaLaunchConfig_t cfg = cudaLaunchConfig_t{};
   cfg.gridDim = dim3(static_cast<unsigned>(tile_blocks + row_blocks), 1, 1);
   cfg.blockDim = dim3(kCombineThreads, 1, 1);
@@ -259,8 +271,7 @@ sv_status launch_combine(const Launch& l) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, chunk_combine_kernel<D, FP16>, l.p, tile_blocks) == cudaSuccess ? SV_OK
-                                                                                                  : SV_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, kernel, l.p) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 
 }  // namespace chunk
@@ -318,7 +329,7 @@ sv_status sv_chunk_attention(const sv_chunk_params* params, sv_stream_t stream) 
   p.scale_log2 = scale * chunk::kLog2e;
   p.row_o = reinterpret_cast<float*>(base + w.row_o);
   p.row_lse = reinterpret_cast<float*>(base + w.row_lse);
-  p.row_units = reinterpret_cast<int4*>(base + w.row_units);
+  p.row_units = reinterpret_cast<int2*>(base + w.row_units);
   p.tile_o = reinterpret_cast<float*>(base + w.tile_o);
   p.tile_lse = reinterpret_cast<float*>(base + w.tile_lse);
   p.tile_units = reinterpret_cast<int4*>(base + w.tile_units);

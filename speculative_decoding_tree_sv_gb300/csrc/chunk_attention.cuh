@@ -43,7 +43,7 @@ struct Params {
   // partials of cut units and what the combine needs of them
   float* row_o;          // [workers][2][16][D]
   float* row_lse;        // [workers][2][16]
-  int4* row_units;       // [B * Hkv]: x = first worker, y = last worker (x: none to merge if x == y)
+  int2* row_units;       // [B * Hkv] first and last worker of the unit
   float* tile_o;         // [ctas][2][256][D]
   float* tile_lse;       // [ctas][2][256]
   int4* tile_units;      // [ctas]: the cut unit that starts in this CTA: first token row, tokens (0: none), KV head, last CTA

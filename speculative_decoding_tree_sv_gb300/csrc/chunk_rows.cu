@@ -158,9 +158,15 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
   int workers;
   Share share;
   {
+    RowSeq mine;  // of sequence `lane`: the only round when there are at most 32
+    mine.pages = 0;
     for (int b0 = 0; b0 < p.batch; b0 += 32) {
       const int b = b0 + lane;
-      long long w = b < p.batch ? row_seq(p, b, worker == 0).pages : 0;
+      RowSeq r;
+      r.pages = 0;
+      if (b < p.batch) r = row_seq(p, b, worker == 0);
+      if (b0 == 0) mine = r;
+      long long w = r.pages;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
       total += w;
@@ -175,7 +181,11 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
     int bsel = p.batch;
     for (int b0 = 0; b0 < p.batch && bsel == p.batch; b0 += 32) {
       const int b = b0 + lane;
-      const long long w = (b < p.batch ? row_seq(p, b, false).pages : 0) * static_cast<long long>(p.num_kv_heads);
+      if (p.batch > 32) {
+        mine.pages = 0;
+        if (b < p.batch) mine = row_seq(p, b, false);
+      }
+      const long long w = mine.pages * static_cast<long long>(p.num_kv_heads);
       long long incl = w;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -187,6 +197,13 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
         const int l = __ffs(hit) - 1;
         bsel = b0 + l;
         base += __shfl_sync(0xffffffffu, incl - w, l);
+        start.seq.s.n0 = __shfl_sync(0xffffffffu, mine.s.n0, l);
+        start.seq.s.n = __shfl_sync(0xffffffffu, mine.s.n, l);
+        start.seq.s.ctx = __shfl_sync(0xffffffffu, mine.s.ctx, l);
+        start.seq.keys.sink_pages = __shfl_sync(0xffffffffu, mine.keys.sink_pages, l);
+        start.seq.keys.first_page = __shfl_sync(0xffffffffu, mine.keys.first_page, l);
+        start.seq.keys.end = __shfl_sync(0xffffffffu, mine.keys.end, l);
+        start.seq.pages = __shfl_sync(0xffffffffu, mine.pages, l);
       } else {
         base += __shfl_sync(0xffffffffu, incl, 31);
       }
@@ -195,22 +212,16 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
     start.kh = 0;
     start.pos = base;
     if (bsel < p.batch) {
-      start.seq = row_seq(p, bsel, false);
       start.kh = static_cast<int>(Share::divide(lo - base, start.seq.pages));
       start.pos = base + static_cast<long long>(start.kh) * start.seq.pages;
     }
   }
-  if (hi <= lo) {
-    griddep_launch_dependents();
-    return;
-  }
-
   // ---- the loads, a ring ahead of the products, running on across pieces
   RowCursor load_cur = start;
   RowPiece lp;
   lp.j0 = lp.j1 = 0;
   int load_j = 0, id_base = 0, ids = 0, issued = 0;
-  bool more = true;
+  bool more = hi > lo;
   auto issue = [&]() {
     if (!more) return;
     if (load_j >= lp.j1) {
@@ -261,7 +272,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
   RowPiece pc;
   int done = 0;
   bool ok = true;
-  while (ok && next_piece(p, cur, lo, hi, pc)) {
+  while (ok && hi > lo && next_piece(p, cur, lo, hi, pc)) {
     const Seq& s = pc.seq.s;
     const Keys& keys = pc.seq.keys;
     const int rows = s.n * p.group;
@@ -414,9 +425,9 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
       }
     }
     if (pc.j0 == 0 && lane == 0) {
-      int last = worker;  // the workers of the unit's first and last page
-      if (!whole) last = share.holder(pc.pos + pc.seq.pages - 1);
-      p.row_units[static_cast<size_t>(pc.b) * p.num_kv_heads + pc.kh] = make_int4(worker, last, 0, 0);
+      // the workers of the unit's first and last page
+      const int last = whole ? worker : share.holder(pc.pos + pc.seq.pages - 1);
+      p.row_units[static_cast<size_t>(pc.b) * p.num_kv_heads + pc.kh] = make_int2(worker, last);
     }
   }
   if (!ok) {
