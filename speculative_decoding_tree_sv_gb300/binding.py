@@ -412,25 +412,22 @@ def _on_device(*tensors) -> None:
     """Every tensor (None is left out) lies on the current CUDA device, where
     the launch goes."""
     import torch
-    current = -1
+    current = torch.cuda.current_device() if torch.cuda.is_initialized() else None
     for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError(f"the library takes device memory; got a tensor on {t.device}")
-        if current < 0:
-            current = torch.cuda.current_device()
-        if t.get_device() != current:
+        if t is not None and t.get_device() != current:
+            if not t.is_cuda:
+                raise ValueError(f"the library takes device memory; got a tensor on {t.device}")
             raise ValueError(f"got a tensor on {t.device}, the current device is cuda:{current}")
 
 
 def _ints(name: str, t, count: Optional[int] = None) -> None:
     """int32, contiguous, of `count` elements."""
     import torch
+    if t.dtype is torch.int32 and t.is_contiguous() and (count is None or t.numel() == count):
+        return
     if t.dtype is not torch.int32 or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor")
-    if count is not None and t.numel() != count:
-        raise ValueError(f"{name} must have {count} elements, got {t.numel()}")
+    raise ValueError(f"{name} must have {count} elements, got {t.numel()}")
 
 
 def _space(workspace):
@@ -443,17 +440,17 @@ def _space(workspace):
 def _pool(k_cache, v_cache):
     """Layers, pages, heads, page size, head dim and layer stride of a cache
     [layers, pages, Hkv, page, D] (or one layer of it, without the first)."""
-    shape = k_cache.shape
-    if len(shape) not in (4, 5) or k_cache.element_size() != 2:
+    shape, stride = k_cache.shape, k_cache.stride()
+    if len(shape) not in (4, 5) or k_cache.itemsize != 2:
         raise ValueError("a cache is [layers, pages, Hkv, page_size, D] or [pages, Hkv, page_size, D] of 16-bit elements")
-    if len(shape) == 4:
-        shape = (1, *shape)
-    if not k_cache.is_contiguous() and not (k_cache.dim() == 5 and k_cache[0].is_contiguous()):
+    if not k_cache.is_contiguous() and not (len(shape) == 5 and k_cache[0].is_contiguous()):
         raise ValueError("a layer of the cache must be contiguous")
-    if v_cache is not None and (v_cache.shape != k_cache.shape or v_cache.dtype is not k_cache.dtype or
-                                v_cache.stride() != k_cache.stride()):
+    if v_cache is not None and (v_cache.stride() != stride or v_cache.shape != shape or
+                                v_cache.dtype is not k_cache.dtype):
         raise ValueError("k_cache and v_cache must have the same shape, type and strides")
-    return (*shape, k_cache.stride(0) if shape[0] > 1 else 0)
+    if len(shape) == 4:
+        return (1, *shape, 0)
+    return (*shape, stride[0] if shape[0] > 1 else 0)
 
 
 def make_chunk_params(*, q, k_cache, v_cache, block_table, ctx_lens, cu_tokens, out, max_tokens: int, lse=None,

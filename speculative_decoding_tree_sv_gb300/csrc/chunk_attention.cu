@@ -340,12 +340,12 @@ sv_status sv_chunk_attention(const sv_chunk_params* params, sv_stream_t stream) 
   l.head_dim = params->head_dim;
   l.fp16 = params->dtype == SV_FP16;
   l.stream = reinterpret_cast<cudaStream_t>(stream);
-  if (p.row_workers > 0) {
-    const sv_status r = chunk::launch_rows(l);
-    if (r != SV_OK) return r;
-  }
   if (p.tile_ctas > 0) {
     const sv_status r = chunk::launch_tiles(l);
+    if (r != SV_OK) return r;
+  }
+  if (p.row_workers > 0) {
+    const sv_status r = chunk::launch_rows(l);
     if (r != SV_OK) return r;
   }
   if (l.head_dim == 128) return l.fp16 ? chunk::launch_combine<128, true>(l) : chunk::launch_combine<128, false>(l);

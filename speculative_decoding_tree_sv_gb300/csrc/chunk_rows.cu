@@ -148,7 +148,10 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
     tma_prefetch_desc(&tm_v);
   }
   __syncthreads();
-  griddep_wait();
+  // Behind the tile kernel of the same call this grid starts once that grid's
+  // CTAs are past their own wait, so the inputs are there already; it runs on
+  // the SMs that the tile kernel leaves free and waits for it at its end.
+  if (p.tile_ctas == 0) griddep_wait();
 
   // ---- this worker's range of the page list
   // consecutive ranges go to different CTAs, so few workers spread over the SMs
@@ -440,6 +443,9 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
     }
     __syncwarp();
   }
+  // The combine waits for this grid; one CTA that waits for the tile kernel
+  // makes that mean both (the last one, so that no free SM is held).
+  if (p.tile_ctas > 0 && blockIdx.x == gridDim.x - 1) griddep_wait();
   griddep_launch_dependents();
 }
 

@@ -363,6 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   griddep_wait();  // everything read below may come from the preceding grid
+  if (p.row_workers > 0) griddep_launch_dependents();  // the row kernel takes the SMs that are free
 
   // Warp-uniform outcome of a bounded wait, by every lane.
   auto wait_all = [&](uint64_t* bar, uint32_t parity) {
@@ -809,7 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  griddep_launch_dependents();  // the partials are written: the combine may run
+  if (p.row_workers == 0) griddep_launch_dependents();  // the partials are written: the combine may run
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
