@@ -50,6 +50,20 @@ __global__ void __launch_bounds__(kWarps * 32) kv_append_kernel(const __grid_con
     }
   }
   if (t >= p.total_tokens) return;
+  // The first vectors of the rows are requested ahead of the search for their
+  // place: four dependent reads that the transfer hides.
+  const int per = p.num_kv_heads * p.vec_per_head;
+  const long long src0 = layer * p.layer_stride + t * p.token_stride;
+  constexpr int kVecs = 8;
+  uint4 val[kVecs];
+  auto request = [&](int e0) {
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      const int e = e0 + 32 * i;
+      if (e < 2 * per) val[i] = e >= per ? __ldcs(p.v + src0 + (e - per)) : __ldcs(p.k + src0 + e);
+    }
+  };
+  request(lane);
   // The sequence of token t: the first b with t < cu_tokens[b + 1].
   int lo = 0, hi = p.batch;  // the answer lies in [lo, hi]; hi == batch: none
   while (hi > lo) {
@@ -78,18 +92,10 @@ __global__ void __launch_bounds__(kWarps * 32) kv_append_kernel(const __grid_con
     return;
   }
   const int row = slot - lp * p.page_size;
-  const int per = p.num_kv_heads * p.vec_per_head;
-  const long long src0 = layer * p.layer_stride + t * p.token_stride;
   const long long dst0 = layer * p.cache_layer_stride +
                          static_cast<long long>(phys) * p.num_kv_heads * p.page_size * p.vec_per_head;
-  constexpr int kVecs = 8;
   for (int e0 = lane; e0 < 2 * per; e0 += 32 * kVecs) {
-    uint4 val[kVecs];
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      const int e = e0 + 32 * i;
-      if (e < 2 * per) val[i] = e >= per ? __ldcs(p.v + src0 + (e - per)) : __ldcs(p.k + src0 + e);
-    }
+    if (e0 != lane) request(e0);
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
       const int e = e0 + 32 * i;
