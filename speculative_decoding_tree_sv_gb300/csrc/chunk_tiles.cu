@@ -436,6 +436,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           return phys;
         };
+        // Q of this piece, once the previous piece's last QK^T is done: behind
+        // the piece's first K tile, but first of all in the CTA's first piece
+        // (the sixteen copies of a K tile take 4000 cycles to issue there).
+        auto load_q = [&]() {
+          if (k > 0 && !wait_all(q_empty, (k - 1) & 1)) return false;
+          if (lane == 0) {
+            const uint32_t bytes = static_cast<uint32_t>(p.tile_tokens * G) * 128u * C::kHalves;
+            mbar_arrive_expect_tx(q_full, bytes * pc.nt);
+            for (int t = 0; t < pc.nt; ++t)
+              for (int h = 0; h < C::kHalves; ++h)
+                tma_load_3d(smem + C::kOffQ + t * C::kTileBytes + h * C::kHalfBytes, &tm_q, q_full, h * 64,
+                            pc.kh * G, pc.n0 + pc.tok0 + t * p.tile_tokens);
+          }
+          q_issued = k + 1;
+          __syncwarp();
+          return true;
+        };
+        if (is_k && k == 0 && !load_q()) { ok = false; break; }
         int row, phys = page_of(pc.ja, &row);
         for (int j = pc.ja; j < pc.je; ++j) {
           int row2 = 0, phys2 = 0;
@@ -454,20 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           row = row2;
           phys = phys2;
-          if (is_k && j == pc.ja) {
-            // Q of this piece, once the previous piece's last QK^T is done
-            if (k > 0 && !wait_all(q_empty, (k - 1) & 1)) { ok = false; break; }
-            if (lane == 0) {
-              const uint32_t bytes = static_cast<uint32_t>(p.tile_tokens * G) * 128u * C::kHalves;
-              mbar_arrive_expect_tx(q_full, bytes * pc.nt);
-              for (int t = 0; t < pc.nt; ++t)
-                for (int h = 0; h < C::kHalves; ++h)
-                  tma_load_3d(smem + C::kOffQ + t * C::kTileBytes + h * C::kHalfBytes, &tm_q, q_full, h * 64,
-                              pc.kh * G, pc.n0 + pc.tok0 + t * p.tile_tokens);
-            }
-            q_issued = k + 1;
-            __syncwarp();
-          }
+          if (is_k && j == pc.ja && k > 0 && !load_q()) { ok = false; break; }
         }
       }
       if (!ok) {
