@@ -20,10 +20,13 @@ constexpr int kCombineThreads = 256;
 constexpr int kCombineWarps = kCombineThreads / 32;
 constexpr int kTileBlocks = 16;  // blocks per cut tile unit: two M tiles x eight runs of 16 rows
 
-// A row unit: its rows, and parts of its pieces where warps are left over, go
-// to the warps, a lane per D / 32 columns, four partial rows in flight.
+// Rows of a row unit (every split-th one): they, and parts of the pieces where
+// warps are left over, go to the warps, a lane per D / 32 columns, four partial
+// rows in flight.  With few units, cut into up to 150 pieces each, a block
+// takes a single row (one sequence of 4000 tokens: 30.6 us with a block per
+// unit, 9.2 us so).
 template <int D, bool FP16>
-__device__ __forceinline__ void combine_rows(const Params& p, int unit) {
+__device__ __forceinline__ void combine_rows(const Params& p, int unit, int row0, int split) {
   constexpr int E = D / 32;
   __shared__ float part_o[kCombineWarps][D];
   __shared__ float part_m[kCombineWarps], part_w[kCombineWarps];
@@ -34,12 +37,12 @@ __device__ __forceinline__ void combine_rows(const Params& p, int unit) {
   const int first = u.x, pieces = u.y - u.x + 1;
   if (s.n == 0 || !in_rows(p, s.n) || first < 0 || u.y >= p.row_workers || pieces <= 1)
     return;  // (a kernel that timed out left no record)
-  const int rows = s.n * p.group;
-  const int parts = pieces <= 4 ? 1 : rows <= 1 ? 8 : rows <= 2 ? 4 : rows <= 4 ? 2 : 1;
+  const int rows = s.n * p.group, here = (rows - row0 + split - 1) / split;  // rows of this block
+  const int parts = pieces <= 4 ? 1 : here <= 1 ? 8 : here <= 2 ? 4 : here <= 4 ? 2 : 1;
   const int part = warp % parts, per = (pieces + parts - 1) / parts;
   const int end = min((part + 1) * per, pieces);
-  for (int r0 = 0; r0 < rows; r0 += kCombineWarps / parts) {
-    const int r = r0 + warp / parts;
+  for (int r0 = 0; r0 < here; r0 += kCombineWarps / parts) {
+    const int r = row0 + (r0 + warp / parts) * split;
     float acc[E], mx = -INFINITY, wsum = 0.f;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
@@ -176,21 +179,31 @@ __device__ __forceinline__ void combine_tiles(const Params& p, int block) {
 }
 
 template <int D, bool FP16, bool ROWS, bool TILES>
-__global__ void __launch_bounds__(kCombineThreads, 6) chunk_combine_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kCombineThreads, 6) chunk_combine_kernel(const __grid_constant__ Params p,
+                                                                            int split) {
   griddep_wait();
   griddep_launch_dependents();
   const int block = blockIdx.x, tile_blocks = TILES ? p.tile_ctas * kTileBlocks : 0;
   if (TILES && block < tile_blocks) combine_tiles<D, FP16>(p, block);
-  if (ROWS && block >= tile_blocks) combine_rows<D, FP16>(p, block - tile_blocks);
+  if (ROWS && block >= tile_blocks)
+    combine_rows<D, FP16>(p, (block - tile_blocks) / split, (block - tile_blocks) % split, split);
 }
 
-bool encode_pool(CUtensorMap* map, const void* base, const Launch& l) {
+bool encode_pool(CUtensorMap* map, const void* base, const Launch& l, bool whole) {
   const cuuint64_t D = static_cast<cuuint64_t>(l.head_dim), H = static_cast<cuuint64_t>(l.p.num_kv_heads);
-  const cuuint64_t dims[4] = {D, kPage, H, static_cast<cuuint64_t>(l.p.num_pages)};
+  const cuuint64_t pages = static_cast<cuuint64_t>(l.p.num_pages);
+  const CUtensorMapDataType type = l.fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  if (whole) {
+    const cuuint64_t dims[5] = {64, kPage, D / 64, H, pages};
+    const cuuint64_t strides[4] = {D * 2, 128, kPage * D * 2, H * kPage * D * 2};
+    const cuuint32_t box[5] = {64, kPage, static_cast<cuuint32_t>(D / 64), 1, 1};
+    return encode_tiled(map, type, 5, const_cast<void*>(base), dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B) == CUDA_SUCCESS;
+  }
+  const cuuint64_t dims[4] = {D, kPage, H, pages};
   const cuuint64_t strides[3] = {D * 2, kPage * D * 2, H * kPage * D * 2};
   const cuuint32_t box[4] = {64, kPage, 1, 1};
-  return encode_tiled(map, l.fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
-                      const_cast<void*>(base), dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B,
+  return encode_tiled(map, type, 4, const_cast<void*>(base), dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B,
                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B) == CUDA_SUCCESS;
 }
 
@@ -258,7 +271,11 @@ sv_status check(const sv_chunk_params* c) {
 template <int D, bool FP16>
 sv_status launch_combine(const Launch& l) {
   const int tile_blocks = l.p.tile_ctas * kTileBlocks;
-  const int row_blocks = l.p.row_workers > 0 ? l.p.batch * l.p.num_kv_heads : 0;
+  const int units = l.p.row_workers > 0 ? l.p.batch * l.p.num_kv_heads : 0;
+  const long long most = static_cast<long long>(l.p.max_tokens) * l.p.group;
+  const int rows = most < kRowUnit ? static_cast<int>(most) : kRowUnit;
+  const int split = units <= 64 ? rows : 1;
+  const int row_blocks = units * split;
   auto* kernel = tile_blocks == 0  ? chunk_combine_kernel<D, FP16, true, false>
                  : row_blocks == 0 ? chunk_combine_kernel<D, FP16, false, true>
                                    : chunk_combine_kernel<D, FP16, true, true>;
@@ -271,7 +288,7 @@ sv_status launch_combine(const Launch& l) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, l.p) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, kernel, l.p, split) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 
 }  // namespace chunk

@@ -145,8 +145,9 @@ struct Launch {
   cudaStream_t stream;
 };
 
-// Tensor map of the pool, 16 rows x 64 columns of one (page, head) per box.
-bool encode_pool(CUtensorMap* map, const void* base, const Launch& l);
+// Tensor map of the pool, 16 rows x 64 columns of one (page, head) per box, or
+// with `whole` every 64-column half of its rows, one after another.
+bool encode_pool(CUtensorMap* map, const void* base, const Launch& l, bool whole);
 
 sv_status launch_rows(const Launch& l);
 sv_status launch_tiles(const Launch& l);

@@ -9,7 +9,8 @@
 // Bound by HBM: a page of K and V (2 * 16 * D * 2 bytes) is read once and
 // takes 2 * 2 * 16 * 16 * D operations, 16 per byte.  What the memory system
 // needs is bytes in flight, so a worker is a single warp with a ring of its
-// own (24 KB, TMA boxes of 16 rows x 128 bytes, 128-byte swizzle), 8 warps
+// own (24 KB; a page's K, and its V, is one TMA box of D / 64 halves of 16 rows
+// x 128 bytes, 128-byte swizzle), 8 warps
 // per SM hold 192 KB in flight, and no barrier joins them: a warp waits only
 // for its own pages.  At 16 rows the products are mma.sync m16n8k16 (the
 // rows fill one such tile; a 128-row tcgen05 tile would be 7/8 empty).
@@ -39,8 +40,10 @@ struct RowCfg {
 };
 
 constexpr float kRescale = 8.0f;  // log2 units: O is rescaled only when a maximum grows by more than 2^8
-// A worker's least share in pages: below it more workers only add pieces to merge.
-constexpr int kMinPages = 2;
+// A range's least pages: shorter ones only add pieces to merge.  One sequence at
+// 8 KV heads: 500 tokens 7.9 / 8.8 us with 2 / 4, 4000 tokens 16.2 / 14.1, 16000
+// 18.4 / 18.3.
+__device__ __forceinline__ int min_pages(long long total) { return total <= 512 ? 2 : 4; }
 
 // What the worker's range holds of a sequence.
 struct RowSeq {
@@ -162,26 +165,35 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
   Share share;
   {
     RowSeq mine;  // of sequence `lane`: the only round when there are at most 32
-    mine.pages = 0;
-    for (int b0 = 0; b0 < p.batch; b0 += 32) {
-      const int b = b0 + lane;
-      RowSeq r;
-      r.pages = 0;
-      if (b < p.batch) r = row_seq(p, b, worker == 0);
-      if (b0 == 0) mine = r;
-      long long w = r.pages;
+    if (p.batch == 1) {
+      mine = row_seq(p, 0, worker == 0);
+      total = mine.pages;
+    } else {
+      mine.pages = 0;
+      for (int b0 = 0; b0 < p.batch; b0 += 32) {
+        const int b = b0 + lane;
+        RowSeq r;
+        r.pages = 0;
+        if (b < p.batch) r = row_seq(p, b, worker == 0);
+        if (b0 == 0) mine = r;
+        long long w = r.pages;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
-      total += w;
+        for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+        total += w;
+      }
     }
     total *= p.num_kv_heads;
-    const long long most = (total + kMinPages - 1) / kMinPages;
+    const long long most = (total + min_pages(total) - 1) / min_pages(total);
     workers = static_cast<int>(most < p.row_workers ? (most > 0 ? most : 1) : p.row_workers);
     share = share_of(total, workers);
     lo = worker < workers ? share.start(worker) : 0;
     hi = worker < workers ? share.start(worker + 1) : 0;
     long long base = 0;
     int bsel = p.batch;
+    if (p.batch == 1) {
+      bsel = 0;
+      start.seq = mine;
+    }
     for (int b0 = 0; b0 < p.batch && bsel == p.batch; b0 += 32) {
       const int b = b0 + lane;
       if (p.batch > 32) {
@@ -214,7 +226,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
     start.b = bsel;
     start.kh = 0;
     start.pos = base;
-    if (bsel < p.batch) {
+    if (bsel < p.batch && hi > lo) {
       start.kh = static_cast<int>(Share::divide(lo - base, start.seq.pages));
       start.pos = base + static_cast<long long>(start.kh) * start.seq.pages;
     }
@@ -256,12 +268,8 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
       const int st = issued % C::kStages;
       uint8_t* dst = ring + st * 2 * C::kPageBytes;
       mbar_arrive_expect_tx(full + st, 2 * C::kPageBytes);
-#pragma unroll
-      for (int h = 0; h < C::kHalves; ++h)
-        tma_load_4d(dst + h * C::kHalfBytes, &tm_k, full + st, h * 64, row, lp.kh, phys);
-#pragma unroll
-      for (int h = 0; h < C::kHalves; ++h)
-        tma_load_4d(dst + C::kPageBytes + h * C::kHalfBytes, &tm_v, full + st, h * 64, row, lp.kh, phys);
+      tma_load_5d(dst, &tm_k, full + st, 0, row, 0, lp.kh, phys);
+      tma_load_5d(dst + C::kPageBytes, &tm_v, full + st, 0, row, 0, lp.kh, phys);
     }
     ++issued;
     ++load_j;
@@ -465,7 +473,7 @@ static sv_status launch(const Launch& l) {
     }
   }
   CUtensorMap tm_k, tm_v;
-  if (!encode_pool(&tm_k, l.k_cache, l) || !encode_pool(&tm_v, l.v_cache, l)) return SV_ERR_CUDA;
+  if (!encode_pool(&tm_k, l.k_cache, l, true) || !encode_pool(&tm_v, l.v_cache, l, true)) return SV_ERR_CUDA;
   cudaLaunchConfig_t cfg = cudaLaunchConfig_t{};
   cfg.gridDim = dim3(static_cast<unsigned>(l.p.row_workers / kRowWarps), 1, 1);
   cfg.blockDim = dim3(kRowWarps * 32, 1, 1);

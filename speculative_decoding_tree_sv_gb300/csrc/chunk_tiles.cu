@@ -838,7 +838,7 @@ static sv_status launch(const Launch& l) {
     }
   }
   CUtensorMap tm_q, tm_k, tm_v;
-  if (!encode_pool(&tm_k, l.k_cache, l) || !encode_pool(&tm_v, l.v_cache, l)) return SV_ERR_CUDA;
+  if (!encode_pool(&tm_k, l.k_cache, l, false) || !encode_pool(&tm_v, l.v_cache, l, false)) return SV_ERR_CUDA;
   {
     const cuuint64_t dims[3] = {D, static_cast<cuuint64_t>(l.p.num_q_heads), static_cast<cuuint64_t>(l.p.total_tokens)};
     const cuuint64_t strides[2] = {D * 2, static_cast<cuuint64_t>(l.p.q_stride) * 2};
