@@ -113,7 +113,8 @@ __device__ __forceinline__ void combine_rows(const Params& p, int unit, int row0
 
 // 16 rows of one M tile of a tile unit: half a warp per 16 rows, two groups of
 // four columns per thread.  The record, then every piece's sum and columns are
-// requested in one round each (two pieces at a time: most cut units have two).
+// requested in one round each (four pieces at a time: most cut units have two, a
+// short chunk over a long context up to 152).
 template <int D, bool FP16>
 __device__ __forceinline__ void combine_tiles(const Params& p, int block) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -137,13 +138,15 @@ __device__ __forceinline__ void combine_tiles(const Params& p, int block) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
   float mx = -INFINITY, wsum = 0.f;
-  constexpr int kBatch = 2;
+  constexpr int kBatch = 4;
   for (int c0 = first; c0 <= last; c0 += kBatch) {
     float l2[kBatch];
     float4 v[kBatch][kCols];
 #pragma unroll
     for (int x = 0; x < kBatch; ++x) {
-      const size_t row = at(min(c0 + x, last));
+      l2[x] = -INFINITY;
+      if (c0 + x > last) continue;
+      const size_t row = at(c0 + x);
       l2[x] = __ldcg(p.tile_lse + row * kTileRows + r);
       const float4* src = reinterpret_cast<const float4*>(p.tile_o) + row * (D / 4) * kTileRows + r;
 #pragma unroll
@@ -152,7 +155,7 @@ __device__ __forceinline__ void combine_tiles(const Params& p, int block) {
 #pragma unroll
     for (int x = 0; x < kBatch; ++x) {
       // a piece without a visible key (or without a tile) has no sum, and its columns say nothing
-      if (c0 + x > last || l2[x] == -INFINITY) continue;
+      if (l2[x] == -INFINITY) continue;
       const float m = fmaxf(mx, l2[x]);
       const float keep = mx == m ? 1.f : ex2(mx - m), f = ex2(l2[x] - m);
       mx = m;
@@ -179,7 +182,7 @@ __device__ __forceinline__ void combine_tiles(const Params& p, int block) {
 }
 
 template <int D, bool FP16, bool ROWS, bool TILES>
-__global__ void __launch_bounds__(kCombineThreads, 6) chunk_combine_kernel(const __grid_constant__ Params p,
+__global__ void __launch_bounds__(kCombineThreads, 4) chunk_combine_kernel(const __grid_constant__ Params p,
                                                                             int split) {
   griddep_wait();
   griddep_launch_dependents();

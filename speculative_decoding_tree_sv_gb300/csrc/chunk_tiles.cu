@@ -143,16 +143,27 @@ __device__ void deal_pieces(const Params& p, int cta, Publish&& publish) {
   long long total = 0, heaviest = 0;
   int units = 0;
   TileSeq mine{};  // of sequence `lane`: the only round when there are at most 32
-  for (int b0 = 0; b0 < p.batch; b0 += 32) {
-    const int b = b0 + lane;
-    TileSeq t{};
-    if (b < p.batch) t = tile_seq(p, b, cta == 0 && p.row_workers == 0);
-    if (b0 == 0) mine = t;
-    long long w = t.weight, h = t.units > 0 ? last_weight(p, t.s, t.units) : 0;
+  auto heaviest_of = [&](const TileSeq& t) {
+    long long h = t.units > 0 ? last_weight(p, t.s, t.units) : 0;
     if (t.units > 1) {
       const long long h2 = full_weight(p, t.s, t.units - 1) - full_weight(p, t.s, t.units - 2);
       h = h2 > h ? h2 : h;
     }
+    return h;
+  };
+  const bool report = cta == 0 && p.row_workers == 0;
+  if (p.batch == 1) {  // (a prompt alone: no sums, less code to fetch)
+    mine = tile_seq(p, 0, report);
+    total = mine.weight;
+    units = mine.units;
+    heaviest = heaviest_of(mine);
+  }
+  for (int b0 = 0; b0 < p.batch && p.batch > 1; b0 += 32) {
+    const int b = b0 + lane;
+    TileSeq t{};
+    if (b < p.batch) t = tile_seq(p, b, report);
+    if (b0 == 0) mine = t;
+    long long w = t.weight, h = heaviest_of(t);
     int u = t.units;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -184,7 +195,7 @@ __device__ void deal_pieces(const Params& p, int cta, Publish&& publish) {
   bool open = hi > lo;
   if (open) {
     long long base = 0;
-    int bsel = p.batch;
+    int bsel = p.batch == 1 ? 0 : p.batch;
     for (int b0 = 0; b0 < p.batch && bsel == p.batch; b0 += 32) {
       const int b = b0 + lane;
       TileSeq t = mine;
