@@ -600,6 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t col_s = t ? C::kColS1 : C::kColS0;
     const uint32_t col_o = t ? C::kColO1 : C::kColO0;
+    const int r_tok = r / G, r_head = r - r_tok * G;  // the row's token within the M tile, and its head
     int tiles_done = 0, pieces_done = 0;
     bool ok = true;
     // Piece -1 is a rehearsal while the first loads are on their way: one tile
@@ -622,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int tok_a = pc.tok0 + t * p.tile_tokens;                  // the M tile's first and last token
       const int tok_b = min(pc.n, tok_a + p.tile_tokens) - 1;
-      const int tok_r = tok_a + r / G;
+      const int tok_r = tok_a + r_tok;
       const bool row_exists = r < p.tile_tokens * G && tok_r < pc.n;
       const int tok = min(tok_r, tok_b);
       const int hi = pc.ctx + tok;  // last visible position
@@ -755,7 +756,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float inv_l = (l_run > 0.f) ? 1.f / l_run : 0.f;
       const float lse2 = (l_run > 0.f) ? m_run + log2f(l_run) : -INFINITY;
       if (pc.slot < 0) {
-        const int head = pc.kh * G + r % G;
+        const int head = pc.kh * G + r_head;
         const long long token = pc.n0 + tok;
         const unsigned long long my_row = reinterpret_cast<unsigned long long>(
             static_cast<uint16_t*>(p.out) + token * p.out_stride + static_cast<long long>(head) * D);
