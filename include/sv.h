@@ -513,13 +513,13 @@ sv_status sv_specpv_full_trees(const int* cand_parents, const int* cand_tokens, 
  * head and layer, a bit copy of 16-bit elements.  new_ctx_lens[b] (optional,
  * must not alias ctx_lens) receives ctx_lens[b] + N_b.  The caller holds
  * pages for those slots (sv_pages_reserve).  Nothing else changes: rows
- * behind cu_tokens[B] are not read.
+ * between cu_tokens[B] and total_tokens are padding.
  *
  * k/v: [num_layers][total_tokens, Hkv, D], token_stride elements from a token
  * to the next (>= Hkv * D; slices of a fused projection's rows are fine),
  * layer_stride from a layer to the next.  k_cache/v_cache as for
  * sv_kv_commit.  All strides are multiples of 8.  head_dim is a multiple of
- * 8; num_layers <= 65535.  A sequence whose lengths do not fit its block
+ * 8; num_layers <= 65535; total_tokens <= 2^30.  A sequence whose lengths do not fit its block
  * table or the token rows is left out (SV_DEVERR_BAD_LENGTH, its length
  * stays); a slot whose page id is out of range is skipped
  * (SV_DEVERR_BAD_PAGE).  workspace optional (error word).
@@ -558,7 +558,7 @@ typedef struct sv_chunk_params {
   int head_dim;           /* D: 64 or 128                                    */
   int page_size;          /* 16                                              */
   int num_pages;          /* pages in this layer's pool (cache dim 0)        */
-  int total_tokens;       /* T = cu_tokens[B] (host copy), or rows of q      */
+  int total_tokens;       /* rows of q: cu_tokens[B] or more, <= 2^30        */
   int max_tokens;         /* >= max_b N_b (host copy)                        */
   int max_pages_per_seq;  /* row length of block_table                       */
   int dtype;              /* sv_dtype of q, the cache and out                */
@@ -599,8 +599,8 @@ sv_status sv_chunk_attention(const sv_chunk_params* params, sv_stream_t stream);
  * prefix of forked sequences) and must not be written; sv_pages_reserve
  * replaces it first.  All results are the same on every run: no atomic's
  * order shows.  page_size >= 1; num_pages <= 2097152; rows <= 65535.
- * workspace: sv_pages_workspace_size bytes, zero-filled once (error word and
- * scratch); release, fork and copy use its error word only.
+ * workspace: sv_pages_workspace_size bytes, zero-filled once (the error word;
+ * the rest is scratch); release, fork and copy use its error word only.
  * ---------------------------------------------------------------------- */
 sv_status sv_pages_workspace_size(int rows, int num_pages, size_t* bytes);
 

@@ -509,6 +509,9 @@ def sv_chunk_attention_workspace_size(params: sv_chunk_params) -> int:
 def sv_chunk_attention(params: sv_chunk_params, stream=None) -> None:
     """Causal attention of every sequence's new tokens over its paged cache,
     which already holds their K/V (see include/sv.h)."""
+    held = getattr(params, "tensors", None)
+    if held is not None:
+        _on_device(held[0])
     _check(load().sv_chunk_attention(ctypes.byref(params), _stream(stream)), "sv_chunk_attention")
 
 
@@ -626,8 +629,8 @@ def sv_pages_compact(block_table, held_pages, page_refs, block_table_out, page_r
     _ints("block_table_out", block_table_out, rows * width)
     _ints("page_refs_out", page_refs_out, pages)
     _ints("num_live", num_live, 1)
-    if _pairs(copy_src, copy_dst, copy_count) < pages // 2:
-        raise ValueError(f"copy_src and copy_dst need room for {pages // 2} entries")
+    if _pairs(copy_src, copy_dst, copy_count) < max(pages // 2, 1):
+        raise ValueError(f"copy_src and copy_dst need room for {max(pages // 2, 1)} entries")
     _on_device(block_table, held_pages, page_refs, block_table_out, page_refs_out, copy_src, copy_dst, copy_count,
                num_live, workspace)
     ws, ws_bytes = _space(workspace)

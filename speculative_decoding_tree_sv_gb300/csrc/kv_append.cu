@@ -131,7 +131,8 @@ extern "C" sv_status sv_kv_append(const void* k, const void* v, long long token_
   if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache)) return SV_ERR_INVALID_ARG;
   if (new_ctx_lens == ctx_lens) return SV_ERR_INVALID_ARG;
   if (workspace != nullptr && workspace_bytes < kWorkspaceHeader) return SV_ERR_WORKSPACE;
-  if (num_layers > 65535 || static_cast<long long>(num_kv_heads) * head_dim > (1 << 27)) return SV_ERR_UNSUPPORTED;
+  if (num_layers > 65535 || total_tokens > (1 << 30) || static_cast<long long>(num_kv_heads) * head_dim > (1 << 27))
+    return SV_ERR_UNSUPPORTED;
   append::Params p;
   p.k = static_cast<const uint4*>(k);
   p.v = static_cast<const uint4*>(v);

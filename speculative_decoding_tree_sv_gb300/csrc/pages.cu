@@ -165,8 +165,8 @@ struct PoolParams {
   int* copy_count;
   int* num_live;
   int* err;
-  int* sharers;   // [num_pages] zero between calls: entries of this call that name the page and share it
-  int* first_row; // [num_pages] zero between calls: INT_MAX - lowest such row
+  int* sharers;   // [num_pages] of pages that writers share: how many of this call's entries name it
+  int* first_row; // [num_pages] the same pages: INT_MAX - lowest such row
   int* taken;     // [num_pages] scratch: free pages by rank (reserve), rank of a moved page (compact)
   int* row_fresh; // [rows] pages a row takes, then their first rank
   int* row_copy;  // [rows] pairs a row appends, then their first index
@@ -266,7 +266,8 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kClusterT
   const int nfree = slice_bitmap<true>(p.refs, s, bits, before, sh.warp_sums);
   if (threadIdx.x == 0) sh.slice_total = nfree;
 
-  // 1. who else of this call writes to a shared page (a warp per row)
+  // 1. the shared pages that rows write to (a warp per row): their scratch, and
+  // whether the row takes part
   for (int b = gwarp; b < p.rows; b += kAllWarps) {
     int first, mid, need;
     bool part = write_range(p, b, lane == 0, &first, &mid, &need);
@@ -279,19 +280,30 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kClusterT
         if (lane == 0) report_error(p.err, SV_DEVERR_BAD_PAGE);
       } else {
         for (int lp = first + lane; lp < mid; lp += 32) {
-          const int page = row[lp];
-          if (p.refs[page] > 1) {
-            atomicAdd(p.sharers + page, 1);
-            atomicMax(p.first_row + page, 0x7fffffff - b);
-          }
+          p.sharers[row[lp]] = 0;
+          p.first_row[row[lp]] = 0;
         }
       }
     }
     if (lane == 0) p.row_copy[b] = part ? 0 : -1;
   }
   cluster_sync_all();
-  // 2. which entries get a page of their own: those are marked ~page in the
-  // table until step 4 (nothing of the counts changes before it)
+  // 2. how many entries of this call name each, and the lowest row
+  for (int b = gwarp; b < p.rows; b += kAllWarps) {
+    int first, mid, need;
+    if (p.row_copy[b] < 0 || !write_range(p, b, false, &first, &mid, &need)) continue;
+    const int* row = p.table + static_cast<size_t>(b) * p.width;
+    for (int lp = first + lane; lp < mid; lp += 32) {
+      const int page = row[lp];
+      if (p.refs[page] > 1) {
+        atomicAdd(p.sharers + page, 1);
+        atomicMax(p.first_row + page, 0x7fffffff - b);
+      }
+    }
+  }
+  cluster_sync_all();
+  // 3. which entries get a page of their own: those are marked ~page in the
+  // table until step 5 (nothing of the counts changes before it)
   for (int b = gwarp; b < p.rows; b += kAllWarps) {
     int first, mid, need;
     int fresh = 0, copies = p.row_copy[b];
@@ -322,7 +334,7 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kClusterT
     }
   }
   cluster_sync_all();
-  // 3. ranks: every CTA sums all rows and keeps the offsets of its own warps'
+  // 4. ranks: every CTA sums all rows and keeps the offsets of its own warps'
   // rows in place; the free pages below the total go to `taken` by rank
   int free_before, free_total;
   cluster_sums(&sh.slice_total, rank, &free_before, &free_total);
@@ -352,7 +364,7 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kClusterT
     }
   }
   cluster_sync_all();
-  // 4. hand them out (or take the marks back)
+  // 5. hand them out (or take the marks back)
   for (int b = gwarp; b < p.rows; b += kAllWarps) {
     int first, mid, need;
     if (p.row_copy[b] < 0 || !write_range(p, b, false, &first, &mid, &need)) continue;
@@ -390,13 +402,7 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kClusterT
     if (enough && lane == 0 && need > p.held[b]) p.row_fresh[b] = -need;  // the new held count, set below
   }
   cluster_sync_all();
-  // 5. the scratch back to zero, the held counts, the list's length
-  for (int i = threadIdx.x; i < s.n; i += kClusterThreads) {
-    if (p.sharers[s.first + i] != 0) {
-      p.sharers[s.first + i] = 0;
-      p.first_row[s.first + i] = 0;
-    }
-  }
+  // 6. the held counts, the list's length
   for (int b = rank * kClusterThreads + threadIdx.x; b < p.rows; b += kClusterCtas * kClusterThreads)
     if (p.row_fresh[b] < 0) p.held[b] = -p.row_fresh[b];
   if (rank == 0 && threadIdx.x == 0) {

@@ -38,7 +38,7 @@ def chunk(**over):
     (dict(batch=0), 1), (dict(batch=65536), 2), (dict(num_kv_heads=0), 1), (dict(num_q_heads=30), 1),
     (dict(num_q_heads=129, num_kv_heads=1), 2), (dict(head_dim=96), 2), (dict(head_dim=256), 2),
     (dict(page_size=32), 2), (dict(num_pages=0), 1), (dict(max_pages_per_seq=0), 1),
-    (dict(max_pages_per_seq=1 << 27), 2), (dict(total_tokens=-1), 1), (dict(max_tokens=-1), 1),
+    (dict(max_pages_per_seq=1 << 27), 2), (dict(total_tokens=-1), 1), (dict(total_tokens=(1 << 30) + 1), 2), (dict(max_tokens=-1), 1),
     (dict(dtype=2), 2), (dict(dtype=-1), 2), (dict(window_tokens=-1), 1), (dict(sink_tokens=-1), 1),
     (dict(window_tokens=(1 << 28) + 1), 2), (dict(flags=1), 1), (dict(sm_scale=float("nan")), 1),
     (dict(sm_scale=float("inf")), 1), (dict(q_stride=4095), 1), (dict(q_stride=4096 + 4), 1),
@@ -84,7 +84,7 @@ def test_append_refuses(lib):
     for bad in (dict(layers=0), dict(pages=0), dict(width=0), dict(batch=0), dict(total=-1), dict(heads=0), dict(page=0),
                 dict(ts=1016), dict(ts=1028), dict(ls=4), dict(ls=-8), dict(cs=4), dict(new=A)):
         assert call(**bad) == 1, bad          # (new: the context lengths themselves)
-    assert call(d=12) == 2 and call(d=0) == 2 and call(layers=65536) == 2
+    assert call(d=12) == 2 and call(d=0) == 2 and call(layers=65536) == 2 and call(total=(1 << 30) + 1) == 2
     assert call(ws=A, wsb=255) == 4
 
 

@@ -243,6 +243,39 @@ def test_other_stream_and_captured_graph():
     assert sv.sv_get_device_error(c.ws) == 0
 
 
+def test_a_call_on_another_current_device_is_refused():
+    c = Case([40], [1], 8, 2, 64, "bf16", seed=15)
+    p = c.params()
+
+    class Elsewhere:  # q as a tensor of the second GPU would answer
+        is_cuda, device = True, "cuda:1"
+
+        def get_device(self):
+            return 1
+
+    p.tensors = (Elsewhere(),) + p.tensors[1:]
+    with pytest.raises(ValueError, match="cuda:1"):
+        sv.sv_chunk_attention(p)
+
+
+def test_one_workspace_for_calls_of_many_shapes():
+    """Nothing in a workspace has to survive from call to call."""
+    cases = [Case([900, 3], [1, 1], 8, 2, 64, "bf16", seed=18), Case([900, 3, 200], [70, 1, 1], 32, 8, 128, "fp16", seed=19),
+             Case([0], [300], 6, 2, 64, "bf16", seed=20)]
+    params = [c.params() for c in cases]
+    size = max(c.ws.numel() for c in cases)
+    ws = torch.full((size,), 0xA5, dtype=torch.uint8, device="cuda")
+    ws[:256] = 0
+    for _ in range(2):
+        for c, p in zip(cases, params):
+            c.out.fill_(7.0)
+            p.workspace, p.workspace_bytes = ws.data_ptr(), size
+            sv.sv_chunk_attention(p)
+            torch.cuda.synchronize()
+            assert sv.sv_get_device_error(ws) == 0
+            c.check()
+
+
 def test_bad_lengths_and_pages_are_reported():
     c = Case([40, 20, 30], [1, 1, 50], 8, 2, 64, "bf16", seed=13)
     assert c.run() == 0

@@ -29,7 +29,9 @@ class DevicePool:
         self.model = oracle.Pool([[-1] * width for _ in range(rows)], [0] * rows, [0] * rows, [0] * pages, page_size)
         self.table, self.held = dev(self.model.table), dev(self.model.held)
         self.ctx, self.refs = dev(self.model.ctx), dev(self.model.refs)
-        self.ws = torch.zeros(sv.sv_pages_workspace_size(rows, pages), dtype=torch.uint8, device="cuda")
+        # scratch with whatever another call left in it; only the error word is zero
+        self.ws = torch.full((sv.sv_pages_workspace_size(rows, pages),), 0x5A, dtype=torch.uint8, device="cuda")
+        self.ws[:256] = 0
         n = max(rows, pages // 2)
         self.src, self.dst = torch.full((n,), -1, dtype=torch.int32, device="cuda"), torch.full((n,), -1, dtype=torch.int32, device="cuda")
         self.count, self.live = dev([0]), dev([0])
