@@ -11,6 +11,7 @@ fails with an error instead of falling back to anything else.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 from ctypes import c_float, c_int, c_longlong, c_size_t, c_void_p
 from typing import Optional
@@ -167,6 +168,26 @@ def load(path: Optional[str] = None):
     return lib
 
 
+_MARSHAL = None
+
+
+def _marshal():
+    """The module that checks and passes the cache operators' tensors."""
+    global _MARSHAL
+    if _MARSHAL is None:
+        load()
+        import torch  # noqa: F401  (its libraries must be in the process)
+        path = _build.marshal_path()
+        if not os.path.exists(path):
+            raise RuntimeError(f"_marshal.so is not built ({path}); run __graft_entry__.build() or "
+                               "python -m speculative_decoding_tree_sv_gb300.build")
+        spec = importlib.util.spec_from_file_location("_marshal", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _MARSHAL = module
+    return _MARSHAL
+
+
 def _ptr(x) -> Optional[int]:
     """Address of a device buffer: None, a raw device address, or a CUDA
     tensor.  A tensor in host memory is refused here, before the library
@@ -189,6 +210,17 @@ def _stream(stream) -> Optional[int]:
     if isinstance(stream, int):
         return stream
     return int(stream.cuda_stream)
+
+
+def _where(stream):
+    """The current device (-1 before CUDA is initialised) and the stream's handle."""
+    import torch
+    if not torch.cuda.is_initialized():
+        return -1, 0
+    device = torch.cuda.current_device()
+    if stream is None:
+        return device, torch._C._cuda_getCurrentRawStream(device)
+    return device, _stream(stream) or 0
 
 
 def _check(status: int, where: str):
@@ -520,33 +552,11 @@ def sv_kv_append(k, v, k_cache, v_cache, block_table, ctx_lens, cu_tokens, new_c
     """Copies a chunk's K/V to its cache slots.  k/v: [layers, T, Hkv, D], or
     [T, Hkv, D] with caches of one layer [pages, Hkv, page_size, D]; heads
     contiguous, any token and layer stride."""
-    layers, pages, Hkv, page, D, cache_stride = _pool(k_cache, v_cache)
-    shape, stride = k.shape, k.stride()
-    if len(shape) != k_cache.dim() - 1 or v.shape != shape or v.stride() != stride:
-        raise ValueError("k and v must have the cache's layers and the same shape and strides")
-    if k.dtype is not k_cache.dtype or v.dtype is not k_cache.dtype:
-        raise ValueError(f"k and v must have the cache's type {k_cache.dtype}")
-    T = shape[-3]
-    if shape[-2] != Hkv or shape[-1] != D or (len(shape) == 4 and shape[0] != layers):
-        raise ValueError(f"k must be [{layers} layers, tokens, {Hkv}, {D}], got {tuple(shape)}")
-    if D > 1 and stride[-1] != 1 or Hkv > 1 and stride[-2] != D:
-        raise ValueError("the heads of k and v must be contiguous")
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [batch, max_pages]")
-    B, width = block_table.shape
-    _ints("block_table", block_table)
-    _ints("ctx_lens", ctx_lens, B)
-    _ints("cu_tokens", cu_tokens, B + 1)
-    if new_ctx_lens is not None:
-        _ints("new_ctx_lens", new_ctx_lens, B)
-    _on_device(k, v, k_cache, v_cache, block_table, ctx_lens, cu_tokens, new_ctx_lens, workspace)
-    ws, ws_bytes = _space(workspace)
-    _check(load().sv_kv_append(k.data_ptr(), v.data_ptr(), stride[-3] if T > 1 else Hkv * D,
-                               stride[0] if layers > 1 else 0, k_cache.data_ptr(), v_cache.data_ptr(),
-                               cache_stride, layers, pages, block_table.data_ptr(), width,
-                               ctx_lens.data_ptr(), cu_tokens.data_ptr(), B, T, Hkv, D, page,
-                               None if new_ctx_lens is None else new_ctx_lens.data_ptr(), ws, ws_bytes,
-                               _stream(stream)), "sv_kv_append")
+    device, handle = _where(stream)
+    status = _marshal().kv_append(k, v, k_cache, v_cache, block_table, ctx_lens, cu_tokens, new_ctx_lens, workspace,
+                                  device, handle)
+    if status != SV_OK:
+        raise SvError(status, "sv_kv_append")
 
 
 def sv_pages_workspace_size(rows: int, num_pages: int) -> int:
@@ -555,69 +565,34 @@ def sv_pages_workspace_size(rows: int, num_pages: int) -> int:
     return int(n.value)
 
 
-def _state(block_table, held_pages, page_refs):
-    """(rows, max pages per row, pages of the pool) of the bookkeeping state."""
-    if block_table.dim() != 2 or page_refs.dim() != 1:
-        raise ValueError("block_table must be [rows, max_pages], page_refs [num_pages]")
-    rows, width = block_table.shape
-    _ints("block_table", block_table)
-    _ints("held_pages", held_pages, rows)
-    _ints("page_refs", page_refs)
-    return rows, width, page_refs.numel()
-
-
-def _pairs(copy_src, copy_dst, copy_count) -> int:
-    """Entries that both lists have room for."""
-    _ints("copy_src", copy_src)
-    _ints("copy_dst", copy_dst)
-    _ints("copy_count", copy_count, 1)
-    return min(copy_src.numel(), copy_dst.numel())
-
-
 def sv_pages_release(keep_lens, block_table, held_pages, page_refs, page_size: int = 16, workspace=None,
                      stream=None) -> None:
     """Gives back the pages behind keep_lens[b] tokens of every row."""
-    rows, width, pages = _state(block_table, held_pages, page_refs)
-    _ints("keep_lens", keep_lens, rows)
-    _on_device(keep_lens, block_table, held_pages, page_refs, workspace)
-    ws, ws_bytes = _space(workspace)
-    _check(load().sv_pages_release(keep_lens.data_ptr(), rows, block_table.data_ptr(), width, held_pages.data_ptr(),
-                                   page_refs.data_ptr(), pages, page_size, ws, ws_bytes, _stream(stream)),
-           "sv_pages_release")
+    device, handle = _where(stream)
+    status = _marshal().pages_release(keep_lens, block_table, held_pages, page_refs, page_size, workspace, device, handle)
+    if status != SV_OK:
+        raise SvError(status, "sv_pages_release")
 
 
 def sv_pages_fork(parents, children, block_table, ctx_lens, held_pages, page_refs, page_size: int = 16,
                   workspace=None, stream=None) -> None:
     """Row children[i] becomes a copy of row parents[i] that shares its pages."""
-    rows, width, pages = _state(block_table, held_pages, page_refs)
-    n = parents.numel()
-    _ints("parents", parents)
-    _ints("children", children, n)
-    _ints("ctx_lens", ctx_lens, rows)
-    _on_device(parents, children, block_table, ctx_lens, held_pages, page_refs, workspace)
-    if n == 0:
-        return
-    ws, ws_bytes = _space(workspace)
-    _check(load().sv_pages_fork(parents.data_ptr(), children.data_ptr(), n, block_table.data_ptr(), rows, width,
-                                ctx_lens.data_ptr(), held_pages.data_ptr(), page_refs.data_ptr(), pages, page_size,
-                                ws, ws_bytes, _stream(stream)), "sv_pages_fork")
+    device, handle = _where(stream)
+    status = _marshal().pages_fork(parents, children, block_table, ctx_lens, held_pages, page_refs, page_size, workspace,
+                                   device, handle)
+    if status != SV_OK:
+        raise SvError(status, "sv_pages_fork")
 
 
 def sv_pages_reserve(ctx_lens, new_lens, block_table, held_pages, page_refs, copy_src, copy_dst, copy_count,
                      page_size: int = 16, workspace=None, stream=None) -> None:
     """Makes the slots ctx_lens[b] .. new_lens[b] - 1 of every row writable and
     lists the pages to copy (sv_pages_copy) for those it had to replace."""
-    rows, width, pages = _state(block_table, held_pages, page_refs)
-    _ints("ctx_lens", ctx_lens, rows)
-    _ints("new_lens", new_lens, rows)
-    if _pairs(copy_src, copy_dst, copy_count) < rows:
-        raise ValueError(f"copy_src and copy_dst need room for {rows} entries")
-    _on_device(ctx_lens, new_lens, block_table, held_pages, page_refs, copy_src, copy_dst, copy_count, workspace)
-    ws, ws_bytes = _space(workspace)
-    _check(load().sv_pages_reserve(ctx_lens.data_ptr(), new_lens.data_ptr(), rows, block_table.data_ptr(), width,
-                                   held_pages.data_ptr(), page_refs.data_ptr(), pages, page_size,
-                                   copy_src.data_ptr(), copy_dst.data_ptr(), copy_count.data_ptr(), ws, ws_bytes,
-                                   _stream(stream)), "sv_pages_reserve")
+    device, handle = _where(stream)
+    status = _marshal().pages_reserve(ctx_lens, new_lens, block_table, held_pages, page_refs, copy_src, copy_dst,
+                                      copy_count, page_size, workspace, device, handle)
+    if status != SV_OK:
+        raise SvError(status, "sv_pages_reserve")
 
 
 def sv_pages_compact(block_table, held_pages, page_refs, block_table_out, page_refs_out, copy_src, copy_dst,
@@ -625,33 +600,21 @@ def sv_pages_compact(block_table, held_pages, page_refs, block_table_out, page_r
     """Moves the used pages to the front of the pool: lists the copies and
     writes the tables and references after them (the outputs may be the
     inputs themselves)."""
-    rows, width, pages = _state(block_table, held_pages, page_refs)
-    _ints("block_table_out", block_table_out, rows * width)
-    _ints("page_refs_out", page_refs_out, pages)
-    _ints("num_live", num_live, 1)
-    if _pairs(copy_src, copy_dst, copy_count) < max(pages // 2, 1):
-        raise ValueError(f"copy_src and copy_dst need room for {max(pages // 2, 1)} entries")
-    _on_device(block_table, held_pages, page_refs, block_table_out, page_refs_out, copy_src, copy_dst, copy_count,
-               num_live, workspace)
-    ws, ws_bytes = _space(workspace)
-    _check(load().sv_pages_compact(block_table.data_ptr(), held_pages.data_ptr(), rows, width, page_refs.data_ptr(),
-                                   pages, block_table_out.data_ptr(), page_refs_out.data_ptr(), copy_src.data_ptr(),
-                                   copy_dst.data_ptr(), copy_count.data_ptr(), num_live.data_ptr(), ws, ws_bytes,
-                                   _stream(stream)), "sv_pages_compact")
+    device, handle = _where(stream)
+    status = _marshal().pages_compact(block_table, held_pages, page_refs, block_table_out, page_refs_out, copy_src,
+                                      copy_dst, copy_count, num_live, workspace, device, handle)
+    if status != SV_OK:
+        raise SvError(status, "sv_pages_compact")
 
 
 def sv_pages_copy(k_cache, v_cache, copy_src, copy_dst, copy_count, workspace=None, stream=None) -> None:
     """Copies the listed pages in every layer.  Caches [layers, pages, ...] of
     five dimensions, or one layer [pages, ...] of four; v_cache may be None.
     Page summaries [pages, Hkv, 2, D] are such a pool too."""
-    layers, pages, Hkv, page, D, stride = _pool(k_cache, v_cache)
-    most = _pairs(copy_src, copy_dst, copy_count)
-    _on_device(k_cache, v_cache, copy_src, copy_dst, copy_count, workspace)
-    ws, ws_bytes = _space(workspace)
-    _check(load().sv_pages_copy(k_cache.data_ptr(), None if v_cache is None else v_cache.data_ptr(), stride, layers,
-                                pages, Hkv * page * D, copy_src.data_ptr(), copy_dst.data_ptr(),
-                                copy_count.data_ptr(), most, ws, ws_bytes, _stream(stream)),
-           "sv_pages_copy")
+    device, handle = _where(stream)
+    status = _marshal().pages_copy(k_cache, v_cache, copy_src, copy_dst, copy_count, workspace, device, handle)
+    if status != SV_OK:
+        raise SvError(status, "sv_pages_copy")
 
 
 TRACE_SLOTS = 16

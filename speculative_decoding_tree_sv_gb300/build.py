@@ -2,15 +2,19 @@
 
 Each CUDA translation unit is compiled in parallel, then linked into one
 shared library with the CUDA runtime linked statically (the library loads on
-machines without a GPU driver; the driver is resolved at first use).
+machines without a GPU driver; the driver is resolved at first use).  Beside
+it goes ``lib/_marshal.so``, the Python module that checks and passes the
+cache operators' tensors (compiled against the installed torch's headers).
 """
 
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -35,6 +39,17 @@ def library_path() -> str:
     return os.path.join(LIBDIR, LIBNAME)
 
 
+def marshal_path() -> str:
+    return os.path.join(LIBDIR, "_marshal.so")
+
+
+def _torch_dir() -> str:
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        raise RuntimeError("torch not found: the Python module compiles against its headers")
+    return spec.submodule_search_locations[0]
+
+
 def _deps():
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
     files.append(os.path.join(INCLUDE, "sv.h"))
@@ -43,10 +58,10 @@ def _deps():
 
 
 def up_to_date() -> bool:
-    lib = library_path()
-    if not os.path.exists(lib):
+    built = [library_path(), marshal_path()]
+    if not all(os.path.exists(f) for f in built):
         return False
-    t = os.path.getmtime(lib)
+    t = min(os.path.getmtime(f) for f in built)
     return all(os.path.getmtime(f) <= t for f in _deps())
 
 
@@ -71,8 +86,23 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stderr}")
         return obj, r.stderr
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    def compile_marshal():
+        obj = os.path.join(objdir, "marshal.o")
+        torch_dir = _torch_dir()
+        include = [os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+                   sysconfig.get_paths()["include"]]
+        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-c", os.path.join(CSRC, "marshal.cpp"), "-o", obj]
+        for path in include:
+            cmd += ["-isystem", path]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed for marshal.cpp:\n{r.stderr}")
+        return obj
+
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        module = ex.submit(compile_marshal)
         results = list(ex.map(compile_one, SOURCES))
+        module_obj = module.result()
     if verbose or ptxas_info:
         for (_, err), src in zip(results, SOURCES):
             if err.strip():
@@ -83,6 +113,14 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, lib)
+    tmp = marshal_path() + ".tmp"
+    # torch's libraries are in the process by the time the module is loaded
+    cmd = ["g++", "-shared", "-o", tmp, module_obj, "-L", LIBDIR, "-l:" + LIBNAME, "-Wl,-rpath,$ORIGIN",
+           "-L", os.path.join(_torch_dir(), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of _marshal.so failed:\n{r.stderr}")
+    os.replace(tmp, marshal_path())
     return lib
 
 
