@@ -3,11 +3,11 @@
 //
 // The state is the block table, the pages held per row and a reference count
 // per page; there is no free list to keep in step with them.  Where pages are
-// taken (reserve) or moved (compact), one cluster of 8 CTAs reads the counts
-// once into shared-memory bitmaps, ranks them by population counts and
-// exchanges its eight totals through distributed shared memory, so the
-// lowest-numbered free pages go out in (row, logical page) order: the same
-// result on every run, in one launch without a wait on another grid.  These
+// taken (reserve) or moved (compact), one cluster of 8 CTAs (a single CTA for
+// small pools) reads the counts once into shared-memory bitmaps, ranks them by
+// population counts and exchanges its totals through distributed shared memory,
+// so the lowest-numbered free pages go out in (row, logical page) order: the
+// same result on every run, in one launch without a wait on another grid.  These
 // kernels are bound by latency (a few dependent loads and cluster barriers);
 // sv_pages_copy is bound by HBM.
 #include <cooperative_groups.h>
@@ -19,7 +19,13 @@
 namespace sv {
 namespace pages {
 
+// CTAs of the pool kernels' cluster; a small pool with a row per warp at most
+// takes a single one, whose barriers are cheaper (reserve, one CTA / eight: 3 rows
+// and 73 pages 3.1 / 6.1 us; 80 rows and 1705 pages 6.7 / 5.1.  Compact: 256 pages
+// 3.2 / 5.0; 8192 pages 12.4 / 7.8).
 constexpr int kClusterCtas = 8;
+constexpr int kSmallPool = 1024;
+constexpr int kSmallRows = 16;
 constexpr int kClusterThreads = 512;
 constexpr int kWarps = kClusterThreads / 32;
 constexpr int kMaxPages = 1 << 21;  // bitmap of an eighth: 32 KB, and as much for its word ranks
@@ -178,9 +184,10 @@ struct Slice {
   int first, n, words;
 };
 
+template <int CTAS>
 __device__ __forceinline__ Slice slice_of(int num_pages, int rank) {
   const int words = (num_pages + 31) / 32;
-  const int per = (words + kClusterCtas - 1) / kClusterCtas;
+  const int per = (words + CTAS - 1) / CTAS;
   Slice s;
   s.first = min(rank * per * 32, num_pages);
   s.n = min((rank + 1) * per * 32, num_pages) - s.first;
@@ -218,13 +225,26 @@ struct PoolShared {
   int warp_sums[kWarps];
 };
 
+// All threads of the kernel.
+template <int CTAS>
+__device__ __forceinline__ void sync_all() {
+  if constexpr (CTAS == 1) __syncthreads();
+  else cluster_sync_all();
+}
+
 // Sum of a value over the cluster's CTAs and over the CTAs before this one.
+template <int CTAS>
 __device__ __forceinline__ void cluster_sums(int* mine, int rank, int* before, int* total) {
+  if constexpr (CTAS == 1) {
+    *before = 0;
+    *total = *mine;
+    return;
+  }
   namespace cg = cooperative_groups;
   cg::cluster_group cl = cg::this_cluster();
   int b = 0, t = 0;
 #pragma unroll
-  for (int r = 0; r < kClusterCtas; ++r) {
+  for (int r = 0; r < CTAS; ++r) {
     const int v = *cl.map_shared_rank(mine, r);
     if (r < rank) b += v;
     t += v;
@@ -250,17 +270,18 @@ __device__ __forceinline__ bool write_range(const PoolParams& p, int b, bool rep
   return true;
 }
 
-__global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kClusterThreads)
+template <int CTAS>
+__global__ void __launch_bounds__(kClusterThreads)
     reserve_kernel(const __grid_constant__ PoolParams p) {
   extern __shared__ uint32_t dyn[];
   __shared__ PoolShared sh;
-  const int rank = cluster_ctarank();
+  const int rank = CTAS == 1 ? 0 : cluster_ctarank();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gwarp = rank * kWarps + warp;
-  constexpr int kAllWarps = kClusterCtas * kWarps;
+  constexpr int kAllWarps = CTAS * kWarps;
   griddep_wait();
   griddep_launch_dependents();
-  const Slice s = slice_of(p.num_pages, rank);
+  const Slice s = slice_of<CTAS>(p.num_pages, rank);
   uint32_t* bits = dyn;
   int* before = reinterpret_cast<int*>(dyn + s.words);
   const int nfree = slice_bitmap<true>(p.refs, s, bits, before, sh.warp_sums);
@@ -287,7 +308,7 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kClusterT
     }
     if (lane == 0) p.row_copy[b] = part ? 0 : -1;
   }
-  cluster_sync_all();
+  sync_all<CTAS>();
   // 2. how many entries of this call name each, and the lowest row
   for (int b = gwarp; b < p.rows; b += kAllWarps) {
     int first, mid, need;
@@ -301,7 +322,7 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kClusterT
       }
     }
   }
-  cluster_sync_all();
+  sync_all<CTAS>();
   // 3. which entries get a page of their own: those are marked ~page in the
   // table until step 5 (nothing of the counts changes before it)
   for (int b = gwarp; b < p.rows; b += kAllWarps) {
@@ -333,11 +354,11 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kClusterT
       p.row_copy[b] = copies;
     }
   }
-  cluster_sync_all();
+  sync_all<CTAS>();
   // 4. ranks: every CTA sums all rows and keeps the offsets of its own warps'
   // rows in place; the free pages below the total go to `taken` by rank
   int free_before, free_total;
-  cluster_sums(&sh.slice_total, rank, &free_before, &free_total);
+  cluster_sums<CTAS>(&sh.slice_total, rank, &free_before, &free_total);
   long long want = 0;  // up to rows * width
   int copies = 0;
   for (int b0 = 0; b0 < p.rows; b0 += kClusterThreads) {
@@ -363,7 +384,7 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kClusterT
       if (((m >> lane) & 1u) && r < want) p.taken[r] = s.first + w * 32 + lane;
     }
   }
-  cluster_sync_all();
+  sync_all<CTAS>();
   // 5. hand them out (or take the marks back)
   for (int b = gwarp; b < p.rows; b += kAllWarps) {
     int first, mid, need;
@@ -401,9 +422,9 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kClusterT
     __syncwarp();
     if (enough && lane == 0 && need > p.held[b]) p.row_fresh[b] = -need;  // the new held count, set below
   }
-  cluster_sync_all();
+  sync_all<CTAS>();
   // 6. the held counts, the list's length
-  for (int b = rank * kClusterThreads + threadIdx.x; b < p.rows; b += kClusterCtas * kClusterThreads)
+  for (int b = rank * kClusterThreads + threadIdx.x; b < p.rows; b += CTAS * kClusterThreads)
     if (p.row_fresh[b] < 0) p.held[b] = -p.row_fresh[b];
   if (rank == 0 && threadIdx.x == 0) {
     *p.copy_count = enough ? copies : 0;
@@ -411,22 +432,23 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kClusterT
   }
 }
 
-__global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kClusterThreads)
+template <int CTAS>
+__global__ void __launch_bounds__(kClusterThreads)
     compact_kernel(const __grid_constant__ PoolParams p) {
   extern __shared__ uint32_t dyn[];
   __shared__ PoolShared sh;
-  const int rank = cluster_ctarank();
+  const int rank = CTAS == 1 ? 0 : cluster_ctarank();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   griddep_wait();
   griddep_launch_dependents();
-  const Slice s = slice_of(p.num_pages, rank);
+  const Slice s = slice_of<CTAS>(p.num_pages, rank);
   uint32_t* bits = dyn;
   int* before = reinterpret_cast<int*>(dyn + s.words);
   const int nlive = slice_bitmap<false>(p.refs_in, s, bits, before, sh.warp_sums);
   if (threadIdx.x == 0) sh.slice_total = nlive;
-  cluster_sync_all();
+  sync_all<CTAS>();
   int live_before, live;
-  cluster_sums(&sh.slice_total, rank, &live_before, &live);
+  cluster_sums<CTAS>(&sh.slice_total, rank, &live_before, &live);
   // used pages below the count: whole words by their prefix, the cut word by its bits
   if (threadIdx.x == 0) {
     int below = 0;
@@ -435,9 +457,9 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kClusterT
     else if (cut > 0) below = before[cut >> 5] + __popc(bits[cut >> 5] & ((1u << (cut & 31)) - 1u));
     sh.below_total = below;
   }
-  cluster_sync_all();
+  sync_all<CTAS>();
   int dummy, below;
-  cluster_sums(&sh.below_total, rank, &dummy, &below);
+  cluster_sums<CTAS>(&sh.below_total, rank, &dummy, &below);
   const int moves = live - below;  // free pages below the count = used pages from it on
   for (int w = warp; w < s.words; w += kWarps) {
     const uint32_t m = bits[w];
@@ -456,8 +478,8 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kClusterT
       }
     }
   }
-  cluster_sync_all();
-  for (int k = rank * kClusterThreads + threadIdx.x; k < moves; k += kClusterCtas * kClusterThreads) {
+  sync_all<CTAS>();
+  for (int k = rank * kClusterThreads + threadIdx.x; k < moves; k += CTAS * kClusterThreads) {
     const int src = p.copy_src[k], dst = p.copy_dst[k];
     const int r = p.refs_in[src];
     p.refs_out[dst] = r;
@@ -468,7 +490,7 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kClusterT
     *p.num_live = live;
   }
   // the tables, a warp per row: a page from the count on follows its move
-  for (int b = rank * kWarps + warp; b < p.rows; b += kClusterCtas * kWarps) {
+  for (int b = rank * kWarps + warp; b < p.rows; b += CTAS * kWarps) {
     int held = p.held[b];
     if (held < 0 || held > p.width) {
       if (lane == 0) report_error(p.err, SV_DEVERR_BAD_LENGTH);
@@ -511,7 +533,7 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kClusterT
       }
     }
   }
-  cluster_sync_all();  // no CTA leaves while another reads its totals
+  sync_all<CTAS>();  // no CTA leaves while another reads its totals
 }
 
 // ---------------------------------------------------------------- copy
@@ -587,23 +609,31 @@ void set_scratch(PoolParams* p, void* workspace, int rows, int num_pages) {
   p->num_pages = num_pages;
 }
 
-size_t pool_smem(int num_pages) {
+// Bitmap and word ranks of one CTA's slice.
+size_t pool_smem(int num_pages, int ctas) {
   const int words = (num_pages + 31) / 32;
-  return static_cast<size_t>((words + kClusterCtas - 1) / kClusterCtas) * 8 + 16;
+  return static_cast<size_t>((words + ctas - 1) / ctas) * 8 + 16;
+}
+
+int pool_ctas(int rows, int num_pages) {
+  return num_pages <= kSmallPool && rows <= kSmallRows ? 1 : kClusterCtas;
 }
 
 template <typename P, typename K>
-sv_status launch(K kernel, const P& p, unsigned grid, unsigned threads, size_t smem, sv_stream_t stream) {
+sv_status launch(K kernel, const P& p, unsigned grid, unsigned threads, size_t smem, sv_stream_t stream,
+                 unsigned cluster = 1) {
   cudaLaunchConfig_t cfg = cudaLaunchConfig_t{};
   cfg.gridDim = dim3(grid, 1, 1);
   cfg.blockDim = dim3(threads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {cluster, 1, 1};
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 
@@ -615,9 +645,12 @@ bool configure_pool() {
   if (cudaGetDevice(&dev) != cudaSuccess) return false;
   std::lock_guard<std::mutex> lock(mu);
   if (dev < 64 && done[dev]) return true;
-  const int most = static_cast<int>(pool_smem(kMaxPages));
-  if (cudaFuncSetAttribute(reserve_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess ||
-      cudaFuncSetAttribute(compact_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess)
+  // (the single CTA's slice of a small pool fits the default)
+  const int most = static_cast<int>(pool_smem(kMaxPages, kClusterCtas));
+  if (cudaFuncSetAttribute(reserve_kernel<kClusterCtas>, cudaFuncAttributeMaxDynamicSharedMemorySize, most) !=
+          cudaSuccess ||
+      cudaFuncSetAttribute(compact_kernel<kClusterCtas>, cudaFuncAttributeMaxDynamicSharedMemorySize, most) !=
+          cudaSuccess)
     return false;
   if (dev < 64) done[dev] = true;
   return true;
@@ -696,8 +729,9 @@ sv_status sv_pages_reserve(const int* ctx_lens, const int* new_lens, int rows, i
   p.copy_count = copy_count;
   p.width = max_pages_per_seq;
   p.page_size = page_size;
-  return pages::launch(pages::reserve_kernel, p, pages::kClusterCtas, pages::kClusterThreads,
-                       pages::pool_smem(num_pages), stream);
+  const int ctas = pages::pool_ctas(rows, num_pages);
+  return pages::launch(ctas == 1 ? pages::reserve_kernel<1> : pages::reserve_kernel<pages::kClusterCtas>, p, ctas,
+                       pages::kClusterThreads, pages::pool_smem(num_pages, ctas), stream, ctas);
 }
 
 sv_status sv_pages_compact(const int* block_table, const int* held_pages, int rows, int max_pages_per_seq,
@@ -725,8 +759,9 @@ sv_status sv_pages_compact(const int* block_table, const int* held_pages, int ro
   p.copy_count = copy_count;
   p.num_live = num_live;
   p.width = max_pages_per_seq;
-  return pages::launch(pages::compact_kernel, p, pages::kClusterCtas, pages::kClusterThreads,
-                       pages::pool_smem(num_pages), stream);
+  const int ctas = pages::pool_ctas(rows, num_pages);
+  return pages::launch(ctas == 1 ? pages::compact_kernel<1> : pages::compact_kernel<pages::kClusterCtas>, p, ctas,
+                       pages::kClusterThreads, pages::pool_smem(num_pages, ctas), stream, ctas);
 }
 
 sv_status sv_pages_copy(void* k_cache, void* v_cache, long long cache_layer_stride, int num_layers,

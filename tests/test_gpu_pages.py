@@ -69,7 +69,7 @@ class DevicePool:
         self.ctx.copy_(dev(lens))
 
 
-@pytest.mark.parametrize("seed,rows,width,pages,page", [(0, 5, 9, 40, 16), (1, 1, 4, 3, 16), (2, 40, 20, 700, 16),
+@pytest.mark.parametrize("seed,rows,width,pages,page", [(0, 5, 9, 40, 16), (1, 1, 4, 3, 16), (2, 40, 20, 700, 16), (6, 16, 9, 1024, 16), (7, 17, 9, 1024, 16),
                                                          (3, 7, 33, 97, 1), (4, 300, 40, 5000, 5), (5, 600, 3, 1111, 64)])
 def test_random_lives_match_the_pool(seed, rows, width, pages, page):
     rng = random.Random(seed)
@@ -119,7 +119,7 @@ def test_random_lives_match_the_pool(seed, rows, width, pages, page):
         m.check()
 
 
-@pytest.mark.parametrize("pages", [31, 32, 33, 255, 256, 257, 8193, 2097152])
+@pytest.mark.parametrize("pages", [31, 32, 33, 255, 256, 257, 1024, 1025, 8193, 2097152])
 def test_pool_sizes_around_the_bitmap_words(pages):
     """The last pages of the pool are found and moved."""
     d = DevicePool(2, 40, pages, Hkv=1, D=8, layers=1) if pages < 10000 else None
