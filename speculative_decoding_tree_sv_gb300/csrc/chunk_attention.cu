@@ -210,9 +210,15 @@ bool encode_pool(CUtensorMap* map, const void* base, const Launch& l, bool whole
                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B) == CUDA_SUCCESS;
 }
 
+// Widths in pages: of units to warps, of a unit to a CTA (kCtaEven of them with few
+// units, where the other SMs would idle), of tile units that surely stay whole.
+constexpr int kWarpPages = 32, kCtaPages = 256, kCtaEven = 64, kWholePages = 64;
+
 // Where the parts of a call lie in its workspace, and which kernels it needs.
 struct Plan {
   int row_workers, tile_ctas;
+  int row_mode, whole_tiles;
+  bool combine;
   size_t row_o, row_lse, row_units, tile_o, tile_lse, tile_units, bytes;
 };
 
@@ -228,6 +234,25 @@ Plan make_plan(const sv_chunk_params* c, int sms) {
   const bool some_small = G <= kRowUnit && !(some_large && least * G > kRowUnit);
   w.row_workers = some_small ? sms * kRowWarps : 0;
   w.tile_ctas = some_large ? sms : 0;
+  // What the host sees of the contexts is the table's width.  Short ones do
+  // without ranges and their combine.  A unit per CTA takes about 0.1 us a page,
+  // the ranges as much for the units' even share of the SMs and 4 us more: 8 units
+  // of 7 / 32 / 63 / 94 pages 4.8 / 7.1 / 9.7 / 12.3 against 8.2 / 8.0 / 9.9 / 11.0
+  // us, 128 of 63 / 94 / 188 10.0 / 13.3 / 34 against 15.2 / 18.3 / 39.  Units to
+  // the warps: 2048 of 7 / 13 / 32 pages 19.3 / 37 / 81 against 31.5 / 49 / 95 us.
+  const long long units = static_cast<long long>(c->batch) * c->num_kv_heads;
+  const int width = c->max_pages_per_seq;
+  if (units <= sms)
+    w.row_mode = width <= 2                                                              ? kRowWarp
+                 : width <= kCtaPages && width * (sms - units) <= kCtaEven * static_cast<long long>(sms) ? kRowCta
+                                                                                         : kRowRanges;
+  else
+    w.row_mode = width <= kWarpPages ? kRowWarp : kRowRanges;
+  // Tile units at one per CTA whose heaviest is below what cutting costs stay
+  // whole anyway; there are at most one more than full ones per sequence.
+  const long long groups = c->total_tokens / (2 * (kTileRows / G)) + c->batch;
+  w.whole_tiles = groups * c->num_kv_heads <= sms && c->max_pages_per_seq <= kWholePages;
+  w.combine = (w.row_workers > 0 && w.row_mode == kRowRanges) || (w.tile_ctas > 0 && !w.whole_tiles);
   size_t at = kWorkspaceHeader;
   auto take = [&](size_t bytes) {
     const size_t o = at;
@@ -273,8 +298,8 @@ sv_status check(const sv_chunk_params* c) {
 
 template <int D, bool FP16>
 sv_status launch_combine(const Launch& l) {
-  const int tile_blocks = l.p.tile_ctas * kTileBlocks;
-  const int units = l.p.row_workers > 0 ? l.p.batch * l.p.num_kv_heads : 0;
+  const int tile_blocks = l.p.whole_tiles ? 0 : l.p.tile_ctas * kTileBlocks;
+  const int units = l.p.row_workers > 0 && l.p.row_mode == kRowRanges ? l.p.batch * l.p.num_kv_heads : 0;
   const long long most = static_cast<long long>(l.p.max_tokens) * l.p.group;
   const int rows = most < kRowUnit ? static_cast<int>(most) : kRowUnit;
   const int split = units <= 64 ? rows : 1;
@@ -354,6 +379,8 @@ sv_status sv_chunk_attention(const sv_chunk_params* params, sv_stream_t stream) 
   p.tile_lse = reinterpret_cast<float*>(base + w.tile_lse);
   p.tile_units = reinterpret_cast<int4*>(base + w.tile_units);
   p.row_workers = w.row_workers;
+  p.row_mode = w.row_mode;
+  p.whole_tiles = w.whole_tiles;
   p.tile_ctas = w.tile_ctas;
   l.k_cache = params->k_cache;
   l.v_cache = params->v_cache;
@@ -368,6 +395,7 @@ sv_status sv_chunk_attention(const sv_chunk_params* params, sv_stream_t stream) 
     const sv_status r = chunk::launch_rows(l);
     if (r != SV_OK) return r;
   }
+  if (!w.combine) return SV_OK;
   if (l.head_dim == 128) return l.fp16 ? chunk::launch_combine<128, true>(l) : chunk::launch_combine<128, false>(l);
   return l.fp16 ? chunk::launch_combine<64, true>(l) : chunk::launch_combine<64, false>(l);
 }

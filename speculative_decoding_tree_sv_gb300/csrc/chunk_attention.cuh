@@ -26,6 +26,13 @@ constexpr int kRowWarps = 8;     // workers per CTA of the row kernel
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kLog2e = 1.44269504088896340736f;
 
+// How the row kernel shares its units out.
+enum RowMode {
+  kRowRanges = 0,  // equal ranges of all pages; the combine merges cut units
+  kRowWarp = 1,    // whole units to the warps in turn
+  kRowCta = 2      // a unit per CTA, its pages shared by the warps
+};
+
 struct Params {
   const void* q;
   const int* block_table;
@@ -48,6 +55,8 @@ struct Params {
   float* tile_lse;       // [ctas][2][256]
   int4* tile_units;      // [ctas]: the cut unit that starts in this CTA: first token row, tokens (0: none), KV head, last CTA
   int row_workers;       // 0: no row kernel in this call
+  int row_mode;          // RowMode
+  int whole_tiles;       // the tile kernel's units stay whole, so that nothing is left to combine
   int tile_ctas;         // 0: no tile kernel in this call
 };
 

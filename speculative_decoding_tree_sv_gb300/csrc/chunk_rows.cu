@@ -16,7 +16,10 @@
 // rows fill one such tile; a 128-row tcgen05 tile would be 7/8 empty).
 //
 // The pages of all units form one list (sequence, KV head, page); worker w
-// takes an equal contiguous range.  Page ids are fetched 32 at a time.  The
+// takes an equal contiguous range, and the combine kernel merges the units that
+// a boundary cuts.  Short contexts (the host sees the table's width) go without
+// it: a warp takes whole units, or a CTA a unit whose pages its warps share and
+// merge in shared memory (RowMode).  Page ids are fetched 32 at a time.  The
 // last page of a sequence may hold anything behind its last token: its box
 // starts at a negative row, so the missing rows in front arrive as zeros and
 // its tokens end at row 15.
@@ -63,10 +66,12 @@ __device__ __forceinline__ RowSeq row_seq(const Params& p, int b, bool report) {
   return r;
 }
 
-// Walks the units of a range in order: sequence b, KV head kh.
+// Walks the units of a range in order: sequence b, KV head kh (or, in the modes
+// without ranges, every step-th unit).
 struct RowCursor {
   long long pos;  // first page position of the current unit
   int b, kh;
+  int unit, step;
   RowSeq seq;
 };
 
@@ -77,6 +82,20 @@ struct RowPiece {
 };
 
 __device__ __forceinline__ bool next_piece(const Params& p, RowCursor& c, long long lo, long long hi, RowPiece& out) {
+  if (p.row_mode != kRowRanges) {
+    for (; c.unit < p.batch * p.num_kv_heads;) {
+      out.b = c.unit / p.num_kv_heads;
+      out.kh = c.unit - out.b * p.num_kv_heads;
+      out.pos = 0;
+      out.seq = row_seq(p, out.b, out.kh == 0);
+      c.unit += c.step;
+      const int warp = threadIdx.x >> 5, pages = out.seq.pages;
+      out.j0 = p.row_mode == kRowCta ? pages * warp / kRowWarps : 0;
+      out.j1 = p.row_mode == kRowCta ? pages * (warp + 1) / kRowWarps : pages;
+      if (out.j0 < out.j1) return true;
+    }
+    return false;
+  }
   while (c.b < p.batch && c.pos < hi) {
     if (c.seq.pages == 0 || c.kh == p.num_kv_heads) {
       ++c.b;
@@ -137,6 +156,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[kRowWarps * C::kStages];
   __shared__ int abort_word;
+  __shared__ float cta_lse[kRowWarps][kRowUnit];
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -146,6 +166,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
   if (lane == 0) {
     for (int i = 0; i < C::kStages; ++i) mbar_init(full + i, 1);
     if (warp == 0) abort_word = 0;
+    for (int r = 0; r < kRowUnit; ++r) cta_lse[warp][r] = -INFINITY;
     fence_mbar_init();
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
@@ -160,10 +181,12 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
   // consecutive ranges go to different CTAs, so few workers spread over the SMs
   const int worker = warp * gridDim.x + blockIdx.x;
   RowCursor start;
-  long long lo, hi, total = 0;
-  int workers;
-  Share share;
-  {
+  long long lo = 0, hi = 1, total = 0;
+  int workers = p.row_workers;
+  Share share{};
+  start.unit = p.row_mode == kRowCta ? blockIdx.x : worker;
+  start.step = p.row_mode == kRowCta ? p.batch * p.num_kv_heads : p.row_workers;  // (a CTA takes one unit)
+  if (p.row_mode == kRowRanges) {
     RowSeq mine;  // of sequence `lane`: the only round when there are at most 32
     if (p.batch == 1) {
       mine = row_seq(p, 0, worker == 0);
@@ -411,7 +434,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
     }
-    const bool whole = pc.j0 == 0 && pc.j1 == pc.seq.pages;
+    const bool whole = p.row_mode != kRowCta && pc.j0 == 0 && pc.j1 == pc.seq.pages;
     const int slot = pc.j0 == 0 ? 1 : 0;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -428,14 +451,16 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
         for (int nb = 0; nb < D / 8; ++nb) dst[nb * 4] = pack2<FP16>(o[nb][2 * i] * inv, o[nb][2 * i + 1] * inv);
         if (tq == 0 && p.lse != nullptr) p.lse[token * p.num_q_heads + head] = lse2 * kLn2;
       } else {
+        // (a CTA's shared unit leaves its rows in the ring, which is empty by now)
         const size_t at = (static_cast<size_t>(worker) * 2 + slot) * kRowUnit + r;
-        float2* dst = reinterpret_cast<float2*>(p.row_o + at * D) + tq;
+        float* row = p.row_mode == kRowCta ? reinterpret_cast<float*>(ring) + r * D : p.row_o + at * D;
+        float2* dst = reinterpret_cast<float2*>(row) + tq;
 #pragma unroll
         for (int nb = 0; nb < D / 8; ++nb) dst[nb * 4] = make_float2(o[nb][2 * i] * inv, o[nb][2 * i + 1] * inv);
-        if (tq == 0) p.row_lse[at] = lse2;
+        if (tq == 0) *(p.row_mode == kRowCta ? &cta_lse[warp][r] : p.row_lse + at) = lse2;
       }
     }
-    if (pc.j0 == 0 && lane == 0) {
+    if (p.row_mode == kRowRanges && pc.j0 == 0 && lane == 0) {
       // the workers of the unit's first and last page
       const int last = whole ? worker : share.holder(pc.pos + pc.seq.pages - 1);
       p.row_units[static_cast<size_t>(pc.b) * p.num_kv_heads + pc.kh] = make_int2(worker, last);
@@ -450,6 +475,41 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
       for (int i = done; i < issued; ++i) mbar_wait(full + i % C::kStages, (i / C::kStages) & 1, &never);
     }
     __syncwarp();
+  }
+  if (p.row_mode == kRowCta) {
+    __syncthreads();
+    if (blockIdx.x < p.batch * p.num_kv_heads && !*abort_flag) {
+      const int b = blockIdx.x / p.num_kv_heads, kh = blockIdx.x - b * p.num_kv_heads;
+      const RowSeq s = row_seq(p, b, false);
+      const int rows = s.pages > 0 ? s.s.n * p.group : 0;
+      constexpr int E = D / 32;  // columns per lane
+      for (int r = warp; r < rows; r += kRowWarps) {
+        float acc[E], mx = -INFINITY, wsum = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 1
+        for (int x = 0; x < kRowWarps; ++x) {
+          const float l2 = cta_lse[x][r];
+          if (l2 == -INFINITY) continue;
+          const float* part = reinterpret_cast<const float*>(smem + x * C::kRingBytes) + r * D;
+          const float m = fmaxf(mx, l2);
+          const float keep = ex2(mx - m), f = ex2(l2 - m);  // keep is 0 at the first, as mx = -inf
+          mx = m;
+          wsum = fmaf(wsum, keep, f);
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] = fmaf(f, part[lane * E + e], acc[e] * keep);
+        }
+        const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+        const int tok = r / p.group, head = kh * p.group + r - tok * p.group;
+        const long long token = s.s.n0 + tok;
+        uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + token * p.out_stride +
+                                                    static_cast<long long>(head) * D) + lane * (E / 2);
+#pragma unroll
+        for (int e = 0; e < E; e += 2) dst[e / 2] = pack2<FP16>(acc[e] * inv, acc[e + 1] * inv);
+        if (lane == 0 && p.lse != nullptr)
+          p.lse[token * p.num_q_heads + head] = wsum > 0.f ? (mx + log2f(wsum)) * kLn2 : -INFINITY;
+      }
+    }
   }
   // The combine waits for this grid; one CTA that waits for the tile kernel
   // makes that mean both (the last one, so that no free SM is held).

@@ -182,7 +182,7 @@ __device__ void deal_pieces(const Params& p, int cta, Publish&& publish) {
   // no more than equal shares with their partials and the combine.
   const long long rounds = share_of(all + p.tile_ctas - 1, p.tile_ctas).each;
   const Share even = share_of(total, p.tile_ctas);
-  const bool whole_units = rounds * heaviest <= even.each + kCutWeight;
+  const bool whole_units = p.whole_tiles || rounds * heaviest <= even.each + kCutWeight;
   if (whole_units) total = all;
   auto weight_of = [&](const TileSeq& t) { return whole_units ? static_cast<long long>(t.units) : t.weight; };
   auto prefix = [&](const TileSeq& t, int m) { return whole_units ? static_cast<long long>(m) : full_weight(p, t.s, m); };

@@ -149,6 +149,26 @@ def test_long_contexts_are_cut_between_workers():
     c.check()
 
 
+@pytest.mark.parametrize("width", [1, 2, 3, 32, 33, 64, 65, 256, 257])
+@pytest.mark.parametrize("batch,Hq,Hkv", [(1, 8, 2), (40, 16, 4)])
+def test_widths_around_the_ways_of_sharing_units(width, batch, Hq, Hkv):
+    """The row kernel shares its units out by the table's width; every sequence
+    fills its own part of it, one all of it."""
+    rng = np.random.default_rng(width)
+    full = (width - 1) * 16  # Case gives the table one entry more than the longest needs
+    ctx = [max(full - 1, 0)] + rng.integers(0, max(full, 1), batch - 1).tolist()
+    new = [1 if full else 0] + [1] * (batch - 1) if full else [1] * batch
+    c = Case(ctx, new, Hq, Hkv, 64, "bf16", seed=width)
+    assert c.run() == 0
+    c.check()
+    short = [i for i in range(batch) if ctx[i] < 200][:3]
+    if batch > 1 and short:  # and with chunks among them
+        new = [40 if i in short else n for i, n in enumerate(new)]
+        c = Case(ctx, new, Hq, Hkv, 64, "fp16", seed=width + 1)
+        assert c.run() == 0
+        c.check()
+
+
 def test_many_sequences():
     rng = np.random.default_rng(5)
     ctx = rng.integers(0, 60, 300).tolist()
