@@ -216,7 +216,7 @@ def _where(stream):
     """The current device (-1 before CUDA is initialised) and the stream's handle."""
     import torch
     if not torch.cuda.is_initialized():
-        return -1, 0
+        return -1, (_stream(stream) or 0) if stream is not None else 0
     device = torch.cuda.current_device()
     if stream is None:
         return device, torch._C._cuda_getCurrentRawStream(device)
@@ -541,10 +541,11 @@ def sv_chunk_attention_workspace_size(params: sv_chunk_params) -> int:
 def sv_chunk_attention(params: sv_chunk_params, stream=None) -> None:
     """Causal attention of every sequence's new tokens over its paged cache,
     which already holds their K/V (see include/sv.h)."""
+    device, handle = _where(stream)
     held = getattr(params, "tensors", None)
-    if held is not None:
+    if held is not None and held[0].get_device() != device:
         _on_device(held[0])
-    _check(load().sv_chunk_attention(ctypes.byref(params), _stream(stream)), "sv_chunk_attention")
+    _check(load().sv_chunk_attention(ctypes.byref(params), handle), "sv_chunk_attention")
 
 
 def sv_kv_append(k, v, k_cache, v_cache, block_table, ctx_lens, cu_tokens, new_ctx_lens=None, workspace=None,

@@ -240,14 +240,20 @@ Plan make_plan(const sv_chunk_params* c, int sms) {
   // of 7 / 32 / 63 / 94 pages 4.8 / 7.1 / 9.7 / 12.3 against 8.2 / 8.0 / 9.9 / 11.0
   // us, 128 of 63 / 94 / 188 10.0 / 13.3 / 34 against 15.2 / 18.3 / 39.  Units to
   // the warps: 2048 of 7 / 13 / 32 pages 19.3 / 37 / 81 against 31.5 / 49 / 95 us.
+  // More units than CTAs, in rounds that are seven tenths full: 256 of up to 82
+  // pages 27.5 against 30.5 us, 1024 of 63 69.6 / 77; 192 of 63 (the second round a
+  // quarter full) 18.9 against 17.3.
   const long long units = static_cast<long long>(c->batch) * c->num_kv_heads;
   const int width = c->max_pages_per_seq;
-  if (units <= sms)
+  const bool fits = static_cast<long long>(c->max_tokens) * G <= kCtaRows;
+  if (fits && units <= sms)
     w.row_mode = width <= 2                                                              ? kRowWarp
                  : width <= kCtaPages && width * (sms - units) <= kCtaEven * static_cast<long long>(sms) ? kRowCta
                                                                                          : kRowRanges;
   else
-    w.row_mode = width <= kWarpPages ? kRowWarp : kRowRanges;
+    w.row_mode = width <= kWarpPages                                                          ? kRowWarp
+                 : fits && width <= kCtaPages && 10 * units >= 7 * sms * ((units + sms - 1) / sms) ? kRowCta
+                                                                                                : kRowRanges;
   // Tile units at one per CTA whose heaviest is below what cutting costs stay
   // whole anyway; there are at most one more than full ones per sequence.
   const long long groups = c->total_tokens / (2 * (kTileRows / G)) + c->batch;
@@ -260,9 +266,11 @@ Plan make_plan(const sv_chunk_params* c, int sms) {
     return o;
   };
   const size_t D = static_cast<size_t>(c->head_dim);
+  // (as large for calls that cut no unit: a workspace for many sequences and
+  // tokens of both kinds then serves fewer of them, whichever kernels they take)
   w.row_o = take(static_cast<size_t>(w.row_workers) * 2 * kRowUnit * D * sizeof(float));
   w.row_lse = take(static_cast<size_t>(w.row_workers) * 2 * kRowUnit * sizeof(float));
-  w.row_units = take(w.row_workers ? static_cast<size_t>(c->batch) * c->num_kv_heads * sizeof(int2) : 0);
+  w.row_units = take(w.row_workers ? static_cast<size_t>(units) * sizeof(int2) : 0);
   w.tile_o = take(static_cast<size_t>(w.tile_ctas) * 2 * kGroupRows * D * sizeof(float));
   w.tile_lse = take(static_cast<size_t>(w.tile_ctas) * 2 * kGroupRows * sizeof(float));
   w.tile_units = take(static_cast<size_t>(w.tile_ctas) * sizeof(int4));

@@ -23,6 +23,7 @@ constexpr int kRowUnit = 16;     // rows of a row-kernel unit
 constexpr int kTileRows = 128;   // rows of an M tile of the tile kernel
 constexpr int kGroupRows = 256;  // rows of a tile-kernel unit: two M tiles
 constexpr int kRowWarps = 8;     // workers per CTA of the row kernel
+constexpr int kCtaRows = 8;      // rows of a unit that a CTA's warps may share (what fits beside their rings)
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kLog2e = 1.44269504088896340736f;
 
@@ -30,7 +31,7 @@ constexpr float kLog2e = 1.44269504088896340736f;
 enum RowMode {
   kRowRanges = 0,  // equal ranges of all pages; the combine merges cut units
   kRowWarp = 1,    // whole units to the warps in turn
-  kRowCta = 2      // a unit per CTA, its pages shared by the warps
+  kRowCta = 2      // whole units to the CTAs in turn, their pages shared by the warps
 };
 
 struct Params {

@@ -39,7 +39,10 @@ struct RowCfg {
   static constexpr int kPageBytes = kPage * D * 2;  // K or V of one page and head
   static constexpr int kStages = (D == 128) ? 3 : 6;
   static constexpr int kRingBytes = kStages * 2 * kPageBytes;  // 24 KB
-  static constexpr int kSmemBytes = kRowWarps * kRingBytes + 1024;
+  // parts of a CTA's unit: [8 warps][rows][D] floats
+  static constexpr int kPartBytes = kRowWarps * kCtaRows * D * 4;
+  static constexpr int kSmemBytes = kRowWarps * kRingBytes + kPartBytes + 1024;
+  static_assert(kSmemBytes + 2048 <= 232448, "shared memory per CTA");
 };
 
 constexpr float kRescale = 8.0f;  // log2 units: O is rescaled only when a maximum grows by more than 2^8
@@ -92,7 +95,7 @@ __device__ __forceinline__ bool next_piece(const Params& p, RowCursor& c, long l
       const int warp = threadIdx.x >> 5, pages = out.seq.pages;
       out.j0 = p.row_mode == kRowCta ? pages * warp / kRowWarps : 0;
       out.j1 = p.row_mode == kRowCta ? pages * (warp + 1) / kRowWarps : pages;
-      if (out.j0 < out.j1) return true;
+      if (pages > 0) return true;  // (a warp's share of a CTA's unit may be empty)
     }
     return false;
   }
@@ -162,11 +165,11 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* ring = smem + warp * C::kRingBytes;
   uint64_t* full = bars + warp * C::kStages;
+  float* parts = reinterpret_cast<float*>(smem + kRowWarps * C::kRingBytes);
   volatile int* abort_flag = &abort_word;
   if (lane == 0) {
     for (int i = 0; i < C::kStages; ++i) mbar_init(full + i, 1);
     if (warp == 0) abort_word = 0;
-    for (int r = 0; r < kRowUnit; ++r) cta_lse[warp][r] = -INFINITY;
     fence_mbar_init();
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
@@ -185,7 +188,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
   int workers = p.row_workers;
   Share share{};
   start.unit = p.row_mode == kRowCta ? blockIdx.x : worker;
-  start.step = p.row_mode == kRowCta ? p.batch * p.num_kv_heads : p.row_workers;  // (a CTA takes one unit)
+  start.step = p.row_mode == kRowCta ? gridDim.x : p.row_workers;
   if (p.row_mode == kRowRanges) {
     RowSeq mine;  // of sequence `lane`: the only round when there are at most 32
     if (p.batch == 1) {
@@ -262,7 +265,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
   bool more = hi > lo;
   auto issue = [&]() {
     if (!more) return;
-    if (load_j >= lp.j1) {
+    while (load_j >= lp.j1) {
       if (!next_piece(p, load_cur, lo, hi, lp)) {
         more = false;
         return;
@@ -306,7 +309,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
   RowPiece pc;
   int done = 0;
   bool ok = true;
-  while (ok && hi > lo && next_piece(p, cur, lo, hi, pc)) {
+  while ((ok || p.row_mode == kRowCta) && hi > lo && next_piece(p, cur, lo, hi, pc)) {
     const Seq& s = pc.seq.s;
     const Keys& keys = pc.seq.keys;
     const int rows = s.n * p.group;
@@ -337,7 +340,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
       for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 
-    for (int j = pc.j0; j < pc.j1; ++j) {
+    for (int j = pc.j0; ok && j < pc.j1; ++j) {
       const int st = done % C::kStages;
       if (!__all_sync(0xffffffffu, mbar_wait(full + st, (done / C::kStages) & 1, abort_flag))) {
         ok = false;
@@ -427,7 +430,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
       __syncwarp();  // every lane has read the stage
       issue();
     }
-    if (!ok) break;
+    if (!ok && p.row_mode != kRowCta) break;
     // ---- the piece's rows
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -435,6 +438,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
     }
     const bool whole = p.row_mode != kRowCta && pc.j0 == 0 && pc.j1 == pc.seq.pages;
+    if (p.row_mode == kRowCta) __syncthreads();  // the unit before is merged
     const int slot = pc.j0 == 0 ? 1 : 0;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -451,13 +455,43 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
         for (int nb = 0; nb < D / 8; ++nb) dst[nb * 4] = pack2<FP16>(o[nb][2 * i] * inv, o[nb][2 * i + 1] * inv);
         if (tq == 0 && p.lse != nullptr) p.lse[token * p.num_q_heads + head] = lse2 * kLn2;
       } else {
-        // (a CTA's shared unit leaves its rows in the ring, which is empty by now)
         const size_t at = (static_cast<size_t>(worker) * 2 + slot) * kRowUnit + r;
-        float* row = p.row_mode == kRowCta ? reinterpret_cast<float*>(ring) + r * D : p.row_o + at * D;
+        float* row = p.row_mode == kRowCta ? parts + (warp * rows + r) * D : p.row_o + at * D;
         float2* dst = reinterpret_cast<float2*>(row) + tq;
 #pragma unroll
         for (int nb = 0; nb < D / 8; ++nb) dst[nb * 4] = make_float2(o[nb][2 * i] * inv, o[nb][2 * i + 1] * inv);
         if (tq == 0) *(p.row_mode == kRowCta ? &cta_lse[warp][r] : p.row_lse + at) = lse2;
+      }
+    }
+    if (p.row_mode == kRowCta) {
+      // the warps' parts of the unit, a row per warp, a lane per D / 32 columns
+      __syncthreads();
+      constexpr int E = D / 32;
+      for (int r = warp; r < rows; r += kRowWarps) {
+        float acc[E], mx = -INFINITY, wsum = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 1
+        for (int x = 0; x < kRowWarps; ++x) {
+          const float l2 = cta_lse[x][r];
+          if (l2 == -INFINITY) continue;
+          const float* part = parts + (x * rows + r) * D + lane * E;
+          const float m_new = fmaxf(mx, l2);
+          const float keep = ex2(mx - m_new), f = ex2(l2 - m_new);  // keep is 0 at the first, as mx = -inf
+          mx = m_new;
+          wsum = fmaf(wsum, keep, f);
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] = fmaf(f, part[e], acc[e] * keep);
+        }
+        const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+        const int row_tok = r / p.group, head = pc.kh * p.group + r - row_tok * p.group;
+        const long long token = s.n0 + row_tok;
+        uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + token * p.out_stride +
+                                                    static_cast<long long>(head) * D) + lane * (E / 2);
+#pragma unroll
+        for (int e = 0; e < E; e += 2) dst[e / 2] = pack2<FP16>(acc[e] * inv, acc[e + 1] * inv);
+        if (lane == 0 && p.lse != nullptr)
+          p.lse[token * p.num_q_heads + head] = wsum > 0.f ? (mx + log2f(wsum)) * kLn2 : -INFINITY;
       }
     }
     if (p.row_mode == kRowRanges && pc.j0 == 0 && lane == 0) {
@@ -475,41 +509,6 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
       for (int i = done; i < issued; ++i) mbar_wait(full + i % C::kStages, (i / C::kStages) & 1, &never);
     }
     __syncwarp();
-  }
-  if (p.row_mode == kRowCta) {
-    __syncthreads();
-    if (blockIdx.x < p.batch * p.num_kv_heads && !*abort_flag) {
-      const int b = blockIdx.x / p.num_kv_heads, kh = blockIdx.x - b * p.num_kv_heads;
-      const RowSeq s = row_seq(p, b, false);
-      const int rows = s.pages > 0 ? s.s.n * p.group : 0;
-      constexpr int E = D / 32;  // columns per lane
-      for (int r = warp; r < rows; r += kRowWarps) {
-        float acc[E], mx = -INFINITY, wsum = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll 1
-        for (int x = 0; x < kRowWarps; ++x) {
-          const float l2 = cta_lse[x][r];
-          if (l2 == -INFINITY) continue;
-          const float* part = reinterpret_cast<const float*>(smem + x * C::kRingBytes) + r * D;
-          const float m = fmaxf(mx, l2);
-          const float keep = ex2(mx - m), f = ex2(l2 - m);  // keep is 0 at the first, as mx = -inf
-          mx = m;
-          wsum = fmaf(wsum, keep, f);
-#pragma unroll
-          for (int e = 0; e < E; ++e) acc[e] = fmaf(f, part[lane * E + e], acc[e] * keep);
-        }
-        const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
-        const int tok = r / p.group, head = kh * p.group + r - tok * p.group;
-        const long long token = s.s.n0 + tok;
-        uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + token * p.out_stride +
-                                                    static_cast<long long>(head) * D) + lane * (E / 2);
-#pragma unroll
-        for (int e = 0; e < E; e += 2) dst[e / 2] = pack2<FP16>(acc[e] * inv, acc[e + 1] * inv);
-        if (lane == 0 && p.lse != nullptr)
-          p.lse[token * p.num_q_heads + head] = wsum > 0.f ? (mx + log2f(wsum)) * kLn2 : -INFINITY;
-      }
-    }
   }
   // The combine waits for this grid; one CTA that waits for the tile kernel
   // makes that mean both (the last one, so that no free SM is held).
