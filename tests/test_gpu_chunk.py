@@ -169,6 +169,76 @@ def test_widths_around_the_ways_of_sharing_units(width, batch, Hq, Hkv):
         c.check()
 
 
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("fp16", 64)])
+@pytest.mark.parametrize("Hq,Hkv,new", [(16, 2, 1), (8, 1, 1), (6, 2, 2), (14, 2, 1), (8, 8, 8), (18, 2, 1), (5, 5, 9)])
+def test_units_shared_by_a_block(Hq, Hkv, new, dtype, D):
+    """Up to eight rows of a unit and a table of up to 63 pages: the warps of a
+    block share it, some of them nothing of the short ones.  (Nine rows: one
+    more than they share.)"""
+    c = Case([977, 0, 1, 110, 128, 15, 500], [new] * 7, Hq, Hkv, D, dtype, seed=Hq + new)
+    assert c.run() == 0
+    c.check()
+
+
+@pytest.mark.parametrize("batch,Hkv,longest", [(60, 4, 1500), (76, 4, 600), (130, 2, 4000), (90, 2, 1500), (610, 4, 520)])
+@pytest.mark.parametrize("window,sink", [(0, 0), (200, 20)])
+def test_more_units_than_blocks(batch, Hkv, longest, window, sink):
+    """In rounds that are nearly full, and in rounds that are not; idle and short
+    sequences among them."""
+    rng = np.random.default_rng(batch)
+    ctx = rng.integers(0, longest, batch)
+    ctx[rng.random(batch) < 0.2] = 3
+    ctx[batch // 2] = longest
+    new = np.where(rng.random(batch) < 0.1, 0, 1)
+    new[0] = 1
+    c = Case(ctx.tolist(), new.tolist(), Hkv * 4, Hkv, 64, "bf16", window=window, sink=sink, seed=batch)
+    assert c.run() == 0
+    c.check()
+
+
+@pytest.mark.parametrize("new", [[40, 1, 70, 1, 3, 130], [1, 40], [0, 33, 1, 0]])
+def test_short_contexts_of_both_kinds(new):
+    """Whole units in both kernels: nothing is merged."""
+    ctx = [100, 0, 15, 300, 31, 64][:len(new)]
+    c = Case(ctx, new, 8, 2, 128, "bf16", seed=21, extra_rows=3)
+    assert c.run() == 0
+    c.check()
+
+
+@pytest.mark.parametrize("batch,longest", [(3, 10), (3, 900), (50, 900), (400, 100), (3, 9000)])
+def test_bad_lengths_and_pages_in_every_way_of_sharing(batch, longest):
+    """A sequence with a wrong length is left out, one with a wrong page id reads
+    zeros there; the others' results stay."""
+    rng = np.random.default_rng(batch + longest)
+    ctx = rng.integers(0, longest, batch).tolist()
+    ctx[1] = longest
+    c = Case(ctx, [1] * batch, 16, 4, 64, "bf16", seed=longest)
+    assert c.run() == 0
+    want = c.out.clone()
+    for at in (0, batch - 1):
+        keep = c.lens[at].clone()
+        for bad in (100000, -1):
+            c.lens[at] = bad
+            c.out.fill_(7.0)
+            assert c.run() == sv.SV_DEVERR_BAD_LENGTH
+            assert (c.out[at] == 7.0).all()
+            rest = torch.arange(batch, device="cuda") != at
+            # cut units move with the lengths, so both are off by the bound above: 2^-8 (A + |out|) + 2e-4 A
+            # each, A at most the largest |v|; 2 x 2e-4 A is less than a tenth of 2^-7 A
+            most = torch.nan_to_num(c.v.float()).abs().max()
+            diff = (c.out[rest].float() - want[rest].float()).abs()
+            assert (diff <= 1.1 * 2.0 ** -7 * (most + want[rest].float().abs())).all()
+        c.lens[at] = keep
+    page = c.table[1, 0].clone()
+    for bad in (c.pages, -7):
+        c.table[1, 0] = bad
+        assert c.run() == sv.SV_DEVERR_BAD_PAGE
+        rest = torch.arange(batch, device="cuda") != 1
+        assert torch.equal(c.out[rest], want[rest]) and torch.isfinite(c.out.float()).all()
+    c.table[1, 0] = page
+    assert c.run() == 0 and torch.equal(c.out, want)
+
+
 def test_many_sequences():
     rng = np.random.default_rng(5)
     ctx = rng.integers(0, 60, 300).tolist()
