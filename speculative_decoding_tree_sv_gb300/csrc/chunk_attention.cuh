@@ -24,6 +24,7 @@ constexpr int kTileRows = 128;   // rows of an M tile of the tile kernel
 constexpr int kGroupRows = 256;  // rows of a tile-kernel unit: two M tiles
 constexpr int kRowWarps = 8;     // workers per CTA of the row kernel
 constexpr int kCtaRows = 8;      // rows of a unit that a CTA's warps may share (what fits beside their rings)
+constexpr int kBlockN = 128;    // keys of a tile
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kLog2e = 1.44269504088896340736f;
 
@@ -107,6 +108,146 @@ __device__ __forceinline__ Keys unit_keys(const Params& p, const Seq& s, int t0,
     k.sink_pages = min((min(p.sink, k.end) + kPage - 1) / kPage, k.first_page);
   }
   return k;
+}
+
+// Weights in eighths of a key: a unit costs its keys plus kUnitKeys (Q load,
+// pipeline fill, epilogue); one M tile costs kHalfUnit eighths of two.
+constexpr int kUnitKeys = 192;
+constexpr int kHalfUnit = 5;
+constexpr long long kMinWeight = 8 * kBlockN;  // a CTA's least share
+// What cutting units costs a call, as weight: the partial rows a CTA writes and
+// the combine, about ten tiles of two M tiles.
+constexpr long long kCutWeight = 10 * 8 * kBlockN;
+// A page of the row kernel (about 0.1 us on an SM) beside a tile's 1024 (1.5 us):
+// 40 / 50 / 60 / 80 measured 98.5 / 96.3 / 100 / 110 us for two chunks of 1024 among 100
+// sequences, 107 / 98.6 / 90.3 / 91.2 for one of 2048 among 32, 191 / 162 / 154 / 156 for
+// eight of 512 among 64.
+constexpr float kPageWeight = 60.f;
+
+// A sequence's units and their weights.
+struct TileSeq {
+  Seq s;
+  int units;         // row groups of one KV head
+  long long weight;  // of one KV head
+};
+
+// What a row group under a window costs at most, in keys (window and sink are
+// at most 2^28, so sums stay in 32 bits).
+__device__ __forceinline__ int weight_cap(const Params& p) {
+  return p.window > 0 ? p.window + 2 * p.tile_tokens + p.sink + kPage : 0x7fffffff - kUnitKeys;
+}
+
+// Weight of the first m row groups, all of them taken as full (m <= units).
+__device__ __forceinline__ long long full_weight(const Params& p, const Seq& s, int m) {
+  const int gt = 2 * p.tile_tokens;
+  int below = m;  // groups whose keys do not reach the cap
+  long long capped = 0;
+  if (p.window > 0) {
+    const int cap = weight_cap(p);
+    below = min(m, cap > s.ctx ? (cap - s.ctx) / gt : 0);
+    capped = static_cast<long long>(m - below) * (cap + kUnitKeys);
+  }
+  const long long n = below;
+  return 8 * (n * (s.ctx + kUnitKeys) + gt * n * (n + 1) / 2 + capped);
+}
+
+__device__ __forceinline__ long long last_weight(const Params& p, const Seq& s, int units) {
+  const bool half = s.n - (units - 1) * 2 * p.tile_tokens <= p.tile_tokens;
+  return static_cast<long long>(half ? kHalfUnit : 8) * (min(s.ctx + s.n, weight_cap(p)) + kUnitKeys);
+}
+
+__device__ __forceinline__ TileSeq tile_seq(const Params& p, int b, bool report) {
+  TileSeq t;
+  t.s = load_seq(p, b, report);
+  t.units = 0;
+  t.weight = 0;
+  if (t.s.n > 0 && !in_rows(p, t.s.n)) {
+    t.units = (t.s.n + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens);
+    t.weight = full_weight(p, t.s, t.units - 1) + last_weight(p, t.s, t.units);
+  }
+  return t;
+}
+
+// A sequence's pages in the row kernel (of one KV head).
+struct RowSeq {
+  Seq s;
+  Keys keys;
+  int pages;
+};
+
+__device__ __forceinline__ RowSeq row_seq(const Params& p, int b, bool report) {
+  RowSeq r;
+  r.s = load_seq(p, b, report);
+  r.pages = 0;
+  if (r.s.n > 0 && in_rows(p, r.s.n)) {
+    r.keys = unit_keys(p, r.s, 0, r.s.n);
+    r.pages = r.keys.sink_pages + (r.keys.end + kPage - 1) / kPage - r.keys.first_page;
+  }
+  return r;
+}
+
+// A call's work, per KV head: the tile kernel's units, their weights' sum and
+// largest, the row kernel's pages.
+struct Work {
+  long long weight, heaviest, pages;
+  int units;
+};
+
+__device__ __forceinline__ Work work_of(const Params& p, const TileSeq& t, const RowSeq& r) {
+  Work w{t.weight, 0, r.pages, t.units};
+  if (t.units > 0) w.heaviest = last_weight(p, t.s, t.units);
+  if (t.units > 1) {
+    const long long full = full_weight(p, t.s, t.units - 1) - full_weight(p, t.s, t.units - 2);
+    w.heaviest = full > w.heaviest ? full : w.heaviest;
+  }
+  return w;
+}
+
+// Adds the lanes' work of a round to `sum`, on every lane.
+__device__ __forceinline__ void add_round(Work& sum, Work w) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    w.weight += __shfl_xor_sync(0xffffffffu, w.weight, o);
+    w.units += __shfl_xor_sync(0xffffffffu, w.units, o);
+    w.pages += __shfl_xor_sync(0xffffffffu, w.pages, o);
+    const long long x = __shfl_xor_sync(0xffffffffu, w.heaviest, o);
+    w.heaviest = x > w.heaviest ? x : w.heaviest;
+  }
+  sum.weight += w.weight;
+  sum.units += w.units;
+  sum.pages += w.pages;
+  sum.heaviest = w.heaviest > sum.heaviest ? w.heaviest : sum.heaviest;
+}
+
+// Whether both kernels cut their units into ranges and share the SMs.
+__device__ __forceinline__ bool side_by_side(const Params& p) {
+  return p.row_workers > 0 && p.tile_ctas > 0 && p.row_mode == kRowRanges && !p.whole_tiles &&
+         p.batch > 1;  // (a sequence alone is of one kind)
+}
+
+// The row kernel's SMs of such a call (0: all of them, behind the tile kernel).
+// It is bound by memory and the tile kernel by arithmetic, so they run beside each
+// other on SMs in proportion to their work: 24 sequences with four chunks of 53 to
+// 370 tokens 53.1 us against 59.8 one behind the other, a chunk of 512 and 24
+// tokens over 4000 keys each 87 / 118, chunks of 1024 and 98 tokens over 1000 100 /
+// 124, a chunk of 100 and 60 tokens over 8000 318 / 335.  Tile units that one per
+// SM leaves whole are cut only when that costs less in both kernels (the first
+// case: 65 us).
+__device__ __forceinline__ int row_sms(const Params& p, const Work& w) {
+  const int sms = p.tile_ctas;
+  if (w.pages == 0) return 0;
+  if (w.weight == 0) return sms;
+  const float rows = static_cast<float>(w.pages) * p.num_kv_heads * kPageWeight;
+  const float tiles = static_cast<float>(w.weight) * p.num_kv_heads;
+  const int units = static_cast<int>(min(static_cast<long long>(w.units) * p.num_kv_heads, static_cast<long long>(sms)));
+  const float even = (rows + tiles) * __fdividef(1.f, static_cast<float>(sms));
+  if (units < sms && fmaxf(static_cast<float>(w.heaviest), __fdividef(rows, static_cast<float>(sms - units))) <=
+                         even + static_cast<float>(kCutWeight))
+    return sms - units;
+  const int x = static_cast<int>(__fdividef(rows, even) + 0.5f);
+  const int use = static_cast<int>(fminf(tiles * (1.f / kMinWeight), static_cast<float>(sms)));
+  if (x < 2 && use == sms) return 0;  // no more than all SMs need afterwards
+  return min(sms - 1, max(x, sms - use));
 }
 
 // Equal shares of `total` positions: worker c holds [start(c), start(c + 1)),

@@ -51,24 +51,6 @@ constexpr float kRescale = 8.0f;  // log2 units: O is rescaled only when a maxim
 // 18.4 / 18.3.
 __device__ __forceinline__ int min_pages(long long total) { return total <= 512 ? 2 : 4; }
 
-// What the worker's range holds of a sequence.
-struct RowSeq {
-  Seq s;
-  Keys keys;
-  int pages;
-};
-
-__device__ __forceinline__ RowSeq row_seq(const Params& p, int b, bool report) {
-  RowSeq r;
-  r.s = load_seq(p, b, report);
-  r.pages = 0;
-  if (r.s.n > 0 && in_rows(p, r.s.n)) {
-    r.keys = unit_keys(p, r.s, 0, r.s.n);
-    r.pages = r.keys.sink_pages + (r.keys.end + kPage - 1) / kPage - r.keys.first_page;
-  }
-  return r;
-}
-
 // Walks the units of a range in order: sequence b, KV head kh (or, in the modes
 // without ranges, every step-th unit).
 struct RowCursor {
@@ -177,12 +159,13 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
   __syncthreads();
   // Behind the tile kernel of the same call this grid starts once that grid's
   // CTAs are past their own wait, so the inputs are there already; it runs on
-  // the SMs that the tile kernel leaves free and waits for it at its end.
+  // the SMs that the tile kernel leaves free and waits for it at its end.  (Should
+  // the two kernels' row_sms ever differ, a CTA only starts later.)
   if (p.tile_ctas == 0) griddep_wait();
 
   // ---- this worker's range of the page list
   // consecutive ranges go to different CTAs, so few workers spread over the SMs
-  const int worker = warp * gridDim.x + blockIdx.x;
+  int worker = warp * gridDim.x + blockIdx.x;
   RowCursor start;
   long long lo = 0, hi = 1, total = 0;
   int workers = p.row_workers;
@@ -191,7 +174,25 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
   start.step = p.row_mode == kRowCta ? gridDim.x : p.row_workers;
   if (p.row_mode == kRowRanges) {
     RowSeq mine;  // of sequence `lane`: the only round when there are at most 32
-    if (p.batch == 1) {
+    int blocks = gridDim.x;
+    if (side_by_side(p)) {
+      Work sum{};
+      for (int b0 = 0; b0 < p.batch; b0 += 32) {
+        const int b = b0 + lane;
+        TileSeq t{};
+        RowSeq r{};
+        if (b < p.batch) {
+          r = row_seq(p, b, worker == 0);
+          t = tile_seq(p, b, false);
+        }
+        if (b0 == 0) mine = r;
+        add_round(sum, work_of(p, t, r));
+      }
+      total = sum.pages;
+      const int own = row_sms(p, sum);
+      if (own > 0) blocks = own;  // the other CTAs find no free SM before the tile kernel's end
+      worker = warp * blocks + blockIdx.x;
+    } else if (p.batch == 1) {
       mine = row_seq(p, 0, worker == 0);
       total = mine.pages;
     } else {
@@ -210,10 +211,12 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
     }
     total *= p.num_kv_heads;
     const long long most = (total + min_pages(total) - 1) / min_pages(total);
-    workers = static_cast<int>(most < p.row_workers ? (most > 0 ? most : 1) : p.row_workers);
+    const int all = blocks * kRowWarps;
+    workers = static_cast<int>(most < all ? (most > 0 ? most : 1) : all);
     share = share_of(total, workers);
-    lo = worker < workers ? share.start(worker) : 0;
-    hi = worker < workers ? share.start(worker + 1) : 0;
+    const bool takes = blockIdx.x < blocks && worker < workers;
+    lo = takes ? share.start(worker) : 0;
+    hi = takes ? share.start(worker + 1) : 0;
     long long base = 0;
     int bsel = p.batch;
     if (p.batch == 1) {

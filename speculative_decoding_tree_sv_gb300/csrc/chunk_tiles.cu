@@ -14,7 +14,8 @@
 // are the softmax of one M tile each, one TMEM lane (row) per thread, warp 2
 // deals the pieces.  Every wait is bounded.
 //
-// Pieces: CTA c takes [W c / C, W (c + 1) / C) of the call's list of units
+// Pieces: CTA c of C (all SMs, or what row_sms leaves) takes
+// [W c / C, W (c + 1) / C) of the call's list of units
 // (sequence, then KV head, then row group), W being the sum of the units'
 // weights.  A weight is the unit's last key position plus a constant, a closed
 // form in the row group, so a range's start is found by one scan over the
@@ -38,19 +39,9 @@ constexpr int kThreads = 384;
 // (softmax warpgroups) = 64512 = 384 x 168, the launch allocation.
 constexpr int kRegsControl = 56;
 constexpr int kRegsSoftmax = 224;
-constexpr int kBlockN = 128;
 constexpr int kPagesPerTile = kBlockN / kPage;
 constexpr float kRescaleThreshold = 8.0f;
 constexpr int kPieceRing = 4;
-// Weights in eighths of a key: a unit costs its keys plus kUnitKeys (Q load,
-// pipeline fill, epilogue); one M tile costs kHalfUnit eighths of two.
-constexpr int kUnitKeys = 192;
-constexpr int kHalfUnit = 5;
-constexpr long long kMinWeight = 8 * kBlockN;  // a CTA's least share
-// What cutting units costs a call, as weight: the partial rows a CTA writes and
-// the combine, about ten tiles of two M tiles.
-constexpr long long kCutWeight = 10 * 8 * kBlockN;
-
 template <int D>
 struct Cfg {
   static constexpr int kHalves = D / 64;
@@ -69,50 +60,6 @@ struct Cfg {
   static constexpr uint32_t kColO0 = 256, kColO1 = 256 + D;
   static_assert(kSmemBytes <= 232448, "shared memory per CTA");
 };
-
-// A sequence's units and their weights.
-struct TileSeq {
-  Seq s;
-  int units;         // row groups of one KV head
-  long long weight;  // of one KV head
-};
-
-// What a row group under a window costs at most, in keys (window and sink are
-// at most 2^28, so sums stay in 32 bits).
-__device__ __forceinline__ int weight_cap(const Params& p) {
-  return p.window > 0 ? p.window + 2 * p.tile_tokens + p.sink + kPage : 0x7fffffff - kUnitKeys;
-}
-
-// Weight of the first m row groups, all of them taken as full (m <= units).
-__device__ __forceinline__ long long full_weight(const Params& p, const Seq& s, int m) {
-  const int gt = 2 * p.tile_tokens;
-  int below = m;  // groups whose keys do not reach the cap
-  long long capped = 0;
-  if (p.window > 0) {
-    const int cap = weight_cap(p);
-    below = min(m, cap > s.ctx ? (cap - s.ctx) / gt : 0);
-    capped = static_cast<long long>(m - below) * (cap + kUnitKeys);
-  }
-  const long long n = below;
-  return 8 * (n * (s.ctx + kUnitKeys) + gt * n * (n + 1) / 2 + capped);
-}
-
-__device__ __forceinline__ long long last_weight(const Params& p, const Seq& s, int units) {
-  const bool half = s.n - (units - 1) * 2 * p.tile_tokens <= p.tile_tokens;
-  return static_cast<long long>(half ? kHalfUnit : 8) * (min(s.ctx + s.n, weight_cap(p)) + kUnitKeys);
-}
-
-__device__ __forceinline__ TileSeq tile_seq(const Params& p, int b, bool report) {
-  TileSeq t;
-  t.s = load_seq(p, b, report);
-  t.units = 0;
-  t.weight = 0;
-  if (t.s.n > 0 && !in_rows(p, t.s.n)) {
-    t.units = (t.s.n + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens);
-    t.weight = full_weight(p, t.s, t.units - 1) + last_weight(p, t.s, t.units);
-  }
-  return t;
-}
 
 // One unit's share of a CTA's range: what the roles need of it.
 struct Piece {
@@ -139,56 +86,41 @@ __device__ __forceinline__ int tile_page(const Piece& pc, int j, int i) {
 template <class Publish>
 __device__ void deal_pieces(const Params& p, int cta, Publish&& publish) {
   const int lane = threadIdx.x & 31;
-  // the call's weight, its units and its heaviest unit (one KV head's)
-  long long total = 0, heaviest = 0;
-  int units = 0;
+  // the call's work, and this kernel's CTAs
+  Work sum{};
+  const bool beside = side_by_side(p);
   TileSeq mine{};  // of sequence `lane`: the only round when there are at most 32
-  auto heaviest_of = [&](const TileSeq& t) {
-    long long h = t.units > 0 ? last_weight(p, t.s, t.units) : 0;
-    if (t.units > 1) {
-      const long long h2 = full_weight(p, t.s, t.units - 1) - full_weight(p, t.s, t.units - 2);
-      h = h2 > h ? h2 : h;
-    }
-    return h;
-  };
   const bool report = cta == 0 && p.row_workers == 0;
   if (p.batch == 1) {  // (a prompt alone: no sums, less code to fetch)
     mine = tile_seq(p, 0, report);
-    total = mine.weight;
-    units = mine.units;
-    heaviest = heaviest_of(mine);
-  }
-  for (int b0 = 0; b0 < p.batch && p.batch > 1; b0 += 32) {
-    const int b = b0 + lane;
-    TileSeq t{};
-    if (b < p.batch) t = tile_seq(p, b, report);
-    if (b0 == 0) mine = t;
-    long long w = t.weight, h = heaviest_of(t);
-    int u = t.units;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      w += __shfl_xor_sync(0xffffffffu, w, o);
-      u += __shfl_xor_sync(0xffffffffu, u, o);
-      const long long x = __shfl_xor_sync(0xffffffffu, h, o);
-      h = x > h ? x : h;
+    sum = work_of(p, mine, RowSeq{});
+  } else {
+    for (int b0 = 0; b0 < p.batch; b0 += 32) {
+      const int b = b0 + lane;
+      TileSeq t{};
+      RowSeq r{};
+      if (b < p.batch) {
+        t = tile_seq(p, b, report);
+        if (beside) r = row_seq(p, b, false);
+      }
+      if (b0 == 0) mine = t;
+      add_round(sum, work_of(p, t, r));
     }
-    total += w;
-    units += u;
-    heaviest = h > heaviest ? h : heaviest;
   }
-  total *= p.num_kv_heads;
-  const long long all = static_cast<long long>(units) * p.num_kv_heads;
+  const int avail = max(1, p.tile_ctas - (beside ? row_sms(p, sum) : 0));
+  long long total = sum.weight * p.num_kv_heads;
+  const long long all = static_cast<long long>(sum.units) * p.num_kv_heads;
   // Whole units, a count each per CTA, when even the heaviest on every CTA costs
   // no more than equal shares with their partials and the combine.
-  const long long rounds = share_of(all + p.tile_ctas - 1, p.tile_ctas).each;
-  const Share even = share_of(total, p.tile_ctas);
-  const bool whole_units = p.whole_tiles || rounds * heaviest <= even.each + kCutWeight;
+  const long long rounds = share_of(all + avail - 1, avail).each;
+  const Share even = share_of(total, avail);
+  const bool whole_units = p.whole_tiles || rounds * sum.heaviest <= even.each + kCutWeight;
   if (whole_units) total = all;
   auto weight_of = [&](const TileSeq& t) { return whole_units ? static_cast<long long>(t.units) : t.weight; };
   auto prefix = [&](const TileSeq& t, int m) { return whole_units ? static_cast<long long>(m) : full_weight(p, t.s, m); };
-  const long long most = whole_units ? p.tile_ctas : total / kMinWeight;
-  const int ctas = static_cast<int>(most < p.tile_ctas ? (most > 0 ? most : 1) : p.tile_ctas);
-  const Share share = !whole_units && ctas == p.tile_ctas ? even : share_of(total, ctas);
+  const long long most = whole_units ? avail : total / kMinWeight;
+  const int ctas = static_cast<int>(most < avail ? (most > 0 ? most : 1) : avail);
+  const Share share = !whole_units && ctas == avail ? even : share_of(total, ctas);
   const long long lo = cta < ctas ? share.start(cta) : 0;
   const long long hi = cta < ctas ? share.start(cta + 1) : 0;
   int4 record = make_int4(0, 0, 0, 0);  // the cut unit that starts here

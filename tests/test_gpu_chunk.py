@@ -205,6 +205,21 @@ def test_short_contexts_of_both_kinds(new):
     c.check()
 
 
+@pytest.mark.parametrize("ctx,new", [
+    ([3000] * 40 + [0], [1] * 40 + [17]),                    # hardly any chunk: most SMs read tokens' pages
+    ([600] + [0], [1] + [1500]),                             # hardly a page
+    ([0, 2000, 17], [700, 400, 1]), ([5000, 1300], [33, 4]),  # whole units and cut ones
+    ([700, 0, 1200], [1, 0, 2]),                             # a chunk announced, none there
+    ([700, 40, 1200], [30, 0, 64]),                          # no short ones
+    ([100, 900, 0] * 25, [1, 40, 5] * 25),                   # more sequences than a warp looks at in one round
+])
+@pytest.mark.parametrize("Hq,Hkv,D,window", [(8, 2, 128, 0), (12, 4, 64, 700), (32, 8, 64, 0)])
+def test_both_kinds_beside_each_other(ctx, new, Hq, Hkv, D, window):
+    c = Case(ctx, new, Hq, Hkv, D, "bf16", window=window, sink=9 if window else 0, seed=sum(new) + Hq)
+    assert c.run(max_tokens=max(new) + 20) == 0
+    c.check()
+
+
 @pytest.mark.parametrize("batch,longest", [(3, 10), (3, 900), (50, 900), (400, 100), (3, 9000)])
 def test_bad_lengths_and_pages_in_every_way_of_sharing(batch, longest):
     """A sequence with a wrong length is left out, one with a wrong page id reads
