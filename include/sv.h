@@ -519,10 +519,11 @@ sv_status sv_specpv_full_trees(const int* cand_parents, const int* cand_tokens, 
  * to the next (>= Hkv * D; slices of a fused projection's rows are fine),
  * layer_stride from a layer to the next.  k_cache/v_cache as for
  * sv_kv_commit.  All strides are multiples of 8.  head_dim is a multiple of
- * 8; num_layers <= 65535; total_tokens <= 2^30.  A sequence whose lengths do not fit its block
- * table or the token rows is left out (SV_DEVERR_BAD_LENGTH, its length
- * stays); a slot whose page id is out of range is skipped
- * (SV_DEVERR_BAD_PAGE).  workspace optional (error word).
+ * 8; num_layers <= 65535; total_tokens <= 2^30.  A sequence whose lengths do
+ * not fit its block table or the token rows, or would pass 2^31 - 1, is left
+ * out (SV_DEVERR_BAD_LENGTH, its length stays); a slot whose
+ * page id is out of range is skipped (SV_DEVERR_BAD_PAGE).  workspace
+ * optional (error word).
  * ---------------------------------------------------------------------- */
 sv_status sv_kv_append(const void* k, const void* v, long long token_stride, long long layer_stride,
                        void* k_cache, void* v_cache, long long cache_layer_stride, int num_layers,
@@ -545,9 +546,9 @@ sv_status sv_kv_append(const void* k, const void* v, long long token_stride, lon
  * only j > L_b + i - W or j < sink_tokens (a token always sees itself).
  * Batches mix sequences of one token, of long chunks and of none (N_b = 0:
  * nothing is written).  Rows of q/out behind cu_tokens[B] are left as they
- * are.  K and V of the positions some row sees are finite; cache slots
- * behind L_b + N_b may hold anything, and pages a window has left behind
- * are not read.
+ * are.  K and V of a sequence's L_b + N_b positions are finite, but for
+ * pages that a window has left behind: those are not read, and slots behind
+ * L_b + N_b may hold anything.
  * ---------------------------------------------------------------------- */
 typedef enum sv_dtype { SV_BF16 = 0, SV_FP16 = 1 } sv_dtype;
 
@@ -562,8 +563,8 @@ typedef struct sv_chunk_params {
   int max_tokens;         /* >= max_b N_b (host copy)                        */
   int max_pages_per_seq;  /* row length of block_table                       */
   int dtype;              /* sv_dtype of q, the cache and out                */
-  int window_tokens;      /* W; 0 = every earlier token is visible           */
-  int sink_tokens;        /* tokens visible whatever the window              */
+  int window_tokens;      /* W <= 2^28; 0 = every earlier token is visible   */
+  int sink_tokens;        /* tokens visible whatever the window, <= 2^28     */
   float sm_scale;         /* softmax scale; <= 0 selects 1/sqrt(D)           */
   int flags;              /* 0                                               */
   long long q_stride;     /* elements from a token of q to the next; 0: Hq*D */
@@ -581,7 +582,8 @@ typedef struct sv_chunk_params {
   size_t workspace_bytes;
 } sv_chunk_params;
 
-/* Bytes of workspace for these parameters on the current device. */
+/* Bytes of workspace for these parameters on the current device: up to 61 MB of
+ * partial results, and 8 bytes per sequence and KV head. */
 sv_status sv_chunk_attention_workspace_size(const sv_chunk_params* params, size_t* bytes);
 
 /* Device errors: SV_DEVERR_BAD_LENGTH for a sequence whose lengths do not fit
@@ -598,7 +600,8 @@ sv_status sv_chunk_attention(const sv_chunk_params* params, sv_stream_t stream);
  * each page (0 = free).  A page named by several rows is shared (the common
  * prefix of forked sequences) and must not be written; sv_pages_reserve
  * replaces it first.  All results are the same on every run: no atomic's
- * order shows.  page_size >= 1; num_pages <= 2097152; rows <= 65535.
+ * order shows.  page_size >= 1; num_pages <= 2097152; rows <= 65535;
+ * max_pages_per_seq <= 2^30.
  * workspace: sv_pages_workspace_size bytes, zero-filled once (the error word;
  * the rest is scratch); release, fork and copy use its error word only.
  * ---------------------------------------------------------------------- */

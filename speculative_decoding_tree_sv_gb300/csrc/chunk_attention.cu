@@ -4,11 +4,11 @@
 // The combine reads each cut unit's pieces: O / l in fp32 and the log2 of the
 // softmax sum, weighs them with 2^(lse_i - max) and divides by the weights'
 // sum.  It is launched as a programmatic dependent of the last attention
-// kernel; a block whose unit was not cut leaves at once.  It is short code on
-// purpose: its instructions come cold on every call, and for a few tokens that
-// is most of its time.  (Merging in the row kernel instead, by the CTA that
-// finishes a unit last, measured slower: 39.5 us against 37.7 for 32 sequences
-// of 1300 tokens, 158 against 148 for four of 50000.)
+// kernel, unless the plan leaves every unit whole; a block whose unit was not
+// cut leaves at once.  It is short code on purpose: its instructions come cold
+// on every call.  (Merging in the row kernel instead, by the CTA that finishes a
+// unit last, measured slower where units are cut: 158 us against 148 for four
+// sequences of 50000 tokens.)
 #include <math.h>
 
 #include "chunk_attention.cuh"

@@ -29,10 +29,12 @@ struct Params {
   int batch, total_tokens, num_pages, max_pages_per_seq, num_kv_heads, vec_per_head, page_size;
 };
 
-// Whether sequence b's chunk lies in the token rows and its slots in the table.
+// Whether sequence b's chunk lies in the token rows, and its slots in the table
+// and below 2^31 (a table of small pages may be longer).
 __device__ __forceinline__ bool fits(const Params& p, int n0, int n1, int L) {
   return n0 >= 0 && n1 >= n0 && n1 <= p.total_tokens && L >= 0 &&
-         static_cast<long long>(L) + (n1 - n0) <= static_cast<long long>(p.max_pages_per_seq) * p.page_size;
+         static_cast<long long>(L) + (n1 - n0) <=
+             min(static_cast<long long>(p.max_pages_per_seq) * p.page_size, 0x7fffffffll);
 }
 
 __global__ void __launch_bounds__(kWarps * 32) kv_append_kernel(const __grid_constant__ Params p) {

@@ -8,6 +8,7 @@
 #define PY_SSIZE_T_CLEAN
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <initializer_list>
 #include <stdexcept>
 #include <string>
@@ -94,6 +95,7 @@ Pool pool(const Tensor& k, const Tensor* v) {
     refuse("a layer of the cache must be contiguous");
   if (v != nullptr && (v->sizes() != k.sizes() || v->scalar_type() != k.scalar_type() || v->strides() != k.strides()))
     refuse("k_cache and v_cache must have the same shape, type and strides");
+  if (d == 5 && k.size(0) > 1 && k.stride(0) < k.select(0, 0).numel()) refuse("the layers of the cache overlap");
   const int64_t o = d - 4;
   return {d == 5 ? small(k.size(0), "layers") : 1, small(k.size(o), "pages"), small(k.size(o + 1), "heads"),
           small(k.size(o + 2), "page size"), small(k.size(o + 3), "head dim"),

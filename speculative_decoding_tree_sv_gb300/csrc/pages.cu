@@ -30,6 +30,7 @@ constexpr int kClusterThreads = 512;
 constexpr int kWarps = kClusterThreads / 32;
 constexpr int kMaxPages = 1 << 21;  // bitmap of an eighth: 32 KB, and as much for its word ranks
 constexpr int kRowThreads = 128;
+constexpr int kMaxWidth = 1 << 30;  // entries of a table row: loops may step past the last
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return a / b + (a % b != 0 ? 1 : 0); }
 
@@ -661,7 +662,7 @@ sv_status check_state(const void* a, const void* b, const void* c, const void* d
                       int num_pages, int page_size) {
   if (!a || !b || !c || !d || !e) return SV_ERR_INVALID_ARG;
   if (rows < 1 || width < 1 || num_pages < 1 || page_size < 1) return SV_ERR_INVALID_ARG;
-  if (rows > 65535 || num_pages > kMaxPages) return SV_ERR_UNSUPPORTED;
+  if (rows > 65535 || num_pages > kMaxPages || width > kMaxWidth) return SV_ERR_UNSUPPORTED;
   return SV_OK;
 }
 

@@ -123,6 +123,7 @@ def test_pages_refuse(lib):
             assert call(**{name: None}) == 1, (call, name)
         for bad in (dict(rows=0), dict(width=0), dict(pages=0)):
             assert call(**bad) == 1
+        assert call(width=(1 << 30) + 1) == 2
         for bad in (dict(rows=65536), dict(pages=(1 << 21) + 1)):
             assert call(**bad) == 2
     assert release(page=0) == 1 and fork(page=0) == 1 and reserve(page=0) == 1
@@ -165,6 +166,9 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         sv.sv_kv_append(h(5, 2, 64), h(5, 2, 64), h(6, 2, 16, 64), h(6, 2, 16, 64), i(2, 3), i(2), i(3))
     with pytest.raises(ValueError, match="layers"):
         sv.sv_kv_append(h(2, 5, 2, 64), h(2, 5, 2, 64), h(3, 6, 2, 16, 64), h(3, 6, 2, 16, 64), i(2, 3), i(2), i(3))
+    one = h(1, 6, 2, 16, 64).expand(3, 6, 2, 16, 64)
+    with pytest.raises(ValueError, match="overlap"):
+        sv.sv_kv_append(h(3, 5, 2, 64), h(3, 5, 2, 64), one, one, i(2, 3), i(2), i(3))
     with pytest.raises(ValueError, match="type"):
         sv.sv_kv_append(h(5, 2, 64).half(), h(5, 2, 64).half(), h(6, 2, 16, 64), h(6, 2, 16, 64), i(2, 3), i(2), i(3))
     with pytest.raises(ValueError, match="same shape and strides"):

@@ -465,6 +465,22 @@ def test_append_leaves_out_what_does_not_fit():
     assert kc[2, :, 15].eq(1).all() and kc[0, :, :4].eq(1).all() and kc[3].abs().sum() == 0
 
 
+def test_append_past_the_last_slot():
+    """A table of 2^27 + 1 pages has room for it, a 32-bit slot does not."""
+    kc = torch.zeros((4, 1, 16, 8), dtype=torch.bfloat16, device="cuda")
+    k = torch.ones((10, 1, 8), dtype=torch.bfloat16, device="cuda")
+    table = torch.zeros((1, (1 << 27) + 1), dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, 10], dtype=torch.int32, device="cuda")
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    after = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for length, fits in ((2 ** 31 - 6, False), (2 ** 31 - 11, True)):
+        lens = torch.tensor([length], dtype=torch.int32, device="cuda")
+        sv.sv_kv_append(k, k, kc, kc.clone(), table, lens, cu, new_ctx_lens=after, workspace=ws)
+        assert sv.sv_get_device_error(ws) == (0 if fits else sv.SV_DEVERR_BAD_LENGTH)
+        assert after.item() == (length + 10 if fits else length)
+        assert kc.float().sum().item() == (80 if fits else 0)
+
+
 def test_prompt_then_tokens_then_a_tree():
     """Append and chunk attention fill the cache that tree verification then
     reads: the root's row of the tree equals the next token's."""
