@@ -365,6 +365,7 @@ sv_status sv_chunk_attention(const sv_chunk_params* params, sv_stream_t stream) 
   p.out = params->out;
   p.lse = params->lse;
   p.err = static_cast<int*>(params->workspace);
+  p.tickets = p.err + 2;  // (in the header)
   p.q_stride = params->q_stride ? params->q_stride : dense;
   p.out_stride = params->out_stride ? params->out_stride : dense;
   p.batch = params->batch;

@@ -43,6 +43,7 @@ struct Params {
   void* out;
   float* lse;
   int* err;
+  int* tickets;          // the tile kernel's whole units: taken, CTAs done; 0 before and after a call
   long long q_stride;    // elements between tokens
   long long out_stride;
   int batch, num_q_heads, num_kv_heads, group, num_pages, max_pages_per_seq, total_tokens, max_tokens;
@@ -186,19 +187,19 @@ __device__ __forceinline__ RowSeq row_seq(const Params& p, int b, bool report) {
   return r;
 }
 
-// A call's work, per KV head: the tile kernel's units, their weights' sum and
-// largest, the row kernel's pages.
+// A call's work, per KV head: the tile kernel's units, their weights' sum, largest
+// and least, the row kernel's pages.
 struct Work {
-  long long weight, heaviest, pages;
+  long long weight, heaviest, lightest, pages;
   int units;
 };
 
 __device__ __forceinline__ Work work_of(const Params& p, const TileSeq& t, const RowSeq& r) {
-  Work w{t.weight, 0, r.pages, t.units};
-  if (t.units > 0) w.heaviest = last_weight(p, t.s, t.units);
+  Work w{t.weight, 0, 1ll << 60, r.pages, t.units};
+  if (t.units > 0) w.heaviest = w.lightest = last_weight(p, t.s, t.units);
   if (t.units > 1) {
-    const long long full = full_weight(p, t.s, t.units - 1) - full_weight(p, t.s, t.units - 2);
-    w.heaviest = full > w.heaviest ? full : w.heaviest;
+    w.heaviest = max(w.heaviest, full_weight(p, t.s, t.units - 1) - full_weight(p, t.s, t.units - 2));
+    w.lightest = min(w.lightest, full_weight(p, t.s, 1));
   }
   return w;
 }
@@ -210,13 +211,14 @@ __device__ __forceinline__ void add_round(Work& sum, Work w) {
     w.weight += __shfl_xor_sync(0xffffffffu, w.weight, o);
     w.units += __shfl_xor_sync(0xffffffffu, w.units, o);
     w.pages += __shfl_xor_sync(0xffffffffu, w.pages, o);
-    const long long x = __shfl_xor_sync(0xffffffffu, w.heaviest, o);
-    w.heaviest = x > w.heaviest ? x : w.heaviest;
+    w.heaviest = max(w.heaviest, __shfl_xor_sync(0xffffffffu, w.heaviest, o));
+    w.lightest = min(w.lightest, __shfl_xor_sync(0xffffffffu, w.lightest, o));
   }
   sum.weight += w.weight;
   sum.units += w.units;
   sum.pages += w.pages;
-  sum.heaviest = w.heaviest > sum.heaviest ? w.heaviest : sum.heaviest;
+  sum.heaviest = max(sum.heaviest, w.heaviest);
+  sum.lightest = min(sum.lightest, w.lightest);
 }
 
 // Whether both kernels cut their units into ranges and share the SMs.

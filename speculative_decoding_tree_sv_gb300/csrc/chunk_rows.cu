@@ -177,6 +177,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
     int blocks = gridDim.x;
     if (side_by_side(p)) {
       Work sum{};
+      sum.lightest = 1ll << 60;
       for (int b0 = 0; b0 < p.batch; b0 += 32) {
         const int b = b0 + lane;
         TileSeq t{};

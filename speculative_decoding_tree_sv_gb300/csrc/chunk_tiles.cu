@@ -82,12 +82,173 @@ __device__ __forceinline__ int tile_page(const Piece& pc, int j, int i) {
   return lp * kPage < pc.end ? lp : -1;
 }
 
-// Deals the CTA's pieces to the other warps (one warp, the ring's producer).
+// The unit of row group m of a sequence, whole.
+__device__ __forceinline__ Piece unit_piece(const Params& p, const Seq& s, int b, int kh, int m) {
+  Piece pc;
+  pc.b = b;
+  pc.kh = kh;
+  pc.tok0 = m * 2 * p.tile_tokens;
+  pc.n0 = s.n0;
+  pc.n = s.n;
+  pc.ctx = s.ctx;
+  const Keys keys = unit_keys(p, s, pc.tok0, min(s.n, pc.tok0 + 2 * p.tile_tokens));
+  pc.sink_pages = keys.sink_pages;
+  pc.sink_tiles = (keys.sink_pages + kPagesPerTile - 1) / kPagesPerTile;
+  pc.first_page = keys.first_page;
+  pc.end = keys.end;
+  pc.ja = 0;
+  pc.je = pc.sink_tiles + ((keys.end + kPage - 1) / kPage - keys.first_page + kPagesPerTile - 1) / kPagesPerTile;
+  pc.nt = s.n - pc.tok0 > p.tile_tokens ? 2 : 1;
+  pc.slot = -1;
+  return pc;
+}
+
+// Whole units: the first by the CTA's number, the others by ticket, in an order
+// that ends with the light ones (32 sequences at a time, their last row groups
+// first).  Which CTA takes a unit does not show in its result.  `mine` is the
+// sequence of the lane, `begun` waits until a piece has been begun: no unit is
+// taken more than one ahead.
+template <class Publish, class Begun>
+__device__ void deal_units(const Params& p, int cta, int ctas, int all, TileSeq mine, Publish&& publish,
+                           Begun&& begun) {
+  const int lane = threadIdx.x & 31;
+  int b0 = 0, level = 0, base = 0;  // units before the level's in that order
+  unsigned has = __ballot_sync(0xffffffffu, mine.units > 0);
+  for (int k = 0;; ++k) {
+    int i = cta < ctas ? cta : all;
+    if (k > 0) {
+      if (all <= ctas || !begun(k - 1)) break;
+      if (lane == 0) i = ctas + atomicAdd(p.tickets, 1);
+      i = __shfl_sync(0xffffffffu, i, 0);
+    }
+    if (i >= all) break;
+    while (b0 < p.batch && (has == 0 || i - base >= __popc(has) * p.num_kv_heads)) {
+      base += __popc(has) * p.num_kv_heads;
+      if (has == 0) {
+        b0 += 32;
+        level = -1;
+        mine = TileSeq{};
+        if (b0 + lane < p.batch) mine = tile_seq(p, b0 + lane, false);
+      }
+      ++level;
+      has = __ballot_sync(0xffffffffu, mine.units > level);
+    }
+    if (b0 >= p.batch) break;
+    const int nth = (i - base) / p.num_kv_heads;
+    const bool it = mine.units > level && __popc(has & ((1u << lane) - 1u)) == nth;
+    const int l = __ffs(__ballot_sync(0xffffffffu, it)) - 1;
+    Seq s;
+    s.n0 = __shfl_sync(0xffffffffu, mine.s.n0, l);
+    s.n = __shfl_sync(0xffffffffu, mine.s.n, l);
+    s.ctx = __shfl_sync(0xffffffffu, mine.s.ctx, l);
+    const int m = __shfl_sync(0xffffffffu, mine.units, l) - 1 - level;
+    if (!publish(unit_piece(p, s, b0 + l, i - base - nth * p.num_kv_heads, m))) break;
+  }
+  // the last CTA to end leaves the counters as they were
+  if (all > ctas && cta < ctas && lane == 0 && atomicAdd(p.tickets + 1, 1) == ctas - 1) {
+    p.tickets[0] = 0;
+    p.tickets[1] = 0;
+  }
+}
+
+// The pieces of the range [lo, hi) of the weights of all units; `record` becomes
+// the cut unit that starts in it.  False when the dealer gave up.
 template <class Publish>
-__device__ void deal_pieces(const Params& p, int cta, Publish&& publish) {
+__device__ __forceinline__ bool deal_range(const Params& p, const Share& share, int cta, long long lo, long long hi,
+                                           TileSeq mine, int4& record, Publish&& publish) {
+  const int lane = threadIdx.x & 31;
+  long long base = 0;
+  int bsel = p.batch == 1 ? 0 : p.batch;
+  for (int b0 = 0; b0 < p.batch && bsel == p.batch; b0 += 32) {
+    const int b = b0 + lane;
+    TileSeq t = mine;
+    if (b0 > 0 || p.batch > 32) {
+      t = TileSeq{};
+      if (b < p.batch) t = tile_seq(p, b, false);
+    }
+    const long long w = t.weight * p.num_kv_heads;
+    long long incl = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, b < p.batch && base + incl > lo);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      bsel = b0 + l;
+      base += __shfl_sync(0xffffffffu, incl - w, l);
+      mine.s.n0 = __shfl_sync(0xffffffffu, t.s.n0, l);
+      mine.s.n = __shfl_sync(0xffffffffu, t.s.n, l);
+      mine.s.ctx = __shfl_sync(0xffffffffu, t.s.ctx, l);
+      mine.units = __shfl_sync(0xffffffffu, t.units, l);
+      mine.weight = __shfl_sync(0xffffffffu, t.weight, l);
+    } else {
+      base += __shfl_sync(0xffffffffu, incl, 31);
+    }
+  }
+  // (all lanes walk the same units from here)
+  TileSeq t = mine;
+  int b = bsel;
+  int kh = 0;
+  long long pos = base;
+  for (; lo - pos >= t.weight; pos += t.weight) ++kh;
+  int m = 0;
+  {
+    int a = 0, e = t.units;  // the row group holding lo: full_weight(m) <= lo - pos < full_weight(m + 1)
+    while (e - a > 1) {
+      const int mid = (a + e) / 2;
+      if (full_weight(p, t.s, mid) <= lo - pos) a = mid;
+      else e = mid;
+    }
+    m = a;
+    pos += full_weight(p, t.s, m);
+  }
+  while (pos < hi) {
+    const long long w = m + 1 < t.units ? full_weight(p, t.s, m + 1) - full_weight(p, t.s, m)
+                                        : last_weight(p, t.s, t.units);
+    Piece pc = unit_piece(p, t.s, b, kh, m);
+    const int tiles = pc.je;
+    // (a boundary's tile in 32-bit floating point: the same from both sides)
+    auto tile_at = [&](long long x) {
+      return min(tiles, static_cast<int>(static_cast<float>(x) * __fdividef(static_cast<float>(tiles), static_cast<float>(w))));
+    };
+    pc.ja = lo > pos ? tile_at(lo - pos) : 0;
+    pc.je = hi < pos + w ? tile_at(hi - pos) : tiles;
+    const bool whole = pc.ja == 0 && pc.je == tiles;
+    pc.slot = whole ? -1 : (pc.ja == 0 ? 1 : 0);
+    if (pc.ja < pc.je) {
+      if (pc.slot == 1)
+        record = make_int4(pc.n0 + pc.tok0, min(pc.n - pc.tok0, 2 * p.tile_tokens), kh, share.holder(pos + w - 1));
+      if (!publish(pc)) return false;
+    } else if (pc.ja > 0) {
+      // less than a tile of a unit that others share: this CTA's piece is empty
+      for (int r = lane; r < kGroupRows; r += 32)
+        p.tile_lse[static_cast<size_t>(cta) * 2 * kGroupRows + r] = -INFINITY;
+    }
+    pos += w;
+    if (++m == t.units) {
+      m = 0;
+      if (++kh == p.num_kv_heads) {
+        kh = 0;
+        do {
+          ++b;
+          if (b < p.batch) t = tile_seq(p, b, false);
+        } while (b < p.batch && t.units == 0);
+        if (b >= p.batch) break;
+      }
+    }
+  }
+  return true;
+}
+
+// Deals the CTA's pieces to the other warps (one warp, the ring's producer).
+template <class Publish, class Begun>
+__device__ void deal_pieces(const Params& p, int cta, Publish&& publish, Begun&& begun) {
   const int lane = threadIdx.x & 31;
   // the call's work, and this kernel's CTAs
   Work sum{};
+  sum.lightest = 1ll << 60;
   const bool beside = side_by_side(p);
   TileSeq mine{};  // of sequence `lane`: the only round when there are at most 32
   const bool report = cta == 0 && p.row_workers == 0;
@@ -108,124 +269,29 @@ __device__ void deal_pieces(const Params& p, int cta, Publish&& publish) {
     }
   }
   const int avail = max(1, p.tile_ctas - (beside ? row_sms(p, sum) : 0));
-  long long total = sum.weight * p.num_kv_heads;
+  const long long total = sum.weight * p.num_kv_heads;
   const long long all = static_cast<long long>(sum.units) * p.num_kv_heads;
-  // Whole units, a count each per CTA, when even the heaviest on every CTA costs
-  // no more than equal shares with their partials and the combine.
+  // Whole units when the CTA that ends last then costs no more than equal shares
+  // with their partials and the combine: it has the heaviest on every round, or
+  // an equal share and a light unit more.
   const long long rounds = share_of(all + avail - 1, avail).each;
   const Share even = share_of(total, avail);
-  const bool whole_units = p.whole_tiles || rounds * sum.heaviest <= even.each + kCutWeight;
-  if (whole_units) total = all;
-  auto weight_of = [&](const TileSeq& t) { return whole_units ? static_cast<long long>(t.units) : t.weight; };
-  auto prefix = [&](const TileSeq& t, int m) { return whole_units ? static_cast<long long>(m) : full_weight(p, t.s, m); };
-  const long long most = whole_units ? avail : total / kMinWeight;
-  const int ctas = static_cast<int>(most < avail ? (most > 0 ? most : 1) : avail);
-  const Share share = !whole_units && ctas == avail ? even : share_of(total, ctas);
-  const long long lo = cta < ctas ? share.start(cta) : 0;
-  const long long hi = cta < ctas ? share.start(cta + 1) : 0;
+  long long longest = even.each + sum.lightest;
+  if (rounds * sum.heaviest < longest) longest = rounds * sum.heaviest;
+  if (longest < sum.heaviest) longest = sum.heaviest;
   int4 record = make_int4(0, 0, 0, 0);  // the cut unit that starts here
-  bool open = hi > lo;
-  if (open) {
-    long long base = 0;
-    int bsel = p.batch == 1 ? 0 : p.batch;
-    for (int b0 = 0; b0 < p.batch && bsel == p.batch; b0 += 32) {
-      const int b = b0 + lane;
-      TileSeq t = mine;
-      if (b0 > 0 || p.batch > 32) {
-        t = TileSeq{};
-        if (b < p.batch) t = tile_seq(p, b, false);
-      }
-      const long long w = weight_of(t) * p.num_kv_heads;
-      long long incl = w;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-      }
-      const unsigned hit = __ballot_sync(0xffffffffu, b < p.batch && base + incl > lo);
-      if (hit) {
-        const int l = __ffs(hit) - 1;
-        bsel = b0 + l;
-        base += __shfl_sync(0xffffffffu, incl - w, l);
-        mine.s.n0 = __shfl_sync(0xffffffffu, t.s.n0, l);
-        mine.s.n = __shfl_sync(0xffffffffu, t.s.n, l);
-        mine.s.ctx = __shfl_sync(0xffffffffu, t.s.ctx, l);
-        mine.units = __shfl_sync(0xffffffffu, t.units, l);
-        mine.weight = __shfl_sync(0xffffffffu, t.weight, l);
-      } else {
-        base += __shfl_sync(0xffffffffu, incl, 31);
-      }
-    }
-    // (all lanes walk the same units from here)
-    TileSeq t = mine;
-    int b = bsel;
-    int kh = 0;
-    long long pos = base;
-    for (const long long w = weight_of(t); lo - pos >= w; pos += w) ++kh;
-    int m = 0;
-    {
-      int a = 0, e = t.units;  // the row group holding lo: prefix(m) <= lo - pos < prefix(m + 1)
-      while (e - a > 1) {
-        const int mid = (a + e) / 2;
-        if (prefix(t, mid) <= lo - pos) a = mid;
-        else e = mid;
-      }
-      m = a;
-      pos += prefix(t, m);
-    }
-    while (pos < hi) {
-      const long long w = m + 1 < t.units ? prefix(t, m + 1) - prefix(t, m)
-                                          : (whole_units ? 1 : last_weight(p, t.s, t.units));
-      Piece pc;
-      pc.b = b;
-      pc.kh = kh;
-      pc.tok0 = m * 2 * p.tile_tokens;
-      pc.n0 = t.s.n0;
-      pc.n = t.s.n;
-      pc.ctx = t.s.ctx;
-      const int t1 = min(t.s.n, pc.tok0 + 2 * p.tile_tokens);
-      const Keys keys = unit_keys(p, t.s, pc.tok0, t1);
-      pc.sink_pages = keys.sink_pages;
-      pc.sink_tiles = (keys.sink_pages + kPagesPerTile - 1) / kPagesPerTile;
-      pc.first_page = keys.first_page;
-      pc.end = keys.end;
-      const int tiles = pc.sink_tiles +
-                        ((keys.end + kPage - 1) / kPage - keys.first_page + kPagesPerTile - 1) / kPagesPerTile;
-      // (a boundary's tile in 32-bit floating point: the same from both sides)
-      auto tile_at = [&](long long x) {
-        return min(tiles, static_cast<int>(static_cast<float>(x) * __fdividef(static_cast<float>(tiles), static_cast<float>(w))));
-      };
-      pc.ja = lo > pos ? tile_at(lo - pos) : 0;
-      pc.je = hi < pos + w ? tile_at(hi - pos) : tiles;
-      pc.nt = t.s.n - pc.tok0 > p.tile_tokens ? 2 : 1;
-      const bool whole = pc.ja == 0 && pc.je == tiles;
-      pc.slot = whole ? -1 : (pc.ja == 0 ? 1 : 0);
-      if (pc.ja < pc.je) {
-        if (pc.slot == 1)
-          record = make_int4(pc.n0 + pc.tok0, t1 - pc.tok0, kh, share.holder(pos + w - 1));
-        if (!publish(pc)) return;
-      } else if (pc.ja > 0) {
-        // less than a tile of a unit that others share: this CTA's piece is empty
-        for (int r = lane; r < kGroupRows; r += 32)
-          p.tile_lse[static_cast<size_t>(cta) * 2 * kGroupRows + r] = -INFINITY;
-      }
-      pos += w;
-      if (++m == t.units) {
-        m = 0;
-        if (++kh == p.num_kv_heads) {
-          kh = 0;
-          do {
-            ++b;
-            if (b < p.batch) t = tile_seq(p, b, false);
-          } while (b < p.batch && t.units == 0);
-          if (b >= p.batch) break;
-        }
-      }
-    }
+  if (p.whole_tiles || (longest <= even.each + kCutWeight && all < (1 << 30))) {
+    if (p.batch == 1 && lane > 0) mine.units = 0;
+    deal_units(p, cta, avail, static_cast<int>(all), mine, publish, begun);
+  } else {
+    const long long most = total / kMinWeight;
+    const int ctas = static_cast<int>(most < avail ? (most > 0 ? most : 1) : avail);
+    const Share share = ctas == avail ? even : share_of(total, ctas);
+    const long long lo = cta < ctas ? share.start(cta) : 0;
+    const long long hi = cta < ctas ? share.start(cta + 1) : 0;
+    if (hi > lo && !deal_range(p, share, cta, lo, hi, mine, record, publish)) return;
   }
-  if (lane == 0) {
-    p.tile_units[cta] = record;
-  }
+  if (lane == 0) p.tile_units[cta] = record;
   Piece end;
   end.je = 0;
   publish(end);
@@ -342,6 +408,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         ++k;
         return true;
+      }, [&](int begun) {
+        if (wait_all(piece_empty + begun % kPieceRing, (begun / kPieceRing) & 1)) return true;
+        give_up();
+        return false;
       });
     } else if (warp == 0 || warp == 3) {
       // ----------------------------------------------- K (and Q) or V loader

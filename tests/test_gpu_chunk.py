@@ -220,6 +220,28 @@ def test_both_kinds_beside_each_other(ctx, new, Hq, Hkv, D, window):
     c.check()
 
 
+@pytest.mark.parametrize("lens", [
+    [1024] * 8, [2048], [128] * 33, [700, 0, 20, 1500, 5], [300, 17, 0] * 30, [40] * 100 + [0] * 40 + [600, 90],
+])
+@pytest.mark.parametrize("Hq,Hkv,D,dtype", [(32, 8, 64, "fp16"), (12, 3, 128, "bf16")])
+def test_more_row_groups_than_blocks(lens, Hq, Hkv, D, dtype):
+    """Whole units taken one after another, in any order, with contexts of
+    different lengths; twice with the same workspace and the same bits."""
+    ctx = [(37 * i) % 500 for i in range(len(lens))]
+    c = Case(ctx, lens, Hq, Hkv, D, dtype, seed=len(lens))
+    p = c.params()
+    outs = []
+    for _ in range(3):
+        c.out.fill_(7.0)
+        sv.sv_chunk_attention(p)
+        torch.cuda.synchronize()
+        assert sv.sv_get_device_error(c.ws) == 0
+        outs.append(c.out.clone())
+    c.check()
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+    assert not c.ws[:256].any()
+
+
 @pytest.mark.parametrize("batch,longest", [(3, 10), (3, 900), (50, 900), (400, 100), (3, 9000)])
 def test_bad_lengths_and_pages_in_every_way_of_sharing(batch, longest):
     """A sequence with a wrong length is left out, one with a wrong page id reads
