@@ -211,8 +211,8 @@ bool encode_pool(CUtensorMap* map, const void* base, const Launch& l, bool whole
 }
 
 // Widths in pages: of units to warps, of a unit to a CTA (kCtaEven of them with few
-// units, where the other SMs would idle), of tile units that surely stay whole.
-constexpr int kWarpPages = 32, kCtaPages = 256, kCtaEven = 64, kWholePages = 64;
+// units, where the other SMs would idle).
+constexpr int kWarpPages = 32, kCtaPages = 256, kCtaEven = 64;
 
 // Where the parts of a call lie in its workspace, and which kernels it needs.
 struct Plan {
@@ -254,10 +254,8 @@ Plan make_plan(const sv_chunk_params* c, int sms) {
     w.row_mode = width <= kWarpPages                                                          ? kRowWarp
                  : fits && width <= kCtaPages && 10 * units >= 7 * sms * ((units + sms - 1) / sms) ? kRowCta
                                                                                                 : kRowRanges;
-  // Tile units at one per CTA whose heaviest is below what cutting costs stay
-  // whole anyway; there are at most one more than full ones per sequence.
-  const long long groups = c->total_tokens / (2 * (kTileRows / G)) + c->batch;
-  w.whole_tiles = groups * c->num_kv_heads <= sms && c->max_pages_per_seq <= kWholePages;
+  // Tile units of which every one costs less than cutting does stay whole anyway.
+  w.whole_tiles = 8ll * (width * kPage + kUnitKeys) <= kCutWeight;
   w.combine = (w.row_workers > 0 && w.row_mode == kRowRanges) || (w.tile_ctas > 0 && !w.whole_tiles);
   size_t at = kWorkspaceHeader;
   auto take = [&](size_t bytes) {

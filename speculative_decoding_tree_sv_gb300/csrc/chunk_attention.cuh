@@ -221,10 +221,9 @@ __device__ __forceinline__ void add_round(Work& sum, Work w) {
   sum.lightest = min(sum.lightest, w.lightest);
 }
 
-// Whether both kernels cut their units into ranges and share the SMs.
+// Whether the two kernels share the SMs.
 __device__ __forceinline__ bool side_by_side(const Params& p) {
-  return p.row_workers > 0 && p.tile_ctas > 0 && p.row_mode == kRowRanges && !p.whole_tiles &&
-         p.batch > 1;  // (a sequence alone is of one kind)
+  return p.row_workers > 0 && p.tile_ctas > 0 && p.row_mode == kRowRanges && p.batch > 1;  // (one is of one kind)
 }
 
 // The row kernel's SMs of such a call (0: all of them, behind the tile kernel).
