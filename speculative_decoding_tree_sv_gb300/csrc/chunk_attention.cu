@@ -11,6 +11,8 @@
 // sequences of 50000 tokens.)
 #include <math.h>
 
+#include <algorithm>
+
 #include "chunk_attention.cuh"
 
 namespace sv {
@@ -213,6 +215,11 @@ bool encode_pool(CUtensorMap* map, const void* base, const Launch& l, bool whole
 // Widths in pages: of units to warps, of a unit to a CTA (kCtaEven of them with few
 // units, where the other SMs would idle).
 constexpr int kWarpPages = 32, kCtaPages = 256, kCtaEven = 64;
+// The largest weight of a unit for which a call leaves out the combine, when its rows
+// fill every SM (a third of it when they fill none): two chunks of 512 after 1500 tokens
+// 33.2 us against 36.7 with it, a prompt of 2048 34.2 / 37.0, but a chunk of 40 after
+// 1000 tokens 21.1 against 15.6 cut into ranges, one of 300 after 1300 31.6 / 25.1.
+constexpr long long kWholeWeight = 24 * 8 * kBlockN;
 
 // Where the parts of a call lie in its workspace, and which kernels it needs.
 struct Plan {
@@ -254,8 +261,14 @@ Plan make_plan(const sv_chunk_params* c, int sms) {
     w.row_mode = width <= kWarpPages                                                          ? kRowWarp
                  : fits && width <= kCtaPages && 10 * units >= 7 * sms * ((units + sms - 1) / sms) ? kRowCta
                                                                                                 : kRowRanges;
-  // Tile units of which every one costs less than cutting does stay whole anyway.
-  w.whole_tiles = 8ll * (width * kPage + kUnitKeys) <= kCutWeight;
+  // Tile units so light that cutting them for the SMs that have none, or less, gains
+  // less than the combine costs (3 us): the heaviest there may be, the more
+  // of the SMs the call's token rows fill.
+  const long long group = 2 * (kTileRows / G);
+  long long keys = static_cast<long long>(width) * kPage;
+  if (c->window_tokens > 0) keys = std::min(keys, static_cast<long long>(c->window_tokens) + c->sink_tokens + group + kPage);
+  const long long filled = std::min<long long>(c->total_tokens / group * c->num_kv_heads, sms);
+  w.whole_tiles = 8 * (keys + kUnitKeys) * (3 * sms - 2 * filled) <= sms * kWholeWeight;
   w.combine = (w.row_workers > 0 && w.row_mode == kRowRanges) || (w.tile_ctas > 0 && !w.whole_tiles);
   size_t at = kWorkspaceHeader;
   auto take = [&](size_t bytes) {

@@ -116,9 +116,11 @@ __device__ __forceinline__ Keys unit_keys(const Params& p, const Seq& s, int t0,
 constexpr int kUnitKeys = 192;
 constexpr int kHalfUnit = 5;
 constexpr long long kMinWeight = 8 * kBlockN;  // a CTA's least share
-// What cutting units costs a call, as weight: the partial rows a CTA writes and
-// the combine, about ten tiles of two M tiles.
-constexpr long long kCutWeight = 10 * 8 * kBlockN;
+// What cutting units costs a call, as weight: the partial rows that CTAs write and
+// the combine reads, about seven tiles of two M tiles (5 / 7 / 12: a chunk of 2048
+// among 32 sequences 90.7 / 79.8 / 79.1 us, one of 300 after 1300 tokens 25.1 / 25.1 /
+// 31.6).
+constexpr long long kCutWeight = 7 * 8 * kBlockN;
 // A page of the row kernel (about 0.1 us on an SM) beside a tile's 1024 (1.5 us):
 // 40 / 50 / 60 / 80 measured 98.5 / 96.3 / 100 / 110 us for two chunks of 1024 among 100
 // sequences, 107 / 98.6 / 90.3 / 91.2 for one of 2048 among 32, 191 / 162 / 154 / 156 for

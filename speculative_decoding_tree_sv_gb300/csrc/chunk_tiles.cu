@@ -274,10 +274,10 @@ __device__ void deal_pieces(const Params& p, int cta, Publish&& publish, NearEnd
   const long long all = static_cast<long long>(sum.units) * p.num_kv_heads;
   // Whole units when the CTA that ends last then costs no more than equal shares
   // with their partials and the combine: it has the heaviest on every round, or
-  // an equal share and a light unit more.
+  // an equal share and half a light unit more.
   const long long rounds = share_of(all + avail - 1, avail).each;
   const Share even = share_of(total, avail);
-  long long longest = even.each + sum.lightest;
+  long long longest = even.each + sum.lightest / 2;
   if (rounds * sum.heaviest < longest) longest = rounds * sum.heaviest;
   if (longest < sum.heaviest) longest = sum.heaviest;
   int4 record = make_int4(0, 0, 0, 0);  // the cut unit that starts here
