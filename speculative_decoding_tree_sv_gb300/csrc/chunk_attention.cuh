@@ -117,9 +117,9 @@ constexpr int kUnitKeys = 192;
 constexpr int kHalfUnit = 5;
 constexpr long long kMinWeight = 8 * kBlockN;  // a CTA's least share
 // What cutting units costs a call, as weight: the partial rows that CTAs write and
-// the combine reads, about seven tiles of two M tiles (5 / 7 / 12: a chunk of 2048
-// among 32 sequences 90.7 / 79.8 / 79.1 us, one of 300 after 1300 tokens 25.1 / 25.1 /
-// 31.6).
+// the combine reads, about seven tiles of two M tiles (7 / 9 / 12: four chunks of
+// 100 after 1500 tokens 29.9 / 31.8 / 31.9 us, one of 300 after 1300 25.0 / 25.1 / 31.1,
+// two of 256 among 130 sequences 276 / 276 / 263).
 constexpr long long kCutWeight = 7 * 8 * kBlockN;
 // A page of the row kernel (about 0.1 us on an SM) beside a tile's 1024 (1.5 us):
 // 40 / 50 / 60 / 80 measured 98.5 / 96.3 / 100 / 110 us for two chunks of 1024 among 100
@@ -159,15 +159,18 @@ __device__ __forceinline__ long long last_weight(const Params& p, const Seq& s, 
   return static_cast<long long>(half ? kHalfUnit : 8) * (min(s.ctx + s.n, weight_cap(p)) + kUnitKeys);
 }
 
-__device__ __forceinline__ TileSeq tile_seq(const Params& p, int b, bool report) {
+__device__ __forceinline__ TileSeq tile_units(const Params& p, int b, bool report) {  // without the weight
   TileSeq t;
   t.s = load_seq(p, b, report);
   t.units = 0;
   t.weight = 0;
-  if (t.s.n > 0 && !in_rows(p, t.s.n)) {
-    t.units = (t.s.n + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens);
-    t.weight = full_weight(p, t.s, t.units - 1) + last_weight(p, t.s, t.units);
-  }
+  if (t.s.n > 0 && !in_rows(p, t.s.n)) t.units = (t.s.n + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens);
+  return t;
+}
+
+__device__ __forceinline__ TileSeq tile_seq(const Params& p, int b, bool report) {
+  TileSeq t = tile_units(p, b, report);
+  if (t.units > 0) t.weight = full_weight(p, t.s, t.units - 1) + last_weight(p, t.s, t.units);
   return t;
 }
 

@@ -247,51 +247,65 @@ __device__ __forceinline__ bool deal_range(const Params& p, const Share& share, 
 template <class Publish, class NearEnd>
 __device__ void deal_pieces(const Params& p, int cta, Publish&& publish, NearEnd&& near_end) {
   const int lane = threadIdx.x & 31;
-  // the call's work, and this kernel's CTAs
-  Work sum{};
-  sum.lightest = 1ll << 60;
   const bool beside = side_by_side(p);
-  TileSeq mine{};  // of sequence `lane`: the only round when there are at most 32
   const bool report = cta == 0 && p.row_workers == 0;
-  if (p.batch == 1) {  // (a prompt alone: no sums, less code to fetch)
-    mine = tile_seq(p, 0, report);
-    sum = work_of(p, mine, RowSeq{});
-  } else {
+  int avail = p.tile_ctas, all = 0;
+  TileSeq mine{};  // of sequence `lane`: the only round when there are at most 32
+  int4 record = make_int4(0, 0, 0, 0);  // the cut unit that starts here
+  bool whole = p.whole_tiles && !beside;
+  if (whole) {  // (no weights: less code to fetch)
     for (int b0 = 0; b0 < p.batch; b0 += 32) {
-      const int b = b0 + lane;
       TileSeq t{};
-      RowSeq r{};
-      if (b < p.batch) {
-        t = tile_seq(p, b, report);
-        if (beside) r = row_seq(p, b, false);
-      }
+      if (b0 + lane < p.batch) t = tile_units(p, b0 + lane, report);
       if (b0 == 0) mine = t;
-      add_round(sum, work_of(p, t, r));
+      all += __reduce_add_sync(0xffffffffu, t.units);
+    }
+    all *= p.num_kv_heads;
+  } else {
+    // the call's work, and this kernel's CTAs
+    Work sum{};
+    sum.lightest = 1ll << 60;
+    if (p.batch == 1) {  // (a prompt alone: no sums)
+      mine = tile_seq(p, 0, report);
+      sum = work_of(p, mine, RowSeq{});
+    } else {
+      for (int b0 = 0; b0 < p.batch; b0 += 32) {
+        const int b = b0 + lane;
+        TileSeq t{};
+        RowSeq r{};
+        if (b < p.batch) {
+          t = tile_seq(p, b, report);
+          if (beside) r = row_seq(p, b, false);
+        }
+        if (b0 == 0) mine = t;
+        add_round(sum, work_of(p, t, r));
+      }
+    }
+    if (beside) avail = max(1, avail - row_sms(p, sum));
+    const long long total = sum.weight * p.num_kv_heads;
+    const long long units = static_cast<long long>(sum.units) * p.num_kv_heads;
+    // Whole units when the CTA that ends last then costs no more than equal shares
+    // with their partials and the combine: it has the heaviest on every round, or
+    // an equal share and half a light unit more.
+    const long long rounds = share_of(units + avail - 1, avail).each;
+    const Share even = share_of(total, avail);
+    long long longest = even.each + sum.lightest / 2;
+    if (rounds * sum.heaviest < longest) longest = rounds * sum.heaviest;
+    if (longest < sum.heaviest) longest = sum.heaviest;
+    whole = p.whole_tiles || (longest <= even.each + kCutWeight && units < (1 << 30));
+    if (whole) {
+      all = static_cast<int>(units);
+      if (p.batch == 1 && lane > 0) mine.units = 0;
+    } else {
+      const long long most = total / kMinWeight;
+      const int ctas = static_cast<int>(most < avail ? (most > 0 ? most : 1) : avail);
+      const Share share = ctas == avail ? even : share_of(total, ctas);
+      const long long lo = cta < ctas ? share.start(cta) : 0;
+      const long long hi = cta < ctas ? share.start(cta + 1) : 0;
+      if (hi > lo && !deal_range(p, share, cta, lo, hi, mine, record, publish)) return;
     }
   }
-  const int avail = max(1, p.tile_ctas - (beside ? row_sms(p, sum) : 0));
-  const long long total = sum.weight * p.num_kv_heads;
-  const long long all = static_cast<long long>(sum.units) * p.num_kv_heads;
-  // Whole units when the CTA that ends last then costs no more than equal shares
-  // with their partials and the combine: it has the heaviest on every round, or
-  // an equal share and half a light unit more.
-  const long long rounds = share_of(all + avail - 1, avail).each;
-  const Share even = share_of(total, avail);
-  long long longest = even.each + sum.lightest / 2;
-  if (rounds * sum.heaviest < longest) longest = rounds * sum.heaviest;
-  if (longest < sum.heaviest) longest = sum.heaviest;
-  int4 record = make_int4(0, 0, 0, 0);  // the cut unit that starts here
-  if (p.whole_tiles || (longest <= even.each + kCutWeight && all < (1 << 30))) {
-    if (p.batch == 1 && lane > 0) mine.units = 0;
-    deal_units(p, cta, avail, static_cast<int>(all), mine, publish, near_end);
-  } else {
-    const long long most = total / kMinWeight;
-    const int ctas = static_cast<int>(most < avail ? (most > 0 ? most : 1) : avail);
-    const Share share = ctas == avail ? even : share_of(total, ctas);
-    const long long lo = cta < ctas ? share.start(cta) : 0;
-    const long long hi = cta < ctas ? share.start(cta + 1) : 0;
-    if (hi > lo && !deal_range(p, share, cta, lo, hi, mine, record, publish)) return;
-  }
+  if (whole) deal_units(p, cta, avail, all, mine, publish, near_end);
   if (lane == 0) p.tile_units[cta] = record;
   Piece end;
   end.je = 0;
