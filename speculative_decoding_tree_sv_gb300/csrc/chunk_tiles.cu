@@ -14,17 +14,21 @@
 // are the softmax of one M tile each, one TMEM lane (row) per thread, warp 2
 // deals the pieces.  Every wait is bounded.
 //
-// Pieces: CTA c of C (all SMs, or what row_sms leaves) takes
-// [W c / C, W (c + 1) / C) of the call's list of units
-// (sequence, then KV head, then row group), W being the sum of the units'
-// weights.  A weight is the unit's last key position plus a constant, a closed
-// form in the row group, so a range's start is found by one scan over the
-// sequences and a binary search; a boundary inside a unit is scaled to a whole
-// tile the same way by both neighbours.  Rings, MMA order and barrier phases
-// run on across pieces.
+// Pieces: a unit's weight is its last key position plus a constant, a closed form
+// in the row group.  Where cutting costs more than it evens out, units stay
+// whole and the CTAs take them one after another by ticket, light ones last
+// (eight prompts of 1024 tokens 76.5 us; 102 in equal ranges).  Else CTA c of C
+// (all SMs, or what row_sms leaves) takes [W c / C, W (c + 1) / C) of the call's
+// list of units (sequence, then KV head, then row group), W being the sum of the
+// weights: a range's start is found by one scan over the sequences and a binary
+// search, and a boundary inside a unit is scaled to a whole tile the same way by
+// both neighbours.  Rings, MMA order and barrier phases run on across pieces.
 //
 // Bound: for long chunks the tensor cores and, next to them, the softmax (the
-// chain scores -> P -> PV -> next scores of each M tile).
+// chain scores -> P -> PV -> next scores of each M tile: 2800 cycles a tile, 2048
+// of them products); for prompts of about a thousand tokens also what a unit adds
+// (8000 cycles: 1200 of mask, 1000 for its last product, 3300 of epilogue, 1300 for
+// the next piece, the slower first tile).
 #include <math.h>
 
 #include <mutex>
