@@ -224,6 +224,7 @@ constexpr long long kWholeWeight = 24 * 8 * kBlockN;
 // Where the parts of a call lie in its workspace, and which kernels it needs.
 struct Plan {
   int row_workers, tile_ctas;
+  int tile_grid;  // of the tile_ctas the workspace has room for
   int row_mode, whole_tiles;
   bool combine;
   size_t row_o, row_lse, row_units, tile_o, tile_lse, tile_units, bytes;
@@ -251,7 +252,14 @@ Plan make_plan(const sv_chunk_params* c, int sms) {
   // pages 27.5 against 30.5 us, 1024 of 63 69.6 / 77; 192 of 63 (the second round a
   // quarter full) 18.9 against 17.3.
   const long long units = static_cast<long long>(c->batch) * c->num_kv_heads;
-  const int width = c->max_pages_per_seq;
+  // (a window's pages and the sink's, should the table be wider; a chunk's own
+  // tokens add to them in the tile kernel)
+  const long long seen = static_cast<long long>(c->window_tokens) + c->sink_tokens;
+  auto pages_of = [&](long long tokens) {
+    const long long most = (seen + tokens) / kPage + 3;
+    return c->window_tokens > 0 ? std::min<long long>(c->max_pages_per_seq, most) : c->max_pages_per_seq;
+  };
+  const long long width = pages_of(kRowUnit);
   const bool fits = static_cast<long long>(c->max_tokens) * G <= kCtaRows;
   if (fits && units <= sms)
     w.row_mode = width <= 2                                                              ? kRowWarp
@@ -265,10 +273,13 @@ Plan make_plan(const sv_chunk_params* c, int sms) {
   // less than the combine costs (3 us): the heaviest there may be, the more
   // of the SMs the call's token rows fill.
   const long long group = 2 * (kTileRows / G);
-  long long keys = static_cast<long long>(width) * kPage;
-  if (c->window_tokens > 0) keys = std::min(keys, static_cast<long long>(c->window_tokens) + c->sink_tokens + group + kPage);
+  const long long keys = pages_of(group) * kPage;
   const long long filled = std::min<long long>(c->total_tokens / group * c->num_kv_heads, sms);
   w.whole_tiles = 8 * (keys + kUnitKeys) * (3 * sms - 2 * filled) <= sms * kWholeWeight;
+  // No more CTAs than the tiles of all units there may be, or than the units.
+  const long long groups = c->total_tokens / group + c->batch;
+  const long long useful = groups * c->num_kv_heads * (w.whole_tiles ? 1 : (keys + kBlockN - 1) / kBlockN + 1);
+  w.tile_grid = static_cast<int>(std::min<long long>(w.tile_ctas, useful));
   w.combine = (w.row_workers > 0 && w.row_mode == kRowRanges) || (w.tile_ctas > 0 && !w.whole_tiles);
   size_t at = kWorkspaceHeader;
   auto take = [&](size_t bytes) {
@@ -401,7 +412,7 @@ sv_status sv_chunk_attention(const sv_chunk_params* params, sv_stream_t stream) 
   p.row_workers = w.row_workers;
   p.row_mode = w.row_mode;
   p.whole_tiles = w.whole_tiles;
-  p.tile_ctas = w.tile_ctas;
+  p.tile_ctas = w.tile_grid;
   l.k_cache = params->k_cache;
   l.v_cache = params->v_cache;
   l.head_dim = params->head_dim;

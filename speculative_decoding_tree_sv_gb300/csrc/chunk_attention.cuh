@@ -60,7 +60,7 @@ struct Params {
   int row_workers;       // 0: no row kernel in this call
   int row_mode;          // RowMode
   int whole_tiles;       // the tile kernel's units stay whole, so that nothing is left to combine
-  int tile_ctas;         // 0: no tile kernel in this call
+  int tile_ctas;         // the tile kernel's grid; 0: no tile kernel in this call
 };
 
 // One sequence's lengths; n is 0 when it has no work (nothing new, or lengths
@@ -240,7 +240,7 @@ __device__ __forceinline__ bool side_by_side(const Params& p) {
 // SM leaves whole are cut only when that costs less in both kernels (the first
 // case: 65 us).
 __device__ __forceinline__ int row_sms(const Params& p, const Work& w) {
-  const int sms = p.tile_ctas;
+  const int sms = p.row_workers / kRowWarps;
   if (w.pages == 0) return 0;
   if (w.weight == 0) return sms;
   const float rows = static_cast<float>(w.pages) * p.num_kv_heads * kPageWeight;

@@ -285,7 +285,7 @@ __device__ void deal_pieces(const Params& p, int cta, Publish&& publish, NearEnd
         add_round(sum, work_of(p, t, r));
       }
     }
-    if (beside) avail = max(1, avail - row_sms(p, sum));
+    if (beside) avail = max(1, min(avail, p.row_workers / kRowWarps - row_sms(p, sum)));
     const long long total = sum.weight * p.num_kv_heads;
     const long long units = static_cast<long long>(sum.units) * p.num_kv_heads;
     // Whole units when the CTA that ends last then costs no more than equal shares
