@@ -34,12 +34,14 @@ __device__ __forceinline__ void combine_rows(const Params& p, int unit, int row0
   __shared__ float part_m[kCombineWarps], part_w[kCombineWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int2 u = p.row_units[unit];
-  const int b = unit / p.num_kv_heads, kh = unit - b * p.num_kv_heads;
-  const Seq s = load_seq(p, b, false);
+  const int b = unit / p.num_kv_heads, kh = unit - b * p.num_kv_heads;  // b: of the row kernel's list
+  const Seq s = load_seq(p, b >> p.row_shift, false);
   const int first = u.x, pieces = u.y - u.x + 1;
-  if (s.n == 0 || !in_rows(p, s.n) || first < 0 || u.y >= p.row_workers || pieces <= 1)
-    return;  // (a kernel that timed out left no record)
-  const int rows = s.n * p.group, here = (rows - row0 + split - 1) / split;  // rows of this block
+  if (s.n == 0 || !in_rows(p, s.n, p.row_shift)) return;
+  const int base = first_row(b, p.row_shift), rows = min(s.n * p.group - base, kRowUnit);
+  if (rows <= row0 || first < 0 || u.y >= p.row_workers || pieces <= 1)
+    return;  // (no such rows; not cut; a kernel that timed out left no record)
+  const int here = (rows - row0 + split - 1) / split;  // rows of this block
   const int parts = pieces <= 4 ? 1 : here <= 1 ? 8 : here <= 2 ? 4 : here <= 4 ? 2 : 1;
   const int part = warp % parts, per = (pieces + parts - 1) / parts;
   const int end = min((part + 1) * per, pieces);
@@ -101,7 +103,7 @@ __device__ __forceinline__ void combine_rows(const Params& p, int unit, int row0
     }
     if (r < rows && part == 0) {
       const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
-      const int tok = r / p.group, head = kh * p.group + r - tok * p.group;
+      const int tok = (base + r) / p.group, head = kh * p.group + base + r - tok * p.group;
       const long long token = s.n0 + tok;
       uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + token * p.out_stride +
                                                   static_cast<long long>(head) * D) + lane * (E / 2);
@@ -213,8 +215,10 @@ bool encode_pool(CUtensorMap* map, const void* base, const Launch& l, bool whole
 }
 
 // Widths in pages: of units to warps, of a unit to a CTA (kCtaEven of them with few
-// units, where the other SMs would idle).
-constexpr int kWarpPages = 32, kCtaPages = 256, kCtaEven = 64;
+// units, where the other SMs would idle), and of the least units that go to the
+// row kernel in two.
+constexpr long long kWarpPages = 32, kCtaPages = 256, kCtaEven = 64;
+constexpr long long kTilePages = 48, kSharedBytes = 64ll << 20;
 // The largest weight of a unit for which a call leaves out the combine, when its rows
 // fill every SM (a third of it when they fill none): two chunks of 512 after 1500 tokens
 // 33.2 us against 36.7 with it, a prompt of 2048 34.2 / 37.0, but a chunk of 40 after
@@ -225,7 +229,7 @@ constexpr long long kWholeWeight = 24 * 8 * kBlockN;
 struct Plan {
   int row_workers, tile_ctas;
   int tile_grid;  // of the tile_ctas the workspace has room for
-  int row_mode, whole_tiles;
+  int row_mode, row_shift, whole_tiles;
   bool combine;
   size_t row_o, row_lse, row_units, tile_o, tile_lse, tile_units, bytes;
 };
@@ -233,40 +237,51 @@ struct Plan {
 Plan make_plan(const sv_chunk_params* c, int sms) {
   const int G = c->num_q_heads / c->num_kv_heads;
   Plan w{};
-  // a sequence of one token has G rows, the longest max_tokens * G; when the
-  // others at their longest leave every one more than the row kernel takes, it
-  // stays out (4.4 us of finding nothing beside a 220 us window chunk; should
-  // the token rows exceed cu_tokens[B], the tile kernel takes the short ones too)
-  const long long least = c->total_tokens - (c->batch - 1ll) * c->max_tokens;
-  const bool some_large = static_cast<long long>(c->max_tokens) * G > kRowUnit;
-  const bool some_small = G <= kRowUnit && !(some_large && least * G > kRowUnit);
-  w.row_workers = some_small ? sms * kRowWarps : 0;
-  w.tile_ctas = some_large ? sms : 0;
-  // What the host sees of the contexts is the table's width.  Short ones do
-  // without ranges and their combine.  A unit per CTA takes about 0.1 us a page,
-  // the ranges as much for the units' even share of the SMs and 4 us more: 8 units
-  // of 7 / 32 / 63 / 94 pages 4.8 / 7.1 / 9.7 / 12.3 against 8.2 / 8.0 / 9.9 / 11.0
-  // us, 128 of 63 / 94 / 188 10.0 / 13.3 / 34 against 15.2 / 18.3 / 39.  Units to
-  // the warps: 2048 of 7 / 13 / 32 pages 19.3 / 37 / 81 against 31.5 / 49 / 95 us.
-  // More units than CTAs, in rounds that are seven tenths full: 256 of up to 82
-  // pages 27.5 against 30.5 us, 1024 of 63 69.6 / 77; 192 of 63 (the second round a
-  // quarter full) 18.9 against 17.3.
-  const long long units = static_cast<long long>(c->batch) * c->num_kv_heads;
-  // (a window's pages and the sink's, should the table be wider; a chunk's own
-  // tokens add to them in the tile kernel)
+  // pages of a run of tokens: the table's width, or a window's and the sink's
   const long long seen = static_cast<long long>(c->window_tokens) + c->sink_tokens;
   auto pages_of = [&](long long tokens) {
     const long long most = (seen + tokens) / kPage + 3;
     return c->window_tokens > 0 ? std::min<long long>(c->max_pages_per_seq, most) : c->max_pages_per_seq;
   };
   const long long width = pages_of(kRowUnit);
+  // a sequence of one token has G rows, the longest max_tokens * G; when the
+  // others at their longest leave every one more than the row kernel takes, it
+  // stays out (4.4 us of finding nothing beside a 220 us window chunk; should
+  // the token rows exceed cu_tokens[B], the tile kernel takes the short ones too)
+  const long long least = c->total_tokens - (c->batch - 1ll) * c->max_tokens;
+  const long long most = static_cast<long long>(c->max_tokens) * G;
+  // Up to 32 rows may go to the row kernel as two units, which read the same pages:
+  // while those stay in the L2 cache, and for more than the few tiles that a CTA
+  // of the tile kernel takes at once (4 sequences of 500 / 1500 tokens at 8 KV
+  // heads 16.1 / 18.3 us against 11.7 / 25.7 in the tile kernel, 16 of 8000 at 2 heads, D
+  // 64, 63 MB, 27.2 / 30.8, but 32 of 2000 at 8 heads, 252 MB, 67 / 62).
+  const long long cache = static_cast<long long>(c->batch) * c->num_kv_heads * width * 4 * kPage * c->head_dim;
+  w.row_shift = G <= 2 * kRowUnit && most > kRowUnit && width > kTilePages && cache <= kSharedBytes;
+  const int rows = kRowUnit << w.row_shift;
+  const bool some_large = most > rows;
+  const bool some_small = G <= rows && !(some_large && least * G > rows);
+  w.row_workers = some_small ? sms * kRowWarps : 0;
+  w.tile_ctas = some_large ? sms : 0;
+  // What the host sees of the contexts is the table's width.  Short ones do
+  // without ranges and their combine.  A unit per CTA takes about 0.1 us a page,
+  // the ranges as much for the units' even share of the SMs and 4 us more: 8 units
+  // of 7 / 32 / 63 / 94 pages 4.8 / 7.1 / 9.7 / 12.3 against 8.2 / 8.0 / 9.9 / 11.0
+  // us, 128 of 63 / 94 / 188 10.0 / 13.3 / 34 against 15.2 / 18.3 / 39.  A warp
+  // takes half a microsecond a page of a unit of its own: 8 units of 8 / 13 / 20 pages
+  // 8.7 / 10.9 / 14.7 against 9.9 / 10.1 / 10.4 us, 256 of 13 / 20 / 32 12.2 / 16.5 /
+  // 23.8 against 15.9 / 18.0 / 20.4, 2048 36 / 50 / 75 against 53 / 68 / 93 (beside
+  // chunks it costs nothing: five tokens with four chunks of 215 to 452 14.9 / 21.2).
+  // More units than CTAs, in rounds that are seven tenths full: 256 of up to 82
+  // pages 27.5 against 30.5 us, 1024 of 63 69.6 / 77; 192 of 63 (the second round a
+  // quarter full) 18.9 against 17.3.
+  const long long units = (static_cast<long long>(c->batch) << w.row_shift) * c->num_kv_heads;
   const bool fits = static_cast<long long>(c->max_tokens) * G <= kCtaRows;
   if (fits && units <= sms)
     w.row_mode = width <= 2                                                              ? kRowWarp
                  : width <= kCtaPages && width * (sms - units) <= kCtaEven * static_cast<long long>(sms) ? kRowCta
                                                                                          : kRowRanges;
   else
-    w.row_mode = width <= kWarpPages                                                          ? kRowWarp
+    w.row_mode = width <= (some_large ? kWarpPages : std::min(kWarpPages, 12 + 10 * units / sms)) ? kRowWarp
                  : fits && width <= kCtaPages && 10 * units >= 7 * sms * ((units + sms - 1) / sms) ? kRowCta
                                                                                                 : kRowRanges;
   // Tile units so light that cutting them for the SMs that have none, or less, gains
@@ -290,12 +305,14 @@ Plan make_plan(const sv_chunk_params* c, int sms) {
   const size_t D = static_cast<size_t>(c->head_dim);
   // (as large for calls that cut no unit: a workspace for many sequences and
   // tokens of both kinds then serves fewer of them, whichever kernels they take)
-  w.row_o = take(static_cast<size_t>(w.row_workers) * 2 * kRowUnit * D * sizeof(float));
-  w.row_lse = take(static_cast<size_t>(w.row_workers) * 2 * kRowUnit * sizeof(float));
-  w.row_units = take(w.row_workers ? static_cast<size_t>(units) * sizeof(int2) : 0);
-  w.tile_o = take(static_cast<size_t>(w.tile_ctas) * 2 * kGroupRows * D * sizeof(float));
-  w.tile_lse = take(static_cast<size_t>(w.tile_ctas) * 2 * kGroupRows * sizeof(float));
-  w.tile_units = take(static_cast<size_t>(w.tile_ctas) * sizeof(int4));
+  const bool small = some_small || (G <= 2 * kRowUnit && !(most > kRowUnit && least * G > 2 * kRowUnit));
+  const size_t workers = small ? static_cast<size_t>(sms) * kRowWarps : 0, ctas = most > kRowUnit ? sms : 0;
+  w.row_o = take(workers * 2 * kRowUnit * D * sizeof(float));
+  w.row_lse = take(workers * 2 * kRowUnit * sizeof(float));
+  w.row_units = take(small ? static_cast<size_t>(c->batch) * 2 * c->num_kv_heads * sizeof(int2) : 0);
+  w.tile_o = take(ctas * 2 * kGroupRows * D * sizeof(float));
+  w.tile_lse = take(ctas * 2 * kGroupRows * sizeof(float));
+  w.tile_units = take(ctas * sizeof(int4));
   w.bytes = at;
   return w;
 }
@@ -329,7 +346,7 @@ sv_status check(const sv_chunk_params* c) {
 template <int D, bool FP16>
 sv_status launch_combine(const Launch& l) {
   const int tile_blocks = l.p.whole_tiles ? 0 : l.p.tile_ctas * kTileBlocks;
-  const int units = l.p.row_workers > 0 && l.p.row_mode == kRowRanges ? l.p.batch * l.p.num_kv_heads : 0;
+  const int units = l.p.row_workers > 0 && l.p.row_mode == kRowRanges ? (l.p.batch << l.p.row_shift) * l.p.num_kv_heads : 0;
   const long long most = static_cast<long long>(l.p.max_tokens) * l.p.group;
   const int rows = most < kRowUnit ? static_cast<int>(most) : kRowUnit;
   const int split = units <= 64 ? rows : 1;
@@ -411,6 +428,7 @@ sv_status sv_chunk_attention(const sv_chunk_params* params, sv_stream_t stream) 
   p.tile_units = reinterpret_cast<int4*>(base + w.tile_units);
   p.row_workers = w.row_workers;
   p.row_mode = w.row_mode;
+  p.row_shift = w.row_shift;
   p.whole_tiles = w.whole_tiles;
   p.tile_ctas = w.tile_grid;
   l.k_cache = params->k_cache;

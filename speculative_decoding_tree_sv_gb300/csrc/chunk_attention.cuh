@@ -2,12 +2,12 @@
 // units' keys lie in tiles, and how the call's work is cut into equal ranges.
 //
 // Sequences whose rows (new tokens x query heads per KV head) fit one 16-row
-// matrix tile go to the row kernel (chunk_rows.cu), the others to the tile
-// kernel (chunk_tiles.cu).  Either way a unit is (sequence, KV head, run of
-// tokens), its work is a list of key pages or 128-key tiles, and the workers
-// (warps, or CTAs) take equal contiguous ranges of the list of all units, so
-// no worker idles beside a long one, whatever the batch.  A unit that a range
-// boundary cuts leaves one fp32 partial per piece (O / l and the log2 of its
+// matrix tile (or two, where make_plan says so) go to the row kernel
+// (chunk_rows.cu), the others to the tile kernel (chunk_tiles.cu).  Either way a unit is (sequence, KV head, run of
+// tokens) and its work a list of key pages or 128-key tiles.  The workers (warps,
+// or CTAs) take whole units where those are short enough, else equal contiguous
+// ranges of the list of all units, so that no worker idles beside a long one,
+// whatever the batch.  A unit that a range boundary cuts leaves one fp32 partial per piece (O / l and the log2 of its
 // softmax sum) for the combine kernel (chunk_attention.cu).
 #pragma once
 
@@ -59,6 +59,7 @@ struct Params {
   int4* tile_units;      // [ctas]: the cut unit that starts in this CTA: first token row, tokens (0: none), KV head, last CTA
   int row_workers;       // 0: no row kernel in this call
   int row_mode;          // RowMode
+  int row_shift;         // 1: the row kernel takes up to 32 rows, 16 per unit (0: up to 16)
   int whole_tiles;       // the tile kernel's units stay whole, so that nothing is left to combine
   int tile_ctas;         // the tile kernel's grid; 0: no tile kernel in this call
 };
@@ -86,8 +87,8 @@ __device__ __forceinline__ Seq load_seq(const Params& p, int b, bool report) {
 
 // Whether the row kernel takes a sequence of n new tokens (a call without it
 // leaves every sequence to the tile kernel).
-__device__ __forceinline__ bool in_rows(const Params& p, int n) {
-  return p.row_workers > 0 && static_cast<long long>(n) * p.group <= kRowUnit;
+__device__ __forceinline__ bool in_rows(const Params& p, int n, int shift) {
+  return p.row_workers > 0 && static_cast<long long>(n) * p.group <= (kRowUnit << shift);
 }
 
 // The key pages of a run of tokens [t0, t1) of a sequence: the sink pages
@@ -164,7 +165,7 @@ __device__ __forceinline__ TileSeq tile_units(const Params& p, int b, bool repor
   t.s = load_seq(p, b, report);
   t.units = 0;
   t.weight = 0;
-  if (t.s.n > 0 && !in_rows(p, t.s.n)) t.units = (t.s.n + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens);
+  if (t.s.n > 0 && !in_rows(p, t.s.n, p.row_shift)) t.units = (t.s.n + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens);
   return t;
 }
 
@@ -181,12 +182,22 @@ struct RowSeq {
   int pages;
 };
 
-__device__ __forceinline__ RowSeq row_seq(const Params& p, int b, bool report) {
+// Entry v of the row kernel's list, batch << shift long (shift: Params::row_shift):
+// sequence v >> shift, its rows from first_row on.
+__device__ __forceinline__ int first_row(int v, int shift) { return (v & shift) * kRowUnit; }
+
+__device__ __forceinline__ RowSeq row_seq(const Params& p, int v, int shift, bool report) {
   RowSeq r;
-  r.s = load_seq(p, b, report);
+  const int r0 = first_row(v, shift);
+  r.s = load_seq(p, v >> shift, report && r0 == 0);
   r.pages = 0;
-  if (r.s.n > 0 && in_rows(p, r.s.n)) {
-    r.keys = unit_keys(p, r.s, 0, r.s.n);
+  if (r.s.n > 0 && in_rows(p, r.s.n, shift) && (shift == 0 || r0 < r.s.n * p.group)) {
+    int t0 = 0, t1 = r.s.n;
+    if (shift > 0) {
+      t0 = r0 / p.group;
+      t1 = min(t1, (r0 + kRowUnit - 1) / p.group + 1);
+    }
+    r.keys = unit_keys(p, r.s, t0, t1);
     r.pages = r.keys.sink_pages + (r.keys.end + kPage - 1) / kPage - r.keys.first_page;
   }
   return r;
@@ -199,8 +210,8 @@ struct Work {
   int units;
 };
 
-__device__ __forceinline__ Work work_of(const Params& p, const TileSeq& t, const RowSeq& r) {
-  Work w{t.weight, 0, 1ll << 60, r.pages, t.units};
+__device__ __forceinline__ Work work_of(const Params& p, const TileSeq& t, long long pages) {
+  Work w{t.weight, 0, 1ll << 60, pages, t.units};
   if (t.units > 0) w.heaviest = w.lightest = last_weight(p, t.s, t.units);
   if (t.units > 1) {
     w.heaviest = max(w.heaviest, full_weight(p, t.s, t.units - 1) - full_weight(p, t.s, t.units - 2));

@@ -1,5 +1,5 @@
 // Chunk attention for sequences of at most 16 query rows per KV head (one
-// decoded token, or a few): the row kernel.
+// decoded token, or a few), in some calls 32 as two units: the row kernel.
 //
 // Mathematics: for the 16 rows (token x query head of the group) of a unit and
 // its keys, O = softmax(scale * Q K^T + mask) V with a running maximum m and
@@ -66,13 +66,14 @@ struct RowPiece {
   RowSeq seq;
 };
 
+template <int SHIFT>
 __device__ __forceinline__ bool next_piece(const Params& p, RowCursor& c, long long lo, long long hi, RowPiece& out) {
   if (p.row_mode != kRowRanges) {
-    for (; c.unit < p.batch * p.num_kv_heads;) {
+    for (; c.unit < (p.batch << SHIFT) * p.num_kv_heads;) {
       out.b = c.unit / p.num_kv_heads;
       out.kh = c.unit - out.b * p.num_kv_heads;
       out.pos = 0;
-      out.seq = row_seq(p, out.b, out.kh == 0);
+      out.seq = row_seq(p, out.b, SHIFT, out.kh == 0);
       c.unit += c.step;
       const int warp = threadIdx.x >> 5, pages = out.seq.pages;
       out.j0 = p.row_mode == kRowCta ? pages * warp / kRowWarps : 0;
@@ -81,11 +82,11 @@ __device__ __forceinline__ bool next_piece(const Params& p, RowCursor& c, long l
     }
     return false;
   }
-  while (c.b < p.batch && c.pos < hi) {
+  while (c.b < (p.batch << SHIFT) && c.pos < hi) {
     if (c.seq.pages == 0 || c.kh == p.num_kv_heads) {
       ++c.b;
       c.kh = 0;
-      if (c.b < p.batch) c.seq = row_seq(p, c.b, false);
+      if (c.b < (p.batch << SHIFT)) c.seq = row_seq(p, c.b, SHIFT, false);
       continue;
     }
     const long long a = lo > c.pos ? lo - c.pos : 0;
@@ -133,7 +134,7 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
   }
 }
 
-template <int D, bool FP16>
+template <int D, bool FP16, int SHIFT>
 __global__ void __launch_bounds__(kRowWarps * 32, 1)
     chunk_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                       const __grid_constant__ Params p) {
@@ -175,34 +176,35 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
   if (p.row_mode == kRowRanges) {
     RowSeq mine;  // of sequence `lane`: the only round when there are at most 32
     int blocks = gridDim.x;
+    const int batch = p.batch << SHIFT;
     if (side_by_side(p)) {
       Work sum{};
       sum.lightest = 1ll << 60;
-      for (int b0 = 0; b0 < p.batch; b0 += 32) {
+      for (int b0 = 0; b0 < batch; b0 += 32) {
         const int b = b0 + lane;
         TileSeq t{};
         RowSeq r{};
-        if (b < p.batch) {
-          r = row_seq(p, b, worker == 0);
-          t = tile_seq(p, b, false);
+        if (b < batch) {
+          r = row_seq(p, b, SHIFT, worker == 0);
+          if (first_row(b, SHIFT) == 0) t = tile_seq(p, b >> SHIFT, false);
         }
         if (b0 == 0) mine = r;
-        add_round(sum, work_of(p, t, r));
+        add_round(sum, work_of(p, t, r.pages));
       }
       total = sum.pages;
       const int own = row_sms(p, sum);
       if (own > 0) blocks = own;  // the other CTAs find no free SM before the tile kernel's end
       worker = warp * blocks + blockIdx.x;
-    } else if (p.batch == 1) {
-      mine = row_seq(p, 0, worker == 0);
+    } else if (batch == 1) {
+      mine = row_seq(p, 0, SHIFT, worker == 0);
       total = mine.pages;
     } else {
       mine.pages = 0;
-      for (int b0 = 0; b0 < p.batch; b0 += 32) {
+      for (int b0 = 0; b0 < batch; b0 += 32) {
         const int b = b0 + lane;
         RowSeq r;
         r.pages = 0;
-        if (b < p.batch) r = row_seq(p, b, worker == 0);
+        if (b < batch) r = row_seq(p, b, SHIFT, worker == 0);
         if (b0 == 0) mine = r;
         long long w = r.pages;
 #pragma unroll
@@ -219,16 +221,16 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
     lo = takes ? share.start(worker) : 0;
     hi = takes ? share.start(worker + 1) : 0;
     long long base = 0;
-    int bsel = p.batch;
-    if (p.batch == 1) {
+    int bsel = batch;
+    if (batch == 1) {
       bsel = 0;
       start.seq = mine;
     }
-    for (int b0 = 0; b0 < p.batch && bsel == p.batch; b0 += 32) {
+    for (int b0 = 0; b0 < batch && bsel == batch; b0 += 32) {
       const int b = b0 + lane;
-      if (p.batch > 32) {
+      if (batch > 32) {
         mine.pages = 0;
-        if (b < p.batch) mine = row_seq(p, b, false);
+        if (b < batch) mine = row_seq(p, b, SHIFT, false);
       }
       const long long w = mine.pages * static_cast<long long>(p.num_kv_heads);
       long long incl = w;
@@ -237,7 +239,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
         const long long v = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += v;
       }
-      const unsigned hit = __ballot_sync(0xffffffffu, b < p.batch && base + incl > lo);
+      const unsigned hit = __ballot_sync(0xffffffffu, b < batch && base + incl > lo);
       if (hit) {
         const int l = __ffs(hit) - 1;
         bsel = b0 + l;
@@ -256,7 +258,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
     start.b = bsel;
     start.kh = 0;
     start.pos = base;
-    if (bsel < p.batch && hi > lo) {
+    if (bsel < batch && hi > lo) {
       start.kh = static_cast<int>(Share::divide(lo - base, start.seq.pages));
       start.pos = base + static_cast<long long>(start.kh) * start.seq.pages;
     }
@@ -270,7 +272,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
   auto issue = [&]() {
     if (!more) return;
     while (load_j >= lp.j1) {
-      if (!next_piece(p, load_cur, lo, hi, lp)) {
+      if (!next_piece<SHIFT>(p, load_cur, lo, hi, lp)) {
         more = false;
         return;
       }
@@ -283,7 +285,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
       const int j = load_j + lane;
       if (j < lp.j1) {
         const int page = j < k.sink_pages ? j : k.first_page + (j - k.sink_pages);
-        ids = p.block_table[static_cast<size_t>(lp.b) * p.max_pages_per_seq + page];
+        ids = p.block_table[static_cast<size_t>(lp.b >> SHIFT) * p.max_pages_per_seq + page];
         if (ids < 0 || ids >= p.num_pages) {
           report_error(p.err, SV_DEVERR_BAD_PAGE);
           ids = p.num_pages;  // outside the pool: the box arrives as zeros
@@ -313,10 +315,10 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
   RowPiece pc;
   int done = 0;
   bool ok = true;
-  while ((ok || p.row_mode == kRowCta) && hi > lo && next_piece(p, cur, lo, hi, pc)) {
+  while ((ok || p.row_mode == kRowCta) && hi > lo && next_piece<SHIFT>(p, cur, lo, hi, pc)) {
     const Seq& s = pc.seq.s;
     const Keys& keys = pc.seq.keys;
-    const int rows = s.n * p.group;
+    const int r0 = first_row(pc.b, SHIFT), rows = SHIFT ? min(s.n * p.group - r0, kRowUnit) : s.n * p.group;
     int tok[2];
     uint32_t qf[D / 16][4];
     {
@@ -326,8 +328,8 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
       for (int i = 0; i < 2; ++i) {
         const int r = g + 8 * i;
         live[i] = r < rows;
-        tok[i] = live[i] ? r / p.group : s.n - 1;
-        const int head = pc.kh * p.group + (live[i] ? r - tok[i] * p.group : 0);
+        tok[i] = live[i] ? (r0 + r) / p.group : s.n - 1;
+        const int head = pc.kh * p.group + (live[i] ? r0 + r - tok[i] * p.group : 0);
         src[i] = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.q) +
                                                    (s.n0 + tok[i]) * p.q_stride + static_cast<long long>(head) * D) + tq;
       }
@@ -451,7 +453,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
       const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
       const float lse2 = l[i] > 0.f ? m[i] + log2f(l[i]) : -INFINITY;
       if (whole) {
-        const int head = pc.kh * p.group + (r - tok[i] * p.group);
+        const int head = pc.kh * p.group + (r0 + r - tok[i] * p.group);
         const long long token = s.n0 + tok[i];
         uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + token * p.out_stride +
                                                     static_cast<long long>(head) * D) + tq;
@@ -520,7 +522,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
   griddep_launch_dependents();
 }
 
-template <int D, bool FP16>
+template <int D, bool FP16, int SHIFT>
 static sv_status launch(const Launch& l) {
   static std::mutex mu;
   static bool done[64] = {false};
@@ -529,7 +531,7 @@ static sv_status launch(const Launch& l) {
   {
     std::lock_guard<std::mutex> lock(mu);
     if (dev >= 64 || !done[dev]) {
-      if (cudaFuncSetAttribute(chunk_rows_kernel<D, FP16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      if (cudaFuncSetAttribute(chunk_rows_kernel<D, FP16, SHIFT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                RowCfg<D>::kSmemBytes) != cudaSuccess)
         return SV_ERR_CUDA;
       if (dev < 64) done[dev] = true;
@@ -547,8 +549,13 @@ static sv_status launch(const Launch& l) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, chunk_rows_kernel<D, FP16>, tm_k, tm_v, l.p) != cudaSuccess) return SV_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, chunk_rows_kernel<D, FP16, SHIFT>, tm_k, tm_v, l.p) != cudaSuccess) return SV_ERR_CUDA;
   return SV_OK;
+}
+
+template <int D, bool FP16>
+static sv_status launch(const Launch& l) {
+  return l.p.row_shift ? launch<D, FP16, 1>(l) : launch<D, FP16, 0>(l);
 }
 
 sv_status launch_rows(const Launch& l) {

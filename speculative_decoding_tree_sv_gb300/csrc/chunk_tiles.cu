@@ -271,18 +271,19 @@ __device__ void deal_pieces(const Params& p, int cta, Publish&& publish, NearEnd
     sum.lightest = 1ll << 60;
     if (p.batch == 1) {  // (a prompt alone: no sums)
       mine = tile_seq(p, 0, report);
-      sum = work_of(p, mine, RowSeq{});
+      sum = work_of(p, mine, 0);
     } else {
       for (int b0 = 0; b0 < p.batch; b0 += 32) {
         const int b = b0 + lane;
         TileSeq t{};
-        RowSeq r{};
+        long long pages = 0;
         if (b < p.batch) {
           t = tile_seq(p, b, report);
-          if (beside) r = row_seq(p, b, false);
+          if (beside)
+            for (int i = 0; i <= p.row_shift; ++i) pages += row_seq(p, (b << p.row_shift) + i, p.row_shift, false).pages;
         }
         if (b0 == 0) mine = t;
-        add_round(sum, work_of(p, t, r));
+        add_round(sum, work_of(p, t, pages));
       }
     }
     if (beside) avail = max(1, min(avail, p.row_workers / kRowWarps - row_sms(p, sum)));

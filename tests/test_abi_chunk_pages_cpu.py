@@ -67,7 +67,10 @@ def test_chunk_workspace_holds_the_partials_of_each_kernel(lib):
     assert rows + tiles <= mixed <= rows + tiles + 16384
     long = size(chunk(batch=1, total_tokens=39))           # one chunk: the tile kernel alone
     assert tiles <= long <= tiles + 16384
-    assert tiles <= size(chunk(num_q_heads=32, num_kv_heads=1, total_tokens=2, max_tokens=1)) <= tiles + 16384
+    # 32 rows per token: either kernel, by the size of the cache that the table's width allows
+    either = size(chunk(num_q_heads=32, num_kv_heads=1, total_tokens=2, max_tokens=1))
+    assert rows + tiles <= either <= rows + tiles + 16384
+    assert size(chunk(num_q_heads=32, num_kv_heads=1, total_tokens=2, max_tokens=1, max_pages_per_seq=200000)) == either
 
 
 def test_append_refuses(lib):

@@ -180,6 +180,20 @@ def test_units_shared_by_a_block(Hq, Hkv, new, dtype, D):
     c.check()
 
 
+@pytest.mark.parametrize("Hq,Hkv,new", [
+    (32, 1, [1, 1, 1, 1]), (20, 1, [1, 1, 1, 1]), (16, 4, [5, 8, 1, 4]), (14, 2, [4, 3, 1, 2]), (3, 1, [10, 6, 5, 0]),
+    (8, 2, [8, 200, 1, 9]), (32, 1, [1, 0, 90, 1]), (8, 8, [32, 17, 16, 33]),
+])
+@pytest.mark.parametrize("ctx,window,sink", [([40, 0, 3, 200], 0, 0), ([1300, 900, 31, 0], 0, 0), ([1300, 900, 31, 700], 100, 7),
+                                             ([9000, 33, 2000, 5], 0, 0)])
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("fp16", 64)])
+def test_up_to_32_rows(Hq, Hkv, new, ctx, window, sink, dtype, D):
+    """17 to 32 rows per KV head: two units of 16, with other lengths among them."""
+    c = Case(ctx, new, Hq, Hkv, D, dtype, window=window, sink=sink, seed=Hq + sum(new))
+    assert c.run() == 0
+    c.check()
+
+
 @pytest.mark.parametrize("batch,Hkv,longest", [(60, 4, 1500), (76, 4, 600), (130, 2, 4000), (90, 2, 1500), (610, 4, 520)])
 @pytest.mark.parametrize("window,sink", [(0, 0), (200, 20)])
 def test_more_units_than_blocks(batch, Hkv, longest, window, sink):
