@@ -37,7 +37,7 @@ __device__ __forceinline__ void combine_rows(const Params& p, int unit, int row0
   const int b = unit / p.num_kv_heads, kh = unit - b * p.num_kv_heads;  // b: of the row kernel's list
   const Seq s = load_seq(p, b >> p.row_shift, false);
   const int first = u.x, pieces = u.y - u.x + 1;
-  if (s.n == 0 || !in_rows(p, s.n, p.row_shift)) return;
+  if (s.n == 0 || !in_rows(p, s.n)) return;
   const int base = first_row(b, p.row_shift), rows = min(s.n * p.group - base, kRowUnit);
   if (rows <= row0 || first < 0 || u.y >= p.row_workers || pieces <= 1)
     return;  // (no such rows; not cut; a kernel that timed out left no record)
@@ -429,6 +429,7 @@ sv_status sv_chunk_attention(const sv_chunk_params* params, sv_stream_t stream) 
   p.row_workers = w.row_workers;
   p.row_mode = w.row_mode;
   p.row_shift = w.row_shift;
+  p.row_limit = w.row_workers > 0 ? chunk::kRowUnit << w.row_shift : 0;
   p.whole_tiles = w.whole_tiles;
   p.tile_ctas = w.tile_grid;
   l.k_cache = params->k_cache;

@@ -59,9 +59,10 @@ struct Params {
   int4* tile_units;      // [ctas]: the cut unit that starts in this CTA: first token row, tokens (0: none), KV head, last CTA
   int row_workers;       // 0: no row kernel in this call
   int row_mode;          // RowMode
-  int row_shift;         // 1: the row kernel takes up to 32 rows, 16 per unit (0: up to 16)
   int whole_tiles;       // the tile kernel's units stay whole, so that nothing is left to combine
   int tile_ctas;         // the tile kernel's grid; 0: no tile kernel in this call
+  int row_limit;         // the most rows of a sequence that go to the row kernel: 16, 32 or (no row kernel) 0
+  int row_shift;         // 1: it takes up to 32 rows, 16 per unit
 };
 
 // One sequence's lengths; n is 0 when it has no work (nothing new, or lengths
@@ -85,10 +86,9 @@ __device__ __forceinline__ Seq load_seq(const Params& p, int b, bool report) {
   return s;
 }
 
-// Whether the row kernel takes a sequence of n new tokens (a call without it
-// leaves every sequence to the tile kernel).
-__device__ __forceinline__ bool in_rows(const Params& p, int n, int shift) {
-  return p.row_workers > 0 && static_cast<long long>(n) * p.group <= (kRowUnit << shift);
+// Whether the row kernel takes a sequence of n > 0 new tokens.
+__device__ __forceinline__ bool in_rows(const Params& p, int n) {
+  return static_cast<long long>(n) * p.group <= p.row_limit;
 }
 
 // The key pages of a run of tokens [t0, t1) of a sequence: the sink pages
@@ -165,7 +165,7 @@ __device__ __forceinline__ TileSeq tile_units(const Params& p, int b, bool repor
   t.s = load_seq(p, b, report);
   t.units = 0;
   t.weight = 0;
-  if (t.s.n > 0 && !in_rows(p, t.s.n, p.row_shift)) t.units = (t.s.n + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens);
+  if (t.s.n > 0 && !in_rows(p, t.s.n)) t.units = (t.s.n + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens);
   return t;
 }
 
@@ -191,7 +191,7 @@ __device__ __forceinline__ RowSeq row_seq(const Params& p, int v, int shift, boo
   const int r0 = first_row(v, shift);
   r.s = load_seq(p, v >> shift, report && r0 == 0);
   r.pages = 0;
-  if (r.s.n > 0 && in_rows(p, r.s.n, shift) && (shift == 0 || r0 < r.s.n * p.group)) {
+  if (r.s.n > 0 && in_rows(p, r.s.n) && (shift == 0 || r0 < r.s.n * p.group)) {
     int t0 = 0, t1 = r.s.n;
     if (shift > 0) {
       t0 = r0 / p.group;

@@ -279,8 +279,11 @@ __device__ void deal_pieces(const Params& p, int cta, Publish&& publish, NearEnd
         long long pages = 0;
         if (b < p.batch) {
           t = tile_seq(p, b, report);
-          if (beside)
-            for (int i = 0; i <= p.row_shift; ++i) pages += row_seq(p, (b << p.row_shift) + i, p.row_shift, false).pages;
+          if (beside) {  // the row kernel's (two units of a sequence see about the same pages)
+            const Keys keys = unit_keys(p, t.s, 0, t.s.n);
+            const int seen = keys.sink_pages + (keys.end + kPage - 1) / kPage - keys.first_page;
+            pages = t.units == 0 && t.s.n > 0 ? seen << p.row_shift : 0;
+          }
         }
         if (b0 == 0) mine = t;
         add_round(sum, work_of(p, t, pages));
