@@ -255,8 +255,9 @@ Plan make_plan(const sv_chunk_params* c, int sms) {
   // of the tile kernel takes at once (4 sequences of 500 / 1500 tokens at 8 KV
   // heads 16.1 / 18.3 us against 11.7 / 25.7 in the tile kernel, 16 of 8000 at 2 heads, D
   // 64, 63 MB, 27.2 / 30.8, but 32 of 2000 at 8 heads, 252 MB, 67 / 62).
-  const long long cache = static_cast<long long>(c->batch) * c->num_kv_heads * width * 4 * kPage * c->head_dim;
-  w.row_shift = G <= 2 * kRowUnit && most > kRowUnit && width > kTilePages && cache <= kSharedBytes;
+  const long long pages = static_cast<long long>(c->batch) * c->num_kv_heads * width;
+  w.row_shift = G <= 2 * kRowUnit && most > kRowUnit && width > kTilePages &&
+                pages <= kSharedBytes / (4 * kPage * c->head_dim);
   const int rows = kRowUnit << w.row_shift;
   const bool some_large = most > rows;
   const bool some_small = G <= rows && !(some_large && least * G > rows);
@@ -275,15 +276,12 @@ Plan make_plan(const sv_chunk_params* c, int sms) {
   // pages 27.5 against 30.5 us, 1024 of 63 69.6 / 77; 192 of 63 (the second round a
   // quarter full) 18.9 against 17.3.
   const long long units = (static_cast<long long>(c->batch) << w.row_shift) * c->num_kv_heads;
-  const bool fits = static_cast<long long>(c->max_tokens) * G <= kCtaRows;
-  if (fits && units <= sms)
-    w.row_mode = width <= 2                                                              ? kRowWarp
-                 : width <= kCtaPages && width * (sms - units) <= kCtaEven * static_cast<long long>(sms) ? kRowCta
-                                                                                         : kRowRanges;
-  else
-    w.row_mode = width <= (some_large ? kWarpPages : std::min(kWarpPages, 12 + 10 * units / sms)) ? kRowWarp
-                 : fits && width <= kCtaPages && 10 * units >= 7 * sms * ((units + sms - 1) / sms) ? kRowCta
-                                                                                                : kRowRanges;
+  const bool fits = most <= kCtaRows;
+  const bool cta_units = fits && width <= kCtaPages &&
+                         (units <= sms ? width * (sms - units) <= kCtaEven * sms
+                                       : 10 * units >= 7 * sms * ((units + sms - 1) / sms));
+  const long long warp_pages = fits && units <= sms ? 2 : some_large ? kWarpPages : std::min(kWarpPages, 12 + 10 * units / sms);
+  w.row_mode = width <= warp_pages ? kRowWarp : cta_units ? kRowCta : kRowRanges;
   // Tile units so light that cutting them for the SMs that have none, or less, gains
   // less than the combine costs (3 us): the heaviest there may be, the more
   // of the SMs the call's token rows fill.
@@ -293,8 +291,8 @@ Plan make_plan(const sv_chunk_params* c, int sms) {
   w.whole_tiles = 8 * (keys + kUnitKeys) * (3 * sms - 2 * filled) <= sms * kWholeWeight;
   // No more CTAs than the tiles of all units there may be, or than the units.
   const long long groups = c->total_tokens / group + c->batch;
-  const long long useful = groups * c->num_kv_heads * (w.whole_tiles ? 1 : (keys + kBlockN - 1) / kBlockN + 1);
-  w.tile_grid = static_cast<int>(std::min<long long>(w.tile_ctas, useful));
+  const double useful = static_cast<double>(groups) * c->num_kv_heads * (w.whole_tiles ? 1 : keys / kBlockN + 2);
+  w.tile_grid = useful < w.tile_ctas ? static_cast<int>(useful) : w.tile_ctas;
   w.combine = (w.row_workers > 0 && w.row_mode == kRowRanges) || (w.tile_ctas > 0 && !w.whole_tiles);
   size_t at = kWorkspaceHeader;
   auto take = [&](size_t bytes) {

@@ -3,12 +3,13 @@
 //
 // Sequences whose rows (new tokens x query heads per KV head) fit one 16-row
 // matrix tile (or two, where make_plan says so) go to the row kernel
-// (chunk_rows.cu), the others to the tile kernel (chunk_tiles.cu).  Either way a unit is (sequence, KV head, run of
-// tokens) and its work a list of key pages or 128-key tiles.  The workers (warps,
-// or CTAs) take whole units where those are short enough, else equal contiguous
-// ranges of the list of all units, so that no worker idles beside a long one,
-// whatever the batch.  A unit that a range boundary cuts leaves one fp32 partial per piece (O / l and the log2 of its
-// softmax sum) for the combine kernel (chunk_attention.cu).
+// (chunk_rows.cu), the others to the tile kernel (chunk_tiles.cu).  Either way a
+// unit is (sequence, KV head, run of tokens) and its work a list of key pages or
+// 128-key tiles.  The workers (warps, or CTAs) take whole units where those are
+// short enough, else equal contiguous ranges of the list of all units, so that no
+// worker idles beside a long one, whatever the batch.  A unit that a range boundary
+// cuts leaves one fp32 partial per piece (O / l and the log2 of its softmax sum)
+// for the combine kernel (chunk_attention.cu).
 #pragma once
 
 #include <cuda_fp16.h>
