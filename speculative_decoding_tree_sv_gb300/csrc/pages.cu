@@ -19,13 +19,14 @@
 namespace sv {
 namespace pages {
 
-// CTAs of the pool kernels' cluster; a small pool with a row per warp at most
-// takes a single one, whose barriers are cheaper (reserve, one CTA / eight: 3 rows
-// and 73 pages 3.1 / 6.1 us; 80 rows and 1705 pages 6.7 / 5.1.  Compact: 256 pages
-// 3.2 / 5.0; 8192 pages 12.4 / 7.8).
+// CTAs of the pool kernels' cluster; a small pool with two rows per warp at most
+// takes a single one, whose barriers are cheaper (a step of release, fork, reserve
+// and copy, one CTA / eight: 3 rows and 73 pages 10.6 / 15.2 us, 18 and 519 15.8 /
+// 18.0, 32 and 389 19.0 / 19.5, 75 and 877 31.5 / 19.0.  Compact: 256 pages 3.4 /
+// 5.0; 3000 pages and 40 rows 7.2 / 6.0).
 constexpr int kClusterCtas = 8;
 constexpr int kSmallPool = 1024;
-constexpr int kSmallRows = 16;
+constexpr int kSmallRows = 32;
 constexpr int kClusterThreads = 512;
 constexpr int kWarps = kClusterThreads / 32;
 constexpr int kMaxPages = 1 << 21;  // bitmap of an eighth: 32 KB, and as much for its word ranks
