@@ -215,10 +215,10 @@ bool encode_pool(CUtensorMap* map, const void* base, const Launch& l, bool whole
 }
 
 // Widths in pages: of units to warps, of a unit to a CTA (kCtaEven of them with few
-// units, where the other SMs would idle), and of the least units that go to the
-// row kernel in two.
+// units, where the other SMs would idle), and of the least units that go to a
+// cluster, or to the row kernel in two.
 constexpr long long kWarpPages = 32, kCtaPages = 256, kCtaEven = 64;
-constexpr long long kTilePages = 48, kSharedBytes = 64ll << 20;
+constexpr long long kClusterPages = 48, kTilePages = 48, kSharedBytes = 64ll << 20;
 // The largest weight of a unit for which a call leaves out the combine, when its rows
 // fill every SM (a third of it when they fill none): two chunks of 512 after 1500 tokens
 // 33.2 us against 36.7 with it, a prompt of 2048 34.2 / 37.0, but a chunk of 40 after
@@ -229,7 +229,7 @@ constexpr long long kWholeWeight = 24 * 8 * kBlockN;
 struct Plan {
   int row_workers, tile_ctas;
   int tile_grid;  // of the tile_ctas the workspace has room for
-  int row_mode, row_shift, whole_tiles;
+  int row_mode, row_shift, row_cluster, whole_tiles;
   bool combine;
   size_t row_o, row_lse, row_units, tile_o, tile_lse, tile_units, bytes;
 };
@@ -282,6 +282,18 @@ Plan make_plan(const sv_chunk_params* c, int sms) {
                                        : 10 * units >= 7 * sms * ((units + sms - 1) / sms));
   const long long warp_pages = fits && units <= sms ? 2 : some_large ? kWarpPages : std::min(kWarpPages, 12 + 10 * units / sms);
   w.row_mode = width <= warp_pages ? kRowWarp : cta_units ? kRowCta : kRowRanges;
+  // Few units of middling length: a cluster of CTAs each, eight pages per warp at
+  // most (longer ones are bound by memory, and their even ranges by less of it).
+  // One sequence at 8 KV heads 8.7 / 9.4 / 10.7 / 13.5 us with 1000 / 2000 / 4000 / 8000
+  // tokens against 10.5 / 11.6 / 12.7 / 15.4 in a CTA or in ranges, but 8.5 / 7.6 with
+  // 500; four of 1000 / 4000 8.5 / 12.7 against 10.4 / 16.4, eight of 2000 12.7 / 14.2.
+  // (Sixteen clusters of eight CTAs do not run at once.)
+  w.row_cluster = 1;
+  const int cluster = units <= 8 ? 8 : units <= 32 ? 4 : units <= 64 ? 2 : 1;
+  if (fits && cluster > 1 && width >= kClusterPages && width <= 8 * kRowWarps * cluster) {
+    w.row_mode = kRowCta;
+    w.row_cluster = cluster;
+  }
   // Tile units so light that cutting them for the SMs that have none, or less, gains
   // less than the combine costs (3 us): the heaviest there may be, the more
   // of the SMs the call's token rows fill.
@@ -427,6 +439,7 @@ sv_status sv_chunk_attention(const sv_chunk_params* params, sv_stream_t stream) 
   p.row_workers = w.row_workers;
   p.row_mode = w.row_mode;
   p.row_shift = w.row_shift;
+  p.row_cluster = w.row_cluster;
   p.row_limit = w.row_workers > 0 ? chunk::kRowUnit << w.row_shift : 0;
   p.whole_tiles = w.whole_tiles;
   p.tile_ctas = w.tile_grid;

@@ -33,7 +33,7 @@ constexpr float kLog2e = 1.44269504088896340736f;
 enum RowMode {
   kRowRanges = 0,  // equal ranges of all pages; the combine merges cut units
   kRowWarp = 1,    // whole units to the warps in turn
-  kRowCta = 2      // whole units to the CTAs in turn, their pages shared by the warps
+  kRowCta = 2      // whole units to the CTAs (or a cluster each), their pages shared by the warps
 };
 
 struct Params {
@@ -64,6 +64,7 @@ struct Params {
   int tile_ctas;         // the tile kernel's grid; 0: no tile kernel in this call
   int row_limit;         // the most rows of a sequence that go to the row kernel: 16, 32 or (no row kernel) 0
   int row_shift;         // 1: it takes up to 32 rows, 16 per unit
+  int row_cluster;       // kRowCta: CTAs (a cluster) per unit; more than one: every unit has its own
 };
 
 // One sequence's lengths; n is 0 when it has no work (nothing new, or lengths

@@ -18,11 +18,12 @@
 // The pages of all units form one list (sequence, KV head, page); worker w
 // takes an equal contiguous range, and the combine kernel merges the units that
 // a boundary cuts.  Short contexts (the host sees the table's width) go without
-// it: a warp takes whole units, or a CTA a unit whose pages its warps share and
-// merge in shared memory (RowMode).  Page ids are fetched 32 at a time.  The
+// it: a warp takes whole units, or a CTA (a cluster, where units are few) a unit
+// whose pages its warps share and merge in shared memory (RowMode).  Page ids are fetched 32 at a time.  The
 // last page of a sequence may hold anything behind its last token: its box
 // starts at a negative row, so the missing rows in front arrive as zeros and
 // its tokens end at row 15.
+#include <cooperative_groups.h>
 #include <math.h>
 
 #include <mutex>
@@ -66,7 +67,7 @@ struct RowPiece {
   RowSeq seq;
 };
 
-template <int SHIFT>
+template <int SHIFT, bool CLUSTER>
 __device__ __forceinline__ bool next_piece(const Params& p, RowCursor& c, long long lo, long long hi, RowPiece& out) {
   if (p.row_mode != kRowRanges) {
     for (; c.unit < (p.batch << SHIFT) * p.num_kv_heads;) {
@@ -75,9 +76,11 @@ __device__ __forceinline__ bool next_piece(const Params& p, RowCursor& c, long l
       out.pos = 0;
       out.seq = row_seq(p, out.b, SHIFT, out.kh == 0);
       c.unit += c.step;
-      const int warp = threadIdx.x >> 5, pages = out.seq.pages;
-      out.j0 = p.row_mode == kRowCta ? pages * warp / kRowWarps : 0;
-      out.j1 = p.row_mode == kRowCta ? pages * (warp + 1) / kRowWarps : pages;
+      const int pages = out.seq.pages;
+      const int warps = CLUSTER ? p.row_cluster * kRowWarps : kRowWarps;
+      const int warp = (threadIdx.x >> 5) + (CLUSTER ? cluster_ctarank() * kRowWarps : 0);
+      out.j0 = p.row_mode == kRowCta ? pages * warp / warps : 0;
+      out.j1 = p.row_mode == kRowCta ? pages * (warp + 1) / warps : pages;
       if (pages > 0) return true;  // (a warp's share of a CTA's unit may be empty)
     }
     return false;
@@ -134,7 +137,7 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
   }
 }
 
-template <int D, bool FP16, int SHIFT>
+template <int D, bool FP16, int SHIFT, bool CLUSTER>
 __global__ void __launch_bounds__(kRowWarps * 32, 1)
     chunk_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                       const __grid_constant__ Params p) {
@@ -173,6 +176,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
   Share share{};
   start.unit = p.row_mode == kRowCta ? blockIdx.x : worker;
   start.step = p.row_mode == kRowCta ? gridDim.x : p.row_workers;
+  if constexpr (CLUSTER) start.unit = blockIdx.x / p.row_cluster;  // (and no other: the grid is no smaller)
   if (p.row_mode == kRowRanges) {
     RowSeq mine;  // of sequence `lane`: the only round when there are at most 32
     int blocks = gridDim.x;
@@ -272,7 +276,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
   auto issue = [&]() {
     if (!more) return;
     while (load_j >= lp.j1) {
-      if (!next_piece<SHIFT>(p, load_cur, lo, hi, lp)) {
+      if (!next_piece<SHIFT, CLUSTER>(p, load_cur, lo, hi, lp)) {
         more = false;
         return;
       }
@@ -313,9 +317,10 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
   const int mi = lane >> 3, mr = lane & 7;
   RowCursor cur = start;
   RowPiece pc;
+  if constexpr (CLUSTER) pc.seq.pages = 0;
   int done = 0;
   bool ok = true;
-  while ((ok || p.row_mode == kRowCta) && hi > lo && next_piece<SHIFT>(p, cur, lo, hi, pc)) {
+  while ((ok || p.row_mode == kRowCta) && hi > lo && next_piece<SHIFT, CLUSTER>(p, cur, lo, hi, pc)) {
     const Seq& s = pc.seq.s;
     const Keys& keys = pc.seq.keys;
     const int r0 = first_row(pc.b, SHIFT), rows = SHIFT ? min(s.n * p.group - r0, kRowUnit) : s.n * p.group;
@@ -490,6 +495,14 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
           for (int e = 0; e < E; ++e) acc[e] = fmaf(f, part[e], acc[e] * keep);
         }
         const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+        if constexpr (CLUSTER) {  // the CTA's part of the row, in the ring: it is empty by now
+          float* part = reinterpret_cast<float*>(smem + r * C::kRingBytes) + lane * E;
+#pragma unroll
+          for (int e = 0; e < E; ++e) part[e] = acc[e] * inv;
+          __syncwarp();
+          if (lane == 0) cta_lse[0][r] = wsum > 0.f ? mx + log2f(wsum) : -INFINITY;
+          continue;
+        }
         const int row_tok = r / p.group, head = pc.kh * p.group + r - row_tok * p.group;
         const long long token = s.n0 + row_tok;
         uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + token * p.out_stride +
@@ -505,6 +518,55 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
       const int last = whole ? worker : share.holder(pc.pos + pc.seq.pages - 1);
       p.row_units[static_cast<size_t>(pc.b) * p.num_kv_heads + pc.kh] = make_int2(worker, last);
     }
+  }
+  if constexpr (CLUSTER) {
+    // the CTAs' parts, a row per CTA
+    const bool any = pc.seq.pages > 0;
+    __syncwarp();
+    cluster_sync_all();
+    if (any && warp == 0) {
+      namespace cg = cooperative_groups;
+      cg::cluster_group cl = cg::this_cluster();
+      constexpr int E = D / 32;
+      const int rows = pc.seq.s.n * p.group;
+      for (int r = cluster_ctarank(); r < rows; r += p.row_cluster) {
+        float acc[E], mx = -INFINITY, wsum = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 1
+        for (int x0 = 0; x0 < p.row_cluster; x0 += 2) {
+          float l2[2], v[2][E];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            l2[x] = *cl.map_shared_rank(&cta_lse[0][r], x0 + x);
+            const float* part = cl.map_shared_rank(reinterpret_cast<float*>(smem + r * C::kRingBytes) + lane * E, x0 + x);
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[x][e] = part[e];
+          }
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (l2[x] == -INFINITY) continue;
+            const float m_new = fmaxf(mx, l2[x]);
+            const float keep = ex2(mx - m_new), f = ex2(l2[x] - m_new);
+            mx = m_new;
+            wsum = fmaf(wsum, keep, f);
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = fmaf(f, v[x][e], acc[e] * keep);
+          }
+        }
+        const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+        const int row_tok = r / p.group, head = pc.kh * p.group + r - row_tok * p.group;
+        const long long token = pc.seq.s.n0 + row_tok;
+        uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + token * p.out_stride +
+                                                    static_cast<long long>(head) * D) + lane * (E / 2);
+#pragma unroll
+        for (int e = 0; e < E; e += 2) dst[e / 2] = pack2<FP16>(acc[e] * inv, acc[e + 1] * inv);
+        if (lane == 0 && p.lse != nullptr)
+          p.lse[token * p.num_q_heads + head] = wsum > 0.f ? (mx + log2f(wsum)) * kLn2 : -INFINITY;
+      }
+    }
+    __syncwarp();
+    cluster_sync_all();  // no CTA leaves while another reads its rows
   }
   if (!ok) {
     if (lane == 0) {
@@ -522,7 +584,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
   griddep_launch_dependents();
 }
 
-template <int D, bool FP16, int SHIFT>
+template <int D, bool FP16, int SHIFT, bool CLUSTER>
 static sv_status launch(const Launch& l) {
   static std::mutex mu;
   static bool done[64] = {false};
@@ -531,7 +593,7 @@ static sv_status launch(const Launch& l) {
   {
     std::lock_guard<std::mutex> lock(mu);
     if (dev >= 64 || !done[dev]) {
-      if (cudaFuncSetAttribute(chunk_rows_kernel<D, FP16, SHIFT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      if (cudaFuncSetAttribute(chunk_rows_kernel<D, FP16, SHIFT, CLUSTER>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                RowCfg<D>::kSmemBytes) != cudaSuccess)
         return SV_ERR_CUDA;
       if (dev < 64) done[dev] = true;
@@ -540,22 +602,26 @@ static sv_status launch(const Launch& l) {
   CUtensorMap tm_k, tm_v;
   if (!encode_pool(&tm_k, l.k_cache, l, true) || !encode_pool(&tm_v, l.v_cache, l, true)) return SV_ERR_CUDA;
   cudaLaunchConfig_t cfg = cudaLaunchConfig_t{};
-  cfg.gridDim = dim3(static_cast<unsigned>(l.p.row_workers / kRowWarps), 1, 1);
+  const int units = l.p.batch * l.p.num_kv_heads;  // (a cluster's grid: one unit each)
+  cfg.gridDim = dim3(static_cast<unsigned>(CLUSTER ? units * l.p.row_cluster : l.p.row_workers / kRowWarps), 1, 1);
   cfg.blockDim = dim3(kRowWarps * 32, 1, 1);
   cfg.dynamicSmemBytes = RowCfg<D>::kSmemBytes;
   cfg.stream = l.stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {static_cast<unsigned>(CLUSTER ? l.p.row_cluster : 1), 1, 1};
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, chunk_rows_kernel<D, FP16, SHIFT>, tm_k, tm_v, l.p) != cudaSuccess) return SV_ERR_CUDA;
+  cfg.numAttrs = CLUSTER ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, chunk_rows_kernel<D, FP16, SHIFT, CLUSTER>, tm_k, tm_v, l.p) != cudaSuccess) return SV_ERR_CUDA;
   return SV_OK;
 }
 
 template <int D, bool FP16>
 static sv_status launch(const Launch& l) {
-  return l.p.row_shift ? launch<D, FP16, 1>(l) : launch<D, FP16, 0>(l);
+  if (l.p.row_cluster > 1) return launch<D, FP16, 0, true>(l);
+  return l.p.row_shift ? launch<D, FP16, 1, false>(l) : launch<D, FP16, 0, false>(l);
 }
 
 sv_status launch_rows(const Launch& l) {

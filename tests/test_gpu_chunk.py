@@ -171,11 +171,12 @@ def test_widths_around_the_ways_of_sharing_units(width, batch, Hq, Hkv):
 
 @pytest.mark.parametrize("dtype,D", [("bf16", 128), ("fp16", 64)])
 @pytest.mark.parametrize("Hq,Hkv,new", [(16, 2, 1), (8, 1, 1), (6, 2, 2), (14, 2, 1), (8, 8, 8), (18, 2, 1), (5, 5, 9)])
-def test_units_shared_by_a_block(Hq, Hkv, new, dtype, D):
-    """Up to eight rows of a unit and a table of up to 63 pages: the warps of a
-    block share it, some of them nothing of the short ones.  (Nine rows: one
-    more than they share.)"""
-    c = Case([977, 0, 1, 110, 128, 15, 500], [new] * 7, Hq, Hkv, D, dtype, seed=Hq + new)
+@pytest.mark.parametrize("longest,batch", [(600, 7), (977, 7), (1900, 2), (1900, 1), (7900, 1)])
+def test_units_shared_by_a_block(Hq, Hkv, new, dtype, D, longest, batch):
+    """Up to eight rows of a unit: the warps of a block, or of a cluster of 2, 4 or
+    8, share it, some of them nothing of the short ones.  (Nine rows: one more than
+    they share.)"""
+    c = Case([longest, 0, 1, 110, 128, 15, 500][:batch], [new] * batch, Hq, Hkv, D, dtype, seed=Hq + new)
     assert c.run() == 0
     c.check()
 
