@@ -583,7 +583,7 @@ typedef struct sv_chunk_params {
 } sv_chunk_params;
 
 /* Bytes of workspace for these parameters on the current device: up to 61 MB of
- * partial results, and 8 bytes per sequence and KV head. */
+ * partial results, and 16 bytes per sequence and KV head. */
 sv_status sv_chunk_attention_workspace_size(const sv_chunk_params* params, size_t* bytes);
 
 /* Device errors: SV_DEVERR_BAD_LENGTH for a sequence whose lengths do not fit

@@ -54,7 +54,7 @@ struct Params {
   // partials of cut units and what the combine needs of them
   float* row_o;          // [workers][2][16][D]
   float* row_lse;        // [workers][2][16]
-  int2* row_units;       // [B * Hkv] first and last worker of the unit
+  int2* row_units;       // [(B << row_shift) * Hkv] first and last worker of the unit
   float* tile_o;         // [ctas][2][256][D]
   float* tile_lse;       // [ctas][2][256]
   int4* tile_units;      // [ctas]: the cut unit that starts in this CTA: first token row, tokens (0: none), KV head, last CTA
@@ -249,9 +249,9 @@ __device__ __forceinline__ bool side_by_side(const Params& p) {
 // other on SMs in proportion to their work: 24 sequences with four chunks of 53 to
 // 370 tokens 53.1 us against 59.8 one behind the other, a chunk of 512 and 24
 // tokens over 4000 keys each 87 / 118, chunks of 1024 and 98 tokens over 1000 100 /
-// 124, a chunk of 100 and 60 tokens over 8000 318 / 335.  Tile units that one per
-// SM leaves whole are cut only when that costs less in both kernels (the first
-// case: 65 us).
+// 124 (88 since whole units go by ticket), a chunk of 100 and 60 tokens over 8000
+// 318 / 335.  Tile units that one per SM leaves whole are cut only when that costs
+// less in both kernels (the first case: 65 us).
 __device__ __forceinline__ int row_sms(const Params& p, const Work& w) {
   const int sms = p.row_workers / kRowWarps;
   if (w.pages == 0) return 0;

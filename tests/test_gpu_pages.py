@@ -69,7 +69,8 @@ class DevicePool:
         self.ctx.copy_(dev(lens))
 
 
-@pytest.mark.parametrize("seed,rows,width,pages,page", [(0, 5, 9, 40, 16), (1, 1, 4, 3, 16), (2, 40, 20, 700, 16), (6, 16, 9, 1024, 16), (7, 17, 9, 1024, 16), (8, 32, 9, 1024, 16), (9, 33, 9, 1024, 16),
+@pytest.mark.parametrize("seed,rows,width,pages,page", [(0, 5, 9, 40, 16), (1, 1, 4, 3, 16), (2, 40, 20, 700, 16), (6, 16, 9, 1024, 16),
+                                                         (7, 17, 9, 1024, 16), (8, 32, 9, 1024, 16), (9, 33, 9, 1024, 16),
                                                          (3, 7, 33, 97, 1), (4, 300, 40, 5000, 5), (5, 600, 3, 1111, 64)])
 def test_random_lives_match_the_pool(seed, rows, width, pages, page):
     rng = random.Random(seed)
