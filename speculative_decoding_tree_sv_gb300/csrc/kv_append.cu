@@ -6,6 +6,7 @@
 // the prefix sums, then requests the K and V rows eight 16-byte vectors per
 // lane at a time (at 8 heads x 128 the whole row of both) before it stores
 // any.  A head's 2 * D bytes stay contiguous in the page.
+#include "strided.h"
 #include "sv_device.cuh"
 
 namespace sv {
@@ -44,7 +45,8 @@ __global__ void __launch_bounds__(kWarps * 32) kv_append_kernel(const __grid_con
   const int layer = blockIdx.y;
   const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (layer == 0) {  // the new lengths, spread over the first layer's CTAs
-    for (int b = blockIdx.x * blockDim.x + threadIdx.x; b < p.batch; b += gridDim.x * blockDim.x) {
+    const Strided own = strided(blockIdx.x, gridDim.x, blockDim.x, threadIdx.x);
+    for (long long b = own.first; b < p.batch; b += own.step) {
       const int n0 = p.cu_tokens[b], n1 = p.cu_tokens[b + 1], L = p.ctx_lens[b];
       const bool ok = fits(p, n0, n1, L);
       if (!ok) report_error(p.err, SV_DEVERR_BAD_LENGTH);

@@ -3,6 +3,7 @@ checks (fake device addresses, no CUDA call on these paths) and the binding's
 checks of tensors."""
 
 import ctypes
+import subprocess
 
 import pytest
 import torch
@@ -188,3 +189,38 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         sv.sv_pages_copy(h(6, 2, 16, 64), None, i(3), i(3), i(2))
     with pytest.raises(ValueError, match="held_pages"):
         sv.sv_pages_release(i(2), i(2, 3), i(3), i(9))
+
+
+STRIDED = r"""
+#include "strided.h"
+extern "C" int walk(unsigned block, unsigned blocks, unsigned thread, int length, int most, long long* out) {
+  const sv::Strided s = sv::strided(block, blocks, 256, thread);
+  int n = 0;
+  for (long long b = s.first; b < length && n < most; b += s.step) out[n++] = b;
+  return n;
+}
+"""
+
+
+def test_append_takes_each_length_once_whatever_the_token_rows(tmp_path):
+    """The lengths are dealt to the threads of a grid that the token rows size, up
+    to 2^30 rows: every entry once, none outside the arrays, and no thread that
+    never ends."""
+    source, module = tmp_path / "walk.cpp", tmp_path / "walk.so"
+    source.write_text(STRIDED)
+    subprocess.run(["g++", "-std=c++17", "-shared", "-fPIC", "-I", build.CSRC, "-o", module, source], check=True)
+    walk = ctypes.CDLL(str(module)).walk
+    walk.argtypes = [ctypes.c_uint, ctypes.c_uint, ctypes.c_uint, ctypes.c_int, ctypes.c_int,
+                     ctypes.POINTER(ctypes.c_longlong)]
+    out = (ctypes.c_longlong * 4096)()
+    for rows in (0, 1, 8, 9, 5000, (1 << 26) - 8, 1 << 26, (1 << 26) + 1, (1 << 27) - 1, 1 << 27, (1 << 28) + 9, 1 << 30):
+        blocks = max(1, -(-rows // 8))
+        for batch in (1, 255, 256, 257, 2000):
+            near = set(range(min(blocks, 9))) | {blocks - 1, blocks // 2}
+            near |= {b for at in (1 << 23, 1 << 24, 1 << 25, 1 << 26) for b in (at - 1, at, at + 1) if b < blocks}
+            taken = []
+            for block in near:
+                for thread in range(256):
+                    n = walk(block, blocks, thread, batch, len(out), out)
+                    taken += out[:n]
+            assert sorted(taken) == list(range(batch)), (rows, batch)
