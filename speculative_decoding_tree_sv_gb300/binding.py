@@ -489,8 +489,9 @@ def make_chunk_params(*, q, k_cache, v_cache, block_table, ctx_lens, cu_tokens, 
                       workspace=None, window_tokens: int = 0, sink_tokens: int = 0,
                       sm_scale: float = 0.0) -> sv_chunk_params:
     """Fill an ``sv_chunk_params`` from torch tensors: q/out [T, Hq, D] (heads
-    contiguous, any token stride), caches [pages, Hkv, 16, D], all bf16 or all
-    fp16; lse fp32 [T, Hq] if wanted.  The result keeps the tensors alive."""
+    contiguous, Hq * D elements or more from a token to the next), caches
+    [pages, Hkv, 16, D], all bf16 or all fp16; lse fp32 [T, Hq] if wanted.  The
+    result keeps the tensors alive."""
     import torch
     if q.dim() != 3 or out.shape != q.shape:
         raise ValueError("q and out must both be [tokens, heads, head_dim]")
@@ -506,6 +507,8 @@ def make_chunk_params(*, q, k_cache, v_cache, block_table, ctx_lens, cu_tokens, 
     for name, t in (("q", q), ("out", out)):
         if D > 1 and t.stride(2) != 1 or Hq > 1 and t.stride(1) != D:
             raise ValueError(f"the heads of {name} must be contiguous")
+        if T > 1 and t.stride(0) < Hq * D:  # (0 is the parameters' word for dense)
+            raise ValueError(f"the rows of {name} overlap: {t.stride(0)} elements from a token to the next")
     if block_table.dim() != 2:
         raise ValueError("block_table must be [batch, max_pages]")
     B, width = block_table.shape

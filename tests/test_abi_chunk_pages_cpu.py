@@ -224,3 +224,24 @@ def test_append_takes_each_length_once_whatever_the_token_rows(tmp_path):
                     n = walk(block, blocks, thread, batch, len(out), out)
                     taken += out[:n]
             assert sorted(taken) == list(range(batch)), (rows, batch)
+
+
+def chunk_tensors():
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    h = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
+    return dict(q=h(5, 8, 64), k_cache=h(6, 2, 16, 64), v_cache=h(6, 2, 16, 64), block_table=i(2, 3), ctx_lens=i(2),
+                cu_tokens=i(3), out=h(5, 8, 64), max_tokens=4)
+
+
+@pytest.mark.parametrize("name", ["q", "out"])
+def test_rows_that_overlap_are_refused(name):
+    """A broadcast row has token stride 0, which the parameters read as dense."""
+    good = chunk_tensors()
+    rows = torch.zeros(5 * 512 + 512, dtype=torch.bfloat16)
+    for stride in (0, 8, 504):
+        with pytest.raises(ValueError, match=f"rows of {name} overlap"):
+            sv.make_chunk_params(**{**good, name: rows.as_strided((5, 8, 64), (stride, 64, 1))})
+    for t in (rows.as_strided((5, 8, 64), (520, 64, 1)), rows[:512].view(1, 8, 64).expand(1, 8, 64)):
+        other = {k: torch.zeros_like(t) for k in ("q", "out")}
+        with pytest.raises(ValueError, match="device memory"):   # (past the check of strides)
+            sv.make_chunk_params(**{**good, **other, name: t})
