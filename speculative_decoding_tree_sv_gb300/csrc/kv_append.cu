@@ -5,7 +5,9 @@
 // One warp per (token, layer): it finds its sequence with a 32-way search of
 // the prefix sums, then requests the K and V rows eight 16-byte vectors per
 // lane at a time (at 8 heads x 128 the whole row of both) before it stores
-// any.  A head's 2 * D bytes stay contiguous in the page.
+// any.  A head's 2 * D bytes stay contiguous in the page.  The next grid starts at
+// this one's end, not before: it may be a tree attention that reads context
+// ahead of its wait (SV_ATTN_EARLY_CONTEXT).
 #include "strided.h"
 #include "sv_device.cuh"
 
@@ -40,7 +42,6 @@ __device__ __forceinline__ bool fits(const Params& p, int n0, int n1, int L) {
 
 __global__ void __launch_bounds__(kWarps * 32) kv_append_kernel(const __grid_constant__ Params p) {
   griddep_wait();
-  griddep_launch_dependents();
   const int lane = threadIdx.x & 31;
   const int layer = blockIdx.y;
   const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);

@@ -10,6 +10,10 @@
 // same result on every run, in one launch without a wait on another grid.  These
 // kernels are bound by latency (a few dependent loads and cluster barriers);
 // sv_pages_copy is bound by HBM.
+//
+// Each waits for the grid before it and signals nothing before its end: tree
+// attention with SV_ATTN_EARLY_CONTEXT reads tables, lengths and context pages as
+// soon as it may start, ahead of its own wait.
 #include <cooperative_groups.h>
 
 #include <mutex>
@@ -79,7 +83,6 @@ struct RowParams {
 // One CTA per row: the entries behind the kept length lose their page.
 __global__ void __launch_bounds__(kRowThreads) release_kernel(const __grid_constant__ RowParams p) {
   griddep_wait();
-  griddep_launch_dependents();
   const int b = blockIdx.x;
   const int keep = p.keep_lens[b];
   const int held = p.held[b];
@@ -122,7 +125,6 @@ struct ForkParams {
 // is left out, so no CTA reads what another writes.
 __global__ void __launch_bounds__(kRowThreads) fork_kernel(const __grid_constant__ ForkParams p) {
   griddep_wait();
-  griddep_launch_dependents();
   const int i = blockIdx.x;
   const int parent = p.parents[i], child = p.children[i];
   int bad = parent < 0 || parent >= p.rows || child < 0 || child >= p.rows || parent == child;
@@ -282,7 +284,6 @@ __global__ void __launch_bounds__(kClusterThreads)
   const int gwarp = rank * kWarps + warp;
   constexpr int kAllWarps = CTAS * kWarps;
   griddep_wait();
-  griddep_launch_dependents();
   const Slice s = slice_of<CTAS>(p.num_pages, rank);
   uint32_t* bits = dyn;
   int* before = reinterpret_cast<int*>(dyn + s.words);
@@ -442,7 +443,6 @@ __global__ void __launch_bounds__(kClusterThreads)
   const int rank = CTAS == 1 ? 0 : cluster_ctarank();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   griddep_wait();
-  griddep_launch_dependents();
   const Slice s = slice_of<CTAS>(p.num_pages, rank);
   uint32_t* bits = dyn;
   int* before = reinterpret_cast<int*>(dyn + s.words);
@@ -559,7 +559,6 @@ constexpr int kCopyPart = kCopyThreads * kCopyVecs;
 // 16 KB, requested whole before any of it is stored.
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constant__ CopyParams p) {
   griddep_wait();
-  griddep_launch_dependents();
   const int n = min(max(*p.count, 0), p.max_copies);
   const int pools = p.v != nullptr ? 2 : 1;
   const long long per_pair = static_cast<long long>(p.num_layers) * pools * p.parts;

@@ -245,3 +245,13 @@ def test_rows_that_overlap_are_refused(name):
         other = {k: torch.zeros_like(t) for k in ("q", "out")}
         with pytest.raises(ValueError, match="device memory"):   # (past the check of strides)
             sv.make_chunk_params(**{**good, **other, name: t})
+
+
+def test_what_writes_the_context_signals_nothing_early():
+    """sv.h says of SV_ATTN_EARLY_CONTEXT that the library's kernels never write
+    tables, lengths or context pages behind an early signal: an attention that
+    starts at the signal would read them half written."""
+    for name in ("kv_append.cu", "pages.cu", "kv_commit.cu"):
+        with open(f"{build.CSRC}/{name}") as f:
+            source = f.read()
+        assert "griddep_wait();" in source and "launch_dependents" not in source, name
