@@ -136,6 +136,7 @@ extern "C" sv_status sv_kv_append(const void* k, const void* v, long long token_
   if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache)) return SV_ERR_INVALID_ARG;
   if (new_ctx_lens == ctx_lens) return SV_ERR_INVALID_ARG;
   if (workspace != nullptr && workspace_bytes < kWorkspaceHeader) return SV_ERR_WORKSPACE;
+  if (!aligned4(workspace)) return SV_ERR_INVALID_ARG;
   if (num_layers > 65535 || total_tokens > (1 << 30) || static_cast<long long>(num_kv_heads) * head_dim > (1 << 27))
     return SV_ERR_UNSUPPORTED;
   append::Params p;

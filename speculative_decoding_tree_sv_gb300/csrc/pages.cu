@@ -686,6 +686,7 @@ sv_status sv_pages_release(const int* keep_lens, int rows, int* block_table, int
                                           max_pages_per_seq, num_pages, page_size);
   if (st != SV_OK) return st;
   if (workspace != nullptr && workspace_bytes < kWorkspaceHeader) return SV_ERR_WORKSPACE;
+  if (!aligned4(workspace)) return SV_ERR_INVALID_ARG;
   pages::RowParams p{keep_lens, block_table, held_pages, page_refs, static_cast<int*>(workspace),
                      max_pages_per_seq, num_pages, page_size};
   return pages::launch(pages::release_kernel, p, rows, pages::kRowThreads, 0, stream);
@@ -701,6 +702,7 @@ sv_status sv_pages_fork(const int* parents, const int* children, int count, int*
   if (st != SV_OK) return st;
   if (count > 65535) return SV_ERR_UNSUPPORTED;
   if (workspace != nullptr && workspace_bytes < kWorkspaceHeader) return SV_ERR_WORKSPACE;
+  if (!aligned4(workspace)) return SV_ERR_INVALID_ARG;
   if (count == 0) return SV_OK;
   pages::ForkParams p{parents, children, block_table, ctx_lens, held_pages, page_refs,
                       static_cast<int*>(workspace), count, rows, max_pages_per_seq, num_pages, page_size};
@@ -717,6 +719,7 @@ sv_status sv_pages_reserve(const int* ctx_lens, const int* new_lens, int rows, i
                                           max_pages_per_seq, num_pages, page_size);
   if (st != SV_OK) return st;
   if (workspace == nullptr || workspace_bytes < pages::workspace_bytes(rows, num_pages)) return SV_ERR_WORKSPACE;
+  if (!aligned4(workspace)) return SV_ERR_INVALID_ARG;
   if (!pages::configure_pool()) return SV_ERR_CUDA;
   pages::PoolParams p{};
   pages::set_scratch(&p, workspace, rows, num_pages);
@@ -747,6 +750,7 @@ sv_status sv_pages_compact(const int* block_table, const int* held_pages, int ro
                                           max_pages_per_seq, num_pages, 1);
   if (st != SV_OK) return st;
   if (workspace == nullptr || workspace_bytes < pages::workspace_bytes(rows, num_pages)) return SV_ERR_WORKSPACE;
+  if (!aligned4(workspace)) return SV_ERR_INVALID_ARG;
   if (!pages::configure_pool()) return SV_ERR_CUDA;
   pages::PoolParams p{};
   pages::set_scratch(&p, workspace, rows, num_pages);
@@ -776,6 +780,7 @@ sv_status sv_pages_copy(void* k_cache, void* v_cache, long long cache_layer_stri
     return SV_ERR_INVALID_ARG;
   if (!aligned16(k_cache) || (v_cache != nullptr && !aligned16(v_cache))) return SV_ERR_INVALID_ARG;
   if (workspace != nullptr && workspace_bytes < kWorkspaceHeader) return SV_ERR_WORKSPACE;
+  if (!aligned4(workspace)) return SV_ERR_INVALID_ARG;
   if (num_layers > 65535 || page_elems > (1 << 26)) return SV_ERR_UNSUPPORTED;
   if (max_copies == 0) return SV_OK;
   const int sms = device_sm_count();

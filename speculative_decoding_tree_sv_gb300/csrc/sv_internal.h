@@ -23,6 +23,7 @@ constexpr int kMaxSplits = 64;
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // Tensor-map encoding through the driver entry point (resolved at first use,
 // so the library loads on machines without a GPU driver).

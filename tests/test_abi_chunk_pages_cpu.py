@@ -255,3 +255,18 @@ def test_what_writes_the_context_signals_nothing_early():
         with open(f"{build.CSRC}/{name}") as f:
             source = f.read()
         assert "griddep_wait();" in source and "launch_dependents" not in source, name
+
+
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_workspaces_off_their_words_are_refused(lib, off):
+    """The error word and the scratch are 32-bit words: a byte offset that is no
+    multiple of four would be a misaligned access on the device."""
+    size = 1 << 40
+    append = lambda w: lib.sv_kv_append(A, A, 1024, 0, A, A, 0, 1, 10, A, 4, A, A, 2, 5, 8, 128, 16, None, w, size, None)  # noqa: E731
+    release = lambda w: lib.sv_pages_release(A, 4, A, 8, A, A, 10, 16, w, size, None)  # noqa: E731
+    fork = lambda w: lib.sv_pages_fork(A, A, 2, A, 4, 8, A, A, A, 10, 16, w, size, None)  # noqa: E731
+    reserve = lambda w: lib.sv_pages_reserve(A, A, 4, A, 8, A, A, 10, 16, A, 2 * A, A, w, size, None)  # noqa: E731
+    compact = lambda w: lib.sv_pages_compact(A, A, 4, 8, A, 10, A, A, A, 2 * A, A, A, w, size, None)  # noqa: E731
+    copy = lambda w: lib.sv_pages_copy(A, A, 0, 1, 10, 64, A, A, A, 3, w, size, None)  # noqa: E731
+    for call in (append, release, fork, reserve, compact, copy):
+        assert call(A + off) == 1
