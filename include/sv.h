@@ -610,7 +610,8 @@ sv_status sv_pages_workspace_size(int rows, int num_pages, size_t* bytes);
 /* Gives back what lies behind keep_lens[b] tokens (a rollback; 0 ends the
  * sequence): the entries from ceil(keep_lens[b] / page_size) to held_pages[b]
  * become -1, their pages lose a reference, held_pages[b] shrinks to match.
- * Rows with nothing behind keep_lens[b] stay as they are. */
+ * Rows with nothing behind keep_lens[b] stay as they are.  The context lengths
+ * are the caller's to lower: they are not an argument. */
 sv_status sv_pages_release(const int* keep_lens, int rows, int* block_table, int max_pages_per_seq,
                            int* held_pages, int* page_refs, int num_pages, int page_size, void* workspace,
                            size_t workspace_bytes, sv_stream_t stream);
@@ -636,8 +637,9 @@ sv_status sv_pages_fork(const int* parents, const int* children, int count, int*
  * for `rows` entries, written in row order) and *copy_count is their number:
  * sv_pages_copy moves them.  If the pool has too few free pages nothing
  * changes, *copy_count is 0 and SV_DEVERR_NO_PAGES is recorded; a row whose
- * new length exceeds its table (SV_DEVERR_BAD_LENGTH), or whose held entries
- * in that range name no page (SV_DEVERR_BAD_PAGE), takes no part. */
+ * new length exceeds its table, or that holds fewer than
+ * ceil(ctx_lens[b] / page_size) pages (SV_DEVERR_BAD_LENGTH), or whose held
+ * entries in that range name no page (SV_DEVERR_BAD_PAGE), takes no part. */
 sv_status sv_pages_reserve(const int* ctx_lens, const int* new_lens, int rows, int* block_table,
                            int max_pages_per_seq, int* held_pages, int* page_refs, int num_pages, int page_size,
                            int* copy_src, int* copy_dst, int* copy_count, void* workspace,

@@ -258,13 +258,14 @@ __device__ __forceinline__ void cluster_sums(int* mine, int rank, int* before, i
 }
 
 // Range of entries a row writes to: [first, need), of which [first, mid) are
-// held.  False when the row takes no part.
+// held.  False when the row takes no part: nothing grows, or it does not hold the
+// pages of its context, or the table has no room.
 __device__ __forceinline__ bool write_range(const PoolParams& p, int b, bool report, int* first, int* mid,
                                             int* need) {
   const int len = p.ctx[b], len2 = p.new_lens[b], held = p.held[b];
   if (len2 <= len) return false;
   const int n = len2 >= 0 ? ceil_div(len2, p.page_size) : 0;
-  if (len < 0 || held < 0 || held > p.width || n > p.width || len / p.page_size > held) {
+  if (len < 0 || held < 0 || held > p.width || n > p.width || ceil_div(len, p.page_size) > held) {
     if (report) report_error(p.err, SV_DEVERR_BAD_LENGTH);
     return false;
   }
