@@ -513,7 +513,8 @@ sv_status sv_specpv_full_trees(const int* cand_parents, const int* cand_tokens, 
  * head and layer, a bit copy of 16-bit elements.  new_ctx_lens[b] (optional,
  * must not alias ctx_lens) receives ctx_lens[b] + N_b.  The caller holds
  * pages for those slots (sv_pages_reserve).  Nothing else changes: rows
- * between cu_tokens[B] and total_tokens are padding.
+ * between cu_tokens[B] and total_tokens are padding.  total_tokens may be 0,
+ * k and v are then not read (and may be NULL).
  *
  * k/v: [num_layers][total_tokens, Hkv, D], token_stride elements from a token
  * to the next (>= Hkv * D; slices of a fused projection's rows are fine),
@@ -545,8 +546,9 @@ sv_status sv_kv_append(const void* k, const void* v, long long token_stride, lon
  * over the positions j <= L_b + i and, with window_tokens = W > 0, of those
  * only j > L_b + i - W or j < sink_tokens (a token always sees itself).
  * Batches mix sequences of one token, of long chunks and of none (N_b = 0:
- * nothing is written).  Rows of q/out behind cu_tokens[B] are left as they
- * are.  K and V of a sequence's L_b + N_b positions are finite, but for
+ * nothing is written).  A call with total_tokens or max_tokens 0 does nothing
+ * (with the first, q and out may be NULL).  Rows of q/out behind cu_tokens[B]
+ * are left as they are.  K and V of a sequence's L_b + N_b positions are finite, but for
  * pages that a window has left behind: those are not read, and slots behind
  * L_b + N_b may hold anything.
  * ---------------------------------------------------------------------- */
@@ -663,7 +665,8 @@ sv_status sv_pages_compact(const int* block_table, const int* held_pages, int ro
  * contiguous (a multiple of 8), pages follow one another, layers are
  * cache_layer_stride elements apart (a multiple of 8).  No page is a source
  * and a destination, or twice a destination: lists of sv_pages_reserve and
- * sv_pages_compact are so.  num_layers <= 65535. */
+ * sv_pages_compact are so.  num_layers <= 65535.  With max_copies 0 the lists
+ * may be NULL. */
 sv_status sv_pages_copy(void* k_cache, void* v_cache, long long cache_layer_stride, int num_layers,
                         int num_pages, int page_elems, const int* copy_src, const int* copy_dst,
                         const int* copy_count, int max_copies, void* workspace, size_t workspace_bytes,

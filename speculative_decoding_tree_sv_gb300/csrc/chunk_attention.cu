@@ -329,8 +329,8 @@ Plan make_plan(const sv_chunk_params* c, int sms) {
 
 sv_status check(const sv_chunk_params* c) {
   if (c == nullptr) return SV_ERR_INVALID_ARG;
-  if (!c->q || !c->k_cache || !c->v_cache || !c->block_table || !c->ctx_lens || !c->cu_tokens || !c->out)
-    return SV_ERR_INVALID_ARG;
+  if (!c->k_cache || !c->v_cache || !c->block_table || !c->ctx_lens || !c->cu_tokens) return SV_ERR_INVALID_ARG;
+  if ((!c->q || !c->out) && c->total_tokens != 0) return SV_ERR_INVALID_ARG;  // (an empty tensor has no address)
   if (c->batch < 1 || c->num_q_heads < 1 || c->num_kv_heads < 1 || c->num_pages < 1 || c->max_pages_per_seq < 1 ||
       c->total_tokens < 0 || c->max_tokens < 0 || c->window_tokens < 0 || c->sink_tokens < 0)
     return SV_ERR_INVALID_ARG;

@@ -125,7 +125,8 @@ extern "C" sv_status sv_kv_append(const void* k, const void* v, long long token_
                                   int num_kv_heads, int head_dim, int page_size, int* new_ctx_lens,
                                   void* workspace, size_t workspace_bytes, sv_stream_t stream) {
   using namespace sv;
-  if (!k || !v || !k_cache || !v_cache || !block_table || !ctx_lens || !cu_tokens) return SV_ERR_INVALID_ARG;
+  if (!k_cache || !v_cache || !block_table || !ctx_lens || !cu_tokens) return SV_ERR_INVALID_ARG;
+  if ((!k || !v) && total_tokens != 0) return SV_ERR_INVALID_ARG;  // (an empty tensor has no address)
   if (num_layers < 1 || num_pages < 1 || max_pages_per_seq < 1 || batch < 1 || total_tokens < 0 ||
       num_kv_heads < 1 || page_size < 1)
     return SV_ERR_INVALID_ARG;

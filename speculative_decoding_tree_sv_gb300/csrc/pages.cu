@@ -775,7 +775,8 @@ sv_status sv_pages_copy(void* k_cache, void* v_cache, long long cache_layer_stri
                         const int* copy_count, int max_copies, void* workspace, size_t workspace_bytes,
                         sv_stream_t stream) {
   using namespace sv;
-  if (!k_cache || !copy_src || !copy_dst || !copy_count) return SV_ERR_INVALID_ARG;
+  if (!k_cache || !copy_count) return SV_ERR_INVALID_ARG;
+  if ((!copy_src || !copy_dst) && max_copies != 0) return SV_ERR_INVALID_ARG;  // (an empty tensor has no address)
   if (num_layers < 1 || num_pages < 1 || page_elems < 8 || page_elems % 8 != 0 || max_copies < 0 ||
       cache_layer_stride < 0 || cache_layer_stride % 8 != 0)
     return SV_ERR_INVALID_ARG;

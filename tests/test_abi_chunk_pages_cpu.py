@@ -270,3 +270,20 @@ def test_workspaces_off_their_words_are_refused(lib, off):
     copy = lambda w: lib.sv_pages_copy(A, A, 0, 1, 10, 64, A, A, A, 3, w, size, None)  # noqa: E731
     for call in (append, release, fork, reserve, compact, copy):
         assert call(A + off) == 1
+
+
+def test_empty_tensors_have_no_address(lib):
+    """A call without token rows, or with an empty list, is a call that has nothing
+    to do, not a null pointer."""
+    empty = chunk(total_tokens=0, q=None, out=None)
+    n = ctypes.c_size_t(0)
+    assert lib.sv_chunk_attention_workspace_size(ctypes.byref(empty), ctypes.byref(n)) == 0 and n.value >= 256
+    assert lib.sv_chunk_attention(ctypes.byref(empty), None) == 0
+    assert lib.sv_chunk_attention(ctypes.byref(chunk(max_tokens=0, q=None)), None) == 1
+    copy = lambda src, dst, most: lib.sv_pages_copy(A, A, 0, 1, 10, 64, src, dst, A, most, None, 0, None)  # noqa: E731
+    assert copy(None, None, 0) == 0 and copy(None, A, 1) == 1 and copy(A, None, 1) == 1
+    if torch.cuda.is_available():
+        return  # the append launches, for the lengths: with real tensors in the GPU tests
+    append = lambda k, v, total: lib.sv_kv_append(k, v, 1024, 0, A, A, 0, 1, 10, A, 4, A, A, 2, total, 8, 128, 16, None,  # noqa: E731
+                                                  None, 0, None)
+    assert append(None, None, 0) == 3 and append(None, A, 1) == 1 and append(A, None, 1) == 1  # 3: no device to launch on

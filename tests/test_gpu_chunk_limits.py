@@ -1,11 +1,12 @@
 """Chunk attention, the append and the page calls where a call is at an end of its
-range: a page of the context that is missing."""
+range: nothing to do, a page of the context that is missing."""
 
 import pytest
 import torch
 
 from speculative_decoding_tree_sv_gb300 import binding as sv
 from tests.gpu_support import ensure_lib
+from tests.test_gpu_chunk import Case
 from tests.test_gpu_pages import DevicePool, dev
 
 pytestmark = pytest.mark.gpu
@@ -14,6 +15,36 @@ pytestmark = pytest.mark.gpu
 @pytest.fixture(scope="module", autouse=True)
 def lib():
     return ensure_lib()
+
+
+# ------------------------------------------------------------- nothing to do
+
+@pytest.mark.parametrize("layers", [0, 1, 3])
+def test_append_of_no_tokens_still_writes_the_lengths(layers):
+    shape = (layers,) if layers else ()
+    kc = torch.ones((*shape, 4, 2, 16, 64), dtype=torch.bfloat16, device="cuda")
+    vc = kc.clone()
+    k = torch.empty((*shape, 0, 2, 64), dtype=torch.bfloat16, device="cuda")
+    lens, after = dev([5, 0, 30]), dev([-1, -1, -1])
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    sv.sv_kv_append(k, k, kc, vc, dev([[0, 1], [2, -1], [3, 0]]), lens, dev([0, 0, 0, 0]), new_ctx_lens=after, workspace=ws)
+    assert sv.sv_get_device_error(ws) == 0 and after.tolist() == [5, 0, 30]
+    assert (kc == 1).all() and (vc == 1).all()
+
+
+def test_attention_of_no_tokens():
+    c = Case([20, 3], [1, 1], 8, 2, 64)
+    q = torch.empty((0, 8, 64), dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty((0, 8), dtype=torch.float32, device="cuda")
+    for most in (0, 4):
+        assert c.run(q=q, out=torch.empty_like(q), lse=lse, cu_tokens=dev([0, 0, 0]), max_tokens=most) == 0
+
+
+def test_copy_of_an_empty_list():
+    k = torch.randn((2, 5, 2, 16, 64), device="cuda").to(torch.bfloat16)
+    want, none = k.clone(), dev([])
+    sv.sv_pages_copy(k, None, none, none, dev([3]))
+    assert torch.equal(k, want)
 
 
 # ------------------------------------------------------------------- pages
