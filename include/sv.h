@@ -545,6 +545,9 @@ sv_status sv_kv_append(const void* k, const void* v, long long token_stride, lon
  *     lse[i,h] = ln sum_j exp(scale * q[i,h] . k_j)
  * over the positions j <= L_b + i and, with window_tokens = W > 0, of those
  * only j > L_b + i - W or j < sink_tokens (a token always sees itself).
+ * Scores, sums, merges and lse are fp32; the weights are rounded to the 16-bit
+ * type for the product with V (in fp16 a weight below 2^-21 of its row's
+ * largest by up to 2^-32 of that).
  * Batches mix sequences of one token, of long chunks and of none (N_b = 0:
  * nothing is written).  A call with total_tokens or max_tokens 0 does nothing
  * (with the first, q and out may be NULL).  Rows of q/out behind cu_tokens[B]

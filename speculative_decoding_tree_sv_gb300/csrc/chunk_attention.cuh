@@ -294,6 +294,13 @@ __device__ __forceinline__ Share share_of(long long total, int workers) {
   return s;
 }
 
+// Weights are 2^(s - m + kLift).  P goes into the second product in 16 bits, and
+// fp16 has no normal numbers below 2^-14 and nothing below 2^-25: lifted by 2^7 (with a
+// running maximum that lags by up to 2^8 they stay below 2^15), what is lost of a
+// weight is at most 2^-32 of its row's largest.  bf16 has the range of fp32.
+template <bool FP16>
+constexpr float kLift = FP16 ? 7.f : 0.f;
+
 template <bool FP16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   if constexpr (FP16) {

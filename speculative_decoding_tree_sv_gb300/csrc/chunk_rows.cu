@@ -4,7 +4,7 @@
 // Mathematics: for the 16 rows (token x query head of the group) of a unit and
 // its keys, O = softmax(scale * Q K^T + mask) V with a running maximum m and
 // sum l per row: m' = max(m, max s), p = 2^(s - m'), l' = l 2^(m - m') +
-// sum p, O' = O 2^(m - m') + p V.
+// sum p, O' = O 2^(m - m') + p V (fp16: p 2^7, see kLift).
 //
 // Bound by HBM: a page of K and V (2 * 16 * D * 2 bytes) is read once and
 // takes 2 * 2 * 16 * 16 * D operations, 16 per byte.  What the memory system
@@ -418,12 +418,12 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
       for (int nb = 0; nb < 2; ++nb)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float mu = m[e >> 1] == -INFINITY ? 0.f : m[e >> 1];
+          const float mu = m[e >> 1] == -INFINITY ? 0.f : m[e >> 1] - kLift<FP16>;
           pr[nb][e] = ex2(fmaf(sc[nb][e], p.scale_log2, -mu));
           l[e >> 1] += pr[nb][e];
         }
-      // P in 16 bits for the second product: an error of half a step per weight
-      // against its row's sum, below the output's own rounding
+      // P in 16 bits for the second product: half a step per weight, relative, so
+      // at most as much again as the output's own rounding
       pf[0] = pack2<FP16>(pr[0][0], pr[0][1]);
       pf[1] = pack2<FP16>(pr[0][2], pr[0][3]);
       pf[2] = pack2<FP16>(pr[1][0], pr[1][1]);
@@ -456,7 +456,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
       const int r = g + 8 * i;
       if (r >= rows) continue;
       const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
-      const float lse2 = l[i] > 0.f ? m[i] + log2f(l[i]) : -INFINITY;
+      const float lse2 = l[i] > 0.f ? m[i] - kLift<FP16> + log2f(l[i]) : -INFINITY;
       if (whole) {
         const int head = pc.kh * p.group + (r0 + r - tok[i] * p.group);
         const long long token = s.n0 + tok[i];

@@ -3,8 +3,9 @@
 //
 // Mathematics as in the row kernel, 128 keys at a time: S = Q K^T in TMEM,
 // p = 2^(scale s - m) with a running maximum m that only moves when it grows by
-// more than 2^8 (until then p stays below 2^8, exact enough in 16 bits: its
-// rounding is relative), O += P V in TMEM with P read from the score columns.
+// more than 2^8 (until then p stays below 2^8, and its rounding to 16 bits is
+// relative: fp16 weights are lifted for that, see kLift), O += P V in TMEM with P
+// read from the score columns.
 //
 // A unit is (sequence, KV head, 256 rows): two 128-row M tiles of 128 / G whole
 // tokens each, both against every K/V tile, so a tile in shared memory (64 KB
@@ -744,7 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_st_wait();
         }
         if (grow) m_run = m_new;
-        const float m_use = (m_run == -INFINITY) ? 0.f : m_run;
+        const float m_use = (m_run == -INFINITY) ? 0.f : m_run - kLift<FP16>;
         // p = 2^(s * scale_log2 - m), packed two at a time
         const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
         const uint64_t nm2 = f2_pack(-m_use, -m_use);
@@ -758,8 +759,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float p2 = ex2(f2_lo(b2)), p3 = ex2(f2_hi(b2));
           acc0 = f2_add(acc0, f2_pack(p0, p1));
           acc1 = f2_add(acc1, f2_pack(p2, p3));
-          // 16-bit P: half a step per weight against its row's sum, below the
-          // output's own rounding
+          // 16-bit P: half a step per weight, relative, so at most as much again
+          // as the output's own rounding
           pk[kk >> 1] = pack2<FP16>(p0, p1);
           pk[(kk >> 1) + 1] = pack2<FP16>(p2, p3);
         }
@@ -782,7 +783,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // over, which is what lets that piece's first PV overwrite O.
       tc_fence_after();
       const float inv_l = (l_run > 0.f) ? 1.f / l_run : 0.f;
-      const float lse2 = (l_run > 0.f) ? m_run + log2f(l_run) : -INFINITY;
+      const float lse2 = (l_run > 0.f) ? m_run - kLift<FP16> + log2f(l_run) : -INFINITY;
       if (pc.slot < 0) {
         const int head = pc.kh * G + r_head;
         const long long token = pc.n0 + tok;

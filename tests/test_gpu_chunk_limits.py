@@ -1,9 +1,22 @@
-"""Chunk attention, the append and the page calls where a call is at an end of its
-range: nothing to do, a page of the context that is missing."""
+"""Chunk attention, the append and the page calls where a call or its numbers are
+at an end of their range: nothing to do, tables far wider than their sequences, a
+wrong sequence among others, weights at the lower end of fp16, a page of the
+context that is missing.
 
+Tolerance, as derived in test_gpu_chunk.py: eps / 2 (A + |out|) + 2e-4 A with
+A = sum p |v| / l.  fp16 adds what its subnormal steps cost: weights are held as
+p 2^7 against a running maximum, so one below 2^-21 is off by at most 2^-25 2^-7 =
+2^-32, n of them by n 2^-32 max |v|; and an output below 2^-14 is rounded to a
+multiple of 2^-24, off by 2^-25 at most.
+"""
+
+import math
+
+import numpy as np
 import pytest
 import torch
 
+import oracle
 from speculative_decoding_tree_sv_gb300 import binding as sv
 from tests.gpu_support import ensure_lib
 from tests.test_gpu_chunk import Case
@@ -15,6 +28,66 @@ pytestmark = pytest.mark.gpu
 @pytest.fixture(scope="module", autouse=True)
 def lib():
     return ensure_lib()
+
+
+def compare(c, rows=None, sm_scale=None):
+    """The rows of the mask (all) against the float64 oracle, lse too; the others
+    as they were (7)."""
+    f = lambda t: t.float().cpu().numpy()  # noqa: E731
+    q, k, v, table = f(c.q), np.nan_to_num(f(c.k)), np.nan_to_num(f(c.v)), c.table.cpu().numpy()
+    kw = dict(window=c.window, sink=c.sink, sm_scale=sm_scale)
+    want, lse = oracle.chunk_attention(q, k, v, table, c.ctx, c.cu_np, **kw)
+    mean, _ = oracle.chunk_attention(q, k, np.abs(v), table, c.ctx, c.cu_np, **kw)
+    got, got_lse = f(c.out), c.lse.cpu().numpy()
+    rows = np.ones(c.T, dtype=bool) if rows is None else rows
+    half = torch.finfo(c.dtype).eps / 2
+    tol = half * (mean + np.abs(want)) * 1.001 + 2e-4 * mean
+    if c.dtype == torch.float16:
+        keys = max(a + b for a, b in zip(c.ctx, c.new))
+        tol += keys * 2.0 ** -32 * np.abs(v).max() + 2.0 ** -25
+    else:
+        tol += torch.finfo(c.dtype).tiny
+    worst = (np.abs(got[:c.T] - want)[rows] / tol[rows]).max()
+    assert worst <= 1.0, worst
+    assert np.abs(got_lse[:c.T] - lse)[rows].max() <= 1e-4
+    assert (got[:c.T][~rows] == 7.0).all() and (got_lse[:c.T][~rows] == 7.0).all()
+
+
+# ------------------------------------------------------------------ numbers
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("ctx,new,Hq,Hkv", [
+    ([600], [1], 8, 2), ([3000], [1], 8, 2), ([900, 3000, 40], [1, 1, 1], 16, 1), ([3000], [5], 4, 1),   # the row kernel
+    ([3000], [40], 8, 2), ([700, 2500], [300, 64], 4, 4), ([2000, 900], [33, 1], 8, 2),                  # and the tile kernel
+])
+def test_weights_below_the_least_fp16_number(ctx, new, Hq, Hkv, D):
+    """One key outweighs the others by 2^25.05 and brings no value of its own: the
+    output is what the others bring, each below half of fp16's least step."""
+    c = Case(ctx, new, Hq, Hkv, D, "fp16", seed=31)
+    c.q.zero_()
+    c.q[..., 0] = 1
+    c.k = torch.where(torch.isnan(c.k), c.k, torch.zeros_like(c.k))
+    c.v.abs_()
+    first = c.table[:, 0].long()
+    c.k[first, :, 0, 0] = 1
+    c.v[first, :, 0] = 0
+    scale = 25.05 * math.log(2)
+    assert c.run(sm_scale=scale) == 0
+    compare(c, sm_scale=scale)
+
+
+@pytest.mark.parametrize("new", [[1], [40]])
+def test_weights_over_the_whole_range_of_fp16(new):
+    c = Case([4000], new, 8, 2, 64, "fp16", seed=32)
+    c.q.mul_(2.0)  # scores over about +- 8 standard deviations of 2: weights from 1 to 2^-30
+    assert c.run() == 0
+    f = lambda t: t.float().cpu().numpy()  # noqa: E731
+    k, v = np.nan_to_num(f(c.k)), np.nan_to_num(f(c.v))
+    want, lse = oracle.chunk_attention(f(c.q), k, v, c.table.cpu().numpy(), c.ctx, c.cu_np)
+    mean, _ = oracle.chunk_attention(f(c.q), k, np.abs(v), c.table.cpu().numpy(), c.ctx, c.cu_np)
+    # scores are twice those of the derivation above: their 32-bit error too
+    tol = 2.0 ** -11 * (mean + np.abs(want)) * 1.001 + 4e-4 * mean + 4100 * 2.0 ** -32 * np.abs(v).max() + 2.0 ** -25
+    assert (np.abs(f(c.out) - want) <= tol).all() and np.abs(c.lse.cpu().numpy() - lse).max() <= 2e-4
 
 
 # ------------------------------------------------------------- nothing to do
