@@ -90,6 +90,49 @@ def test_weights_over_the_whole_range_of_fp16(new):
     assert (np.abs(f(c.out) - want) <= tol).all() and np.abs(c.lse.cpu().numpy() - lse).max() <= 2e-4
 
 
+# ------------------------------------------------------------------ tables
+
+@pytest.mark.parametrize("width", [300, 2048])
+@pytest.mark.parametrize("ctx,new,Hq,Hkv,D,dtype,window,sink", [
+    ([511], [1], 8, 2, 64, "bf16", 0, 0), ([1000, 0, 37, 1600] * 4, [1] * 16, 32, 8, 128, "bf16", 0, 0),
+    ([500] * 4, [100, 33, 200, 17], 16, 4, 64, "fp16", 0, 0), ([0] * 3, [1024, 300, 1], 8, 2, 128, "bf16", 0, 0),
+    ([700, 40, 1300, 9], [7, 1, 8, 300], 8, 2, 64, "bf16", 0, 0), ([900, 3000], [1, 120], 8, 2, 128, "fp16", 500, 20),
+])
+def test_tables_far_wider_than_their_sequences(ctx, new, Hq, Hkv, D, dtype, window, sink, width):
+    """An engine's table has one width whatever its sequences hold; entries behind
+    them are -1."""
+    c = Case(ctx, new, Hq, Hkv, D, dtype, window=window, sink=sink, seed=width + len(ctx))
+    wide = torch.full((c.B, width), -1, dtype=torch.int32, device="cuda")
+    wide[:, :c.table.shape[1]] = c.table
+    c.table = wide
+    assert c.run() == 0
+    compare(c)
+
+
+@pytest.mark.parametrize("batch,longest,new", [(3, 10, 1), (3, 900, 1), (50, 900, 1), (400, 100, 1), (3, 9000, 1),
+                                               (5, 2000, 40), (70, 700, 20)])
+def test_a_wrong_length_leaves_the_others_right(batch, longest, new):
+    """The work is shared out anew without the sequence: the others' rows are
+    compared with the oracle, element by element, and their lse."""
+    rng = np.random.default_rng(batch + longest)
+    ctx = rng.integers(0, longest, batch).tolist()
+    ctx[1] = longest
+    news = [new] + [1 if i % 2 else new for i in range(1, batch)]
+    c = Case(ctx, news, 16, 4, 64, "bf16", seed=longest)
+    assert c.run() == 0
+    compare(c)
+    for at in (0, batch // 2, batch - 1):
+        for bad in (100000, -1):
+            c.lens[at] = bad
+            c.out.fill_(7.0)
+            c.lse.fill_(7.0)
+            assert c.run() == sv.SV_DEVERR_BAD_LENGTH
+            rows = np.ones(c.T, dtype=bool)
+            rows[c.cu_np[at]:c.cu_np[at + 1]] = False
+            compare(c, rows)
+        c.lens[at] = ctx[at]
+
+
 # ------------------------------------------------------------- nothing to do
 
 @pytest.mark.parametrize("layers", [0, 1, 3])
