@@ -517,6 +517,9 @@ def make_chunk_params(*, q, k_cache, v_cache, block_table, ctx_lens, cu_tokens, 
     _ints("cu_tokens", cu_tokens, B + 1)
     if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (T, Hq) or not lse.is_contiguous()):
         raise ValueError(f"lse must be a contiguous float32 tensor of shape {(T, Hq)}")
+    for name, n in (("max_tokens", max_tokens), ("window_tokens", window_tokens), ("sink_tokens", sink_tokens)):
+        if not -1 << 31 <= int(n) < 1 << 31:  # (a field would keep the low 32 bits)
+            raise ValueError(f"{name} does not fit 32 bits: {n}")
     _on_device(q, k_cache, v_cache, block_table, ctx_lens, cu_tokens, out, lse, workspace)
     p = sv_chunk_params()
     p.batch, p.num_q_heads, p.num_kv_heads, p.head_dim = B, Hq, Hkv, D

@@ -287,3 +287,11 @@ def test_empty_tensors_have_no_address(lib):
     append = lambda k, v, total: lib.sv_kv_append(k, v, 1024, 0, A, A, 0, 1, 10, A, 4, A, A, 2, total, 8, 128, 16, None,  # noqa: E731
                                                   None, 0, None)
     assert append(None, None, 0) == 3 and append(None, A, 1) == 1 and append(A, None, 1) == 1  # 3: no device to launch on
+
+
+@pytest.mark.parametrize("name", ["max_tokens", "window_tokens", "sink_tokens"])
+def test_counts_past_32_bits_are_refused(name):
+    """ctypes would keep the low 32 bits: 2^32 + 5 would be a window of 5."""
+    for value in (1 << 31, (1 << 32) + 5, -(1 << 31) - 1):
+        with pytest.raises(ValueError, match=f"{name} does not fit 32 bits"):
+            sv.make_chunk_params(**{**chunk_tensors(), name: value})
