@@ -179,7 +179,7 @@ def _marshal():
         import torch  # noqa: F401  (its libraries must be in the process)
         path = _build.marshal_path()
         if not os.path.exists(path):
-            raise RuntimeError(f"_marshal.so is not built ({path}); run __graft_entry__.build() or "
+            raise RuntimeError(f"the tensor module of this torch is not built ({path}); run __graft_entry__.build() or "
                                "python -m speculative_decoding_tree_sv_gb300.build")
         spec = importlib.util.spec_from_file_location("_marshal", path)
         module = importlib.util.module_from_spec(spec)

@@ -2,20 +2,24 @@
 
 Each CUDA translation unit is compiled in parallel, then linked into one
 shared library with the CUDA runtime linked statically (the library loads on
-machines without a GPU driver; the driver is resolved at first use).  Beside
-it goes ``lib/_marshal.so``, the Python module that checks and passes the
-cache operators' tensors (compiled against the installed torch's headers).
+machines without a GPU driver; the driver is resolved at first use).  Where
+torch is installed, the Python module that checks and passes the cache
+operators' tensors goes beside it.  That module reads torch's own objects, so it
+is compiled against the installed torch's headers and its file name carries the
+torch and Python it was built for: another pair builds its own.
 """
 
 from __future__ import annotations
 
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
 import sysconfig
 from concurrent.futures import ThreadPoolExecutor
+from typing import Optional
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
@@ -39,15 +43,28 @@ def library_path() -> str:
     return os.path.join(LIBDIR, LIBNAME)
 
 
-def marshal_path() -> str:
-    return os.path.join(LIBDIR, "_marshal.so")
-
-
-def _torch_dir() -> str:
+def _torch_dir() -> Optional[str]:
+    """Where torch is installed; None without it."""
     spec = importlib.util.find_spec("torch")
     if spec is None or not spec.submodule_search_locations:
-        raise RuntimeError("torch not found: the Python module compiles against its headers")
+        return None
     return spec.submodule_search_locations[0]
+
+
+def _torch_version(torch_dir: str) -> str:
+    with open(os.path.join(torch_dir, "version.py")) as f:
+        found = re.search(r"^__version__\s*(?::[^=]*)?=\s*['\"]([^'\"]+)", f.read(), re.M)
+    if found is None:
+        raise RuntimeError(f"no __version__ in {torch_dir}/version.py")
+    return found.group(1)
+
+
+def marshal_path() -> Optional[str]:
+    """The tensor module of this Python and the installed torch; None without torch."""
+    torch_dir = _torch_dir()
+    if torch_dir is None:
+        return None
+    return os.path.join(LIBDIR, f"_marshal-torch{_torch_version(torch_dir)}{sysconfig.get_config_var('EXT_SUFFIX')}")
 
 
 def _deps():
@@ -58,7 +75,7 @@ def _deps():
 
 
 def up_to_date() -> bool:
-    built = [library_path(), marshal_path()]
+    built = [f for f in (library_path(), marshal_path()) if f is not None]
     if not all(os.path.exists(f) for f in built):
         return False
     t = min(os.path.getmtime(f) for f in built)
@@ -86,7 +103,11 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stderr}")
         return obj, r.stderr
 
+    module = marshal_path()
+
     def compile_marshal():
+        if module is None:
+            return None
         obj = os.path.join(objdir, "marshal.o")
         torch_dir = _torch_dir()
         include = [os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
@@ -100,9 +121,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         return obj
 
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        module = ex.submit(compile_marshal)
+        marshal = ex.submit(compile_marshal)
         results = list(ex.map(compile_one, SOURCES))
-        module_obj = module.result()
     if verbose or ptxas_info:
         for (_, err), src in zip(results, SOURCES):
             if err.strip():
@@ -113,14 +133,19 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, lib)
-    tmp = marshal_path() + ".tmp"
+    module_obj = marshal.result()  # (the library is in place, whatever became of it)
+    if module_obj is None:
+        if verbose:
+            sys.stderr.write("torch is not installed: built without the tensor module\n")
+        return lib
+    tmp = module + ".tmp"
     # torch's libraries are in the process by the time the module is loaded
     cmd = ["g++", "-shared", "-o", tmp, module_obj, "-L", LIBDIR, "-l:" + LIBNAME, "-Wl,-rpath,$ORIGIN",
            "-L", os.path.join(_torch_dir(), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"link of _marshal.so failed:\n{r.stderr}")
-    os.replace(tmp, marshal_path())
+        raise RuntimeError(f"link of {os.path.basename(module)} failed:\n{r.stderr}")
+    os.replace(tmp, module)
     return lib
 
 
