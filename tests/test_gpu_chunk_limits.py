@@ -1,7 +1,7 @@
 """Chunk attention, the append and the page calls where a call or its numbers are
-at an end of their range: nothing to do, tables far wider than their sequences, a
-wrong sequence among others, weights at the lower end of fp16, a page of the
-context that is missing.
+at an end of their range: nothing to do (or nothing yet, in a captured step), tables
+far wider than their sequences, a wrong sequence among others, weights at the lower
+end of fp16, a page of the context that is missing, two streams at once.
 
 Tolerance, as derived in test_gpu_chunk.py: eps / 2 (A + |out|) + 2e-4 A with
 A = sum p |v| / l.  fp16 adds what its subnormal steps cost: weights are held as
@@ -193,3 +193,60 @@ def test_reserve_wants_the_pages_of_the_context(rows):
     d.set_ctx([16] + start[1:-1] + [33])
     assert d.reserve([40] + [0] * (rows - 1)) == d.model.reserve([40] + [0] * (rows - 1)) == [] and d.error() == 0
     d.same()
+
+
+# ------------------------------------------------------------------- steps
+
+@pytest.mark.parametrize("batch,Hq,Hkv,width,most", [
+    (1, 8, 2, 100, 1), (3, 8, 2, 20, 1), (3, 8, 2, 2, 1), (40, 16, 4, 300, 1),     # the row kernel's ways of sharing
+    (1, 8, 2, 100, 300), (4, 32, 8, 300, 200), (40, 16, 4, 20, 64), (2, 64, 2, 50, 1),  # the tile kernel, both, and cut units
+])
+def test_a_step_in_which_no_sequence_brings_a_token(batch, Hq, Hkv, width, most):
+    """A captured step of fixed size: all its rows are padding, later they are not."""
+    c = Case([min(5 + i, width * 16 - most) for i in range(batch)], [1] * batch, Hq, Hkv, 64, seed=batch)
+    c.table = torch.cat([c.table, torch.full((batch, width), -1, dtype=torch.int32, device="cuda")], 1).contiguous()
+    p = c.params(max_tokens=most)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        sv.sv_chunk_attention(p)
+    cu = c.cu.clone()
+    for _ in range(2):
+        c.cu.zero_()
+        c.out.fill_(7.0)
+        c.lse.fill_(7.0)
+        graph.replay()
+        assert sv.sv_get_device_error(c.ws) == 0 and (c.out == 7.0).all() and (c.lse == 7.0).all()
+        c.cu.copy_(cu)
+        graph.replay()
+        assert sv.sv_get_device_error(c.ws) == 0
+        compare(c)
+
+
+def test_two_streams_at_once():
+    """Calls of every kind on two streams, each with its own workspace and pages."""
+    steps = [[Case([900, 3, 200], [70, 1, 1], 32, 8, 128, "fp16", seed=41), Case([3000, 40], [1, 1], 8, 2, 64, seed=42)],
+             [Case([0, 700], [300, 1], 8, 2, 128, seed=43), Case([500] * 30, [1] * 30, 16, 4, 64, "fp16", seed=44)]]
+    params = [[c.params() for c in cases] for cases in steps]
+    pools = [DevicePool(3, 8, 40), DevicePool(40, 8, 1100)]
+    news = [dev([33] * 3), dev([20] * 40)]
+    streams = [torch.cuda.Stream() for _ in steps]
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for s, calls, d, new in zip(streams, params, pools, news):
+            with torch.cuda.stream(s):
+                for p in calls:
+                    sv.sv_chunk_attention(p)
+                sv.sv_pages_reserve(d.ctx, new, d.table, d.held, d.refs, d.src, d.dst, d.count, workspace=d.ws)
+                sv.sv_pages_copy(d.k, d.v, d.src, d.dst, d.count, workspace=d.ws)
+                sv.sv_pages_release(d.ctx, d.table, d.held, d.refs, workspace=d.ws)
+    for s, calls, d, new in zip(streams, params, pools, news):
+        with torch.cuda.stream(s):
+            sv.sv_pages_reserve(d.ctx, new, d.table, d.held, d.refs, d.src, d.dst, d.count, workspace=d.ws)
+    torch.cuda.synchronize()
+    for cases in steps:
+        for c in cases:
+            assert sv.sv_get_device_error(c.ws) == 0
+            compare(c)
+    for d, new in zip(pools, news):
+        assert d.error() == 0 and d.model.reserve(new.tolist()) == []
+        d.same()
