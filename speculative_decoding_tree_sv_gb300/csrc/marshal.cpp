@@ -1,7 +1,7 @@
 // Argument marshalling of the cache operators' Python calls: checks the tensors
 // and hands their addresses to the C entry points of include/sv.h.
 //
-// An append of one token is 3.5 us of GPU time; checked and marshalled in
+// An append of one token is about 5 us of GPU time; checked and marshalled in
 // Python its call took 10.7 us of host time (a page release 6.3), so these six
 // calls do it here.  The module sees tensors through torch's own Python object
 // and computes nothing.

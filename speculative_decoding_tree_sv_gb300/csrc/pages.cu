@@ -25,9 +25,9 @@ namespace pages {
 
 // CTAs of the pool kernels' cluster; a small pool with two rows per warp at most
 // takes a single one, whose barriers are cheaper (a step of release, fork, reserve
-// and copy, one CTA / eight: 3 rows and 73 pages 10.6 / 15.2 us, 18 and 519 15.8 /
-// 18.0, 32 and 389 19.0 / 19.5, 75 and 877 31.5 / 19.0.  Compact: 256 pages 3.4 /
-// 5.0; 3000 pages and 40 rows 7.2 / 6.0).
+// and copy, one CTA / eight: 3 rows and 73 pages 10.6 / 15.5 us, 18 and 519 15.2 /
+// 17.3, 32 and 389 16.8 / 17.6, 75 and 877 31.6 / 19.4.  Compact: 256 pages 3.0 /
+// 5.9; 1000 pages and 40 rows 4.8 / 5.6, which reserve's limit on rows leaves).
 constexpr int kClusterCtas = 8;
 constexpr int kSmallPool = 1024;
 constexpr int kSmallRows = 32;
