@@ -43,8 +43,10 @@
  *     unsupported.
  *   - A workspace must be zero-filled once after allocation (for example with
  *     cudaMemset) and must not be shared by calls that may run concurrently.
- *     Each call leaves its workspace ready for the next call; after a call
- *     that reported a device error or a timeout, zero it again.
+ *     It serves one operator (the page calls count as one): each call leaves
+ *     it ready for that operator's next call, of any sizes that it is large
+ *     enough for, not for another operator.  After a call that reported a
+ *     device error or a timeout, zero it again.
  *   - Symbols are thread-safe; per-stream ordering is the caller's.
  */
 #ifndef SV_H_
@@ -593,7 +595,9 @@ sv_status sv_chunk_attention_workspace_size(const sv_chunk_params* params, size_
 
 /* Device errors: SV_DEVERR_BAD_LENGTH for a sequence whose lengths do not fit
  * its block table, max_tokens or the token rows (its rows are not written);
- * SV_DEVERR_BAD_PAGE for a page id out of range (its keys read as zero). */
+ * SV_DEVERR_BAD_PAGE for a page id out of range (its keys read as zero);
+ * SV_DEVERR_TIMEOUT where a wait ran out, which 256 rows over more than about
+ * 10^8 keys may take by themselves. */
 sv_status sv_chunk_attention(const sv_chunk_params* params, sv_stream_t stream);
 
 /* ------------------------------------------------------------------------
