@@ -20,8 +20,12 @@
  *
  *   sv_kv_append       copy of a chunk's K/V (a prompt, or one token) into
  *                      its cache slots;
+ *   sv_rope_append     the same with the position rotation of Q and K on the
+ *                      way, one layer per call;
  *   sv_chunk_attention causal attention of each sequence's chunk of new
  *                      tokens over its paged cache, one layer per call;
+ *   sv_sample_tokens   the next token of each row of logits (temperature,
+ *                      top-k, top-p, min-p; given random numbers);
  *   sv_pages_*         which sequence holds which page: fork, reserve (with
  *                      copy on write), release, compact, and the page copy
  *                      they ask for.
@@ -83,7 +87,8 @@ enum {
   SV_DEVERR_BAD_TREE = 6,    /* a tree has no nodes or more than max_nodes  */
   SV_DEVERR_BAD_LENGTH = 7,  /* a token or page count outside its range     */
   SV_DEVERR_NO_PAGES = 8,    /* the pool has fewer free pages than asked for */
-  SV_DEVERR_BAD_ROW = 9      /* a table row outside the table, or in use    */
+  SV_DEVERR_BAD_ROW = 9,     /* a table row outside the table, or in use    */
+  SV_DEVERR_BAD_VALUE = 10   /* a logit or a setting that no token follows from */
 };
 
 /* Library ABI version (incremented on incompatible changes). */
@@ -536,6 +541,69 @@ sv_status sv_kv_append(const void* k, const void* v, long long token_stride, lon
                        sv_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Append of new tokens' K/V with the position rotation of Q and K on the way
+ * (one layer): what stands between the projections of a layer and its
+ * attention, in one launch.
+ *
+ * Token i of sequence b (N_b = cu_tokens[b+1] - cu_tokens[b] new tokens, 0
+ * allowed) has position x = ctx_lens[b] + i, or positions[t] of its token row
+ * t.  In every head of q and k pair j < rotary_dim / 2, the elements (j, j +
+ * rotary_dim / 2) or with `interleaved` (2 j, 2 j + 1), turns by x *
+ * inv_freq[j]:
+ *     (a, c) -> amplitude * (a cos - c sin, a sin + c cos);
+ * elements from rotary_dim on stay as they are.  The rotated q goes to q_out,
+ * k and v (a bit copy) to cache slot ctx_lens[b] + i as in sv_kv_append.
+ * Angles are exact to 2^-24 of half a turn at every 32-bit position; products
+ * are fp32, rounded once.  Rows behind cu_tokens[B] are padding: nothing of
+ * them is written.  q_out may be q itself with the same stride; otherwise the
+ * outputs overlap no input.
+ * ---------------------------------------------------------------------- */
+typedef enum sv_dtype { SV_BF16 = 0, SV_FP16 = 1, SV_FP32 = 2 } sv_dtype;
+
+typedef struct sv_rope_params {
+  int batch;              /* B                                               */
+  int num_q_heads;        /* Hq; 0: there is no q                            */
+  int num_kv_heads;       /* Hkv                                             */
+  int head_dim;           /* D: a multiple of 16, at most 256                */
+  int rotary_dim;         /* elements of a head that turn: a multiple of 16  */
+  int page_size;          /* >= 1                                            */
+  int num_pages;
+  int total_tokens;       /* rows of q, k and v: cu_tokens[B] or more, <= 2^30 */
+  int max_pages_per_seq;  /* row length of block_table                       */
+  int dtype;              /* SV_BF16 or SV_FP16, of all tensors              */
+  int interleaved;        /* which elements form a pair                      */
+  int flags;              /* 0                                               */
+  float amplitude;        /* of cos and sin; 0 selects 1                     */
+  long long q_stride;     /* elements from a token to the next; 0: Hq * D    */
+  long long q_out_stride; /* the same for q_out                              */
+  long long kv_stride;    /* the same for k and v; 0: Hkv * D                */
+
+  const void* q;          /* [T, Hq, D], heads contiguous                    */
+  const void* k;          /* [T, Hkv, D]                                     */
+  const void* v;          /* [T, Hkv, D]                                     */
+  void* q_out;            /* [T, Hq, D] (written)                            */
+  void* k_cache;          /* [num_pages, Hkv, page_size, D]                  */
+  void* v_cache;
+  const int* block_table; /* int32 [B, max_pages_per_seq]                    */
+  const int* ctx_lens;    /* int32 [B] L_b >= 0                              */
+  const int* cu_tokens;   /* int32 [B+1] prefix sums of N_b, cu_tokens[0] = 0 */
+  const int* positions;   /* optional int32 [T], any value                   */
+  const float* inv_freq;  /* [rotary_dim / 2], radians per position, below
+                             1024 in magnitude (others give NaN)             */
+  int* new_ctx_lens;      /* optional int32 [B]: ctx_lens[b] + N_b; must not
+                             alias ctx_lens                                  */
+  void* workspace;        /* optional (NULL, or >= 256 bytes zero-filled
+                             once): error word                               */
+  size_t workspace_bytes;
+} sv_rope_params;
+
+/* Device errors: SV_DEVERR_BAD_LENGTH for a sequence whose lengths do not fit
+ * its block table or the token rows, or would pass 2^31 - 1 (left out: its
+ * length stays, its q rows are not written); SV_DEVERR_BAD_PAGE for a slot whose
+ * page id is out of range (skipped; its q row is written). */
+sv_status sv_rope_append(const sv_rope_params* params, sv_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * Attention of a chunk of new tokens over the paged cache (one layer).
  *
  * The forward that precedes tree verification: a prompt processed in chunks,
@@ -557,8 +625,6 @@ sv_status sv_kv_append(const void* k, const void* v, long long token_stride, lon
  * pages that a window has left behind: those are not read, and slots behind
  * L_b + N_b may hold anything.
  * ---------------------------------------------------------------------- */
-typedef enum sv_dtype { SV_BF16 = 0, SV_FP16 = 1 } sv_dtype;
-
 typedef struct sv_chunk_params {
   int batch;              /* B, 1..65535                                     */
   int num_q_heads;        /* Hq                                              */
@@ -569,7 +635,7 @@ typedef struct sv_chunk_params {
   int total_tokens;       /* rows of q: cu_tokens[B] or more, <= 2^30        */
   int max_tokens;         /* >= max_b N_b (host copy)                        */
   int max_pages_per_seq;  /* row length of block_table                       */
-  int dtype;              /* sv_dtype of q, the cache and out                */
+  int dtype;              /* SV_BF16 or SV_FP16, of q, the cache and out     */
   int window_tokens;      /* W <= 2^28; 0 = every earlier token is visible   */
   int sink_tokens;        /* tokens visible whatever the window, <= 2^28     */
   float sm_scale;         /* softmax scale; <= 0 selects 1/sqrt(D)           */
@@ -599,6 +665,57 @@ sv_status sv_chunk_attention_workspace_size(const sv_chunk_params* params, size_
  * SV_DEVERR_TIMEOUT where a wait ran out, which 256 rows over more than about
  * 10^8 keys may take by themselves. */
 sv_status sv_chunk_attention(const sv_chunk_params* params, sv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Sampling of one token per row of logits.
+ *
+ * With w_i = exp((logits[r, i] - max) / temperature[r]) and the entries of a
+ * row in descending order (equal ones: lower index first), the kept entries are
+ * the longest prefix of that order within all of
+ *   top_k[r]  entries (0 or less: all);
+ *   top_p[r]: the fewest entries whose weights sum to top_p[r] or more of the
+ *             weights of the top_k ones (1 or more: all; at least one entry);
+ *   min_p[r]: entries of weight >= min_p[r] (the largest weight is 1).
+ * tokens[r] is the smallest index x whose kept weights up to and including x
+ * sum to more than uniforms[r] of all kept ones.  temperature[r] = 0 takes the
+ * first of the order.  logprobs[r] is the natural logarithm of the token's
+ * share of the kept weights; probs[r, :] are all shares, 0 for the others: the
+ * draft distributions of sv_sample_accept, and their tokens, from a draft
+ * model's logits.
+ *
+ * Logits of -inf are entries that do not exist.  A row without any other
+ * entry, with +inf or NaN among its logits, or with a setting that is NaN, a
+ * temperature that is negative or infinite, or a uniform outside [0, 1), gets
+ * token -1 (and logprob and probs NaN), and the error word records
+ * SV_DEVERR_BAD_VALUE.
+ *
+ * Weights have an absolute error below 2^-36 (below 2^-34 of a weight under
+ * 2^-13) and are summed as 64-bit integers, so that neither the order of sums
+ * nor the size of the vocabulary shows in the tokens; entries below 2^-46 of
+ * the largest are never drawn.
+ * ---------------------------------------------------------------------- */
+typedef struct sv_sample_params {
+  int rows;                 /* R                                             */
+  int vocab;                /* V: 1..2^18                                    */
+  int dtype;                /* sv_dtype of the logits                        */
+  int flags;                /* 0                                             */
+  long long logits_stride;  /* elements from a row to the next; 0: V         */
+  long long probs_stride;   /* the same for probs                            */
+  const void* logits;       /* [R, V]                                        */
+  const float* uniforms;    /* fp32 [R], in [0, 1)                           */
+  const float* temperature; /* optional fp32 [R]; NULL: 1                    */
+  const int* top_k;         /* optional int32 [R]                            */
+  const float* top_p;       /* optional fp32 [R]                             */
+  const float* min_p;       /* optional fp32 [R]                             */
+  int* tokens;              /* int32 [R] (written)                           */
+  float* logprobs;          /* optional fp32 [R] (written)                   */
+  float* probs;             /* optional fp32 [R, V] (written)                */
+  void* workspace;          /* optional (NULL, or >= 256 bytes zero-filled
+                               once): error word                             */
+  size_t workspace_bytes;
+} sv_sample_params;
+
+sv_status sv_sample_tokens(const sv_sample_params* params, sv_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * Pages of the cache: which sequence holds which.

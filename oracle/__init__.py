@@ -18,6 +18,8 @@ verification hot path computes, written from the method descriptions:
   cache (window and sink tokens included), and the append of its K/V.
 * ``pages``      — the page bookkeeping: fork, reserve with copy on write,
   release, compact, as a pool in plain Python.
+* ``decode``     — the append with the position rotation, and sampling of a
+  token from a row of logits (temperature, top-k, top-p, min-p).
 * ``sampling``   — stochastic (temperature > 0) acceptance: speculative
   sampling node by node over the tree, residual draws for the bonus token.
 
@@ -41,6 +43,7 @@ from .attention import (  # noqa: F401
 from .accept import greedy_accept  # noqa: F401
 from .chunk import chunk_attention, chunk_visible, kv_append  # noqa: F401
 from .commit import kv_commit  # noqa: F401
+from .decode import kept, rope_append, rotate, sample_token  # noqa: F401
 from .pages import Pool, copy_pages  # noqa: F401
 from .sampling import inverse_cdf, node_verify, speculative_tree_accept, target_probs  # noqa: F401
 from .retrieval import (  # noqa: F401

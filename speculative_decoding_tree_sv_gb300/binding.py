@@ -24,14 +24,14 @@ STATUS_NAMES = {0: "SV_OK", 1: "SV_ERR_INVALID_ARG", 2: "SV_ERR_UNSUPPORTED", 3:
 # device error codes (sv_deverr in include/sv.h)
 SV_DEVERR_NONE, SV_DEVERR_TIMEOUT, SV_DEVERR_BAD_PARENT, SV_DEVERR_BAD_PAGE = 0, 1, 2, 3
 SV_DEVERR_BAD_PATH, SV_DEVERR_DEPTH, SV_DEVERR_BAD_TREE = 4, 5, 6
-SV_DEVERR_BAD_LENGTH, SV_DEVERR_NO_PAGES, SV_DEVERR_BAD_ROW = 7, 8, 9
-SV_BF16, SV_FP16 = 0, 1
+SV_DEVERR_BAD_LENGTH, SV_DEVERR_NO_PAGES, SV_DEVERR_BAD_ROW, SV_DEVERR_BAD_VALUE = 7, 8, 9, 10
+SV_BF16, SV_FP16, SV_FP32 = 0, 1, 2
 SV_ATTN_EARLY_CONTEXT = 1
 SV_ATTN_KERNEL_PAIRED = 2
 SV_ATTN_KERNEL_WIDE = 4
 SV_ATTN_KERNEL_DEALT = 8
 DEVICE_ERRORS = {0: "none", 1: "timeout", 2: "bad parent", 3: "bad page", 4: "bad path", 5: "depth",
-                 6: "bad tree", 7: "bad length", 8: "no pages", 9: "bad row"}
+                 6: "bad tree", 7: "bad length", 8: "no pages", 9: "bad row", 10: "bad value"}
 
 
 class SvError(RuntimeError):
@@ -75,6 +75,28 @@ class sv_chunk_params(ctypes.Structure):
         ("q", c_void_p), ("k_cache", c_void_p), ("v_cache", c_void_p), ("block_table", c_void_p),
         ("ctx_lens", c_void_p), ("cu_tokens", c_void_p), ("out", c_void_p), ("lse", c_void_p),
         ("workspace", c_void_p), ("workspace_bytes", c_size_t),
+    ]
+
+
+class sv_rope_params(ctypes.Structure):
+    _fields_ = [
+        ("batch", c_int), ("num_q_heads", c_int), ("num_kv_heads", c_int), ("head_dim", c_int),
+        ("rotary_dim", c_int), ("page_size", c_int), ("num_pages", c_int), ("total_tokens", c_int),
+        ("max_pages_per_seq", c_int), ("dtype", c_int), ("interleaved", c_int), ("flags", c_int),
+        ("amplitude", c_float), ("q_stride", c_longlong), ("q_out_stride", c_longlong), ("kv_stride", c_longlong),
+        ("q", c_void_p), ("k", c_void_p), ("v", c_void_p), ("q_out", c_void_p), ("k_cache", c_void_p),
+        ("v_cache", c_void_p), ("block_table", c_void_p), ("ctx_lens", c_void_p), ("cu_tokens", c_void_p),
+        ("positions", c_void_p), ("inv_freq", c_void_p), ("new_ctx_lens", c_void_p), ("workspace", c_void_p),
+        ("workspace_bytes", c_size_t),
+    ]
+
+
+class sv_sample_params(ctypes.Structure):
+    _fields_ = [
+        ("rows", c_int), ("vocab", c_int), ("dtype", c_int), ("flags", c_int), ("logits_stride", c_longlong),
+        ("probs_stride", c_longlong), ("logits", c_void_p), ("uniforms", c_void_p), ("temperature", c_void_p),
+        ("top_k", c_void_p), ("top_p", c_void_p), ("min_p", c_void_p), ("tokens", c_void_p), ("logprobs", c_void_p),
+        ("probs", c_void_p), ("workspace", c_void_p), ("workspace_bytes", c_size_t),
     ]
 
 
@@ -151,6 +173,8 @@ def load(path: Optional[str] = None):
             ("sv_kv_append", [V, V, L, L, V, V, L, I, I, V, I, V, V, I, I, I, I, I, V, V, Z, V]),
             ("sv_chunk_attention_workspace_size", [P(sv_chunk_params), P(Z)]),
             ("sv_chunk_attention", [P(sv_chunk_params), V]),
+            ("sv_rope_append", [P(sv_rope_params), V]),
+            ("sv_sample_tokens", [P(sv_sample_params), V]),
             ("sv_pages_workspace_size", [I, I, P(Z)]),
             ("sv_pages_release", [V, I, V, I, V, V, I, I, V, Z, V]),
             ("sv_pages_fork", [V, V, I, V, I, I, V, V, V, I, I, V, Z, V]),
@@ -564,6 +588,34 @@ def sv_kv_append(k, v, k_cache, v_cache, block_table, ctx_lens, cu_tokens, new_c
                                   device, handle)
     if status != SV_OK:
         raise SvError(status, "sv_kv_append")
+
+
+def sv_rope_append(q, k, v, q_out, k_cache, v_cache, block_table, ctx_lens, cu_tokens, inv_freq, *, positions=None,
+                   interleaved: bool = False, amplitude: float = 1.0, new_ctx_lens=None, workspace=None,
+                   stream=None) -> None:
+    """Rotates q and k to their positions, writes q to q_out and k, v to their
+    cache slots (see include/sv.h).  q/q_out [T, Hq, D] (both None: there is no
+    q; q_out may be q), k/v [T, Hkv, D], heads contiguous, any token stride;
+    caches of one layer [pages, Hkv, page_size, D]; inv_freq float32
+    [rotary_dim / 2]."""
+    device, handle = _where(stream)
+    status = _marshal().rope_append(q, k, v, q_out, k_cache, v_cache, block_table, ctx_lens, cu_tokens, inv_freq, positions,
+                                    bool(interleaved), amplitude, new_ctx_lens, workspace, device, handle)
+    if status != SV_OK:
+        raise SvError(status, "sv_rope_append")
+
+
+def sv_sample_tokens(logits, uniforms, tokens, *, temperature=None, top_k=None, top_p=None, min_p=None, logprobs=None,
+                     probs=None, workspace=None, stream=None) -> None:
+    """Draws a token per row of logits [R, V] (float32, bfloat16 or float16,
+    rows contiguous, any row stride) with the given uniforms (see include/sv.h
+    for the filters' order).  The settings are tensors of R elements (float32,
+    top_k int32) or None for none."""
+    device, handle = _where(stream)
+    status = _marshal().sample_tokens(logits, uniforms, tokens, temperature, top_k, top_p, min_p, logprobs, probs, workspace,
+                                      device, handle)
+    if status != SV_OK:
+        raise SvError(status, "sv_sample_tokens")
 
 
 def sv_pages_workspace_size(rows: int, num_pages: int) -> int:

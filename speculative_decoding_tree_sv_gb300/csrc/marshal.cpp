@@ -2,7 +2,7 @@
 // and hands their addresses to the C entry points of include/sv.h.
 //
 // An append of one token is about 5 us of GPU time; checked and marshalled in
-// Python its call took 10.7 us of host time (a page release 6.3), so these six
+// Python its call took 10.7 us of host time (a page release 6.3), so these
 // calls do it here.  The module sees tensors through torch's own Python object
 // and computes nothing.
 #define PY_SSIZE_T_CLEAN
@@ -161,6 +161,151 @@ sv_status kv_append(const Args& a) {
                       small(T, "tokens"), p.heads, p.dim, p.page, data(after), bytes(ws), size(ws), stream(a, 10));
 }
 
+// [T, heads, D] with contiguous heads and rows that do not overlap: elements from
+// a token to the next.
+int64_t rows_of(const Tensor& t, const char* name, int64_t T, int64_t heads, int64_t dim) {
+  if (t.dim() != 3 || t.size(0) != T || t.size(1) != heads || t.size(2) != dim)
+    refuse(std::string(name) + " must be [" + std::to_string(T) + " tokens, " + std::to_string(heads) + ", " +
+           std::to_string(dim) + "], got " + shape_of(t));
+  if ((dim > 1 && t.stride(2) != 1) || (heads > 1 && t.stride(1) != dim))
+    refuse("the heads of " + std::string(name) + " must be contiguous");
+  if (T <= 1) return 0;  // (the parameters' word for dense)
+  if (t.stride(0) < heads * dim) refuse("the rows of " + std::string(name) + " overlap");
+  return t.stride(0);
+}
+
+// fp32, contiguous, of `count` elements.
+const Tensor* floats(const Args& a, int i, const char* name, int64_t count) {
+  if (a.at[i] == Py_None) return nullptr;
+  const Tensor* t = a.tensor(i, name);
+  if (t->scalar_type() != at::kFloat || !t->is_contiguous() || t->numel() != count)
+    refuse(std::string(name) + " must be a contiguous float32 tensor of " + std::to_string(count) + " elements");
+  return t;
+}
+
+float number32(const Args& a, int i) {
+  const double v = PyFloat_AsDouble(a.at[i]);
+  if (v == -1.0 && PyErr_Occurred()) throw std::exception();
+  return static_cast<float>(v);
+}
+
+int half_type(const Tensor& t, const char* name) {
+  if (t.scalar_type() == at::kBFloat16) return SV_BF16;
+  if (t.scalar_type() == at::kHalf) return SV_FP16;
+  refuse(std::string(name) + " must be bfloat16 or float16");
+}
+
+sv_status rope_append(const Args& a) {
+  const Tensor *q = a.tensor(0, "q", true), &k = *a.tensor(1, "k"), &v = *a.tensor(2, "v");
+  const Tensor *out = a.tensor(3, "q_out", true), &kc = *a.tensor(4, "k_cache"), &vc = *a.tensor(5, "v_cache");
+  const Pool pl = pool(kc, &vc);
+  if (kc.dim() != 4) refuse("the caches must be one layer, [pages, Hkv, page_size, D]");
+  if ((q == nullptr) != (out == nullptr)) refuse("q and q_out come together");
+  sv_rope_params p = {};
+  p.dtype = half_type(kc, "the cache");
+  for (const Tensor* t : {q, out, &k, &v})
+    if (t != nullptr && t->scalar_type() != kc.scalar_type())
+      refuse(std::string("q, k, v and q_out must have the cache's type ") + c10::toString(kc.scalar_type()));
+  if (k.dim() != 3) refuse("k must be [tokens, heads, head_dim], got " + shape_of(k));
+  const int64_t T = k.size(0);
+  p.kv_stride = rows_of(k, "k", T, pl.heads, pl.dim);
+  if (rows_of(v, "v", T, pl.heads, pl.dim) != p.kv_stride) refuse("k and v must have the same strides");
+  if (q != nullptr) {
+    if (q->dim() != 3) refuse("q must be [tokens, heads, head_dim], got " + shape_of(*q));
+    p.num_q_heads = small(q->size(1), "heads");
+    p.q_stride = rows_of(*q, "q", T, q->size(1), pl.dim);
+    p.q_out_stride = rows_of(*out, "q_out", T, q->size(1), pl.dim);
+  }
+  const Tensor* table = a.ints(6, "block_table");
+  if (table->dim() != 2) refuse("block_table must be [batch, max_pages]");
+  const int64_t B = table->size(0);
+  const Tensor *ctx = a.ints(7, "ctx_lens", B), *cu = a.ints(8, "cu_tokens", B + 1);
+  const Tensor* freq = a.tensor(9, "inv_freq");
+  if (freq->scalar_type() != at::kFloat || !freq->is_contiguous() || freq->dim() != 1)
+    refuse("inv_freq must be a contiguous float32 tensor of one dimension");
+  const Tensor* pos = a.at[10] == Py_None ? nullptr : a.ints(10, "positions", T);
+  const Tensor* after = a.at[13] == Py_None ? nullptr : a.ints(13, "new_ctx_lens", B);
+  const Tensor* ws = a.tensor(14, "workspace", true);
+  a.on_device({q, &k, &v, out, &kc, &vc, table, ctx, cu, freq, pos, after, ws});
+  p.batch = small(B, "batch");
+  p.num_kv_heads = pl.heads;
+  p.head_dim = pl.dim;
+  p.rotary_dim = small(2 * freq->numel(), "rotary dim");
+  p.page_size = pl.page;
+  p.num_pages = pl.pages;
+  p.total_tokens = small(T, "tokens");
+  p.max_pages_per_seq = small(table->size(1), "max_pages");
+  p.interleaved = a.number(11) != 0;
+  p.amplitude = number32(a, 12);
+  p.q = bytes(q);
+  p.k = k.data_ptr();
+  p.v = v.data_ptr();
+  p.q_out = bytes(out);
+  p.k_cache = kc.data_ptr();
+  p.v_cache = vc.data_ptr();
+  p.block_table = data(table);
+  p.ctx_lens = data(ctx);
+  p.cu_tokens = data(cu);
+  p.positions = data(pos);
+  p.inv_freq = static_cast<const float*>(freq->data_ptr());
+  p.new_ctx_lens = data(after);
+  p.workspace = bytes(ws);
+  p.workspace_bytes = size(ws);
+  return sv_rope_append(&p, stream(a, 16));
+}
+
+// Elements from a row to the next of [R, V] with contiguous rows that do not overlap.
+int64_t matrix(const Tensor& t, const char* name, int64_t rows, int64_t cols) {
+  if (t.dim() != 2 || t.size(0) != rows || t.size(1) != cols)
+    refuse(std::string(name) + " must be [" + std::to_string(rows) + ", " + std::to_string(cols) + "], got " + shape_of(t));
+  if (cols > 1 && t.stride(1) != 1) refuse("the rows of " + std::string(name) + " must be contiguous");
+  if (rows <= 1) return 0;
+  if (t.stride(0) < cols) refuse("the rows of " + std::string(name) + " overlap");
+  return t.stride(0);
+}
+
+sv_status sample_tokens(const Args& a) {
+  const Tensor& logits = *a.tensor(0, "logits");
+  if (logits.dim() != 2) refuse("logits must be [rows, vocabulary], got " + shape_of(logits));
+  const int64_t R = logits.size(0), V = logits.size(1);
+  sv_sample_params p = {};
+  p.dtype = logits.scalar_type() == at::kFloat ? static_cast<int>(SV_FP32) : -1;
+  if (p.dtype < 0) {
+    if (logits.scalar_type() != at::kBFloat16 && logits.scalar_type() != at::kHalf)
+      refuse("logits must be float32, bfloat16 or float16");
+    p.dtype = half_type(logits, "logits");
+  }
+  p.logits_stride = matrix(logits, "logits", R, V);
+  const Tensor* u = floats(a, 1, "uniforms", R);
+  if (u == nullptr) refuse("uniforms must be a tensor");
+  const Tensor* tokens = a.ints(2, "tokens", R);
+  const Tensor* temperature = floats(a, 3, "temperature", R);
+  const Tensor* top_k = a.at[4] == Py_None ? nullptr : a.ints(4, "top_k", R);
+  const Tensor *top_p = floats(a, 5, "top_p", R), *min_p = floats(a, 6, "min_p", R);
+  const Tensor *logprobs = floats(a, 7, "logprobs", R), *probs = a.tensor(8, "probs", true);
+  if (probs != nullptr) {
+    if (probs->scalar_type() != at::kFloat) refuse("probs must be float32");
+    p.probs_stride = matrix(*probs, "probs", R, V);
+  }
+  const Tensor* ws = a.tensor(9, "workspace", true);
+  a.on_device({&logits, u, tokens, temperature, top_k, top_p, min_p, logprobs, probs, ws});
+  auto f = [](const Tensor* t) { return t ? static_cast<float*>(t->data_ptr()) : nullptr; };
+  p.rows = small(R, "rows");
+  p.vocab = small(V, "vocabulary");
+  p.logits = logits.data_ptr();
+  p.uniforms = f(u);
+  p.temperature = f(temperature);
+  p.top_k = data(top_k);
+  p.top_p = f(top_p);
+  p.min_p = f(min_p);
+  p.tokens = data(tokens);
+  p.logprobs = f(logprobs);
+  p.probs = f(probs);
+  p.workspace = bytes(ws);
+  p.workspace_bytes = size(ws);
+  return sv_sample_tokens(&p, stream(a, 11));
+}
+
 sv_status pages_release(const Args& a) {
   const State s = state(a, 1, 2, 3);
   const Tensor *keep = a.ints(0, "keep_lens", s.rows), *ws = a.tensor(5, "workspace", true);
@@ -236,6 +381,8 @@ PyMethodDef method(const char* name) {
 }
 
 PyMethodDef methods[] = {method<kv_append, 11>("kv_append"),
+                         method<rope_append, 17>("rope_append"),
+                         method<sample_tokens, 12>("sample_tokens"),
                          method<pages_release, 8>("pages_release"),
                          method<pages_fork, 10>("pages_fork"),
                          method<pages_reserve, 12>("pages_reserve"),
