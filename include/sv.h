@@ -24,6 +24,8 @@
  *                      way, one layer per call;
  *   sv_chunk_attention causal attention of each sequence's chunk of new
  *                      tokens over its paged cache, one layer per call;
+ *   sv_prefix_attention  the same for groups of sequences that share the
+ *                      pages of a prefix, which is read once per group;
  *   sv_sample_tokens   the next token of each row of logits (temperature,
  *                      top-k, top-p, min-p; given random numbers);
  *   sv_pages_*         which sequence holds which page: fork, reserve (with
@@ -665,6 +667,60 @@ sv_status sv_chunk_attention_workspace_size(const sv_chunk_params* params, size_
  * SV_DEVERR_TIMEOUT where a wait ran out, which 256 rows over more than about
  * 10^8 keys may take by themselves. */
 sv_status sv_chunk_attention(const sv_chunk_params* params, sv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Attention of sequences that share a prefix (one layer).
+ *
+ * The result is sv_chunk_attention's without a window, bit for bit the same on
+ * every run; what differs is what is read.  The sequences cu_groups[g] ..
+ * cu_groups[g+1] - 1 form group g (consecutive rows of block_table; a group may
+ * hold one sequence, or none), and the first prefix_lens[g] tokens of each lie
+ * in the same pages (as sv_pages_fork and sv_pages_reserve leave them: the whole
+ * pages of the parent).  Those pages, as the group's first row names them, are
+ * read once for all new tokens of the group; the entries of its other rows for
+ * them are not read.  Every sequence's own tokens from prefix_lens[g] on are
+ * read as always.  prefix_lens[g] is a multiple of page_size and at most the
+ * ctx_lens of each of the group's sequences; 0 shares nothing.
+ * ---------------------------------------------------------------------- */
+typedef struct sv_prefix_params {
+  int batch;              /* the fields of sv_chunk_params, as there ...     */
+  int num_q_heads;
+  int num_kv_heads;
+  int head_dim;
+  int page_size;
+  int num_pages;
+  int total_tokens;
+  int max_tokens;
+  int max_pages_per_seq;
+  int dtype;
+  int num_groups;         /* 1..batch                                        */
+  int max_group_tokens;   /* >= the new tokens of any group (host copy)      */
+  float sm_scale;
+  int flags;              /* 0                                               */
+  long long q_stride;
+  long long out_stride;
+
+  const void* q;
+  const void* k_cache;
+  const void* v_cache;
+  const int* block_table;
+  const int* ctx_lens;
+  const int* cu_tokens;
+  const int* cu_groups;   /* int32 [num_groups+1], from 0 to batch           */
+  const int* prefix_lens; /* int32 [num_groups]                              */
+  void* out;
+  float* lse;
+  void* workspace;
+  size_t workspace_bytes;
+} sv_prefix_params;
+
+/* Bytes of workspace for these parameters on the current device. */
+sv_status sv_prefix_attention_workspace_size(const sv_prefix_params* params, size_t* bytes);
+
+/* Device errors: as sv_chunk_attention; SV_DEVERR_BAD_LENGTH also for a group
+ * whose sequences or prefix do not fit the above (the rows of its sequences are
+ * not written, those of the others are). */
+sv_status sv_prefix_attention(const sv_prefix_params* params, sv_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * Sampling of one token per row of logits.

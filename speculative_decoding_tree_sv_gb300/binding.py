@@ -78,6 +78,18 @@ class sv_chunk_params(ctypes.Structure):
     ]
 
 
+class sv_prefix_params(ctypes.Structure):
+    _fields_ = [
+        ("batch", c_int), ("num_q_heads", c_int), ("num_kv_heads", c_int), ("head_dim", c_int),
+        ("page_size", c_int), ("num_pages", c_int), ("total_tokens", c_int), ("max_tokens", c_int),
+        ("max_pages_per_seq", c_int), ("dtype", c_int), ("num_groups", c_int), ("max_group_tokens", c_int),
+        ("sm_scale", c_float), ("flags", c_int), ("q_stride", c_longlong), ("out_stride", c_longlong),
+        ("q", c_void_p), ("k_cache", c_void_p), ("v_cache", c_void_p), ("block_table", c_void_p),
+        ("ctx_lens", c_void_p), ("cu_tokens", c_void_p), ("cu_groups", c_void_p), ("prefix_lens", c_void_p),
+        ("out", c_void_p), ("lse", c_void_p), ("workspace", c_void_p), ("workspace_bytes", c_size_t),
+    ]
+
+
 class sv_rope_params(ctypes.Structure):
     _fields_ = [
         ("batch", c_int), ("num_q_heads", c_int), ("num_kv_heads", c_int), ("head_dim", c_int),
@@ -174,6 +186,8 @@ def load(path: Optional[str] = None):
             ("sv_chunk_attention_workspace_size", [P(sv_chunk_params), P(Z)]),
             ("sv_chunk_attention", [P(sv_chunk_params), V]),
             ("sv_rope_append", [P(sv_rope_params), V]),
+            ("sv_prefix_attention_workspace_size", [P(sv_prefix_params), P(Z)]),
+            ("sv_prefix_attention", [P(sv_prefix_params), V]),
             ("sv_sample_tokens", [P(sv_sample_params), V]),
             ("sv_pages_workspace_size", [I, I, P(Z)]),
             ("sv_pages_release", [V, I, V, I, V, V, I, I, V, Z, V]),
@@ -516,6 +530,22 @@ def make_chunk_params(*, q, k_cache, v_cache, block_table, ctx_lens, cu_tokens, 
     contiguous, Hq * D elements or more from a token to the next), caches
     [pages, Hkv, 16, D], all bf16 or all fp16; lse fp32 [T, Hq] if wanted.  The
     result keeps the tensors alive."""
+    p = sv_chunk_params()
+    for name, n in (("window_tokens", window_tokens), ("sink_tokens", sink_tokens)):
+        _fits32(name, n)
+    _fill_chunk(p, q, k_cache, v_cache, block_table, ctx_lens, cu_tokens, out, max_tokens, lse, workspace, sm_scale)
+    p.window_tokens, p.sink_tokens = int(window_tokens), int(sink_tokens)
+    return p
+
+
+def _fits32(name: str, n) -> None:
+    if not -1 << 31 <= int(n) < 1 << 31:  # (a field would keep the low 32 bits)
+        raise ValueError(f"{name} does not fit 32 bits: {n}")
+
+
+def _fill_chunk(p, q, k_cache, v_cache, block_table, ctx_lens, cu_tokens, out, max_tokens, lse, workspace, sm_scale):
+    """Checks the tensors that both attentions over the paged cache take and
+    fills their fields."""
     import torch
     if q.dim() != 3 or out.shape != q.shape:
         raise ValueError("q and out must both be [tokens, heads, head_dim]")
@@ -541,16 +571,13 @@ def make_chunk_params(*, q, k_cache, v_cache, block_table, ctx_lens, cu_tokens, 
     _ints("cu_tokens", cu_tokens, B + 1)
     if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (T, Hq) or not lse.is_contiguous()):
         raise ValueError(f"lse must be a contiguous float32 tensor of shape {(T, Hq)}")
-    for name, n in (("max_tokens", max_tokens), ("window_tokens", window_tokens), ("sink_tokens", sink_tokens)):
-        if not -1 << 31 <= int(n) < 1 << 31:  # (a field would keep the low 32 bits)
-            raise ValueError(f"{name} does not fit 32 bits: {n}")
+    _fits32("max_tokens", max_tokens)
     _on_device(q, k_cache, v_cache, block_table, ctx_lens, cu_tokens, out, lse, workspace)
-    p = sv_chunk_params()
     p.batch, p.num_q_heads, p.num_kv_heads, p.head_dim = B, Hq, Hkv, D
     p.page_size, p.num_pages, p.total_tokens, p.max_tokens = page, pages, T, int(max_tokens)
     p.max_pages_per_seq = width
     p.dtype = SV_BF16 if q.dtype == torch.bfloat16 else SV_FP16
-    p.window_tokens, p.sink_tokens, p.sm_scale, p.flags = int(window_tokens), int(sink_tokens), float(sm_scale), 0
+    p.sm_scale, p.flags = float(sm_scale), 0
     p.q_stride = q.stride(0) if T > 1 else 0
     p.out_stride = out.stride(0) if T > 1 else 0
     p.q, p.k_cache, p.v_cache, p.out = q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr()
@@ -558,7 +585,6 @@ def make_chunk_params(*, q, k_cache, v_cache, block_table, ctx_lens, cu_tokens, 
     p.lse = None if lse is None else lse.data_ptr()
     p.workspace, p.workspace_bytes = _space(workspace)
     p.tensors = (q, k_cache, v_cache, block_table, ctx_lens, cu_tokens, out, lse, workspace)
-    return p
 
 
 def sv_chunk_attention_workspace_size(params: sv_chunk_params) -> int:
@@ -576,6 +602,45 @@ def sv_chunk_attention(params: sv_chunk_params, stream=None) -> None:
     if held is not None and held[0].get_device() != device:
         _on_device(held[0])
     _check(load().sv_chunk_attention(ctypes.byref(params), handle), "sv_chunk_attention")
+
+
+def make_prefix_params(*, q, k_cache, v_cache, block_table, ctx_lens, cu_tokens, cu_groups, prefix_lens, out,
+                       max_tokens: int, max_group_tokens: int, lse=None, workspace=None,
+                       sm_scale: float = 0.0) -> sv_prefix_params:
+    """Fill an ``sv_prefix_params`` from torch tensors: those of
+    ``make_chunk_params``, the groups' prefix sums over the sequences and each
+    group's shared tokens, both int32.  The result keeps the tensors alive."""
+    p = sv_prefix_params()
+    if cu_groups.numel() < 2:
+        raise ValueError("cu_groups must have one element more than there are groups")
+    groups = cu_groups.numel() - 1
+    _ints("cu_groups", cu_groups)
+    _ints("prefix_lens", prefix_lens, groups)
+    _fits32("max_group_tokens", max_group_tokens)
+    _fill_chunk(p, q, k_cache, v_cache, block_table, ctx_lens, cu_tokens, out, max_tokens, lse, workspace, sm_scale)
+    _on_device(cu_groups, prefix_lens)
+    p.num_groups, p.max_group_tokens = groups, int(max_group_tokens)
+    p.cu_groups, p.prefix_lens = cu_groups.data_ptr(), prefix_lens.data_ptr()
+    p.tensors += (cu_groups, prefix_lens)
+    return p
+
+
+def sv_prefix_attention_workspace_size(params: sv_prefix_params) -> int:
+    n = c_size_t(0)
+    _check(load().sv_prefix_attention_workspace_size(ctypes.byref(params), ctypes.byref(n)),
+           "sv_prefix_attention_workspace_size")
+    return int(n.value)
+
+
+def sv_prefix_attention(params: sv_prefix_params, stream=None) -> None:
+    """Causal attention of every sequence's new tokens over its paged cache,
+    whose prefix the sequences of a group share and which is read once for all
+    of them (see include/sv.h)."""
+    device, handle = _where(stream)
+    held = getattr(params, "tensors", None)
+    if held is not None and held[0].get_device() != device:
+        _on_device(held[0])
+    _check(load().sv_prefix_attention(ctypes.byref(params), handle), "sv_prefix_attention")
 
 
 def sv_kv_append(k, v, k_cache, v_cache, block_table, ctx_lens, cu_tokens, new_ctx_lens=None, workspace=None,

@@ -28,7 +28,7 @@ LIBDIR = os.path.join(PKG, "lib")
 LIBNAME = "libsv.so"
 SOURCES = ["abi.cu", "tree_attention.cu", "tree_attention_wide.cu", "tree_attention_dealt.cu", "greedy_accept.cu",
            "sample_accept.cu", "kv_commit.cu", "retrieval.cu", "kv_append.cu", "rope_append.cu", "sample_tokens.cu", "pages.cu",
-           "chunk_attention.cu", "chunk_rows.cu", "chunk_tiles.cu"]
+           "chunk_attention.cu", "chunk_rows.cu", "chunk_tiles.cu", "prefix_attention.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

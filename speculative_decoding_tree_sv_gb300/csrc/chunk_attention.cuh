@@ -36,7 +36,12 @@ enum RowMode {
   kRowCta = 2      // whole units to the CTAs (or a cluster each), their pages shared by the warps
 };
 
+struct Seq;
+struct PrefixSeq;
+
 struct Params {
+  using Entry = Seq;                      // what a unit's list entry is
+  static constexpr bool kPrefix = false;  // entries are sequences
   const void* q;
   const int* block_table;
   const int* ctx_lens;
@@ -67,10 +72,37 @@ struct Params {
   int row_cluster;       // kRowCta: CTAs (a cluster) per unit; more than one: every unit has its own
 };
 
+// Attention over shared prefixes: the list of entries is the groups' prefixes, then
+// the sequences with what lies behind their prefix.  `batch` counts the entries.
+// Both parts of a row go to fp32 rows, which the call's combine merges.
+struct PrefixParams : Params {
+  using Entry = PrefixSeq;
+  static constexpr bool kPrefix = true;
+  const int* cu_groups;
+  const int* prefix_lens;
+  int num_groups, num_seqs, max_group_tokens;
+  int compact;        // rows of the arrays below go by the sequences' order (see load_seq), else by token rows
+  long long rows;     // tokens of one part
+  float* whole_o;     // [2 parts][rows][Hq][D] O / l of units that no boundary cuts
+  float* whole_lse;   // [2 parts][rows][Hq]
+  int2* tile_rec;     // [2 parts][rows][Hkv] at a tile unit's first token: first and last CTA, -1 where it is whole
+};
+
 // One sequence's lengths; n is 0 when it has no work (nothing new, or lengths
 // that do not fit).
 struct Seq {
   int n0, n, ctx;
+};
+
+// An entry of the prefix list.  A group's prefix: its sequences' token rows, every one
+// of which sees the positions below ctx = end.  A sequence: as Seq, from first_page on.
+enum PrefixPart { kShared = 0, kOwn = 1, kAlone = 2 };  // kAlone: a sequence whose prefix is not shared
+struct PrefixSeq {
+  int n0, n, ctx;
+  int row;         // of the block table
+  int first_page;
+  int part;
+  int at;          // its first token's row in the part's arrays
 };
 
 __device__ __forceinline__ Seq load_seq(const Params& p, int b, bool report) {
@@ -86,6 +118,91 @@ __device__ __forceinline__ Seq load_seq(const Params& p, int b, bool report) {
     s.n = 0;
   }
   return s;
+}
+
+// A group is shared while its sequences bring less than an M tile of rows each: beyond,
+// reading the prefix once for all saves the tile kernel little and costs it the fp32
+// rows.
+struct Group {
+  int first, last, n0, n, prefix;  // sequences [first, last), their token rows, shared tokens
+  bool ok, shared;
+};
+
+__device__ __forceinline__ Group load_group(const PrefixParams& p, int g) {
+  Group x{p.cu_groups[g], p.cu_groups[g + 1], 0, 0, p.prefix_lens[g], false, false};
+  if (x.first < 0 || x.last < x.first || x.last > p.num_seqs) return x;
+  x.n0 = p.cu_tokens[x.first];
+  const int n1 = p.cu_tokens[x.last];
+  x.n = n1 - x.n0;
+  x.ok = x.n0 >= 0 && n1 >= x.n0 && n1 <= p.total_tokens && x.n <= p.max_group_tokens && x.prefix >= 0 &&
+         x.prefix % kPage == 0 && x.prefix / kPage <= p.max_pages_per_seq;
+  const int seqs = x.last - x.first;
+  x.shared = x.ok && x.prefix > 0 && seqs > 1 && x.n < static_cast<long long>(seqs) * p.tile_tokens;
+  return x;
+}
+
+// The group of sequence b: the first whose end lies behind it.
+__device__ __forceinline__ int group_of(const PrefixParams& p, int b) {
+  int lo = 0, hi = p.num_groups - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) / 2;
+    if (p.cu_groups[mid + 1] > b) hi = mid;
+    else lo = mid + 1;
+  }
+  return lo;
+}
+
+// Row of token t of the group in the part's arrays.  A shared group has fewer than
+// tile_tokens per sequence, so its rows fit between its sequences' (compact).
+__device__ __forceinline__ int part_row(const PrefixParams& p, const Group& x, int t) {
+  return p.compact ? x.first * p.tile_tokens + (t - x.n0) : t;
+}
+
+// Sequence b of group x.
+__device__ __forceinline__ PrefixSeq own_part(const PrefixParams& p, const Group& x, int b, bool report) {
+  PrefixSeq s;
+  s.n0 = p.cu_tokens[b];
+  const int n1 = p.cu_tokens[b + 1];
+  s.ctx = p.ctx_lens[b];
+  s.n = n1 - s.n0;
+  s.row = b;
+  const bool ok = x.ok && b >= x.first && b < x.last && s.n0 >= x.n0 && n1 >= s.n0 && n1 <= x.n0 + x.n &&
+                  s.n <= p.max_tokens && s.ctx >= x.prefix &&
+                  static_cast<long long>(s.ctx) + s.n <= static_cast<long long>(p.max_pages_per_seq) * kPage;
+  if (!ok) {
+    if (report) report_error(p.err, SV_DEVERR_BAD_LENGTH);
+    s.n = 0;
+  }
+  s.part = x.shared ? kOwn : kAlone;
+  s.first_page = x.shared ? x.prefix / kPage : 0;
+  s.at = part_row(p, x, s.n0);
+  return s;
+}
+
+__device__ __forceinline__ PrefixSeq load_seq(const PrefixParams& p, int v, bool report) {
+  if (v >= p.num_groups) {
+    const int b = v - p.num_groups;
+    return own_part(p, load_group(p, group_of(p, b)), b, report);
+  }
+  const Group x = load_group(p, v);
+  if (!x.ok && report) report_error(p.err, SV_DEVERR_BAD_LENGTH);
+  return {x.n0, x.shared ? x.n : 0, x.prefix, x.first, 0, kShared, part_row(p, x, x.n0)};
+}
+
+// An entry's row of the block table.
+__device__ __forceinline__ int table_row(const Seq&, int b) { return b; }
+__device__ __forceinline__ int table_row(const PrefixSeq& s, int) { return s.row; }
+
+// The lane's entry, on every lane.
+__device__ __forceinline__ Seq from_lane(const Seq& s, int lane) {
+  return {__shfl_sync(0xffffffffu, s.n0, lane), __shfl_sync(0xffffffffu, s.n, lane),
+          __shfl_sync(0xffffffffu, s.ctx, lane)};
+}
+__device__ __forceinline__ PrefixSeq from_lane(const PrefixSeq& s, int lane) {
+  return {__shfl_sync(0xffffffffu, s.n0, lane),  __shfl_sync(0xffffffffu, s.n, lane),
+          __shfl_sync(0xffffffffu, s.ctx, lane), __shfl_sync(0xffffffffu, s.row, lane),
+          __shfl_sync(0xffffffffu, s.first_page, lane), __shfl_sync(0xffffffffu, s.part, lane),
+          __shfl_sync(0xffffffffu, s.at, lane)};
 }
 
 // Whether the row kernel takes a sequence of n > 0 new tokens.
@@ -114,6 +231,10 @@ __device__ __forceinline__ Keys unit_keys(const Params& p, const Seq& s, int t0,
   return k;
 }
 
+__device__ __forceinline__ Keys unit_keys(const PrefixParams&, const PrefixSeq& s, int, int t1) {
+  return {0, s.first_page, s.part == kShared ? s.ctx : s.ctx + t1};
+}
+
 // Weights in eighths of a key: a unit costs its keys plus kUnitKeys (Q load,
 // pipeline fill, epilogue); one M tile costs kHalfUnit eighths of two.
 constexpr int kUnitKeys = 192;
@@ -131,8 +252,9 @@ constexpr long long kCutWeight = 7 * 8 * kBlockN;
 constexpr float kPageWeight = 60.f;
 
 // A sequence's units and their weights.
+template <class P>
 struct TileSeq {
-  Seq s;
+  typename P::Entry s;
   int units;         // row groups of one KV head
   long long weight;  // of one KV head
 };
@@ -162,8 +284,22 @@ __device__ __forceinline__ long long last_weight(const Params& p, const Seq& s, 
   return static_cast<long long>(half ? kHalfUnit : 8) * (min(s.ctx + s.n, weight_cap(p)) + kUnitKeys);
 }
 
-__device__ __forceinline__ TileSeq tile_units(const Params& p, int b, bool report) {  // without the weight
-  TileSeq t;
+// (of a prefix every token sees the same keys)
+__device__ __forceinline__ long long full_weight(const PrefixParams& p, const PrefixSeq& s, int m) {
+  const long long n = m;
+  const long long grows = s.part == kShared ? 0 : 2ll * p.tile_tokens * n * (n + 1) / 2;
+  return 8 * (n * (s.ctx - s.first_page * kPage + kUnitKeys) + grows);
+}
+
+__device__ __forceinline__ long long last_weight(const PrefixParams& p, const PrefixSeq& s, int units) {
+  const bool half = s.n - (units - 1) * 2 * p.tile_tokens <= p.tile_tokens;
+  const int end = s.part == kShared ? s.ctx : s.ctx + s.n;
+  return static_cast<long long>(half ? kHalfUnit : 8) * (end - s.first_page * kPage + kUnitKeys);
+}
+
+template <class P>
+__device__ __forceinline__ TileSeq<P> tile_units(const P& p, int b, bool report) {  // without the weight
+  TileSeq<P> t;
   t.s = load_seq(p, b, report);
   t.units = 0;
   t.weight = 0;
@@ -171,15 +307,17 @@ __device__ __forceinline__ TileSeq tile_units(const Params& p, int b, bool repor
   return t;
 }
 
-__device__ __forceinline__ TileSeq tile_seq(const Params& p, int b, bool report) {
-  TileSeq t = tile_units(p, b, report);
+template <class P>
+__device__ __forceinline__ TileSeq<P> tile_seq(const P& p, int b, bool report) {
+  TileSeq<P> t = tile_units(p, b, report);
   if (t.units > 0) t.weight = full_weight(p, t.s, t.units - 1) + last_weight(p, t.s, t.units);
   return t;
 }
 
 // A sequence's pages in the row kernel (of one KV head).
+template <class P>
 struct RowSeq {
-  Seq s;
+  typename P::Entry s;
   Keys keys;
   int pages;
 };
@@ -188,8 +326,9 @@ struct RowSeq {
 // sequence v >> shift, its rows from first_row on.
 __device__ __forceinline__ int first_row(int v, int shift) { return (v & shift) * kRowUnit; }
 
-__device__ __forceinline__ RowSeq row_seq(const Params& p, int v, int shift, bool report) {
-  RowSeq r;
+template <class P>
+__device__ __forceinline__ RowSeq<P> row_seq(const P& p, int v, int shift, bool report) {
+  RowSeq<P> r;
   const int r0 = first_row(v, shift);
   r.s = load_seq(p, v >> shift, report && r0 == 0);
   r.pages = 0;
@@ -212,7 +351,8 @@ struct Work {
   int units;
 };
 
-__device__ __forceinline__ Work work_of(const Params& p, const TileSeq& t, long long pages) {
+template <class P>
+__device__ __forceinline__ Work work_of(const P& p, const TileSeq<P>& t, long long pages) {
   Work w{t.weight, 0, 1ll << 60, pages, t.units};
   if (t.units > 0) w.heaviest = w.lightest = last_weight(p, t.s, t.units);
   if (t.units > 1) {
@@ -313,8 +453,9 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 
 // ------------------------------------------------- host side of the parts
 
-struct Launch {
-  Params p;
+template <class P>
+struct LaunchOf {
+  P p;
   const void* k_cache;
   const void* v_cache;
   int head_dim;
@@ -322,12 +463,17 @@ struct Launch {
   cudaStream_t stream;
 };
 
+using Launch = LaunchOf<Params>;
+using PrefixLaunch = LaunchOf<PrefixParams>;
+
 // Tensor map of the pool, 16 rows x 64 columns of one (page, head) per box, or
 // with `whole` every 64-column half of its rows, one after another.
-bool encode_pool(CUtensorMap* map, const void* base, const Launch& l, bool whole);
+bool encode_pool(CUtensorMap* map, const void* base, const Params& p, int head_dim, bool fp16, bool whole);
 
 sv_status launch_rows(const Launch& l);
+sv_status launch_rows(const PrefixLaunch& l);
 sv_status launch_tiles(const Launch& l);
+sv_status launch_tiles(const PrefixLaunch& l);
 
 }  // namespace chunk
 }  // namespace sv

@@ -54,21 +54,23 @@ __device__ __forceinline__ int min_pages(long long total) { return total <= 512 
 
 // Walks the units of a range in order: sequence b, KV head kh (or, in the modes
 // without ranges, every step-th unit).
+template <class P>
 struct RowCursor {
   long long pos;  // first page position of the current unit
   int b, kh;
   int unit, step;
-  RowSeq seq;
+  RowSeq<P> seq;
 };
 
+template <class P>
 struct RowPiece {
   int b, kh, j0, j1;  // pages [j0, j1) of the unit's seq.pages
   long long pos;
-  RowSeq seq;
+  RowSeq<P> seq;
 };
 
-template <int SHIFT, bool CLUSTER>
-__device__ __forceinline__ bool next_piece(const Params& p, RowCursor& c, long long lo, long long hi, RowPiece& out) {
+template <int SHIFT, bool CLUSTER, class P>
+__device__ __forceinline__ bool next_piece(const P& p, RowCursor<P>& c, long long lo, long long hi, RowPiece<P>& out) {
   if (p.row_mode != kRowRanges) {
     for (; c.unit < (p.batch << SHIFT) * p.num_kv_heads;) {
       out.b = c.unit / p.num_kv_heads;
@@ -137,10 +139,10 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
   }
 }
 
-template <int D, bool FP16, int SHIFT, bool CLUSTER>
+template <int D, bool FP16, int SHIFT, bool CLUSTER, class P>
 __global__ void __launch_bounds__(kRowWarps * 32, 1)
     chunk_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                      const __grid_constant__ Params p) {
+                      const __grid_constant__ P p) {
   using C = RowCfg<D>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[kRowWarps * C::kStages];
@@ -170,7 +172,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
   // ---- this worker's range of the page list
   // consecutive ranges go to different CTAs, so few workers spread over the SMs
   int worker = warp * gridDim.x + blockIdx.x;
-  RowCursor start;
+  RowCursor<P> start;
   long long lo = 0, hi = 1, total = 0;
   int workers = p.row_workers;
   Share share{};
@@ -178,7 +180,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
   start.step = p.row_mode == kRowCta ? gridDim.x : p.row_workers;
   if constexpr (CLUSTER) start.unit = blockIdx.x / p.row_cluster;  // (and no other: the grid is no smaller)
   if (p.row_mode == kRowRanges) {
-    RowSeq mine;  // of sequence `lane`: the only round when there are at most 32
+    RowSeq<P> mine;  // of sequence `lane`: the only round when there are at most 32
     int blocks = gridDim.x;
     const int batch = p.batch << SHIFT;
     if (side_by_side(p)) {
@@ -186,8 +188,8 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
       sum.lightest = 1ll << 60;
       for (int b0 = 0; b0 < batch; b0 += 32) {
         const int b = b0 + lane;
-        TileSeq t{};
-        RowSeq r{};
+        TileSeq<P> t{};
+        RowSeq<P> r{};
         if (b < batch) {
           r = row_seq(p, b, SHIFT, worker == 0);
           if (first_row(b, SHIFT) == 0) t = tile_seq(p, b >> SHIFT, false);
@@ -206,7 +208,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
       mine.pages = 0;
       for (int b0 = 0; b0 < batch; b0 += 32) {
         const int b = b0 + lane;
-        RowSeq r;
+        RowSeq<P> r;
         r.pages = 0;
         if (b < batch) r = row_seq(p, b, SHIFT, worker == 0);
         if (b0 == 0) mine = r;
@@ -248,9 +250,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
         const int l = __ffs(hit) - 1;
         bsel = b0 + l;
         base += __shfl_sync(0xffffffffu, incl - w, l);
-        start.seq.s.n0 = __shfl_sync(0xffffffffu, mine.s.n0, l);
-        start.seq.s.n = __shfl_sync(0xffffffffu, mine.s.n, l);
-        start.seq.s.ctx = __shfl_sync(0xffffffffu, mine.s.ctx, l);
+        start.seq.s = from_lane(mine.s, l);
         start.seq.keys.sink_pages = __shfl_sync(0xffffffffu, mine.keys.sink_pages, l);
         start.seq.keys.first_page = __shfl_sync(0xffffffffu, mine.keys.first_page, l);
         start.seq.keys.end = __shfl_sync(0xffffffffu, mine.keys.end, l);
@@ -268,8 +268,8 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
     }
   }
   // ---- the loads, a ring ahead of the products, running on across pieces
-  RowCursor load_cur = start;
-  RowPiece lp;
+  RowCursor<P> load_cur = start;
+  RowPiece<P> lp;
   lp.j0 = lp.j1 = 0;
   int load_j = 0, id_base = 0, ids = 0, issued = 0;
   bool more = hi > lo;
@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
       const int j = load_j + lane;
       if (j < lp.j1) {
         const int page = j < k.sink_pages ? j : k.first_page + (j - k.sink_pages);
-        ids = p.block_table[static_cast<size_t>(lp.b >> SHIFT) * p.max_pages_per_seq + page];
+        ids = p.block_table[static_cast<size_t>(table_row(lp.seq.s, lp.b >> SHIFT)) * p.max_pages_per_seq + page];
         if (ids < 0 || ids >= p.num_pages) {
           report_error(p.err, SV_DEVERR_BAD_PAGE);
           ids = p.num_pages;  // outside the pool: the box arrives as zeros
@@ -315,13 +315,13 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
 
   const int g = lane >> 2, tq = lane & 3;  // fragment rows g, g + 8; columns 2 tq, 2 tq + 1
   const int mi = lane >> 3, mr = lane & 7;
-  RowCursor cur = start;
-  RowPiece pc;
+  RowCursor<P> cur = start;
+  RowPiece<P> pc;
   if constexpr (CLUSTER) pc.seq.pages = 0;
   int done = 0;
   bool ok = true;
   while ((ok || p.row_mode == kRowCta) && hi > lo && next_piece<SHIFT, CLUSTER>(p, cur, lo, hi, pc)) {
-    const Seq& s = pc.seq.s;
+    const typename P::Entry& s = pc.seq.s;
     const Keys& keys = pc.seq.keys;
     const int r0 = first_row(pc.b, SHIFT), rows = SHIFT ? min(s.n * p.group - r0, kRowUnit) : s.n * p.group;
     int tok[2];
@@ -457,6 +457,17 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
       if (r >= rows) continue;
       const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
       const float lse2 = l[i] > 0.f ? m[i] - kLift<FP16> + log2f(l[i]) : -INFINITY;
+      if constexpr (P::kPrefix) {
+        if (whole && s.part != kAlone) {
+          const int head = pc.kh * p.group + (r0 + r - tok[i] * p.group);
+          const size_t at = (static_cast<size_t>(s.part) * p.rows + s.at + tok[i]) * p.num_q_heads + head;
+          float2* dst = reinterpret_cast<float2*>(p.whole_o + at * D) + tq;
+#pragma unroll
+          for (int nb = 0; nb < D / 8; ++nb) dst[nb * 4] = make_float2(o[nb][2 * i] * inv, o[nb][2 * i + 1] * inv);
+          if (tq == 0) p.whole_lse[at] = lse2;
+          continue;
+        }
+      }
       if (whole) {
         const int head = pc.kh * p.group + (r0 + r - tok[i] * p.group);
         const long long token = s.n0 + tok[i];
@@ -584,8 +595,8 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
   griddep_launch_dependents();
 }
 
-template <int D, bool FP16, int SHIFT, bool CLUSTER>
-static sv_status launch(const Launch& l) {
+template <int D, bool FP16, int SHIFT, bool CLUSTER, class P>
+static sv_status launch(const LaunchOf<P>& l) {
   static std::mutex mu;
   static bool done[64] = {false};
   int dev = 0;
@@ -593,14 +604,15 @@ static sv_status launch(const Launch& l) {
   {
     std::lock_guard<std::mutex> lock(mu);
     if (dev >= 64 || !done[dev]) {
-      if (cudaFuncSetAttribute(chunk_rows_kernel<D, FP16, SHIFT, CLUSTER>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      if (cudaFuncSetAttribute(chunk_rows_kernel<D, FP16, SHIFT, CLUSTER, P>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                RowCfg<D>::kSmemBytes) != cudaSuccess)
         return SV_ERR_CUDA;
       if (dev < 64) done[dev] = true;
     }
   }
   CUtensorMap tm_k, tm_v;
-  if (!encode_pool(&tm_k, l.k_cache, l, true) || !encode_pool(&tm_v, l.v_cache, l, true)) return SV_ERR_CUDA;
+  if (!encode_pool(&tm_k, l.k_cache, l.p, D, FP16, true) || !encode_pool(&tm_v, l.v_cache, l.p, D, FP16, true))
+    return SV_ERR_CUDA;
   cudaLaunchConfig_t cfg = cudaLaunchConfig_t{};
   const int units = l.p.batch * l.p.num_kv_heads;  // (a cluster's grid: one unit each)
   cfg.gridDim = dim3(static_cast<unsigned>(CLUSTER ? units * l.p.row_cluster : l.p.row_workers / kRowWarps), 1, 1);
@@ -614,20 +626,26 @@ static sv_status launch(const Launch& l) {
   attr[1].val.clusterDim = {static_cast<unsigned>(CLUSTER ? l.p.row_cluster : 1), 1, 1};
   cfg.attrs = attr;
   cfg.numAttrs = CLUSTER ? 2 : 1;
-  if (cudaLaunchKernelEx(&cfg, chunk_rows_kernel<D, FP16, SHIFT, CLUSTER>, tm_k, tm_v, l.p) != cudaSuccess) return SV_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, chunk_rows_kernel<D, FP16, SHIFT, CLUSTER, P>, tm_k, tm_v, l.p) != cudaSuccess) return SV_ERR_CUDA;
   return SV_OK;
 }
 
-template <int D, bool FP16>
-static sv_status launch(const Launch& l) {
-  if (l.p.row_cluster > 1) return launch<D, FP16, 0, true>(l);
+template <int D, bool FP16, class P>
+static sv_status launch(const LaunchOf<P>& l) {
+  if constexpr (!P::kPrefix) {
+    if (l.p.row_cluster > 1) return launch<D, FP16, 0, true>(l);
+  }
   return l.p.row_shift ? launch<D, FP16, 1, false>(l) : launch<D, FP16, 0, false>(l);
 }
 
-sv_status launch_rows(const Launch& l) {
+template <class P>
+static sv_status launch_any(const LaunchOf<P>& l) {
   if (l.head_dim == 128) return l.fp16 ? launch<128, true>(l) : launch<128, false>(l);
   return l.fp16 ? launch<64, true>(l) : launch<64, false>(l);
 }
+
+sv_status launch_rows(const Launch& l) { return launch_any(l); }
+sv_status launch_rows(const PrefixLaunch& l) { return launch_any(l); }
 
 }  // namespace chunk
 }  // namespace sv

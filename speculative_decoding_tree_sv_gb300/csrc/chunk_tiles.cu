@@ -33,6 +33,7 @@
 #include <math.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "chunk_attention.cuh"
 
@@ -75,7 +76,23 @@ struct Piece {
   int n0, n, ctx;       // the sequence
   int sink_pages, sink_tiles, first_page, end;
 };
-static_assert(sizeof(Piece) * kPieceRing <= 512, "piece ring");
+struct PrefixPiece : Piece {
+  int row, part, at;
+};
+static_assert(sizeof(PrefixPiece) * kPieceRing <= 512, "piece ring");
+template <class P>
+using PieceOf = std::conditional_t<P::kPrefix, PrefixPiece, Piece>;
+
+// A piece's row of the block table, and one past its sequence's (or prefix's) last position.
+__device__ __forceinline__ int table_row(const Piece& pc) { return pc.b; }
+__device__ __forceinline__ int table_row(const PrefixPiece& pc) { return pc.row; }
+__device__ __forceinline__ int all_keys(const Piece& pc) { return pc.ctx + pc.n; }
+__device__ __forceinline__ int all_keys(const PrefixPiece& pc) { return pc.part == kShared ? pc.ctx : pc.ctx + pc.n; }
+// The last position that token `tok` sees.
+__device__ __forceinline__ int last_seen(const Piece& pc, int tok) { return pc.ctx + tok; }
+__device__ __forceinline__ int last_seen(const PrefixPiece& pc, int tok) {
+  return pc.part == kShared ? pc.ctx - 1 : pc.ctx + tok;
+}
 
 // Logical page `i` (0..7) of tile j of a piece; -1 if no row sees it.
 __device__ __forceinline__ int tile_page(const Piece& pc, int j, int i) {
@@ -88,8 +105,9 @@ __device__ __forceinline__ int tile_page(const Piece& pc, int j, int i) {
 }
 
 // The unit of row group m of a sequence, whole.
-__device__ __forceinline__ Piece unit_piece(const Params& p, const Seq& s, int b, int kh, int m) {
-  Piece pc;
+template <class P>
+__device__ __forceinline__ PieceOf<P> unit_piece(const P& p, const typename P::Entry& s, int b, int kh, int m) {
+  PieceOf<P> pc;
   pc.b = b;
   pc.kh = kh;
   pc.tok0 = m * 2 * p.tile_tokens;
@@ -105,7 +123,19 @@ __device__ __forceinline__ Piece unit_piece(const Params& p, const Seq& s, int b
   pc.je = pc.sink_tiles + ((keys.end + kPage - 1) / kPage - keys.first_page + kPagesPerTile - 1) / kPagesPerTile;
   pc.nt = s.n - pc.tok0 > p.tile_tokens ? 2 : 1;
   pc.slot = -1;
+  if constexpr (P::kPrefix) {
+    pc.row = s.row;
+    pc.part = s.part;
+    pc.at = s.at;
+  }
   return pc;
+}
+
+// Where the rows of a unit of a shared group lie: which CTAs hold pieces of it.
+__device__ __forceinline__ void note_unit(const Params&, const Piece&, int, int) {}
+__device__ __forceinline__ void note_unit(const PrefixParams& p, const PrefixPiece& pc, int first, int last) {
+  if (pc.part != kAlone && (threadIdx.x & 31) == 0)
+    p.tile_rec[(static_cast<size_t>(pc.part) * p.rows + pc.at + pc.tok0) * p.num_kv_heads + pc.kh] = make_int2(first, last);
 }
 
 // Whole units: the first by the CTA's number, the others by ticket, in an order
@@ -114,8 +144,8 @@ __device__ __forceinline__ Piece unit_piece(const Params& p, const Seq& s, int b
 // sequence of the lane; `near_end` waits until the K tiles of a piece are all
 // requested, a few tiles before its end (a prompt of 2048: 46.9 us when the next
 // unit is taken as soon as the last is begun).
-template <class Publish, class NearEnd>
-__device__ void deal_units(const Params& p, int cta, int ctas, int all, TileSeq mine, Publish&& publish,
+template <class P, class Publish, class NearEnd>
+__device__ void deal_units(const P& p, int cta, int ctas, int all, TileSeq<P> mine, Publish&& publish,
                            NearEnd&& near_end) {
   const int lane = threadIdx.x & 31;
   int b0 = 0, level = 0, base = 0;  // units before the level's in that order
@@ -133,7 +163,7 @@ __device__ void deal_units(const Params& p, int cta, int ctas, int all, TileSeq 
       if (has == 0) {
         b0 += 32;
         level = -1;
-        mine = TileSeq{};
+        mine = TileSeq<P>{};
         if (b0 + lane < p.batch) mine = tile_seq(p, b0 + lane, false);
       }
       ++level;
@@ -143,12 +173,11 @@ __device__ void deal_units(const Params& p, int cta, int ctas, int all, TileSeq 
     const int nth = (i - base) / p.num_kv_heads;
     const bool it = mine.units > level && __popc(has & ((1u << lane) - 1u)) == nth;
     const int l = __ffs(__ballot_sync(0xffffffffu, it)) - 1;
-    Seq s;
-    s.n0 = __shfl_sync(0xffffffffu, mine.s.n0, l);
-    s.n = __shfl_sync(0xffffffffu, mine.s.n, l);
-    s.ctx = __shfl_sync(0xffffffffu, mine.s.ctx, l);
+    const typename P::Entry s = from_lane(mine.s, l);
     const int m = __shfl_sync(0xffffffffu, mine.units, l) - 1 - level;
-    if (!publish(unit_piece(p, s, b0 + l, i - base - nth * p.num_kv_heads, m))) break;
+    const PieceOf<P> pc = unit_piece(p, s, b0 + l, i - base - nth * p.num_kv_heads, m);
+    note_unit(p, pc, -1, -1);
+    if (!publish(pc)) break;
   }
   // the last CTA to end leaves the counters as they were
   if (all > ctas && cta < ctas && lane == 0 && atomicAdd(p.tickets + 1, 1) == ctas - 1) {
@@ -159,17 +188,17 @@ __device__ void deal_units(const Params& p, int cta, int ctas, int all, TileSeq 
 
 // The pieces of the range [lo, hi) of the weights of all units; `record` becomes
 // the cut unit that starts in it.  False when the dealer gave up.
-template <class Publish>
-__device__ __forceinline__ bool deal_range(const Params& p, const Share& share, int cta, long long lo, long long hi,
-                                           TileSeq mine, int4& record, Publish&& publish) {
+template <class P, class Publish>
+__device__ __forceinline__ bool deal_range(const P& p, const Share& share, int cta, long long lo, long long hi,
+                                           TileSeq<P> mine, int4& record, Publish&& publish) {
   const int lane = threadIdx.x & 31;
   long long base = 0;
   int bsel = p.batch == 1 ? 0 : p.batch;
   for (int b0 = 0; b0 < p.batch && bsel == p.batch; b0 += 32) {
     const int b = b0 + lane;
-    TileSeq t = mine;
+    TileSeq<P> t = mine;
     if (b0 > 0 || p.batch > 32) {
-      t = TileSeq{};
+      t = TileSeq<P>{};
       if (b < p.batch) t = tile_seq(p, b, false);
     }
     const long long w = t.weight * p.num_kv_heads;
@@ -184,9 +213,7 @@ __device__ __forceinline__ bool deal_range(const Params& p, const Share& share, 
       const int l = __ffs(hit) - 1;
       bsel = b0 + l;
       base += __shfl_sync(0xffffffffu, incl - w, l);
-      mine.s.n0 = __shfl_sync(0xffffffffu, t.s.n0, l);
-      mine.s.n = __shfl_sync(0xffffffffu, t.s.n, l);
-      mine.s.ctx = __shfl_sync(0xffffffffu, t.s.ctx, l);
+      mine.s = from_lane(t.s, l);
       mine.units = __shfl_sync(0xffffffffu, t.units, l);
       mine.weight = __shfl_sync(0xffffffffu, t.weight, l);
     } else {
@@ -194,7 +221,7 @@ __device__ __forceinline__ bool deal_range(const Params& p, const Share& share, 
     }
   }
   // (all lanes walk the same units from here)
-  TileSeq t = mine;
+  TileSeq<P> t = mine;
   int b = bsel;
   int kh = 0;
   long long pos = base;
@@ -213,7 +240,7 @@ __device__ __forceinline__ bool deal_range(const Params& p, const Share& share, 
   while (pos < hi) {
     const long long w = m + 1 < t.units ? full_weight(p, t.s, m + 1) - full_weight(p, t.s, m)
                                         : last_weight(p, t.s, t.units);
-    Piece pc = unit_piece(p, t.s, b, kh, m);
+    PieceOf<P> pc = unit_piece(p, t.s, b, kh, m);
     const int tiles = pc.je;
     // (a boundary's tile in 32-bit floating point: the same from both sides)
     auto tile_at = [&](long long x) {
@@ -224,7 +251,12 @@ __device__ __forceinline__ bool deal_range(const Params& p, const Share& share, 
     const bool whole = pc.ja == 0 && pc.je == tiles;
     pc.slot = whole ? -1 : (pc.ja == 0 ? 1 : 0);
     if (pc.ja < pc.je) {
-      if (pc.slot == 1)
+      bool alone = true;  // (the rows of a shared group are merged by a rule of their own)
+      if constexpr (P::kPrefix) {
+        alone = pc.part == kAlone;
+        if (!alone && pc.ja == 0) note_unit(p, pc, whole ? -1 : cta, whole ? -1 : share.holder(pos + w - 1));
+      }
+      if (pc.slot == 1 && alone)
         record = make_int4(pc.n0 + pc.tok0, min(pc.n - pc.tok0, 2 * p.tile_tokens), kh, share.holder(pos + w - 1));
       if (!publish(pc)) return false;
     } else if (pc.ja > 0) {
@@ -249,18 +281,18 @@ __device__ __forceinline__ bool deal_range(const Params& p, const Share& share, 
 }
 
 // Deals the CTA's pieces to the other warps (one warp, the ring's producer).
-template <class Publish, class NearEnd>
-__device__ void deal_pieces(const Params& p, int cta, Publish&& publish, NearEnd&& near_end) {
+template <class P, class Publish, class NearEnd>
+__device__ void deal_pieces(const P& p, int cta, Publish&& publish, NearEnd&& near_end) {
   const int lane = threadIdx.x & 31;
   const bool beside = side_by_side(p);
   const bool report = cta == 0 && p.row_workers == 0;
   int avail = p.tile_ctas, all = 0;
-  TileSeq mine{};  // of sequence `lane`: the only round when there are at most 32
+  TileSeq<P> mine{};  // of sequence `lane`: the only round when there are at most 32
   int4 record = make_int4(0, 0, 0, 0);  // the cut unit that starts here
   bool whole = p.whole_tiles && !beside;
   if (whole) {  // (no weights: less code to fetch)
     for (int b0 = 0; b0 < p.batch; b0 += 32) {
-      TileSeq t{};
+      TileSeq<P> t{};
       if (b0 + lane < p.batch) t = tile_units(p, b0 + lane, report);
       if (b0 == 0) mine = t;
       all += __reduce_add_sync(0xffffffffu, t.units);
@@ -276,7 +308,7 @@ __device__ void deal_pieces(const Params& p, int cta, Publish&& publish, NearEnd
     } else {
       for (int b0 = 0; b0 < p.batch; b0 += 32) {
         const int b = b0 + lane;
-        TileSeq t{};
+        TileSeq<P> t{};
         long long pages = 0;
         if (b < p.batch) {
           t = tile_seq(p, b, report);
@@ -316,7 +348,7 @@ __device__ void deal_pieces(const Params& p, int cta, Publish&& publish, NearEnd
   }
   if (whole) deal_units(p, cta, avail, all, mine, publish, near_end);
   if (lane == 0) p.tile_units[cta] = record;
-  Piece end;
+  PieceOf<P> end{};
   end.je = 0;
   publish(end);
 }
@@ -327,11 +359,12 @@ __device__ __forceinline__ uint32_t column_bits(int a, int b, int w) {
   return hi > lo ? (0xffffffffu >> (32 - (hi - lo))) << lo : 0u;
 }
 
-template <int D, bool FP16>
+template <int D, bool FP16, class P>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Params p) {
+                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ P p) {
   using C = Cfg<D>;
+  using Piece = PieceOf<P>;
   constexpr int KS = C::kKStages, VS = C::kVStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -455,15 +488,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Piece pc = pieces[k % kPieceRing];
         piece_done(k);
         if (pc.je == 0) break;
-        const int last_page = (pc.ctx + pc.n - 1) / kPage;
-        const int ragged = (pc.ctx + pc.n) % kPage;
+        const int last_page = (all_keys(pc) - 1) / kPage;
+        const int ragged = all_keys(pc) % kPage;
         auto page_of = [&](int j, int* row) {
           int phys = p.num_pages;  // outside the pool: the box arrives as zeros
           *row = 0;
           if (lane < kPagesPerTile) {
             const int lp = tile_page(pc, j, lane);
             if (lp >= 0) {
-              phys = p.block_table[static_cast<size_t>(pc.b) * p.max_pages_per_seq + lp];
+              phys = p.block_table[static_cast<size_t>(table_row(pc)) * p.max_pages_per_seq + lp];
               if (phys < 0 || phys >= p.num_pages) {
                 report_error(p.err, SV_DEVERR_BAD_PAGE);
                 phys = p.num_pages;
@@ -655,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tok_r = tok_a + r_tok;
       const bool row_exists = r < p.tile_tokens * G && tok_r < pc.n;
       const int tok = min(tok_r, tok_b);
-      const int hi = pc.ctx + tok;  // last visible position
+      const int hi = last_seen(pc, tok);
       const int lo = p.window > 0 ? max(0, hi - p.window + 1) : 0;
       float m_run = -INFINITY;
       float l_run = 0.f;
@@ -664,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int j = pc.ja + it;
         const bool sink_tile = j < pc.sink_tiles;
         const int base = sink_tile ? j * kBlockN : pc.first_page * kPage + (j - pc.sink_tiles) * kBlockN;
-        const bool masked = !rehearsal && (sink_tile || base + kBlockN > pc.ctx + tok_a + 1 ||
+        const bool masked = !rehearsal && (sink_tile || base + kBlockN > last_seen(pc, tok_a) + 1 ||
                             (p.window > 0 && base <= pc.ctx + tok_b - p.window));
         if (!rehearsal && !wait_all(s_full + t, (tiles_done + it) & 1)) { ok = false; break; }
         tc_fence_after();
@@ -676,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // last page ends at its column 15, `shift` columns of zeros before it.
           int whole = sink_tile ? pc.sink_pages * kPage - base : kBlockN;
           int shift = 0, page_col = kBlockN;
-          const int seq_end = pc.ctx + pc.n;
+          const int seq_end = all_keys(pc);
           if (!sink_tile && seq_end % kPage != 0) {
             const int c = seq_end / kPage * kPage - base;
             if (c < kBlockN) {
@@ -784,7 +817,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const float inv_l = (l_run > 0.f) ? 1.f / l_run : 0.f;
       const float lse2 = (l_run > 0.f) ? m_run - kLift<FP16> + log2f(l_run) : -INFINITY;
-      if (pc.slot < 0) {
+      bool to_out = pc.slot < 0;
+      if constexpr (P::kPrefix) {
+        if (pc.slot < 0 && pc.part != kAlone) {
+          to_out = false;
+          const size_t at = (static_cast<size_t>(pc.part) * p.rows + pc.at + tok) * p.num_q_heads + pc.kh * G + r_head;
+          float4* dst = reinterpret_cast<float4*>(p.whole_o + at * D);
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(lane_base + col_o + c * 32, o);
+            tmem_ld_wait();
+            if (row_exists) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                dst[c * 8 + e] = make_float4(__uint_as_float(o[4 * e]) * inv_l, __uint_as_float(o[4 * e + 1]) * inv_l,
+                                             __uint_as_float(o[4 * e + 2]) * inv_l, __uint_as_float(o[4 * e + 3]) * inv_l);
+            }
+          }
+          if (row_exists) p.whole_lse[at] = lse2;
+        }
+      }
+      if (to_out) {
         const int head = pc.kh * G + r_head;
         const long long token = pc.n0 + tok;
         const unsigned long long my_row = reinterpret_cast<unsigned long long>(
@@ -828,7 +882,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (row_exists && p.lse != nullptr) p.lse[token * p.num_q_heads + head] = lse2 * kLn2;
-      } else {
+      } else if (pc.slot >= 0) {
         // partial rows, four columns of 128 rows together so that a warp's
         // 16-byte stores are contiguous: [cta][slot][M tile][D / 4][128] float4
         const size_t part = (static_cast<size_t>(cta) * 2 + pc.slot) * 2 + t;
@@ -863,8 +917,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D, bool FP16>
-static sv_status launch(const Launch& l) {
+template <int D, bool FP16, class P>
+static sv_status launch(const LaunchOf<P>& l) {
   static std::mutex mu;
   static bool done[64] = {false};
   int dev = 0;
@@ -872,14 +926,15 @@ static sv_status launch(const Launch& l) {
   {
     std::lock_guard<std::mutex> lock(mu);
     if (dev >= 64 || !done[dev]) {
-      if (cudaFuncSetAttribute(chunk_tiles_kernel<D, FP16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      if (cudaFuncSetAttribute(chunk_tiles_kernel<D, FP16, P>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                Cfg<D>::kSmemBytes) != cudaSuccess)
         return SV_ERR_CUDA;
       if (dev < 64) done[dev] = true;
     }
   }
   CUtensorMap tm_q, tm_k, tm_v;
-  if (!encode_pool(&tm_k, l.k_cache, l, false) || !encode_pool(&tm_v, l.v_cache, l, false)) return SV_ERR_CUDA;
+  if (!encode_pool(&tm_k, l.k_cache, l.p, D, FP16, false) || !encode_pool(&tm_v, l.v_cache, l.p, D, FP16, false))
+    return SV_ERR_CUDA;
   {
     const cuuint64_t dims[3] = {D, static_cast<cuuint64_t>(l.p.num_q_heads), static_cast<cuuint64_t>(l.p.total_tokens)};
     const cuuint64_t strides[2] = {D * 2, static_cast<cuuint64_t>(l.p.q_stride) * 2};
@@ -899,15 +954,19 @@ static sv_status launch(const Launch& l) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, chunk_tiles_kernel<D, FP16>, tm_q, tm_k, tm_v, l.p) != cudaSuccess)
+  if (cudaLaunchKernelEx(&cfg, chunk_tiles_kernel<D, FP16, P>, tm_q, tm_k, tm_v, l.p) != cudaSuccess)
     return SV_ERR_CUDA;
   return SV_OK;
 }
 
-sv_status launch_tiles(const Launch& l) {
+template <class P>
+static sv_status launch_any(const LaunchOf<P>& l) {
   if (l.head_dim == 128) return l.fp16 ? launch<128, true>(l) : launch<128, false>(l);
   return l.fp16 ? launch<64, true>(l) : launch<64, false>(l);
 }
+
+sv_status launch_tiles(const Launch& l) { return launch_any(l); }
+sv_status launch_tiles(const PrefixLaunch& l) { return launch_any(l); }
 
 }  // namespace chunk
 }  // namespace sv
