@@ -8,19 +8,27 @@
 // sum passes u times the sum.  A token is a comparison of sums of up to 2^18 terms
 // with borders that may lie 2^-20 apart, so weights are 64-bit integers in units
 // of 2^-45: sums are exact, the same in any order, and only the weights' own error
-// (2^-36 of the largest, see weight_of) can move a border.
+// (2^-36 of the largest, see weights4) can move a border.
 //
 // A cluster of CTAs takes a row, each holds its slice in shared memory as fp32; all
-// further passes read that.  The threshold of a top-k or top-p is found without a
-// sort of the row: a histogram of 2048 bins over the distance from the maximum (1/32
-// of a power of two each) in numbers and weights, summed over the cluster, finds
-// the bin of the threshold; its entries (a few hundred of a usual row; where there
-// are more, the bin is split by the bits of the logits and then of the indices)
-// are sorted in every CTA alike.  A thread holds a run of consecutive entries, so
-// that one scan of the threads' sums finds the token's run.
+// further passes read that.  No filter sorts the row:
+//   * a top-k of up to kFew: the entries that every thread saw largest on loading its
+//     part are 512 per CTA; with b the least over the CTAs of their (k / CTAs)-th
+//     largest, at least k entries are >= b, and seldom many more.  Those are listed
+//     and sorted by the first CTA, which has the kept ones whole and draws from them;
+//   * otherwise a histogram of 2048 bins over the distance from the maximum (1/32 of a
+//     power of two each) in numbers and, for top-p, weights, summed over the cluster,
+//     finds the threshold's bin; the entries down to it, or where they are many the
+//     bin's alone, are listed and sorted (a bin of more than kMost is first split by
+//     the bits of the logits and then of the indices).  Entries below a V-th of 1 -
+//     top_p together weigh less than what top-p leaves out, so they stay out of the
+//     bins;
+//   * where the kept entries are many, or for min-p alone, a thread sums a run of
+//     consecutive entries, so that one scan of the threads' sums finds the run of the
+//     token.
 //
 // Bound by HBM for large batches in principle (the logits are read once), in fact
-// by the passes over shared memory and the weights' arithmetic.
+// by the weights' arithmetic and the passes over shared memory.
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -40,9 +48,13 @@ constexpr int kBins = 2048;
 constexpr int kBinBits = 11;
 constexpr int kBinsPerOctave = 32;
 constexpr int kMost = 2048;        // entries that are sorted
+constexpr int kWhole = 512;        // kept ones that are listed whole: more are quicker summed in place
+constexpr int kFew = 128;
 constexpr int kIndexBits = 18;
 constexpr int kUnit = 45;          // weights in units of 2^-45: sums of 2^18 stay below 2^63
 constexpr uint32_t kIndexMask = (1u << kIndexBits) - 1;
+
+using u64 = unsigned long long;
 
 struct Params {
   const void* logits;
@@ -62,7 +74,7 @@ struct Params {
 
 // 2^(j/32) in units of 2^-45, and as the sum of two floats.
 struct Power {
-  unsigned long long fixed;
+  u64 fixed;
   float hi, lo;
 };
 __device__ const Power kPowers[32] = {
@@ -116,18 +128,11 @@ __device__ __forceinline__ float2 exponent_of(const Row& r, float l) {
   return make_float2(yh, yl);
 }
 
-// A weight in units of 2^-45.  Down to 2^-14 by 2^(j/32) from the table and 2^r - 1,
-// |r| <= 1/64, from its series, each product with its rounding error beside it:
-// 2^-37 of the weight.  Below, where a weight is worth no more than 2^-14 of the
-// sum, by the hardware's power (2^-22 of it).
-__device__ __forceinline__ unsigned long long weight_of(const Row& row, float l, const Power* powers) {
+// A weight of 2^-16 or more in units of 2^-45: 2^(j/32) from the table and 2^r - 1, |r|
+// <= 1/64, from its series, each product with its rounding error beside it: off by
+// 2^-37 of the weight.
+__device__ __forceinline__ u64 weight_near(const Row& row, float l, const Power* powers) {
   const float2 y = exponent_of(row, l);
-  if (!(y.x > -47.f)) return 0;
-  if (y.x < -14.f) {
-    const float k = rintf(y.x);
-    const float v = ex2((y.x - k) + y.y);
-    return __float2uint_rn(v * __uint_as_float(static_cast<uint32_t>(127 + kUnit + static_cast<int>(k)) << 23));
-  }
   const float j32 = rintf(y.x * 32.f);
   const float r0 = fmaf(j32, -1.f / 32.f, y.x);
   const int j = static_cast<int>(j32);
@@ -151,11 +156,65 @@ __device__ __forceinline__ unsigned long long weight_of(const Row& row, float l,
   const int i2 = __float2int_rn(rest * 0x1p43f);
   const long long w = static_cast<long long>(t.fixed) + (static_cast<long long>(i1) << 21) + (static_cast<long long>(i2) << 2);
   const int s = -(j >> 5);
-  return s == 0 ? w : static_cast<unsigned long long>(w + (1ll << (s - 1))) >> s;
+  return s == 0 ? w : static_cast<u64>(w + (1ll << (s - 1))) >> s;
+}
+
+// The sum of far weights, those below 2^-15: by a polynomial of degree six for 2^f (2^-26;
+// 2^-23 of a weight with its 24 bits and the exponent's rounding), two at a time, added
+// in fp32 over a thread's run.  A far weight is worth no more than 2^-15 of the row's
+// sum and a run's no more than 2^-9, so this is off by 2^-39 a weight and 2^-33 a run at
+// most.  What is to stay out, and any exponent below -100, is below `least_logit`.
+// EXACT: l - m is a float (16-bit logits: but for entries of 2^-16 of the maximum or
+// less, where the difference's own rounding is as small).
+struct Far {
+  uint64_t sum;
+  float least_logit;
+};
+template <bool EXACT>
+__device__ __forceinline__ void add_far(const Row& r, const float4& v, Far& far) {
+  constexpr float kMagic = 12582912.f;  // 1.5 * 2^23
+  auto two = [](float x) { return f2_pack(x, x); };
+  const uint64_t minus1 = two(-1.f), nm = two(-r.m), nc = two(-r.chi), chi = two(r.chi), clo = two(r.clo);
+  const float c = far.least_logit;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint64_t l = h ? f2_pack(fmaxf(v.z, c), fmaxf(v.w, c)) : f2_pack(fmaxf(v.x, c), fmaxf(v.y, c));
+    const uint64_t dh = f2_add(l, nm);
+    const uint64_t y = f2_mul(dh, nc);  // minus the exponent
+    uint64_t yl = f2_fma(dh, chi, y);
+    if constexpr (!EXACT) {
+      const uint64_t b = f2_fma(l, minus1, dh), t = f2_fma(b, minus1, dh);
+      yl = f2_fma(f2_add(f2_fma(t, minus1, l), f2_fma(b, minus1, nm)), chi, yl);
+    }
+    yl = f2_fma(dh, clo, yl);
+    const uint64_t k = f2_add(y, two(kMagic));
+    const uint64_t kf = f2_add(k, two(-kMagic));
+    const uint64_t f = f2_fma(f2_fma(kf, minus1, y), minus1, yl);
+    uint64_t e = f2_fma(f, two(0x1.444004p-13f), two(0x1.5f0896p-10f));
+    e = f2_fma(f, e, two(0x1.3b2a1cp-7f));
+    e = f2_fma(f, e, two(0x1.c6af6cp-5f));
+    e = f2_fma(f, e, two(0x1.ebfbe0p-3f));
+    e = f2_fma(f, e, two(0x1.62e430p-1f));
+    e = f2_fma(f, e, two(1.f));
+    // 2^-k: the exponent field from the whole number at the bottom of k
+    constexpr int kOne = (127 << 23) + static_cast<int>(0x4b400000u << 23);
+    const int p0 = kOne - (__float_as_int(f2_lo(k)) << 23), p1 = kOne - (__float_as_int(f2_hi(k)) << 23);
+    far.sum = f2_fma(e, f2_pack(__int_as_float(p0), __int_as_float(p1)), far.sum);
+  }
+}
+
+// One weight, far or near, in units of 2^-45.
+__device__ __noinline__ u64 weight_of(Row row, float l, const Power* powers) {
+  const float2 y = exponent_of(row, l);
+  if (!(y.x > -47.f)) return 0;
+  if (y.x > -15.f) return weight_near(row, l, powers);
+  Far far{0, -INFINITY};
+  add_far<false>(row, make_float4(l, -INFINITY, l, -INFINITY), far);  // (the others: NaN)
+  return __float2uint_rn(f2_lo(far.sum) * 0x1p44f);  // (twice: entries 0 and 2)
 }
 
 // A weight as fp32, however small.
-__device__ __forceinline__ float weight32(const Row& row, float l) {
+__device__ __noinline__ float weight32(Row row, float l) {
   const float2 y = exponent_of(row, l);
   if (!(y.x > -150.f)) return 0.f;
   const float k = rintf(y.x);
@@ -164,42 +223,114 @@ __device__ __forceinline__ float weight32(const Row& row, float l) {
   return v * __uint_as_float(static_cast<uint32_t>(127 + h) << 23) * __uint_as_float(static_cast<uint32_t>(127 + e - h) << 23);
 }
 
-// Logits as integers in the same order (no NaN; -0 has become 0), and the place in
+// Logits as integers in the same order (no NaN; -0 is 0), and the place in
 // the descending order: the logit above, the index below it, lower indices first.
 __device__ __forceinline__ uint32_t key_of(float l) {
-  const uint32_t u = __float_as_uint(l);
+  const uint32_t u = __float_as_uint(l + 0.f);
   return u ^ (static_cast<uint32_t>(static_cast<int>(u) >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float logit_of(uint32_t key) {
   return __uint_as_float((key & 0x80000000u) ? key ^ 0x80000000u : ~key);
 }
-__device__ __forceinline__ unsigned long long place_of(float l, int index) {
-  return (static_cast<unsigned long long>(key_of(l)) << kIndexBits) | (kIndexMask - static_cast<uint32_t>(index));
+__device__ __forceinline__ u64 place_of(float l, int index) {
+  return (static_cast<u64>(key_of(l)) << kIndexBits) | (kIndexMask - static_cast<uint32_t>(index));
 }
-__device__ __forceinline__ int index_of(unsigned long long place) {
+__device__ __forceinline__ int index_of(u64 place) {
   return static_cast<int>(kIndexMask - (static_cast<uint32_t>(place) & kIndexMask));
+}
+
+// x * f, f >= 0 a float, rounded down (UP: up): the 88 bits of x and f's 24-bit
+// significand, shifted.  (FP64 would do, but has two lanes per SM here: one product
+// by every thread of a CTA takes 250 cycles, a quotient thousands.)  Below 2^64.
+template <bool UP>
+__device__ __forceinline__ u64 times(u64 x, float f) {
+  const uint32_t bits = __float_as_uint(f);
+  const int e = bits >> 23;
+  const u64 m = (bits & 0x7fffffu) | (e ? 0x800000u : 0u);
+  const int shift = 150 - max(e, 1);  // f = m 2^-shift
+  const u64 lo = x * m, hi = __umul64hi(x, m);
+  u64 q, rest;
+  if (shift <= 0) {
+    return lo << -shift;
+  } else if (shift < 64) {
+    q = (hi << (64 - shift)) | (lo >> shift);
+    rest = lo << (64 - shift);
+  } else if (shift < 128) {
+    q = hi >> (shift - 64);
+    rest = lo | (shift > 64 ? hi << (128 - shift) : 0);
+  } else {
+    q = 0;
+    rest = lo | hi;
+  }
+  return q + (UP && rest != 0 ? 1 : 0);
 }
 
 // The bin of the threshold and what lies above it.
 struct Pick {
   int bin, in_bin;
-  unsigned long long above, above_mass;
+  u64 above, above_mass;
 };
+
+// The cluster's barrier: an mbarrier in every CTA that one thread of each CTA arrives
+// on, between __syncthreads.  (The hardware's wants every warp together, which the
+// compiler does not promise inline assembly behind loops that threads leave one by
+// one, and its wait has no limit.)  Where a wait gives up, `dead` is set and
+// sv_get_device_error tells.
+struct Barrier {
+  uint64_t arrived;
+  uint32_t phase;
+  int dead;
+};
+__device__ __noinline__ void cluster_arrive(Barrier* b, int cluster) {
+  __syncwarp();
+  __syncthreads();
+  if (threadIdx.x < cluster) {
+    uint32_t remote;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(&b->arrived)), "r"(threadIdx.x));
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
+  }
+}
+__device__ __noinline__ void cluster_wait(Barrier* b, int* err) {
+  if (threadIdx.x == 0) {
+    const uint32_t parity = b->phase++ & 1;
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t i = 1;; ++i) {
+      uint32_t ok;
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok)
+          : "r"(smem_u32(&b->arrived)), "r"(parity)
+          : "memory");
+      if (ok) break;
+      if ((i & 63u) == 0 && globaltimer_ns() - t0 > kWaitTimeoutNs) {
+        b->dead = 1;
+        report_error(err, SV_DEVERR_TIMEOUT);
+        break;
+      }
+    }
+  }
+  __syncwarp();
+  __syncthreads();
+}
 
 struct Shared {
   Power powers[32];
-  unsigned long long scan[kWarps], scan2[kWarps];
-  unsigned long long best[kWarps];
+  Barrier barrier;
+  u64 scan[kWarps];
+  u64 best[kWarps];
   // read by the other CTAs of the cluster
-  unsigned long long top;        // the slice's first place
-  unsigned long long count, mass;  // of the histogram's part
-  unsigned long long sum;        // kept weights
+  u64 top;              // the slice's first place
+  u64 count, mass, all;  // of the histogram's part; all weights of the slice
+  u64 sum;              // kept weights
+  u64 found;            // the threshold
   Pick pick;
+  uint32_t low;         // key that (top_k / CTAs) of the slice's entries reach
   int listed;
   // own
-  unsigned long long found, found_mass;
-  int run;
-  unsigned long long before;
+  int cut, run;
+  u64 before;
 };
 
 template <class T>
@@ -207,32 +338,51 @@ __device__ __forceinline__ T peer(const T* local, int rank) {
   return *cooperative_groups::this_cluster().map_shared_rank(const_cast<T*>(local), rank);
 }
 
-__device__ __forceinline__ void sync_cluster(int cluster) {
-  if (cluster > 1) cluster_sync_all();
-  else __syncthreads();
-}
-
-// Inclusive sums over the block's threads; the block's sum in `all`.
-__device__ __forceinline__ unsigned long long block_scan(unsigned long long v, unsigned long long* slots,
-                                                         unsigned long long& all) {
+// Sum over the block's threads up to and including this one.
+__device__ __noinline__ u64 block_scan(u64 v, u64* slots) {
+  __syncwarp();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const unsigned long long u = __shfl_up_sync(0xffffffffu, v, o);
+    const u64 u = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += u;
   }
   __syncthreads();  // the slots' last readers are done
   if (lane == 31) slots[warp] = v;
   __syncthreads();
-  unsigned long long before = 0;
-  all = 0;
+  u64 before = lane < warp ? slots[lane] : 0;  // (kWarps <= 32)
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    const unsigned long long s = slots[w];
-    if (w < warp) before += s;
-    all += s;
+  for (int o = kWarps / 2; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+  return __shfl_sync(0xffffffffu, before, 0) + v;
+}
+// ... over all of them, by the slots that block_scan left (before the next one).
+__device__ __forceinline__ u64 block_all(const u64* slots) {
+  u64 v = slots[threadIdx.x & (kWarps - 1)];
+#pragma unroll
+  for (int o = kWarps / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Descending order of a[0 .. size), a power of two.
+__device__ __noinline__ void sort(u64* a, int size) {
+  __syncwarp();
+  __syncthreads();
+  for (int len = 2; len <= size; len *= 2) {
+    for (int step = len / 2; step > 0; step /= 2) {
+      for (int i = threadIdx.x; i < size / 2; i += kThreads) {
+        const int x = 2 * i - (i & (step - 1)), y = x + step;
+        const u64 vx = a[x], vy = a[y];
+        if ((vx < vy) == ((x & len) == 0)) {
+          a[x] = vy;
+          a[y] = vx;
+        }
+      }
+      // (steps up to 32 stay within a warp's 64 entries)
+      if (step > 32 || (step == 1 && len >= 64)) __syncthreads();
+      else __syncwarp();
+    }
   }
-  return before + v;
+  __syncthreads();
 }
 
 template <int TYPE>
@@ -256,7 +406,7 @@ struct Element<SV_FP16> {
 __device__ __forceinline__ int chunk_at(int q) { return q + (q >> 3); }
 
 template <int TYPE>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ Params p) {
   using E = Element<TYPE>;
   using T = typename E::Type;
   constexpr int V = 16 / sizeof(T);  // entries of a 16-byte vector
@@ -267,8 +417,8 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
   uint32_t* bin_count = reinterpret_cast<uint32_t*>(smem + p.val_bytes);
   uint32_t* bin_lo = bin_count + kBins;
   uint32_t* bin_hi = bin_lo + kBins;
-  unsigned long long* sorted = reinterpret_cast<unsigned long long*>(bin_count);  // (when the bins are read)
-  unsigned long long* list = reinterpret_cast<unsigned long long*>(bin_hi + kBins);
+  u64* sorted = reinterpret_cast<u64*>(bin_count);  // (when the bins are read)
+  u64* list = reinterpret_cast<u64*>(bin_hi + kBins);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cs = p.cluster;
   const int rank = cs > 1 ? static_cast<int>(cluster_ctarank()) : 0;
@@ -277,16 +427,42 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
   const int chunks = (n + 3) / 4;
   const int per = (p.slice / 4 + kThreads - 1) / kThreads;  // chunks of a thread's run
   if (tid < 32) s.powers[tid] = kPowers[tid];
+  if (tid == 0) {
+    mbar_init(&s.barrier.arrived, cs);
+    s.barrier.phase = 0;
+    s.barrier.dead = 0;
+    fence_mbar_init();
+  }
+  // Every CTA has started and its barrier is ready when this one is waited for below.
+  __syncthreads();
+  if (cs > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  auto arrive = [&] {
+    if (cs > 1) cluster_arrive(&s.barrier, cs);
+  };
+  auto wait = [&] {
+    if (cs > 1) cluster_wait(&s.barrier, p.err);
+  };
+  // False where a CTA did not come: the others leave too.
+  auto meet = [&] {
+    arrive();
+    wait();
+    if (cs == 1) __syncthreads();
+    return cs == 1 || !s.barrier.dead;
+  };
   griddep_wait();
+  const float temperature = p.temperature ? p.temperature[row] : 1.f;
+  const int top_k = p.top_k ? p.top_k[row] : 0;
+  const float top_p = p.top_p ? p.top_p[row] : 1.f;
+  const float min_p = p.min_p ? p.min_p[row] : 0.f;
+  const float u = p.uniforms[row];
 
-  // ---- the slice, and its first entry in the order
+  // ---- the slice, and the first entry in the order of each thread's part
   float best = -INFINITY;
   int best_at = 0;
   {
     const T* src = static_cast<const T*>(p.logits) + row * p.logits_stride + first;
     auto put = [&](int x, float v) {
-      v += 0.f;                        // -0 becomes 0
-      v = v < INFINITY ? v : INFINITY;  // NaN too
+      v = fminf(v, INFINITY);  // (NaN becomes infinite)
       scalars[chunk_at(x >> 2) * 4 + (x & 3)] = v;
       if (v > best) {
         best = v;
@@ -311,8 +487,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
         const T* e = reinterpret_cast<const T*>(&in[a]);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          v[i] = E::get(e[i]) + 0.f;
-          v[i] = v[i] < INFINITY ? v[i] : INFINITY;
+          v[i] = fminf(E::get(e[i]), INFINITY);
         }
         if (lead == 0) {
 #pragma unroll
@@ -322,9 +497,8 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
 #pragma unroll
           for (int i = 0; i < V; ++i) scalars[chunk_at((x + i) >> 2) * 4 + ((x + i) & 3)] = v[i];
         }
-        float mx = v[0];
-#pragma unroll
-        for (int i = 1; i < V; ++i) mx = fmaxf(mx, v[i]);
+        float mx = max3(v[0], v[1], fmaxf(v[2], v[3]));
+        if constexpr (V == 8) mx = max3(mx, max3(v[4], v[5], v[6]), v[7]);
         if (mx > best) {
           best = mx;
 #pragma unroll
@@ -338,42 +512,51 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
       else scalars[chunk_at(x >> 2) * 4 + (x & 3)] = -INFINITY;
     }
   }
-  auto warp_max = [](unsigned long long v) {
+  auto warp_max = [](u64 v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-      const unsigned long long u = __shfl_xor_sync(0xffffffffu, v, o);
-      v = u > v ? u : v;
+      const u64 w = __shfl_xor_sync(0xffffffffu, v, o);
+      v = w > v ? w : v;
     }
     return v;
   };
   {
-    const unsigned long long w = warp_max(best == -INFINITY ? 0 : place_of(best, first + best_at));
+    const u64 w = warp_max(best == -INFINITY ? 0 : place_of(best, first + best_at));
     if (lane == 0) s.best[warp] = w;
+  }
+  if (tid == 0) {
+    s.run = -1;
+    s.listed = 0;
+  }
+  const bool few = top_k > 1 && top_k <= kFew && top_k < p.vocab;
+  if (few) {  // the upper bits of the part's (top_k / CTAs)-th largest of the threads' best
+    const int want = (top_k + cs - 1) / cs;
+    const uint32_t key = best == -INFINITY ? 0 : key_of(best);
+    uint32_t low = 0;
+    for (uint32_t bit = 0x80000000u; bit >= 0x1000u; bit >>= 1) {
+      const int have = __syncthreads_count(key >= (low | bit));
+      if (have >= want) low |= bit;
+      if (have == want) break;
+    }
+    if (tid == 0) s.low = low;
   }
   __syncthreads();
   if (warp == 0) {
-    const unsigned long long w = warp_max(lane < kWarps ? s.best[lane] : 0);
+    const u64 w = warp_max(lane < kWarps ? s.best[lane] : 0);
     if (lane == 0) s.top = w;
   }
-  sync_cluster(cs);
-  unsigned long long top = 0;
-  for (int r = 0; r < cs; ++r) {
-    const unsigned long long u = cs > 1 ? peer(&s.top, r) : s.top;
-    top = u > top ? u : top;
-  }
+  __syncthreads();
+  if (cs > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (!meet()) return;
+  const u64 top = warp_max(lane < cs ? (cs > 1 ? peer(&s.top, lane) : s.top) : 0);
 
-  // ---- the row's settings
-  const float temperature = p.temperature ? p.temperature[row] : 1.f;
-  const int top_k = p.top_k ? p.top_k[row] : 0;
-  const float top_p = p.top_p ? p.top_p[row] : 1.f;
-  const float min_p = p.min_p ? p.min_p[row] : 0.f;
-  const float u = p.uniforms[row];
   const bool bad = top == 0 || logit_of(static_cast<uint32_t>(top >> kIndexBits)) == INFINITY ||
                    !(temperature >= 0.f && temperature < INFINITY) || !(u >= 0.f && u < 1.f) || top_p != top_p ||
                    min_p != min_p;
   const bool only_first = temperature == 0.f || top_k == 1 || top_p <= 0.f || min_p > 1.f;
   float* prow = p.probs ? p.probs + row * p.probs_stride + first : nullptr;
   if (bad || only_first) {
+    arrive();
     if (rank == 0 && tid == 0) {
       p.tokens[row] = bad ? -1 : index_of(top);
       if (p.logprobs) p.logprobs[row] = bad ? NAN : 0.f;
@@ -383,42 +566,249 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
       const int one = index_of(top) - first;
       for (int x = tid; x < n; x += kThreads) prow[x] = bad ? NAN : (x == one ? 1.f : 0.f);
     }
-    sync_cluster(cs);  // no CTA leaves while another reads its slots
+    wait();  // no CTA leaves while another reads its slots
     return;
   }
   Row r;
   r.m = logit_of(static_cast<uint32_t>(top >> kIndexBits));
   {
-    const double c = 1.4426950408889634 / static_cast<double>(temperature);
-    r.chi = static_cast<float>(fmin(c, 1e37));  // (beyond, equal logits alone have weight)
-    r.clo = c < 1e37 ? static_cast<float>(c - static_cast<double>(r.chi)) : 0.f;
+    // the quotient and its remainder's, 2^-46 of it; beyond 10^37 equal logits alone have weight
+    constexpr float kLog2eHi = 0x1.715476p+0f, kLog2eLo = 0x1.4ae0cp-26f;
+    const float c = kLog2eHi / temperature;
+    r.chi = fminf(c, 1e37f);
+    r.clo = c < 1e37f && temperature < 1e30f ? (fmaf(-c, temperature, kLog2eHi) + kLog2eLo) / temperature : 0.f;
   }
   const float bin_scale = r.chi * kBinsPerOctave;
+  // Above near_logit weights are near (2^-15 or nearly), below gone_logit nothing.  (The
+  // margin keeps both below the maximum.)  All are near at temperatures past 10^35, and
+  // below a millionth of the maximum, where floats next to it are whole powers apart.
+  const float margin = fabsf(r.m) * 0x1p-22f;
+  const bool all_near = !(100.f / r.chi < 1e37f && margin * r.chi < 1.f);
+  const float near_logit = all_near ? -INFINITY : r.m - 15.f / r.chi - margin;
+  const float gone_logit = all_near ? -INFINITY : r.m - 100.f / r.chi - margin;
+  const u64 least = min_p > 0.f ? times<true>(1ull << kUnit, min_p) : 0;
+  const bool by_k = top_k > 0 && top_k < p.vocab, by_p = top_p < 1.f;
 
-  // Calls f(logit, index) for the thread's run, in order, but for entries of -inf.
+  // Rounded to a whole number by the sum with 2^23; -inf lies in the last bin.
+  auto bin_of = [&](float l) {
+    return static_cast<int>(__float_as_uint(fminf((r.m - l) * bin_scale, kBins - 1.f) + 8388608.f) & (kBins - 1));
+  };
+  auto most_of = [](const float4& v) { return max3(v.x, v.y, fmaxf(v.z, v.w)); };
+  // The near entries of a chunk by their bits in the run; the chunk without them.
+  auto take_near = [&](float4& v, int x) {
+    u64 bits = 0;
+    if (max3(v.x, v.y, fmaxf(v.z, v.w)) > near_logit) {
+      const int at = x - first - tid * per * 4;
+      if (v.x > near_logit) bits |= 1ull << at, v.x = -INFINITY;
+      if (v.y > near_logit) bits |= 2ull << at, v.y = -INFINITY;
+      if (v.z > near_logit) bits |= 4ull << at, v.z = -INFINITY;
+      if (v.w > near_logit) bits |= 8ull << at, v.w = -INFINITY;
+    }
+    return bits;
+  };
+  auto far_sum = [&](const Far& far) {
+    return all_near ? 0 : static_cast<u64>(__float2ull_rn((f2_lo(far.sum) + f2_hi(far.sum)) * 0x1p45f));
+  };
+  auto scalar_at = [&](int x) { return scalars[chunk_at(x >> 2) * 4 + (x & 3)]; };
+  auto entry = [](const float4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; };
+  // Calls f(chunk, index of its first entry) for the thread's run, in order.
   auto each = [&](auto&& f) {
     const int q1 = min((tid + 1) * per, chunks);
-    for (int q = tid * per; q < q1; ++q) {
-      const float4 v = vals[chunk_at(q)];
-      const int x = first + 4 * q;
-      if (v.x > -INFINITY) f(v.x, x);
-      if (v.y > -INFINITY) f(v.y, x + 1);
-      if (v.z > -INFINITY) f(v.z, x + 2);
-      if (v.w > -INFINITY) f(v.w, x + 3);
-    }
+#pragma unroll 1
+    for (int q = tid * per; q < q1; ++q) f(vals[chunk_at(q)], first + 4 * q);
   };
-  auto bin_of = [&](float l) { return min(kBins - 1, static_cast<int>((r.m - l) * bin_scale)); };
+  // Sum over the cluster of a value per CTA, and over the ranks before this one.
+  auto over_cluster = [&](const u64* slot, u64& before) {
+    const u64 x = lane < cs ? (cs > 1 ? peer(slot, lane) : *slot) : 0;
+    u64 to = x;
+#pragma unroll
+    for (int o = 1; o < kMaxCluster; o <<= 1) {
+      const u64 v = __shfl_up_sync(0xffffffffu, to, o);
+      if (lane >= o) to += v;
+    }
+    before = __shfl_sync(0xffffffffu, to - x, rank);
+    return __shfl_sync(0xffffffffu, to, kMaxCluster - 1);
+  };
+  // Lists the entries that `take` wants, chunks above whose largest entry `skip` says
+  // there are none left out; the cluster's number of them (more than kMost: not all
+  // are there).  (The count of the list before is read by now.)
+  auto gather = [&](auto&& skip, auto&& take) {
+    if (tid == 0) s.listed = 0;
+    __syncthreads();
+    each([&](const float4& v, int x) {
+      if (skip(most_of(v))) return;
+#pragma unroll 1
+      for (int i = 0; i < 4; ++i) {
+        const float l = entry(v, i);
+        if (!(l > -INFINITY) || !take(l, x + i)) continue;
+        const int at = atomicAdd(&s.listed, 1);
+        if (at < kMost) list[at] = place_of(l, x + i);
+      }
+    });
+    if (!meet()) return -1;
+    const int have = lane < cs ? (cs > 1 ? peer(&s.listed, lane) : s.listed) : 0;
+    return static_cast<int>(__reduce_add_sync(0xffffffffu, have));
+  };
+  // The cluster's listed entries, m <= kMost, in `sorted` (one CTA); its size.
+  auto pull = [&](int m) {
+    int size = 2;
+    while (size < m) size *= 2;
+    const int have = lane < cs ? (cs > 1 ? peer(&s.listed, lane) : s.listed) : 0;
+    int to = have;
+#pragma unroll
+    for (int o = 1; o < kMaxCluster; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, to, o);
+      if (lane >= o) to += v;
+    }
+    int ends[kMaxCluster];
+#pragma unroll
+    for (int k = 0; k < kMaxCluster; ++k) ends[k] = __shfl_sync(0xffffffffu, to, k);
+    for (int i = tid; i < size; i += kThreads) {
+      int rank_of = 0, from = 0;
+#pragma unroll
+      for (int k = 0; k + 1 < kMaxCluster; ++k)
+        if (i >= ends[k]) rank_of = k + 1, from = ends[k];
+      sorted[i] = i >= m ? 0 : cs > 1 ? peer(list + (i - from), rank_of) : list[i];
+    }
+    return size;
+  };
+  auto logit_at = [&](int i) { return logit_of(static_cast<uint32_t>(sorted[i] >> kIndexBits)); };
+  constexpr int kPer = kMost / kThreads;  // sorted entries of a thread
+  auto answer = [&](int index, u64 w, u64 total) {
+    p.tokens[row] = index;
+    if (!p.logprobs) return;
+    float lp;
+    if (2 * w > total) {
+      lp = log1pf(-static_cast<float>(total - w) / static_cast<float>(total));
+    } else {  // (the weight of a rare token has few bits: its exponent)
+      const float l = E::get(static_cast<const T*>(p.logits)[row * p.logits_stride + index]) + 0.f;
+      const float2 y = exponent_of(r, l);
+      lp = (y.x + y.y) * 0.693147180559945f - logf(static_cast<float>(total) * 0x1p-45f);
+    }
+    p.logprobs[row] = lp;
+  };
+  // The end where the list has every entry down to the last kept one and more: of its
+  // first `count`, with `goal` those whose weights reach it (0: top_p of theirs), and
+  // the least weight; the first CTA draws.
+  auto draw_from_list = [&](int m, int count, bool limit, u64 goal) {
+    if (rank > 0) {  // (the first CTA writes over these once all have arrived)
+      if (prow)
+        for (int x = tid; x < n; x += kThreads) prow[x] = 0.f;
+      arrive();
+    } else {
+      int size = pull(m);
+      arrive();
+      if (prow)
+        for (int x = tid; x < n; x += kThreads) prow[x] = 0.f;
+      sort(sorted, size);
+      const int run = (count + kThreads - 1) / kThreads;  // entries of a thread
+      u64 w[kPer], own = 0;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int x = tid * run + i;
+        w[i] = 0;
+        if (i < run) w[i] = weight_of(r, x < count ? logit_at(x) : -INFINITY, s.powers);
+        own += w[i];
+      }
+      u64 at = block_scan(own, s.scan) - own;
+      if (limit && goal == 0) goal = max(1ull, times<true>(block_all(s.scan), top_p));
+      if (tid == 0) s.cut = count;
+      __syncthreads();
+      int kept = 0;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        if (limit && at < goal && at + w[i] >= goal) s.cut = tid * run + i + 1;
+        at += w[i];
+      }
+      __syncthreads();
+      const int cut = s.cut;
+      // (least is at most the first weight)
+      u64 place[kPer];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int x = tid * run + i;
+        const bool keep = i < run && x < cut && w[i] >= least;
+        place[i] = keep ? (static_cast<u64>(kIndexMask - index_of(sorted[x])) << (kUnit + 1)) | w[i] : 0;
+        kept += keep;
+      }
+      kept = static_cast<int>(block_scan(kept, s.scan));
+      kept = static_cast<int>(block_all(s.scan));
+      size = 2;
+      while (size < cut) size *= 2;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (i < run && tid * run + i < size) sorted[tid * run + i] = place[i];
+      for (int i = kThreads * run + tid; i < size; i += kThreads) sorted[i] = 0;
+      sort(sorted, size);  // by index
+      constexpr u64 kWeight = (1ull << (kUnit + 1)) - 1;
+      own = 0;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int x = tid * run + i;
+        place[i] = i < run && x < kept ? sorted[x] : 0;
+        own += place[i] & kWeight;
+      }
+      at = block_scan(own, s.scan) - own;
+      const u64 total = block_all(s.scan), target = times<false>(total, u);
+      if (prow) {  // the other slices' zeros are written
+        wait();
+        __syncthreads();
+      }
+      const float inv = 1.f / (static_cast<float>(total) * 0x1p-45f);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const u64 x = place[i] & kWeight;
+        if (i >= run || tid * run + i >= kept) break;
+        const int index = static_cast<int>(kIndexMask - static_cast<uint32_t>(place[i] >> (kUnit + 1)));
+        if (at <= target && at + x > target) answer(index, x, total);
+        at += x;
+        if (prow) {  // (this CTA's slice is the row's first)
+          const float l = E::get(static_cast<const T*>(p.logits)[row * p.logits_stride + index]) + 0.f;
+          prow[index] = weight32(r, l) * inv;
+        }
+      }
+    }
+    if (rank > 0 || !prow) wait();  // no CTA leaves while another reads its list
+  };
+
+  if (few) {
+    uint32_t low = lane < cs ? (cs > 1 ? peer(&s.low, lane) : s.low) : 0xffffffffu;
+    low = __reduce_min_sync(0xffffffffu, low);
+    const float bound = low <= key_of(-INFINITY) ? -INFINITY : logit_of(low);
+    const int m = gather([&](float l) { return l < bound; }, [&](float l, int) { return l >= bound; });
+    if (m < 0) return;
+    if (m <= kMost) {
+      draw_from_list(m, min(top_k, m), by_p, 0);
+      return;
+    }
+  }
 
   // ---- the threshold: the place of the last entry that top-k and top-p keep
-  unsigned long long threshold = 0;  // (nothing is as low)
+  u64 threshold = 0;  // (nothing is as low)
+  bool over = false;  // the token is drawn, or a CTA did not come
+  auto gone = [&] {
+    over = true;
+    return static_cast<u64>(0);
+  };
   // The place of the entry with which the number of entries (BY_MASS: their weight)
-  // in order reaches the target, 0 if they never do.  With `whole`, where the entries
-  // down to it are few, `whole` becomes their number and `sorted` holds them all.
-  // target < 0: top_p of the row's weight.
-  auto find = [&](bool by_mass, double share, unsigned long long target, int* whole) -> unsigned long long {
-    int bin = -1, shift = 32 + kIndexBits;
-    unsigned long long prefix = 0, above = 0, above_mass = 0;
-    int in_bin = 0;
+  // in order reaches the target, 0 if they never do.  Target 0: top_p of the row's
+  // weight.  Where few entries lead up to it the row ends here.
+  auto find = [&](bool by_mass, u64 target) -> u64 {
+    int bin = -1, shift = 32 + kIndexBits, in_bin = 0, m = 0;
+    u64 prefix = 0, above = 0, above_mass = 0;
+    // what weighs less than `light` is never kept (see above; 1 - top_p rounded down), and
+    // an entry beyond this exponent weighs less
+    float reach = INFINITY;
+    if (by_mass) {
+      const u64 light = times<false>(1ull << kUnit, (1.f - top_p) * (1.f - 0x1p-20f)) / static_cast<u64>(p.vocab);
+      reach = static_cast<float>(kUnit - 63 + __clzll(max(light, 1ull))) + 0.5f;
+    }
+    bool near_only = by_mass;
+    auto counts = [&](float l) {
+      return near_only ? l > near_logit : by_mass ? (r.m - l) * r.chi < reach : l > -INFINITY;
+    };
+    const u64 given = target;
+    bool whole = false;
     for (int round = 0;; ++round) {
       const int bits = min(shift, kBinBits);
       const int next = round == 0 ? shift : shift - bits;
@@ -427,263 +817,299 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
         if (by_mass) bin_lo[b] = bin_hi[b] = 0;
       }
       __syncthreads();
-      each([&](float l, int index) {
+      u64 all = 0;
+      auto put = [&](float l, int index, u64 w) {
+        if (!counts(l)) return;
         int d = bin_of(l);
         if (round > 0) {
-          const unsigned long long place = place_of(l, index);
+          const u64 place = place_of(l, index);
           if (d != bin || (place >> shift) != prefix) return;
           d = (1 << bits) - 1 - static_cast<int>((place >> next) & ((1 << bits) - 1));
         }
         atomicAdd(bin_count + d, 1u);
         if (by_mass) {
-          const unsigned long long w = weight_of(r, l, s.powers);
           const uint32_t lo = static_cast<uint32_t>(w);
           const uint32_t old = atomicAdd(bin_lo + d, lo);
           const uint32_t hi = static_cast<uint32_t>(w >> 32) + (old + lo < old ? 1u : 0u);
           if (hi) atomicAdd(bin_hi + d, hi);
         }
-      });
-      sync_cluster(cs);
+      };
+      // first of the near entries alone, with all weights' sum
+      if (by_mass && near_only) {
+        u64 large = 0;  // of the run: the near entries
+        Far far{0, gone_logit};
+        each([&](float4 v, int x) {
+          large |= take_near(v, x);
+          add_far<TYPE != SV_FP32>(r, v, far);
+        });
+        all = far_sum(far);
+        for (; large != 0; large &= large - 1) {
+          const int x = tid * per * 4 + __ffsll(large) - 1;
+          const float l = scalar_at(x);
+          const u64 w = weight_near(r, l, s.powers);
+          all += w;
+          put(l, first + x, w);
+        }
+      } else {
+        each([&](const float4& v, int x) {
+          if (!counts(most_of(v))) return;
+#pragma unroll 1
+          for (int i = 0; i < 4; ++i) {
+            const float l = entry(v, i);
+            put(l, x + i, by_mass && counts(l) ? weight_of(r, l, s.powers) : 0);
+          }
+        });
+      }
+      if (by_mass && near_only) {
+        block_scan(all, s.scan);
+        const u64 sum = block_all(s.scan);
+        if (tid == 0) s.all = sum;
+      }
+      if (!meet()) return gone();
+      if (by_mass && near_only && target == 0) {
+        u64 unused;
+        target = max(1ull, times<true>(over_cluster(&s.all, unused), top_p));
+      }
       // this CTA's part of the bins, over the cluster
       const int part = kBins / cs, each_bins = max(1, part / kThreads);
       const int b0 = rank * part + tid * each_bins;
-      unsigned long long c = 0, ms = 0;
-      uint32_t cnt[4];
-      unsigned long long mass[4];
+      auto bin_sum = [&](int b, u64& c, u64& w) {
+        uint32_t x[kMaxCluster], lo[kMaxCluster], hi[kMaxCluster];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        cnt[i] = 0;
-        mass[i] = 0;
-        if (i < each_bins && tid * each_bins < part) {
-          for (int k = 0; k < cs; ++k) {
-            cnt[i] += cs > 1 ? peer(bin_count + b0 + i, k) : bin_count[b0 + i];
-            if (by_mass)
-              mass[i] += cs > 1 ? (static_cast<unsigned long long>(peer(bin_hi + b0 + i, k)) << 32) + peer(bin_lo + b0 + i, k)
-                                : (static_cast<unsigned long long>(bin_hi[b0 + i]) << 32) + bin_lo[b0 + i];
+        for (int k = 0; k < kMaxCluster; ++k) {
+          x[k] = lo[k] = hi[k] = 0;
+          if (k >= cs) continue;
+          x[k] = cs > 1 ? peer(bin_count + b, k) : bin_count[b];
+          if (!by_mass) continue;
+          lo[k] = cs > 1 ? peer(bin_lo + b, k) : bin_lo[b];
+          hi[k] = cs > 1 ? peer(bin_hi + b, k) : bin_hi[b];
+        }
+#pragma unroll
+        for (int k = 0; k < kMaxCluster; ++k) {
+          c += x[k];
+          w += (static_cast<u64>(hi[k]) << 32) + lo[k];
+        }
+      };
+      u64 c = 0, ms = 0;
+      if (tid * each_bins < part)
+        for (int i = 0; i < each_bins; ++i) bin_sum(b0 + i, c, ms);
+      u64 at_c = block_scan(c, s.scan) - c, at_m = 0;
+      if (warp == 0) {
+        const u64 sum = block_all(s.scan);
+        if (lane == 0) s.count = sum;
+      }
+      if (by_mass) {
+        at_m = block_scan(ms, s.scan) - ms;
+        if (warp == 0) {
+          const u64 sum = block_all(s.scan);
+          if (lane == 0) s.mass = sum;
+        }
+      }
+      if (!meet()) return gone();
+      // of the CTAs, a lane each: what lies before this one, and whose part has the target
+      const u64 pc = lane < cs ? (cs > 1 ? peer(&s.count, lane) : s.count) : 0;
+      const u64 pm = lane < cs && by_mass ? (cs > 1 ? peer(&s.mass, lane) : s.mass) : 0;
+      u64 to_c = pc, to_m = pm;
+#pragma unroll
+      for (int o = 1; o < kMaxCluster; o <<= 1) {
+        const u64 uc = __shfl_up_sync(0xffffffffu, to_c, o), um = __shfl_up_sync(0xffffffffu, to_m, o);
+        if (lane >= o) to_c += uc, to_m += um;
+      }
+      const unsigned owners = __ballot_sync(0xffffffffu, lane < cs && (by_mass ? to_m : to_c) >= target);
+      if (owners == 0) {
+        if (!by_mass || !near_only) return 0;
+        near_only = false;  // once more, with the far entries
+        round = -1;
+        if (!meet()) return gone();
+        continue;
+      }
+      const int owner = __ffs(owners) - 1;
+      if (rank == owner) {
+        at_c += __shfl_sync(0xffffffffu, to_c - pc, rank);
+        at_m += __shfl_sync(0xffffffffu, to_m - pm, rank);
+        const u64 at = by_mass ? at_m : at_c;
+        if (at < target && at + (by_mass ? ms : c) >= target) {
+          for (int b = b0;; ++b) {
+            c = ms = 0;
+            bin_sum(b, c, ms);
+            if (b + 1 < b0 + each_bins && (by_mass ? at_m + ms : at_c + c) < target) {
+              at_c += c;
+              at_m += ms;
+              continue;
+            }
+            s.pick = Pick{b, static_cast<int>(c), at_c, at_m};
+            break;
           }
         }
-        c += cnt[i];
-        ms += mass[i];
       }
-      unsigned long long all_c, all_m = 0;
-      const unsigned long long incl_c = block_scan(c, s.scan, all_c);
-      const unsigned long long incl_m = by_mass ? block_scan(ms, s.scan2, all_m) : 0;
-      if (tid == 0) {
-        s.count = all_c;
-        s.mass = all_m;
-      }
-      sync_cluster(cs);
-      unsigned long long base_c = 0, base_m = 0, sum_c = 0, sum_m = 0, edge[kMaxCluster];
-#pragma unroll
-      for (int k = 0; k < kMaxCluster; ++k) {
-        if (k < cs) {
-          if (k == rank) base_c = sum_c, base_m = sum_m;
-          sum_c += cs > 1 ? peer(&s.count, k) : s.count;
-          sum_m += cs > 1 ? peer(&s.mass, k) : s.mass;
-        }
-        edge[k] = by_mass ? sum_m : sum_c;
-      }
-      if (by_mass && round == 0 && target == 0)
-        target = max(1ull, static_cast<unsigned long long>(ceil(share * static_cast<double>(sum_m))));
-      if ((by_mass ? sum_m : sum_c) < target) return 0;  // (round 0 alone)
-      int owner = 0;
-#pragma unroll
-      for (int k = kMaxCluster - 1; k >= 0; --k)
-        if (k < cs && edge[k] >= target) owner = k;
-      const unsigned long long end = by_mass ? base_m + incl_m : base_c + incl_c;
-      const unsigned long long start = end - (by_mass ? ms : c);
-      if (rank == owner && start < target && end >= target) {
-        unsigned long long ac = base_c + incl_c - c, am = base_m + incl_m - ms;
-        int b = b0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (b == b0 + i && i + 1 < each_bins && (by_mass ? am + mass[i] : ac + cnt[i]) < target) {
-            ac += cnt[i];
-            am += mass[i];
-            ++b;
-          }
-        }
-        s.pick.bin = b;
-        s.pick.in_bin = static_cast<int>(cnt[b - b0]);
-        s.pick.above = ac;
-        s.pick.above_mass = am;
-      }
-      sync_cluster(cs);
+      if (!meet()) return gone();
       const Pick got = cs > 1 ? peer(&s.pick, owner) : s.pick;
       above += got.above;
       above_mass += got.above_mass;
-      target -= by_mass ? got.above_mass : got.above;
       in_bin = got.in_bin;
       if (round == 0) {
         bin = got.bin;
+        whole = above + in_bin <= kWhole;
       } else {
-        prefix = (prefix << bits) | static_cast<unsigned long long>((1 << bits) - 1 - got.bin);
+        prefix = (prefix << bits) | static_cast<u64>((1 << bits) - 1 - got.bin);
         shift = next;
       }
+      if (whole) break;
+      target -= by_mass ? got.above_mass : got.above;
       if (in_bin <= kMost) break;
       __syncthreads();  // (one CTA: the pick is read)
     }
-    // ---- the bin's entries (or all down to it), sorted in every CTA
-    const bool gather = whole != nullptr && shift == 32 + kIndexBits && above + in_bin <= kMost;
-    if (tid == 0) s.listed = 0;
-    __syncthreads();
-    each([&](float l, int index) {
-      const int d = bin_of(l);
-      if (gather ? d > bin : d != bin) return;
-      const unsigned long long place = place_of(l, index);
-      if (shift < 32 + kIndexBits && (place >> shift) != prefix) return;
-      list[atomicAdd(&s.listed, 1)] = place;
-    });
-    sync_cluster(cs);
-    int m = 0;
-    for (int k = 0; k < cs; ++k) {
-      const int have = cs > 1 ? peer(&s.listed, k) : s.listed;
-      for (int i = tid; i < have; i += kThreads) sorted[m + i] = cs > 1 ? peer(list + i, k) : list[i];
-      m += have;
+    // the bin's entries, or all down to it (of the bin, those in the histogram and, for
+    // top-p, maybe lighter ones, which come behind them)
+    if (whole) {
+      m = gather([&](float l) { return bin_of(l) > bin; }, [&](float l, int) { return bin_of(l) <= bin; });
+      if (m < 0) return gone();
+      if (m <= kMost) {
+        draw_from_list(m, by_mass ? m : static_cast<int>(given), by_p, by_mass ? target : 0);
+        return gone();
+      }
+      if (!meet()) return gone();  // the numbers listed are read
     }
-    int size = 2;
-    while (size < m) size *= 2;
-    for (int i = m + tid; i < size; i += kThreads) sorted[i] = 0;
-    __syncthreads();
-    for (int len = 2; len <= size; len *= 2) {
-      for (int step = len / 2; step > 0; step /= 2) {
-        for (int i = tid; i < size / 2; i += kThreads) {
-          const int a = 2 * i - (i & (step - 1)), b = a + step;
-          const unsigned long long x = sorted[a], y = sorted[b];
-          if ((x < y) == ((a & len) == 0)) {
-            sorted[a] = y;
-            sorted[b] = x;
-          }
+    m = gather([&](float l) { return bin_of(l) > bin; },
+               [&](float l, int index) {
+                 if (bin_of(l) != bin || !counts(l)) return false;
+                 if (shift < 32 + kIndexBits && (place_of(l, index) >> shift) != prefix) return false;
+                 return true;
+               });
+    if (m < 0) return gone();
+    if (whole) target -= by_mass ? above_mass : above;
+    if (rank == 0) {
+      const int size = pull(m);
+      sort(sorted, size);
+      if (!by_mass) {
+        if (tid == 0) s.found = sorted[target - 1];
+      } else {
+        u64 w[kPer], own = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const int x = tid * kPer + i;
+          w[i] = x < m ? weight_of(r, logit_at(x), s.powers) : 0;
+          own += w[i];
         }
-        // (steps up to 32 stay within a warp's 64 entries)
-        if (step > 32 || (step == 1 && len >= 64)) __syncthreads();
-        else __syncwarp();
-      }
-    }
-    __syncthreads();
-    if (gather) *whole = m;
-    if (!by_mass) return sorted[(gather ? above : 0) + target - 1];
-    if (tid == 0) s.found = 0;
-    constexpr int kPer = kMost / kThreads;
-    unsigned long long w[kPer], mine = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int x = tid * kPer + i;
-      w[i] = x < m ? weight_of(r, logit_of(static_cast<uint32_t>(sorted[x] >> kIndexBits)), s.powers) : 0;
-      mine += w[i];
-    }
-    unsigned long long sum;
-    const unsigned long long end = block_scan(mine, s.scan, sum);
-    unsigned long long at = end - mine;
-    if (at < target && end >= target) {
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        if (at < target && at + w[i] >= target) s.found = sorted[tid * kPer + i];
-        at += w[i];
-      }
-    }
-    __syncthreads();
-    return s.found;
-  };
-  // Sum over the cluster of the weights at or above a place.
-  auto kept_sum = [&](unsigned long long place, unsigned long long least, unsigned long long& end,
-                      unsigned long long& mine, unsigned long long& base) -> unsigned long long {
-    const float floor_logit = place ? logit_of(static_cast<uint32_t>(place >> kIndexBits)) : -INFINITY;
-    const int floor_index = place ? index_of(place) : 0;
-    mine = 0;
-    each([&](float l, int index) {
-      if (l < floor_logit || (l == floor_logit && index > floor_index)) return;
-      const unsigned long long w = weight_of(r, l, s.powers);
-      if (w >= least) mine += w;
-    });
-    unsigned long long sum;
-    end = block_scan(mine, s.scan, sum);
-    if (tid == 0) s.sum = sum;
-    sync_cluster(cs);
-    unsigned long long total = 0;
-    base = 0;
-    for (int k = 0; k < cs; ++k) {
-      const unsigned long long x = cs > 1 ? peer(&s.sum, k) : s.sum;
-      if (k < rank) base += x;
-      total += x;
-    }
-    return total;
-  };
-  unsigned long long end, mine, base;
-  const bool by_p = top_p < 1.f;
-  if (top_k > 0 && top_k < p.vocab) {
-    int whole = 0;
-    threshold = find(false, 0.0, static_cast<unsigned long long>(top_k), &whole);
-    if (by_p && threshold != 0 && whole > 0) {
-      // the entries kept so far lie sorted in every CTA
-      constexpr int kPer = kMost / kThreads;
-      const int m = min(whole, top_k);
-      unsigned long long w[kPer], part = 0, sum;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int x = tid * kPer + i;
-        w[i] = x < m ? weight_of(r, logit_of(static_cast<uint32_t>(sorted[x] >> kIndexBits)), s.powers) : 0;
-        part += w[i];
-      }
-      const unsigned long long to = block_scan(part, s.scan, sum);
-      const unsigned long long target =
-          max(1ull, static_cast<unsigned long long>(ceil(static_cast<double>(top_p) * static_cast<double>(sum))));
-      unsigned long long at = to - part;
-      if (at < target && to >= target) {
+        u64 at = block_scan(own, s.scan) - own;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
           if (at < target && at + w[i] >= target) s.found = sorted[tid * kPer + i];
           at += w[i];
         }
       }
-      __syncthreads();
-      threshold = s.found;
-    } else if (by_p) {
-      const unsigned long long sum = kept_sum(threshold, 0, end, mine, base);
-      threshold = find(true, 0.0, max(1ull, static_cast<unsigned long long>(ceil(static_cast<double>(top_p) *
-                                                                                 static_cast<double>(sum)))), nullptr);
     }
-  } else if (by_p) {
-    threshold = find(true, static_cast<double>(top_p), 0, nullptr);
+    if (!meet()) return gone();
+    return cs > 1 ? peer(&s.found, 0) : s.found;
+  };
+  // Sum over the cluster of the weights at or above a place.
+  auto kept_sum = [&](u64 place, u64 floor_weight, u64& end, u64& mine, u64& base) -> u64 {
+    const float floor_logit = place ? logit_of(static_cast<uint32_t>(place >> kIndexBits)) : -INFINITY;
+    const int floor_index = place ? index_of(place) : 0x7fffffff;
+    mine = 0;
+    const bool filtered = place != 0 || floor_weight != 0;
+    // with min-p the entries that may pass are weighed one by one, the others left out
+    const float one_by_one = floor_weight != 0 ? r.m - (log2f(1.f / min_p) + 1.f) / r.chi - margin : near_logit;
+    u64 large = 0;  // of the run: entries to be weighed one by one
+    Far far{0, gone_logit};
+    each([&](float4 v, int x) {
+      const float most = most_of(v);
+      if (most < floor_logit || (floor_weight != 0 && most <= one_by_one)) return;
+      if (most > one_by_one || filtered) {
+        const int at = x - first - tid * per * 4;
+        auto look = [&](float& l, int i) {
+          const bool in = l > floor_logit || (l == floor_logit && x + i <= floor_index);
+          if (in && l > one_by_one) large |= 1ull << (at + i);
+          if (!in || l > one_by_one || floor_weight != 0) l = -INFINITY;
+        };
+        look(v.x, 0);
+        look(v.y, 1);
+        look(v.z, 2);
+        look(v.w, 3);
+      }
+      add_far<TYPE != SV_FP32>(r, v, far);
+    });
+    mine = far_sum(far);
+    for (; large != 0; large &= large - 1) {
+      const u64 w = weight_of(r, scalar_at(tid * per * 4 + __ffsll(large) - 1), s.powers);
+      if (w >= floor_weight) mine += w;
+    }
+    end = block_scan(mine, s.scan);
+    const u64 sum = block_all(s.scan);
+    if (tid == 0) s.sum = sum;
+    if (!meet()) return gone();
+    return over_cluster(&s.sum, base);
+  };
+  // top_k, then top_p of what it keeps: where its entries were not listed, of a first
+  // sum of them.  The last sum is the draw's.
+  enum { kByCount, kByMass, kShareOfKept, kDraw };
+  u64 end, mine, base, total;
+  int step = by_k ? kByCount : by_p ? kByMass : kDraw;
+  u64 goal = by_k ? static_cast<u64>(top_k) : 0;
+  for (;;) {
+    if (step == kShareOfKept || step == kDraw) {
+      total = kept_sum(threshold, step == kDraw ? least : 0, end, mine, base);
+      if (over) return;
+      if (step == kDraw) break;
+      goal = max(1ull, times<true>(total, top_p));
+      step = kByMass;
+    }
+    threshold = find(step == kByMass, goal);
+    if (over) return;
+    step = step == kByCount && by_p ? kShareOfKept : kDraw;
   }
+  arrive();  // (this CTA reads no other's memory from here)
 
   // ---- the draw, in index order
-  const unsigned long long least = min_p > 0.f ? static_cast<unsigned long long>(ceil(static_cast<double>(min_p) * 0x1p45)) : 0;
-  const unsigned long long total = kept_sum(threshold, least, end, mine, base);
-  const unsigned long long target = static_cast<unsigned long long>(static_cast<double>(u) * static_cast<double>(total));
+  const u64 target = times<false>(total, u);
   const float floor_logit = threshold ? logit_of(static_cast<uint32_t>(threshold >> kIndexBits)) : -INFINITY;
   const int floor_index = threshold ? index_of(threshold) : 0x7fffffff;
-  if (base + end - mine <= target && target < base + end) {  // one thread of the cluster
-    unsigned long long at = base + end - mine;
-    bool open = true;
-    each([&](float l, int index) {
-      if (!open || l < floor_logit || (l == floor_logit && index > floor_index)) return;
-      const unsigned long long w = weight_of(r, l, s.powers);
-      if (w < least) return;
-      at += w;
-      if (at <= target) return;
-      open = false;
-      p.tokens[row] = index;
-      if (p.logprobs) {
-        const float2 y = exponent_of(r, l);
-        float lp;
-        if (2 * w > total) lp = log1pf(-static_cast<float>(total - w) / static_cast<float>(total));
-        else lp = (y.x + y.y) * 0.693147180559945f - logf(static_cast<float>(total) * 0x1p-45f);
-        p.logprobs[row] = lp;
+  auto keeps = [&](float l, int index) {
+    return l > -INFINITY && (l > floor_logit || (l == floor_logit && index <= floor_index));
+  };
+  if (base + end - mine <= target && target < base + end) {  // one thread of the cluster: its run has the token
+    s.run = tid;
+    s.before = base + end - mine;
+  }
+  __syncthreads();
+  if (s.run >= 0 && warp == 0) {
+    // (the weights one by one may sum to a little less than the run's sum: the last then)
+    u64 at = s.before, w_last = 0;
+    int x_last = -1;
+    const int x1 = min((s.run + 1) * per, chunks) * 4;
+    for (int x0 = s.run * per * 4; x0 < x1; x0 += 32) {
+      const int x = x0 + lane;
+      const float l = x < x1 ? scalar_at(x) : -INFINITY;
+      bool kept = keeps(l, first + x);
+      u64 w = weight_of(r, kept ? l : -INFINITY, s.powers);
+      if (w < least) kept = false, w = 0;
+      u64 sum = w;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const u64 v = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += v;
       }
-    });
+      const unsigned hit = __ballot_sync(0xffffffffu, at + sum > target), some = __ballot_sync(0xffffffffu, kept);
+      const int pick = hit ? __ffs(hit) - 1 : 31 - __clz(some);
+      if (hit || some) {
+        x_last = x0 + pick;
+        w_last = __shfl_sync(0xffffffffu, w, pick);
+      }
+      if (hit) break;
+      at += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    if (lane == 0 && x_last >= 0) answer(first + x_last, w_last, total);
   }
   if (prow) {
     const float inv = 1.f / (static_cast<float>(total) * 0x1p-45f);
     for (int x = tid; x < n; x += kThreads) {
-      const float l = scalars[chunk_at(x >> 2) * 4 + (x & 3)];
+      const float l = scalar_at(x);
       float v = 0.f;
-      if (l > floor_logit || (l == floor_logit && first + x <= floor_index))
-        if (l > -INFINITY && (least == 0 || weight_of(r, l, s.powers) >= least)) v = weight32(r, l) * inv;
+      if (keeps(l, first + x) && (least == 0 || weight_of(r, l, s.powers) >= least)) v = weight32(r, l) * inv;
       prow[x] = v;
     }
   }
-  sync_cluster(cs);  // no CTA leaves while another reads its slots
+  wait();  // no CTA leaves while another reads its slots
 }
 
 template <int TYPE>
