@@ -48,6 +48,7 @@ constexpr int kBins = 2048;
 constexpr int kBinBits = 11;
 constexpr int kBinsPerOctave = 32;
 constexpr int kMost = 2048;        // entries that are sorted
+static_assert(3 * kBins * 4 <= 2 * kMost * 8, "the bins lie where the lists do");
 constexpr int kWhole = 512;        // kept ones that are listed whole: more are quicker summed in place
 constexpr int kFew = 128;
 constexpr int kIndexBits = 18;
@@ -69,7 +70,9 @@ struct Params {
   float* probs;
   int* err;
   int vocab, slice, cluster;
-  uint32_t val_bytes;  // of the slice in shared memory
+  int per;               // 16-byte vectors of a thread's run
+  uint32_t per_inverse;  // 2^18 / per, rounded up: exact quotients of up to 2^13
+  uint32_t val_bytes;    // of the slice in shared memory
 };
 
 // 2^(j/32) in units of 2^-45, and as the sum of two floats.
@@ -319,9 +322,10 @@ struct Shared {
   Power powers[32];
   Barrier barrier;
   u64 scan[kWarps];
-  u64 best[kWarps];
+  uint32_t best[kWarps];
   // read by the other CTAs of the cluster
-  u64 top;              // the slice's first place
+  uint32_t top;         // key of the slice's largest
+  int first;            // and its first index
   u64 count, mass, all;  // of the histogram's part; all weights of the slice
   u64 sum;              // kept weights
   u64 found;            // the threshold
@@ -363,23 +367,47 @@ __device__ __forceinline__ u64 block_all(const u64* slots) {
   return v;
 }
 
-// Descending order of a[0 .. size), a power of two.
+// Descending order of a[0 .. size), a power of two.  Up to an entry per thread the
+// steps within a warp are exchanges of registers.
 __device__ __noinline__ void sort(u64* a, int size) {
+  const int tid = threadIdx.x;
   __syncwarp();
   __syncthreads();
-  for (int len = 2; len <= size; len *= 2) {
-    for (int step = len / 2; step > 0; step /= 2) {
-      for (int i = threadIdx.x; i < size / 2; i += kThreads) {
-        const int x = 2 * i - (i & (step - 1)), y = x + step;
-        const u64 vx = a[x], vy = a[y];
-        if ((vx < vy) == ((x & len) == 0)) {
-          a[x] = vy;
-          a[y] = vx;
+  if (size <= kThreads) {
+    u64 v = tid < size ? a[tid] : 0;
+    for (int len = 2; len <= size; len *= 2) {
+      const bool descending = (tid & len) == 0;
+      for (int step = len / 2; step > 0; step /= 2) {
+        u64 w;
+        if (step >= 32) {
+          __syncthreads();
+          if (tid < size) a[tid] = v;
+          __syncthreads();
+          w = tid < size ? a[tid ^ step] : 0;
+        } else {
+          w = __shfl_xor_sync(0xffffffffu, v, step);
         }
+        const bool first = (tid & step) == 0;
+        v = (first == descending) == (v > w) ? v : w;
       }
-      // (steps up to 32 stay within a warp's 64 entries)
-      if (step > 32 || (step == 1 && len >= 64)) __syncthreads();
-      else __syncwarp();
+    }
+    __syncthreads();
+    if (tid < size) a[tid] = v;
+  } else {
+    for (int len = 2; len <= size; len *= 2) {
+      for (int step = len / 2; step > 0; step /= 2) {
+        for (int i = tid; i < size / 2; i += kThreads) {
+          const int x = 2 * i - (i & (step - 1)), y = x + step;
+          const u64 vx = a[x], vy = a[y];
+          if ((vx < vy) == ((x & len) == 0)) {
+            a[x] = vy;
+            a[y] = vx;
+          }
+        }
+        // (steps up to 32 stay within a warp's 64 entries)
+        if (step > 32 || (step == 1 && len >= 64)) __syncthreads();
+        else __syncwarp();
+      }
     }
   }
   __syncthreads();
@@ -389,21 +417,85 @@ template <int TYPE>
 struct Element {
   using Type = float;
   static __device__ __forceinline__ float get(float v) { return v; }
+  static __device__ __forceinline__ float lowest() { return -INFINITY; }
 };
 template <>
 struct Element<SV_BF16> {
   using Type = uint16_t;
   static __device__ __forceinline__ float get(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
+  static __device__ __forceinline__ uint16_t lowest() { return 0xff80; }
 };
 template <>
 struct Element<SV_FP16> {
   using Type = uint16_t;
   static __device__ __forceinline__ float get(uint16_t v) { return __half2float(__ushort_as_half(v)); }
+  static __device__ __forceinline__ uint16_t lowest() { return 0xfc00; }
 };
 
-// The slice of one CTA: chunk q of four entries lies at q + q / 8 (threads that read
-// runs of 1, 2, 4 or 8 chunks each then meet no bank twice).
-__device__ __forceinline__ int chunk_at(int q) { return q + (q >> 3); }
+template <int TYPE>
+__device__ __forceinline__ float4 four(const uint4& v, int half) {
+  if constexpr (TYPE == SV_FP32) {
+    return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+  } else {
+    const uint32_t a = half ? v.z : v.x, b = half ? v.w : v.y;
+    if constexpr (TYPE == SV_BF16) {
+      return make_float4(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u), __uint_as_float(b << 16),
+                         __uint_as_float(b & 0xffff0000u));
+    } else {
+      const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&a));
+      const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&b));
+      return make_float4(x.x, x.y, y.x, y.y);
+    }
+  }
+}
+
+__device__ __forceinline__ float most_of(const float4& v) { return max3(v.x, v.y, fmaxf(v.z, v.w)); }
+
+// What a thread's run adds up to: the far weights, and by their bits the entries to be
+// weighed one by one.
+struct Limits {
+  float logit;        // only entries from this place on count
+  int index;
+  float one_by_one;   // entries above are weighed one by one
+  float gone;         // entries below weigh nothing
+  bool filtered;      // some entries do not count
+  bool few;           // none but those above one_by_one count
+};
+struct Added {
+  u64 far, large;
+};
+template <int TYPE>
+__device__ __noinline__ Added add_run(const uint4* run, int vecs, int x, Row r, Limits c) {
+  Far far{0, c.gone};
+  u64 large = 0;
+  int at = 0;
+  for (int j = 0; j < vecs; ++j) {
+    const uint4 raw = run[j];
+#pragma unroll
+    for (int h = 0; h < (TYPE == SV_FP32 ? 1 : 2); ++h, at += 4) {
+      float4 v = four<TYPE>(raw, h);
+      const float most = most_of(v);
+      if (most < c.logit || (c.few && most <= c.one_by_one)) continue;
+      if (most > c.one_by_one || c.filtered) {
+        unsigned bits = 0;
+        auto look = [&](float& l, int i) {
+          const bool in = l > c.logit || (l == c.logit && x + at + i <= c.index);
+          const bool one = in && l > c.one_by_one;
+          bits |= one ? 1u << i : 0u;
+          l = !in || one || c.few ? -INFINITY : l;
+        };
+        look(v.x, 0);
+        look(v.y, 1);
+        look(v.z, 2);
+        look(v.w, 3);
+        large |= static_cast<u64>(bits) << at;
+      }
+      add_far<TYPE != SV_FP32>(r, v, far);
+    }
+  }
+  const float sum = f2_lo(far.sum) + f2_hi(far.sum);
+  return {c.gone == -INFINITY ? 0 : static_cast<u64>(__float2ull_rn(sum * 0x1p45f)), large};
+}
 
 template <int TYPE>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ Params p) {
@@ -412,20 +504,28 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   constexpr int V = 16 / sizeof(T);  // entries of a 16-byte vector
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ Shared s;
-  float4* vals = reinterpret_cast<float4*>(smem);
-  float* scalars = reinterpret_cast<float*>(smem);
+  // The slice as it came, a thread's run of `per` vectors at an odd stride, so that the
+  // threads of a warp meet in no bank.
+  uint4* vals = reinterpret_cast<uint4*>(smem);
+  T* scalars = reinterpret_cast<T*>(smem);
+  // The bins, and once they are read the lists.
   uint32_t* bin_count = reinterpret_cast<uint32_t*>(smem + p.val_bytes);
   uint32_t* bin_lo = bin_count + kBins;
   uint32_t* bin_hi = bin_lo + kBins;
-  u64* sorted = reinterpret_cast<u64*>(bin_count);  // (when the bins are read)
-  u64* list = reinterpret_cast<u64*>(bin_hi + kBins);
+  u64* sorted = reinterpret_cast<u64*>(bin_count);
+  u64* list = sorted + kMost;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cs = p.cluster;
   const int rank = cs > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int row = blockIdx.x / cs;
   const int first = min(rank * p.slice, p.vocab), n = min(p.slice, p.vocab - first);
-  const int chunks = (n + 3) / 4;
-  const int per = (p.slice / 4 + kThreads - 1) / kThreads;  // chunks of a thread's run
+  const int all_vecs = (n + V - 1) / V, per = p.per;
+  const int run_at = tid * per * V;                             // the run's first entry in the slice
+  const int run_vecs = max(0, min(per, all_vecs - tid * per));
+  const uint4* run = vals + tid * (per | 1);
+  auto place_in = [&](int vec) {
+    return (per & 1) ? vec : vec + static_cast<int>((static_cast<unsigned>(vec) * p.per_inverse) >> 18);
+  };
   if (tid < 32) s.powers[tid] = kPowers[tid];
   if (tid == 0) {
     mbar_init(&s.barrier.arrived, cs);
@@ -456,21 +556,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   const float min_p = p.min_p ? p.min_p[row] : 0.f;
   const float u = p.uniforms[row];
 
-  // ---- the slice, and the first entry in the order of each thread's part
+  // ---- the slice, and the largest entry of each thread's part (infinite for NaN)
   float best = -INFINITY;
-  int best_at = 0;
   {
     const T* src = static_cast<const T*>(p.logits) + row * p.logits_stride + first;
-    auto put = [&](int x, float v) {
-      v = fminf(v, INFINITY);  // (NaN becomes infinite)
-      scalars[chunk_at(x >> 2) * 4 + (x & 3)] = v;
-      if (v > best) {
-        best = v;
-        best_at = x;
-      }
+    auto put = [&](int x) {
+      const T e = src[x];
+      scalars[place_in(x / V) * V + x % V] = e;
+      best = fmaxf(best, fminf(E::get(e), INFINITY));
     };
     const int lead = min(n, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(src) & 15)) % 16 / sizeof(T)));
-    if (tid < lead) put(tid, E::get(src[tid]));
     const int vecs = (n - lead) / V;
     const uint4* body = reinterpret_cast<const uint4*>(src + lead);
     constexpr int kAhead = 4;
@@ -481,60 +576,47 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         if (i0 + a * kThreads < vecs) in[a] = __ldcs(body + i0 + a * kThreads);
 #pragma unroll
       for (int a = 0; a < kAhead; ++a) {
-        if (i0 + a * kThreads >= vecs) continue;
-        const int x = lead + (i0 + a * kThreads) * V;
-        float v[V];
-        const T* e = reinterpret_cast<const T*>(&in[a]);
+        const int i = i0 + a * kThreads;
+        if (i >= vecs) continue;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          v[i] = fminf(E::get(e[i]), INFINITY);
+        for (int h = 0; h < V / 4; ++h) {
+          const float4 v = four<TYPE>(in[a], h);
+          best = max3(best, fminf(v.x, INFINITY), fminf(v.y, INFINITY));
+          best = max3(best, fminf(v.z, INFINITY), fminf(v.w, INFINITY));
         }
         if (lead == 0) {
-#pragma unroll
-          for (int c = 0; c < V / 4; ++c)
-            vals[chunk_at(x / 4 + c)] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+          vals[place_in(i)] = in[a];
         } else {
+          const T* e = reinterpret_cast<const T*>(&in[a]);
 #pragma unroll
-          for (int i = 0; i < V; ++i) scalars[chunk_at((x + i) >> 2) * 4 + ((x + i) & 3)] = v[i];
-        }
-        float mx = max3(v[0], v[1], fmaxf(v[2], v[3]));
-        if constexpr (V == 8) mx = max3(mx, max3(v[4], v[5], v[6]), v[7]);
-        if (mx > best) {
-          best = mx;
-#pragma unroll
-          for (int i = V - 1; i >= 0; --i)
-            if (v[i] == mx) best_at = x + i;
+          for (int k = 0; k < V; ++k) {
+            const int x = lead + i * V + k;
+            scalars[place_in(x / V) * V + x % V] = e[k];
+          }
         }
       }
     }
-    for (int x = lead + vecs * V + tid; x < chunks * 4; x += kThreads) {
-      if (x < n) put(x, E::get(src[x]));
-      else scalars[chunk_at(x >> 2) * 4 + (x & 3)] = -INFINITY;
+    for (int x = tid; x < lead; x += kThreads) put(x);
+    for (int x = lead + vecs * V + tid; x < all_vecs * V; x += kThreads) {
+      if (x < n) put(x);
+      else scalars[place_in(x / V) * V + x % V] = E::lowest();
     }
   }
-  auto warp_max = [](u64 v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const u64 w = __shfl_xor_sync(0xffffffffu, v, o);
-      v = w > v ? w : v;
-    }
-    return v;
-  };
+  const uint32_t best_key = best == -INFINITY ? 0 : key_of(best);
   {
-    const u64 w = warp_max(best == -INFINITY ? 0 : place_of(best, first + best_at));
-    if (lane == 0) s.best[warp] = w;
+    const uint32_t k = __reduce_max_sync(0xffffffffu, best_key);
+    if (lane == 0) s.best[warp] = k;
   }
   if (tid == 0) {
     s.run = -1;
-    s.listed = 0;
+    s.first = 0x7fffffff;
   }
   const bool few = top_k > 1 && top_k <= kFew && top_k < p.vocab;
   if (few) {  // the upper bits of the part's (top_k / CTAs)-th largest of the threads' best
     const int want = (top_k + cs - 1) / cs;
-    const uint32_t key = best == -INFINITY ? 0 : key_of(best);
     uint32_t low = 0;
     for (uint32_t bit = 0x80000000u; bit >= 0x1000u; bit >>= 1) {
-      const int have = __syncthreads_count(key >= (low | bit));
+      const int have = __syncthreads_count(best_key >= (low | bit));
       if (have >= want) low |= bit;
       if (have == want) break;
     }
@@ -542,35 +624,60 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   }
   __syncthreads();
   if (warp == 0) {
-    const u64 w = warp_max(lane < kWarps ? s.best[lane] : 0);
-    if (lane == 0) s.top = w;
+    const uint32_t k = __reduce_max_sync(0xffffffffu, lane < kWarps ? s.best[lane] : 0);
+    if (lane == 0) s.top = k;
   }
   __syncthreads();
   if (cs > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   if (!meet()) return;
-  const u64 top = warp_max(lane < cs ? (cs > 1 ? peer(&s.top, lane) : s.top) : 0);
+  const uint32_t top = __reduce_max_sync(0xffffffffu, lane < cs ? (cs > 1 ? peer(&s.top, lane) : s.top) : 0);
+  const float most = logit_of(top);
 
-  const bool bad = top == 0 || logit_of(static_cast<uint32_t>(top >> kIndexBits)) == INFINITY ||
+  const bool bad = top == 0 || most == INFINITY ||
                    !(temperature >= 0.f && temperature < INFINITY) || !(u >= 0.f && u < 1.f) || top_p != top_p ||
                    min_p != min_p;
   const bool only_first = temperature == 0.f || top_k == 1 || top_p <= 0.f || min_p > 1.f;
   float* prow = p.probs ? p.probs + row * p.probs_stride + first : nullptr;
-  if (bad || only_first) {
+  // Calls f(four entries, index of the first) for the thread's run, in order.
+  auto each = [&](auto&& f) {
+#pragma unroll 1
+    for (int j = 0; j < run_vecs; ++j) {
+      const uint4 raw = run[j];
+#pragma unroll 1
+      for (int h = 0; h < V / 4; ++h) f(four<TYPE>(raw, h), first + run_at + j * V + 4 * h);
+    }
+  };
+  if (bad) {
     arrive();
     if (rank == 0 && tid == 0) {
-      p.tokens[row] = bad ? -1 : index_of(top);
-      if (p.logprobs) p.logprobs[row] = bad ? NAN : 0.f;
-      if (bad) report_error(p.err, SV_DEVERR_BAD_VALUE);
+      p.tokens[row] = -1;
+      if (p.logprobs) p.logprobs[row] = NAN;
+      report_error(p.err, SV_DEVERR_BAD_VALUE);
     }
-    if (prow) {
-      const int one = index_of(top) - first;
-      for (int x = tid; x < n; x += kThreads) prow[x] = bad ? NAN : (x == one ? 1.f : 0.f);
-    }
+    if (prow)
+      for (int x = tid; x < n; x += kThreads) prow[x] = NAN;
     wait();  // no CTA leaves while another reads its slots
     return;
   }
+  if (only_first) {
+    each([&](const float4& v, int x) {
+      if (most_of(v) < most) return;
+      atomicMin(&s.first, v.x == most ? x : v.y == most ? x + 1 : v.z == most ? x + 2 : x + 3);
+    });
+    if (!meet()) return;
+    const int one = __reduce_min_sync(0xffffffffu, lane < cs ? (cs > 1 ? peer(&s.first, lane) : s.first) : 0x7fffffff);
+    arrive();
+    if (rank == 0 && tid == 0) {
+      p.tokens[row] = one;
+      if (p.logprobs) p.logprobs[row] = 0.f;
+    }
+    if (prow)
+      for (int x = tid; x < n; x += kThreads) prow[x] = first + x == one ? 1.f : 0.f;
+    wait();
+    return;
+  }
   Row r;
-  r.m = logit_of(static_cast<uint32_t>(top >> kIndexBits));
+  r.m = most;
   {
     // the quotient and its remainder's, 2^-46 of it; beyond 10^37 equal logits alone have weight
     constexpr float kLog2eHi = 0x1.715476p+0f, kLog2eLo = 0x1.4ae0cp-26f;
@@ -593,30 +700,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   auto bin_of = [&](float l) {
     return static_cast<int>(__float_as_uint(fminf((r.m - l) * bin_scale, kBins - 1.f) + 8388608.f) & (kBins - 1));
   };
-  auto most_of = [](const float4& v) { return max3(v.x, v.y, fmaxf(v.z, v.w)); };
-  // The near entries of a chunk by their bits in the run; the chunk without them.
-  auto take_near = [&](float4& v, int x) {
-    u64 bits = 0;
-    if (max3(v.x, v.y, fmaxf(v.z, v.w)) > near_logit) {
-      const int at = x - first - tid * per * 4;
-      if (v.x > near_logit) bits |= 1ull << at, v.x = -INFINITY;
-      if (v.y > near_logit) bits |= 2ull << at, v.y = -INFINITY;
-      if (v.z > near_logit) bits |= 4ull << at, v.z = -INFINITY;
-      if (v.w > near_logit) bits |= 8ull << at, v.w = -INFINITY;
-    }
-    return bits;
-  };
-  auto far_sum = [&](const Far& far) {
-    return all_near ? 0 : static_cast<u64>(__float2ull_rn((f2_lo(far.sum) + f2_hi(far.sum)) * 0x1p45f));
-  };
-  auto scalar_at = [&](int x) { return scalars[chunk_at(x >> 2) * 4 + (x & 3)]; };
+  auto scalar_at = [&](int x) { return E::get(scalars[place_in(x / V) * V + x % V]); };
   auto entry = [](const float4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; };
-  // Calls f(chunk, index of its first entry) for the thread's run, in order.
-  auto each = [&](auto&& f) {
-    const int q1 = min((tid + 1) * per, chunks);
-#pragma unroll 1
-    for (int q = tid * per; q < q1; ++q) f(vals[chunk_at(q)], first + 4 * q);
-  };
   // Sum over the cluster of a value per CTA, and over the ranks before this one.
   auto over_cluster = [&](const u64* slot, u64& before) {
     const u64 x = lane < cs ? (cs > 1 ? peer(slot, lane) : *slot) : 0;
@@ -836,17 +921,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       };
       // first of the near entries alone, with all weights' sum
       if (by_mass && near_only) {
-        u64 large = 0;  // of the run: the near entries
-        Far far{0, gone_logit};
-        each([&](float4 v, int x) {
-          large |= take_near(v, x);
-          add_far<TYPE != SV_FP32>(r, v, far);
-        });
-        all = far_sum(far);
-        for (; large != 0; large &= large - 1) {
-          const int x = tid * per * 4 + __ffsll(large) - 1;
+        const Added run_sum = add_run<TYPE>(run, run_vecs, first + run_at, r,
+                                            Limits{-INFINITY, 0x7fffffff, near_logit, gone_logit, false, false});
+        all = run_sum.far;
+        for (u64 large = run_sum.large; large != 0; large &= large - 1) {
+          const int x = run_at + __ffsll(large) - 1;
           const float l = scalar_at(x);
-          const u64 w = weight_near(r, l, s.powers);
+          const u64 w = weight_of(r, l, s.powers);
           all += w;
           put(l, first + x, w);
         }
@@ -1006,32 +1087,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   auto kept_sum = [&](u64 place, u64 floor_weight, u64& end, u64& mine, u64& base) -> u64 {
     const float floor_logit = place ? logit_of(static_cast<uint32_t>(place >> kIndexBits)) : -INFINITY;
     const int floor_index = place ? index_of(place) : 0x7fffffff;
-    mine = 0;
-    const bool filtered = place != 0 || floor_weight != 0;
     // with min-p the entries that may pass are weighed one by one, the others left out
-    const float one_by_one = floor_weight != 0 ? r.m - (log2f(1.f / min_p) + 1.f) / r.chi - margin : near_logit;
-    u64 large = 0;  // of the run: entries to be weighed one by one
-    Far far{0, gone_logit};
-    each([&](float4 v, int x) {
-      const float most = most_of(v);
-      if (most < floor_logit || (floor_weight != 0 && most <= one_by_one)) return;
-      if (most > one_by_one || filtered) {
-        const int at = x - first - tid * per * 4;
-        auto look = [&](float& l, int i) {
-          const bool in = l > floor_logit || (l == floor_logit && x + i <= floor_index);
-          if (in && l > one_by_one) large |= 1ull << (at + i);
-          if (!in || l > one_by_one || floor_weight != 0) l = -INFINITY;
-        };
-        look(v.x, 0);
-        look(v.y, 1);
-        look(v.z, 2);
-        look(v.w, 3);
-      }
-      add_far<TYPE != SV_FP32>(r, v, far);
-    });
-    mine = far_sum(far);
-    for (; large != 0; large &= large - 1) {
-      const u64 w = weight_of(r, scalar_at(tid * per * 4 + __ffsll(large) - 1), s.powers);
+    const bool least_too = floor_weight != 0;
+    const float one_by_one = least_too ? r.m - (log2f(1.f / min_p) + 1.f) / r.chi - margin : near_logit;
+    const Added run_sum = add_run<TYPE>(run, run_vecs, first + run_at, r,
+                                        Limits{floor_logit, floor_index, one_by_one, gone_logit, place != 0, least_too});
+    mine = least_too ? 0 : run_sum.far;
+    for (u64 large = run_sum.large; large != 0; large &= large - 1) {
+      const u64 w = weight_of(r, scalar_at(run_at + __ffsll(large) - 1), s.powers);
       if (w >= floor_weight) mine += w;
     }
     end = block_scan(mine, s.scan);
@@ -1076,8 +1139,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     // (the weights one by one may sum to a little less than the run's sum: the last then)
     u64 at = s.before, w_last = 0;
     int x_last = -1;
-    const int x1 = min((s.run + 1) * per, chunks) * 4;
-    for (int x0 = s.run * per * 4; x0 < x1; x0 += 32) {
+    const int x1 = min((s.run + 1) * per * V, n);
+    for (int x0 = s.run * per * V; x0 < x1; x0 += 32) {
       const int x = x0 + lane;
       const float l = x < x1 ? scalar_at(x) : -INFINITY;
       bool kept = keeps(l, first + x);
@@ -1184,9 +1247,11 @@ extern "C" sv_status sv_sample_tokens(const sv_sample_params* c, sv_stream_t str
          c->vocab >= 2048 * p.cluster)
     p.cluster *= 2;
   p.slice = ((c->vocab + p.cluster - 1) / p.cluster + 7) / 8 * 8;
-  const int chunks = p.slice / 4;
-  p.val_bytes = static_cast<uint32_t>((chunks + chunks / 8 + 1) * 16);
-  const size_t smem = p.val_bytes + 3 * sample::kBins * 4 + sample::kMost * 8;
+  const int vecs = p.slice / (c->dtype == SV_FP32 ? 4 : 8);
+  p.per = (vecs + sample::kThreads - 1) / sample::kThreads;
+  p.per_inverse = ((1u << 18) + p.per - 1) / p.per;
+  p.val_bytes = static_cast<uint32_t>((vecs + (p.per & 1 ? 0 : vecs / p.per) + 1) * 16);
+  const size_t smem = p.val_bytes + 2 * sample::kMost * 8;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (c->dtype == SV_FP32) return sample::launch<SV_FP32>(p, c->rows, smem, s);
   return c->dtype == SV_FP16 ? sample::launch<SV_FP16>(p, c->rows, smem, s) : sample::launch<SV_BF16>(p, c->rows, smem, s);
