@@ -367,50 +367,64 @@ __device__ __forceinline__ u64 block_all(const u64* slots) {
   return v;
 }
 
-// Descending order of a[0 .. size), a power of two.  Up to an entry per thread the
-// steps within a warp are exchanges of registers.
+// Descending order of a[0 .. size), a power of two: N consecutive entries per thread, steps
+// within a thread and a warp in registers.
+template <int N>
 __device__ __noinline__ void sort(u64* a, int size) {
   const int tid = threadIdx.x;
+  const bool in = tid * N < size;
+  u64 v[N];
   __syncwarp();
   __syncthreads();
-  if (size <= kThreads) {
-    u64 v = tid < size ? a[tid] : 0;
-    for (int len = 2; len <= size; len *= 2) {
-      const bool descending = (tid & len) == 0;
-      for (int step = len / 2; step > 0; step /= 2) {
-        u64 w;
-        if (step >= 32) {
-          __syncthreads();
-          if (tid < size) a[tid] = v;
-          __syncthreads();
-          w = tid < size ? a[tid ^ step] : 0;
-        } else {
-          w = __shfl_xor_sync(0xffffffffu, v, step);
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = in ? a[tid * N + i] : 0;
+  for (int len = 2; len <= size; len *= 2) {
+    for (int step = len / 2; step >= N; step /= 2) {
+      const bool first = (tid * N & step) == 0, descending = (tid * N & len) == 0;
+      if (step >= 32 * N) {
+        __syncthreads();
+        if (in) {
+#pragma unroll
+          for (int i = 0; i < N; ++i) a[tid * N + i] = v[i];
         }
-        const bool first = (tid & step) == 0;
-        v = (first == descending) == (v > w) ? v : w;
+        __syncthreads();
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        u64 w;
+        if (step >= 32 * N) w = in ? a[(tid * N ^ step) + i] : 0;
+        else w = __shfl_xor_sync(0xffffffffu, v[i], step / N);
+        v[i] = (first == descending) == (v[i] > w) ? v[i] : w;
       }
     }
-    __syncthreads();
-    if (tid < size) a[tid] = v;
-  } else {
-    for (int len = 2; len <= size; len *= 2) {
-      for (int step = len / 2; step > 0; step /= 2) {
-        for (int i = tid; i < size / 2; i += kThreads) {
-          const int x = 2 * i - (i & (step - 1)), y = x + step;
-          const u64 vx = a[x], vy = a[y];
-          if ((vx < vy) == ((x & len) == 0)) {
-            a[x] = vy;
-            a[y] = vx;
-          }
+#pragma unroll
+    for (int step = N / 2; step > 0; step /= 2) {
+      if (step > len / 2) continue;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        if (i & step) continue;
+        const bool descending = ((tid * N + i) & len) == 0;
+        if ((v[i] < v[i | step]) == descending) {
+          const u64 w = v[i];
+          v[i] = v[i | step];
+          v[i | step] = w;
         }
-        // (steps up to 32 stay within a warp's 64 entries)
-        if (step > 32 || (step == 1 && len >= 64)) __syncthreads();
-        else __syncwarp();
       }
     }
   }
   __syncthreads();
+  if (in) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) a[tid * N + i] = v[i];
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ void sort(u64* a, int size) {
+  static_assert(kMost <= 4 * kThreads, "entries per thread");
+  if (size <= kThreads) sort<1>(a, size);
+  else if (size <= 2 * kThreads) sort<2>(a, size);
+  else sort<4>(a, size);
 }
 
 template <int TYPE>
@@ -736,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   };
   // The cluster's listed entries, m <= kMost, in `sorted` (one CTA); its size.
   auto pull = [&](int m) {
-    int size = 2;
+    int size = 4;
     while (size < m) size *= 2;
     const int have = lane < cs ? (cs > 1 ? peer(&s.listed, lane) : s.listed) : 0;
     int to = have;
@@ -818,7 +832,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       }
       kept = static_cast<int>(block_scan(kept, s.scan));
       kept = static_cast<int>(block_all(s.scan));
-      size = 2;
+      size = 4;
       while (size < cut) size *= 2;
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
@@ -881,6 +895,40 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   auto find = [&](bool by_mass, u64 target) -> u64 {
     int bin = -1, shift = 32 + kIndexBits, in_bin = 0, m = 0;
     u64 prefix = 0, above = 0, above_mass = 0;
+    if (by_mass) {
+      // the near entries listed, with all weights' sum: mostly they weigh enough
+      if (tid == 0) s.listed = 0;
+      __syncthreads();
+      const Added run_sum = add_run<TYPE>(run, run_vecs, first + run_at, r,
+                                          Limits{-INFINITY, 0x7fffffff, near_logit, gone_logit, false, false});
+      u64 near = 0;
+      for (u64 large = run_sum.large; large != 0; large &= large - 1) {
+        const int x = run_at + __ffsll(large) - 1;
+        const float l = scalar_at(x);
+        near += weight_of(r, l, s.powers);
+        const int at = atomicAdd(&s.listed, 1);
+        if (at < kMost) list[at] = place_of(l, first + x);
+      }
+      block_scan(near, s.scan);
+      const u64 near_sum = block_all(s.scan);
+      block_scan(near + run_sum.far, s.scan);
+      const u64 sum = block_all(s.scan);
+      if (tid == 0) {
+        s.mass = near_sum;
+        s.all = sum;
+      }
+      if (!meet()) return gone();
+      u64 unused;
+      if (target == 0) target = max(1ull, times<true>(over_cluster(&s.all, unused), top_p));
+      const bool enough = over_cluster(&s.mass, unused) >= target;
+      const int have = lane < cs ? (cs > 1 ? peer(&s.listed, lane) : s.listed) : 0;
+      const int listed = static_cast<int>(__reduce_add_sync(0xffffffffu, have));
+      if (enough && listed <= kMost) {
+        draw_from_list(listed, listed, true, target);
+        return gone();
+      }
+      if (!meet()) return gone();  // the numbers listed are read
+    }
     // what weighs less than `light` is never kept (see above; 1 - top_p rounded down), and
     // an entry beyond this exponent weighs less
     float reach = INFINITY;
@@ -888,10 +936,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       const u64 light = times<false>(1ull << kUnit, (1.f - top_p) * (1.f - 0x1p-20f)) / static_cast<u64>(p.vocab);
       reach = static_cast<float>(kUnit - 63 + __clzll(max(light, 1ull))) + 0.5f;
     }
-    bool near_only = by_mass;
-    auto counts = [&](float l) {
-      return near_only ? l > near_logit : by_mass ? (r.m - l) * r.chi < reach : l > -INFINITY;
-    };
+    auto counts = [&](float l) { return by_mass ? (r.m - l) * r.chi < reach : l > -INFINITY; };
     const u64 given = target;
     bool whole = false;
     for (int round = 0;; ++round) {
@@ -902,7 +947,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         if (by_mass) bin_lo[b] = bin_hi[b] = 0;
       }
       __syncthreads();
-      u64 all = 0;
       auto put = [&](float l, int index, u64 w) {
         if (!counts(l)) return;
         int d = bin_of(l);
@@ -919,38 +963,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           if (hi) atomicAdd(bin_hi + d, hi);
         }
       };
-      // first of the near entries alone, with all weights' sum
-      if (by_mass && near_only) {
-        const Added run_sum = add_run<TYPE>(run, run_vecs, first + run_at, r,
-                                            Limits{-INFINITY, 0x7fffffff, near_logit, gone_logit, false, false});
-        all = run_sum.far;
-        for (u64 large = run_sum.large; large != 0; large &= large - 1) {
-          const int x = run_at + __ffsll(large) - 1;
-          const float l = scalar_at(x);
-          const u64 w = weight_of(r, l, s.powers);
-          all += w;
-          put(l, first + x, w);
-        }
-      } else {
-        each([&](const float4& v, int x) {
-          if (!counts(most_of(v))) return;
+      each([&](const float4& v, int x) {
+        if (!counts(most_of(v))) return;
 #pragma unroll 1
-          for (int i = 0; i < 4; ++i) {
-            const float l = entry(v, i);
-            put(l, x + i, by_mass && counts(l) ? weight_of(r, l, s.powers) : 0);
-          }
-        });
-      }
-      if (by_mass && near_only) {
-        block_scan(all, s.scan);
-        const u64 sum = block_all(s.scan);
-        if (tid == 0) s.all = sum;
-      }
+        for (int i = 0; i < 4; ++i) {
+          const float l = entry(v, i);
+          put(l, x + i, by_mass && counts(l) ? weight_of(r, l, s.powers) : 0);
+        }
+      });
       if (!meet()) return gone();
-      if (by_mass && near_only && target == 0) {
-        u64 unused;
-        target = max(1ull, times<true>(over_cluster(&s.all, unused), top_p));
-      }
       // this CTA's part of the bins, over the cluster
       const int part = kBins / cs, each_bins = max(1, part / kThreads);
       const int b0 = rank * part + tid * each_bins;
@@ -997,13 +1018,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         if (lane >= o) to_c += uc, to_m += um;
       }
       const unsigned owners = __ballot_sync(0xffffffffu, lane < cs && (by_mass ? to_m : to_c) >= target);
-      if (owners == 0) {
-        if (!by_mass || !near_only) return 0;
-        near_only = false;  // once more, with the far entries
-        round = -1;
-        if (!meet()) return gone();
-        continue;
-      }
+      if (owners == 0) return 0;  // (round 0 alone)
       const int owner = __ffs(owners) - 1;
       if (rank == owner) {
         at_c += __shfl_sync(0xffffffffu, to_c - pc, rank);
