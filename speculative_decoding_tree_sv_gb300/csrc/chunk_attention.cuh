@@ -86,6 +86,11 @@ struct PrefixParams : Params {
   float* whole_o;     // [2 parts][rows][Hq][D] O / l of units that no boundary cuts
   float* whole_lse;   // [2 parts][rows][Hq]
   int2* tile_rec;     // [2 parts][rows][Hkv] at a tile unit's first token: first and last CTA, -1 where it is whole
+  // written by the call's first kernel (prefix_attention.cu)
+  int4* entries;      // [batch][2] the entries (PrefixSeq)
+  longlong2* starts;  // [batch] pages of the row kernel and weight of the tile kernel before the entry, per KV head
+  struct Work* work;  // their sums
+  int* alone;         // whether an entry shares nothing
 };
 
 // One sequence's lengths; n is 0 when it has no work (nothing new, or lengths
@@ -142,11 +147,11 @@ __device__ __forceinline__ Group load_group(const PrefixParams& p, int g) {
 }
 
 // The group of sequence b: the first whose end lies behind it.
-__device__ __forceinline__ int group_of(const PrefixParams& p, int b) {
-  int lo = 0, hi = p.num_groups - 1;
+__device__ __forceinline__ int group_of(const int* cu_groups, int groups, int b) {
+  int lo = 0, hi = groups - 1;
   while (lo < hi) {
     const int mid = (lo + hi) / 2;
-    if (p.cu_groups[mid + 1] > b) hi = mid;
+    if (cu_groups[mid + 1] > b) hi = mid;
     else lo = mid + 1;
   }
   return lo;
@@ -179,14 +184,27 @@ __device__ __forceinline__ PrefixSeq own_part(const PrefixParams& p, const Group
   return s;
 }
 
-__device__ __forceinline__ PrefixSeq load_seq(const PrefixParams& p, int v, bool report) {
-  if (v >= p.num_groups) {
-    const int b = v - p.num_groups;
-    return own_part(p, load_group(p, group_of(p, b)), b, report);
+__device__ __forceinline__ PrefixSeq load_seq(const PrefixParams& p, int v, bool) {
+  const int4 a = __ldcg(p.entries + 2 * v), b = __ldcg(p.entries + 2 * v + 1);
+  return {a.x, a.y, a.z, a.w, b.x, b.y, b.z};
+}
+
+// The last entry that starts at or before `pos` of the row kernel's pages (PAGES) or the
+// tile kernel's weights, 32 probes at a time; every lane returns it.
+template <bool PAGES>
+__device__ __forceinline__ int entry_at(const PrefixParams& p, long long pos) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = p.batch;  // starts[lo] <= pos
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32;
+    const int k = lo + lane * step;
+    bool le = false;
+    if (k < hi) le = (PAGES ? __ldcg(&p.starts[k].x) : __ldcg(&p.starts[k].y)) <= pos;
+    const int last = 31 - __clz(__ballot_sync(0xffffffffu, le) | 1u);
+    lo += last * step;
+    hi = min(hi, lo + step);
   }
-  const Group x = load_group(p, v);
-  if (!x.ok && report) report_error(p.err, SV_DEVERR_BAD_LENGTH);
-  return {x.n0, x.shared ? x.n : 0, x.prefix, x.first, 0, kShared, part_row(p, x, x.n0)};
+  return lo;
 }
 
 // An entry's row of the block table.

@@ -183,7 +183,14 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
     RowSeq<P> mine;  // of sequence `lane`: the only round when there are at most 32
     int blocks = gridDim.x;
     const int batch = p.batch << SHIFT;
-    if (side_by_side(p)) {
+    if constexpr (P::kPrefix) {
+      mine = RowSeq<P>{};
+      const Work sum = *p.work;
+      total = sum.pages;
+      const int own = side_by_side(p) ? row_sms(p, sum) : 0;
+      if (own > 0) blocks = own;
+      worker = warp * blocks + blockIdx.x;
+    } else if (side_by_side(p)) {
       Work sum{};
       sum.lightest = 1ll << 60;
       for (int b0 = 0; b0 < batch; b0 += 32) {
@@ -228,11 +235,18 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
     hi = takes ? share.start(worker + 1) : 0;
     long long base = 0;
     int bsel = batch;
-    if (batch == 1) {
+    if constexpr (P::kPrefix) {
+      if (hi > lo) {
+        bsel = entry_at<true>(p, Share::divide(lo, p.num_kv_heads));
+        base = __ldcg(&p.starts[bsel].x) * p.num_kv_heads;
+        start.seq = row_seq(p, bsel, SHIFT, false);
+      }
+    }
+    if (!P::kPrefix && batch == 1) {
       bsel = 0;
       start.seq = mine;
     }
-    for (int b0 = 0; b0 < batch && bsel == batch; b0 += 32) {
+    for (int b0 = 0; !P::kPrefix && b0 < batch && bsel == batch; b0 += 32) {
       const int b = b0 + lane;
       if (batch > 32) {
         mine.pages = 0;
@@ -632,10 +646,12 @@ static sv_status launch(const LaunchOf<P>& l) {
 
 template <int D, bool FP16, class P>
 static sv_status launch(const LaunchOf<P>& l) {
-  if constexpr (!P::kPrefix) {
+  if constexpr (P::kPrefix) {
+    return launch<D, FP16, 0, false>(l);
+  } else {
     if (l.p.row_cluster > 1) return launch<D, FP16, 0, true>(l);
+    return l.p.row_shift ? launch<D, FP16, 1, false>(l) : launch<D, FP16, 0, false>(l);
   }
-  return l.p.row_shift ? launch<D, FP16, 1, false>(l) : launch<D, FP16, 0, false>(l);
 }
 
 template <class P>

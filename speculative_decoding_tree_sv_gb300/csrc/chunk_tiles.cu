@@ -194,7 +194,12 @@ __device__ __forceinline__ bool deal_range(const P& p, const Share& share, int c
   const int lane = threadIdx.x & 31;
   long long base = 0;
   int bsel = p.batch == 1 ? 0 : p.batch;
-  for (int b0 = 0; b0 < p.batch && bsel == p.batch; b0 += 32) {
+  if constexpr (P::kPrefix) {
+    bsel = entry_at<false>(p, Share::divide(lo, p.num_kv_heads));
+    base = __ldcg(&p.starts[bsel].y) * p.num_kv_heads;
+    mine = tile_seq(p, bsel, false);
+  }
+  for (int b0 = 0; !P::kPrefix && b0 < p.batch && bsel == p.batch; b0 += 32) {
     const int b = b0 + lane;
     TileSeq<P> t = mine;
     if (b0 > 0 || p.batch > 32) {
@@ -302,7 +307,9 @@ __device__ void deal_pieces(const P& p, int cta, Publish&& publish, NearEnd&& ne
     // the call's work, and this kernel's CTAs
     Work sum{};
     sum.lightest = 1ll << 60;
-    if (p.batch == 1) {  // (a prompt alone: no sums)
+    if constexpr (P::kPrefix) {
+      sum = *p.work;
+    } else if (p.batch == 1) {  // (a prompt alone: no sums)
       mine = tile_seq(p, 0, report);
       sum = work_of(p, mine, 0);
     } else {
@@ -336,6 +343,7 @@ __device__ void deal_pieces(const P& p, int cta, Publish&& publish, NearEnd&& ne
     whole = p.whole_tiles || (longest <= even.each + kCutWeight && units < (1 << 30));
     if (whole) {
       all = static_cast<int>(units);
+      if (P::kPrefix && lane < p.batch) mine = tile_seq(p, lane, false);
       if (p.batch == 1 && lane > 0) mine.units = 0;
     } else {
       const long long most = total / kMinWeight;

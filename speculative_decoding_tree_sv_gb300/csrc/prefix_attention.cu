@@ -24,6 +24,98 @@
 namespace sv {
 namespace chunk {
 
+constexpr int kEntryThreads = 1024;
+constexpr int kStagedGroups = 2048;
+
+// The list's entries, where each starts and their sums, in one CTA: the kernels that
+// follow read an entry with one load (made by every warp of theirs from the lengths,
+// over 80 entries, this took 20 us).
+__global__ void __launch_bounds__(kEntryThreads) prefix_entries_kernel(const __grid_constant__ PrefixParams p) {
+  __shared__ int s_groups[kStagedGroups + 1];
+  __shared__ long long s_pages[32], s_weight[32];
+  __shared__ Work s_work[32];
+  __shared__ int s_alone;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) s_alone = 0;
+  griddep_wait();
+  griddep_launch_dependents();  // (they wait for this grid's end)
+  const int threads = blockDim.x, warps = threads / 32;
+  const bool staged = p.num_groups <= kStagedGroups;
+  if (staged)
+    for (int i = tid; i <= p.num_groups; i += threads) s_groups[i] = p.cu_groups[i];
+  __syncthreads();
+  Work sum{};
+  sum.lightest = 1ll << 60;
+  long long pages_before = 0, weight_before = 0;
+  for (int v0 = 0; v0 < p.batch; v0 += threads) {
+    const int v = v0 + tid;
+    PrefixSeq s{};
+    TileSeq<PrefixParams> t{};
+    long long pages = 0;
+    if (v < p.batch) {
+      const int g = v < p.num_groups ? v : group_of(staged ? s_groups : p.cu_groups, p.num_groups, v - p.num_groups);
+      const Group x = load_group(p, g);
+      if (v < p.num_groups) {
+        if (!x.ok) report_error(p.err, SV_DEVERR_BAD_LENGTH);
+        s = {x.n0, x.shared ? x.n : 0, x.prefix, x.first, 0, kShared, part_row(p, x, x.n0)};
+      } else {
+        s = own_part(p, x, v - p.num_groups, true);
+        if (s.part == kAlone && s.n > 0) s_alone = 1;
+      }
+      p.entries[2 * v] = make_int4(s.n0, s.n, s.ctx, s.row);
+      p.entries[2 * v + 1] = make_int4(s.first_page, s.part, s.at, 0);
+      t.s = s;
+      if (s.n > 0 && in_rows(p, s.n)) {
+        const Keys k = unit_keys(p, s, 0, s.n);
+        pages = (k.end + kPage - 1) / kPage - k.first_page;
+      } else if (s.n > 0) {
+        t.units = (s.n + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens);
+        t.weight = full_weight(p, s, t.units - 1) + last_weight(p, s, t.units);
+      }
+    }
+    long long to_p = pages, to_w = t.weight;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long up = __shfl_up_sync(0xffffffffu, to_p, o), uw = __shfl_up_sync(0xffffffffu, to_w, o);
+      if (lane >= o) to_p += up, to_w += uw;
+    }
+    if (lane == 31) {
+      s_pages[warp] = to_p;
+      s_weight[warp] = to_w;
+    }
+    Work mine{};
+    mine.lightest = 1ll << 60;
+    add_round(mine, work_of(p, t, pages));
+    if (lane == 0) s_work[warp] = mine;
+    __syncthreads();
+    long long bp = lane < warp ? s_pages[lane] : 0, bw = lane < warp ? s_weight[lane] : 0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      bp += __shfl_xor_sync(0xffffffffu, bp, o);
+      bw += __shfl_xor_sync(0xffffffffu, bw, o);
+    }
+    if (v < p.batch) p.starts[v] = make_longlong2(pages_before + bp + to_p - pages, weight_before + bw + to_w - t.weight);
+    Work round{};
+    round.lightest = 1ll << 60;
+    Work other{};
+    other.lightest = 1ll << 60;
+    if (lane < warps) other = s_work[lane];
+    add_round(round, other);
+    pages_before += round.pages;
+    weight_before += round.weight;
+    sum.weight += round.weight;
+    sum.units += round.units;
+    sum.pages += round.pages;
+    sum.heaviest = max(sum.heaviest, round.heaviest);
+    sum.lightest = min(sum.lightest, round.lightest);
+    __syncthreads();
+  }
+  if (tid == 0) {
+    *p.work = sum;
+    *p.alone = s_alone;
+  }
+}
+
 // The pieces of a row's part: piece i lies `o_step` columns of four (`l_step` sums)
 // behind the worker's before, a unit's first one in its worker's second slot.
 struct Pieces {
@@ -74,85 +166,170 @@ __device__ __forceinline__ Pieces pieces_of(const PrefixParams& p, int v, int pa
   return x;
 }
 
-// 16 rows of an M tile's worth of a shared group's rows: half a warp per 16 rows, one
-// or two groups of four columns per thread, four pieces in flight.
-template <int D, bool FP16>
-__device__ __forceinline__ void combine_shared(const PrefixParams& p, int g, int kh, int tile, int sub) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Group x = load_group(p, g);
-  const int r = sub * 16 + (lane & 15), i = tile * p.tile_tokens + r / p.group, hg = r % p.group;
-  if (!x.shared || r >= p.tile_tokens * p.group || i >= x.n) return;
-  const int t = x.n0 + i;
-  // the sequence of token t: most bring one
-  int b = x.first + i;
-  if (b >= x.last || p.cu_tokens[b] > t || p.cu_tokens[b + 1] <= t) {
-    int lo = x.first, hi = x.last - 1;
+// The sequence of token t of entry g (most bring one token), false where no row of it is
+// to be written.
+__device__ __forceinline__ bool sequence_of(const PrefixParams& p, const PrefixSeq& g, int t, int& b, PrefixSeq& s) {
+  b = min(g.row + (t - g.n0), p.num_seqs - 1);
+  s = load_seq(p, p.num_groups + b, false);
+  if (t < s.n0 || t >= s.n0 + s.n) {
+    int lo = g.row, hi = p.num_seqs - 1;
     while (lo < hi) {
       const int mid = (lo + hi) / 2;
       if (p.cu_tokens[mid + 1] > t) hi = mid;
       else lo = mid + 1;
     }
     b = lo;
+    s = load_seq(p, p.num_groups + b, false);
   }
-  const PrefixSeq s = own_part(p, x, b, false);
-  if (s.n == 0 || t < s.n0 || t >= s.n0 + s.n) return;
-  constexpr int kCols = D / 4 / (2 * kCombineWarps);
-  const int col = (warp * 2 + (lane >> 4)) * kCols;
-  float acc[kCols][4], mx = -INFINITY, wsum = 0.f;
+  return s.part == kOwn && t >= s.n0 && t < s.n0 + s.n;
+}
+
+// Rows of a group of up to 16, whose prefix may lie in 150 pieces: `warps` warps of the
+// block per row share its pieces, a lane per D / 32 columns, four pieces in flight.  (One
+// sample over 16000 tokens, half a warp per piece after the other: 128 us of call.)
+template <int D, bool FP16>
+__device__ __forceinline__ void combine_few(const PrefixParams& p, int g, int kh, int block, int warps) {
+  constexpr int E = D / 32;
+  __shared__ float part_o[kCombineWarps][D];
+  __shared__ float part_m[kCombineWarps], part_w[kCombineWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = block * (kCombineWarps / warps) + warp / warps, part = warp % warps;
+  const PrefixSeq x = load_seq(p, g, false);
+  if (x.n == 0 || !in_rows(p, x.n)) return;
+  const int i = r / p.group, hg = r - i * p.group, t = x.n0 + i;
+  int b = 0;
+  PrefixSeq s;
+  const bool live = i < x.n && sequence_of(p, x, t, b, s);
+  float acc[E], mx = -INFINITY, wsum = 0.f;
 #pragma unroll
-  for (int c = 0; c < kCols; ++c)
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  auto add = [&](float l2, float weight, const float* v) {
+    if (l2 == -INFINITY) return;
+    const float m = fmaxf(mx, l2);
+    const float keep = ex2(mx - m), f = ex2(l2 - m);  // keep is 0 at the first, as mx = -inf
+    mx = m;
+    wsum = fmaf(wsum, keep, weight * f);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) acc[c][e] = 0.f;
+    for (int e = 0; e < E; ++e) acc[e] = fmaf(f, v[e], acc[e] * keep);
+  };
+  if (live) {
+    const Pieces parts[2] = {pieces_of<D>(p, g, kShared, x.n, x.at, i, hg, kh),
+                             pieces_of<D>(p, p.num_groups + b, kOwn, s.n, s.at, t - s.n0, hg, kh)};
+    const int all = parts[0].count + parts[1].count;
 #pragma unroll 1
-  for (int part = kShared; part <= kOwn; ++part) {
-    const Pieces u = part == kShared ? pieces_of<D>(p, g, part, x.n, part_row(p, x, x.n0), i, hg, kh)
-                                     : pieces_of<D>(p, p.num_groups + b, part, s.n, s.at, t - s.n0, hg, kh);
-    constexpr int kBatch = 4;
-#pragma unroll 1
-    for (int c0 = 0; c0 < u.count; c0 += kBatch) {
-      float l2[kBatch];
-      float4 v[kBatch][kCols];
+    for (int j0 = part; j0 < all; j0 += 4 * warps) {
+      float l2[4], v[4][E];
 #pragma unroll
-      for (int y = 0; y < kBatch; ++y) {
+      for (int y = 0; y < 4; ++y) {
+        const int j = j0 + y * warps;
         l2[y] = -INFINITY;
-        if (c0 + y >= u.count) continue;
-        const int slot = (u.first + c0 + y) * 2 + (c0 + y == 0 ? 1 : 0);
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[y][e] = 0.f;
+        if (j >= all) continue;
+        const Pieces& u = j < parts[0].count ? parts[0] : parts[1];
+        const int piece = j < parts[0].count ? j : j - parts[0].count;
+        const int slot = (u.first + piece) * 2 + (piece == 0 ? 1 : 0);
         l2[y] = __ldcg(u.lse + static_cast<size_t>(slot) * u.l_step);
-        const float4* src = u.o + slot * u.o_step;
-#pragma unroll
-        for (int c = 0; c < kCols; ++c) v[y][c] = __ldcg(src + (col + c) * u.col_step);
-      }
-#pragma unroll
-      for (int y = 0; y < kBatch; ++y) {
-        if (l2[y] == -INFINITY) continue;  // (a piece without a tile has no sum, and its columns say nothing)
-        const float m = fmaxf(mx, l2[y]);
-        const float keep = mx == m ? 1.f : ex2(mx - m), f = ex2(l2[y] - m);
-        mx = m;
-        wsum = wsum * keep + f;
-#pragma unroll
-        for (int c = 0; c < kCols; ++c) {
-          acc[c][0] = fmaf(f, v[y][c].x, acc[c][0] * keep);
-          acc[c][1] = fmaf(f, v[y][c].y, acc[c][1] * keep);
-          acc[c][2] = fmaf(f, v[y][c].z, acc[c][2] * keep);
-          acc[c][3] = fmaf(f, v[y][c].w, acc[c][3] * keep);
+        const float* src = reinterpret_cast<const float*>(u.o + slot * u.o_step) + lane * E;
+        if constexpr (E == 4) {
+          const float4 f = __ldcg(reinterpret_cast<const float4*>(src));
+          v[y][0] = f.x, v[y][1] = f.y, v[y][2] = f.z, v[y][3] = f.w;
+        } else {
+          const float2 f = __ldcg(reinterpret_cast<const float2*>(src));
+          v[y][0] = f.x, v[y][1] = f.y;
         }
       }
+#pragma unroll
+      for (int y = 0; y < 4; ++y) add(l2[y], 1.f, v[y]);
+    }
+  }
+  if (warps > 1) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) part_o[warp][e * 32 + lane] = acc[e];
+    if (lane == 0) {
+      part_m[warp] = mx;
+      part_w[warp] = wsum;
+    }
+    __syncthreads();
+    if (part > 0) return;
+#pragma unroll 1
+    for (int y = 1; y < warps; ++y) {
+      float v[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = part_o[warp + y][e * 32 + lane];
+      add(part_m[warp + y], part_w[warp + y], v);
+    }
+  }
+  if (!live) return;
+  const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+  const int head = kh * p.group + hg;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + t * p.out_stride +
+                                              static_cast<long long>(head) * D) + lane * (E / 2);
+#pragma unroll
+  for (int e = 0; e < E; e += 2) dst[e / 2] = pack2<FP16>(acc[e] * inv, acc[e + 1] * inv);
+  if (lane == 0 && p.lse != nullptr)
+    p.lse[static_cast<long long>(t) * p.num_q_heads + head] = wsum > 0.f ? (mx + log2f(wsum)) * kLn2 : -INFINITY;
+}
+
+// 16 rows of an M tile's worth of a larger group's rows and 16 of its D / 4 columns of
+// four: half a warp per 16 rows, eight pieces in flight.
+template <int D, bool FP16>
+__device__ __forceinline__ void combine_shared(const PrefixParams& p, int g, int kh, int tile, int sub) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const PrefixSeq x = load_seq(p, g, false);
+  const int col = (sub % (D / 64)) * 16 + warp * 2 + (lane >> 4);
+  const int r = sub / (D / 64) * 16 + (lane & 15), i = tile * p.tile_tokens + r / p.group, hg = r % p.group;
+  if (r >= p.tile_tokens * p.group || i >= x.n || in_rows(p, x.n)) return;
+  const int t = x.n0 + i;
+  int b;
+  PrefixSeq s;
+  if (!sequence_of(p, x, t, b, s)) return;
+  const Pieces parts[2] = {pieces_of<D>(p, g, kShared, x.n, x.at, i, hg, kh),
+                           pieces_of<D>(p, p.num_groups + b, kOwn, s.n, s.at, t - s.n0, hg, kh)};
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float mx = -INFINITY, wsum = 0.f;
+  const int all = parts[0].count + parts[1].count;
+  constexpr int kBatch = 8;
+#pragma unroll 1
+  for (int j0 = 0; j0 < all; j0 += kBatch) {
+    float l2[kBatch];
+    float4 v[kBatch];
+#pragma unroll
+    for (int y = 0; y < kBatch; ++y) {
+      const int j = j0 + y;
+      l2[y] = -INFINITY;
+      if (j >= all) continue;
+      const Pieces& u = j < parts[0].count ? parts[0] : parts[1];
+      const int piece = j < parts[0].count ? j : j - parts[0].count;
+      const int slot = (u.first + piece) * 2 + (piece == 0 ? 1 : 0);
+      l2[y] = __ldcg(u.lse + static_cast<size_t>(slot) * u.l_step);
+      v[y] = __ldcg(u.o + slot * u.o_step + col * u.col_step);
+    }
+#pragma unroll
+    for (int y = 0; y < kBatch; ++y) {
+      if (l2[y] == -INFINITY) continue;  // (a piece without a tile has no sum, and its columns say nothing)
+      const float m = fmaxf(mx, l2[y]);
+      const float keep = mx == m ? 1.f : ex2(mx - m), f = ex2(l2[y] - m);
+      mx = m;
+      wsum = wsum * keep + f;
+      acc.x = fmaf(f, v[y].x, acc.x * keep);
+      acc.y = fmaf(f, v[y].y, acc.y * keep);
+      acc.z = fmaf(f, v[y].z, acc.z * keep);
+      acc.w = fmaf(f, v[y].w, acc.w * keep);
     }
   }
   const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
   const int head = kh * p.group + hg;
   uint2* dst = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + t * p.out_stride + static_cast<long long>(head) * D) + col;
-#pragma unroll
-  for (int c = 0; c < kCols; ++c)
-    dst[c] = make_uint2(pack2<FP16>(acc[c][0] * inv, acc[c][1] * inv), pack2<FP16>(acc[c][2] * inv, acc[c][3] * inv));
+  *dst = make_uint2(pack2<FP16>(acc.x * inv, acc.y * inv), pack2<FP16>(acc.z * inv, acc.w * inv));
   if (col == 0 && p.lse != nullptr)
     p.lse[static_cast<long long>(t) * p.num_q_heads + head] = wsum > 0.f ? (mx + log2f(wsum)) * kLn2 : -INFINITY;
 }
 
 // Blocks: cut tile units and row units of sequences that share nothing, then the
-// shared groups' rows.
+// shared groups' rows, those of groups of up to 16 rows first.
 struct Blocks {
-  int tiles, rows, split, group_tiles, group_subs;
+  int tiles, rows, split, few, few_blocks, warps, group_tiles, group_subs;
 };
 
 template <int D, bool FP16>
@@ -161,6 +338,7 @@ __global__ void __launch_bounds__(kCombineThreads, 4) prefix_combine_kernel(cons
   griddep_wait();
   griddep_launch_dependents();
   int block = blockIdx.x;
+  if (block < n.tiles + n.rows && __ldcg(p.alone) == 0) return;
   if (block < n.tiles) {
     combine_tiles<D, FP16>(p, block);
     return;
@@ -171,6 +349,12 @@ __global__ void __launch_bounds__(kCombineThreads, 4) prefix_combine_kernel(cons
     return;
   }
   block -= n.rows;
+  if (block < n.few) {
+    const int unit = block / n.few_blocks;
+    combine_few<D, FP16>(p, unit / p.num_kv_heads, unit % p.num_kv_heads, block % n.few_blocks, n.warps);
+    return;
+  }
+  block -= n.few;
   const int sub = block % n.group_subs;
   block /= n.group_subs;
   const int tile = block % n.group_tiles;
@@ -182,7 +366,7 @@ struct PrefixPlan {
   int row_workers, tile_ctas, group_tokens;
   int compact;
   long long rows;
-  size_t row_o, row_lse, row_units, tile_o, tile_lse, tile_units, whole_o, whole_lse, tile_rec, bytes;
+  size_t row_o, row_lse, row_units, tile_o, tile_lse, tile_units, whole_o, whole_lse, tile_rec, entries, starts, bytes;
 };
 
 static PrefixPlan make_plan(const sv_prefix_params* c, int sms) {
@@ -217,6 +401,8 @@ static PrefixPlan make_plan(const sv_prefix_params* c, int sms) {
   w.whole_o = take(2 * rows * c->num_q_heads * D * sizeof(float));
   w.whole_lse = take(2 * rows * c->num_q_heads * sizeof(float));
   w.tile_rec = take(2 * rows * c->num_kv_heads * sizeof(int2));
+  w.entries = take(entries * 2 * sizeof(int4));
+  w.starts = take(entries * sizeof(longlong2));
   w.bytes = at;
   return w;
 }
@@ -261,6 +447,19 @@ static sv_status check(const sv_prefix_params* c) {
   return SV_OK;
 }
 
+static sv_status launch_entries(const PrefixLaunch& l) {
+  cudaLaunchConfig_t cfg = cudaLaunchConfig_t{};
+  cfg.gridDim = dim3(1, 1, 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(std::min((l.p.batch + 31) / 32 * 32, kEntryThreads)), 1, 1);
+  cfg.stream = l.stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, prefix_entries_kernel, l.p) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+}
+
 template <int D, bool FP16>
 static sv_status launch_combine(const PrefixLaunch& l, int group_tokens) {
   const PrefixParams& p = l.p;
@@ -270,10 +469,17 @@ static sv_status launch_combine(const PrefixLaunch& l, int group_tokens) {
   const int units = p.row_workers > 0 ? (p.num_seqs << p.row_shift) * p.num_kv_heads : 0;
   n.split = units <= 64 ? static_cast<int>(std::min<long long>(most, kRowUnit)) : 1;
   n.rows = units * n.split;
-  n.group_tiles = (group_tokens + p.tile_tokens - 1) / p.tile_tokens;
-  n.group_subs = static_cast<int>((static_cast<long long>(std::min(group_tokens, p.tile_tokens)) * p.group + 15) / 16);
-  const long long shared = static_cast<long long>(p.num_groups) * p.num_kv_heads * n.group_tiles * n.group_subs;
-  const long long blocks = n.tiles + n.rows + shared;
+  // (with few units a row gets a block of its own)
+  const int group_units = p.num_groups * p.num_kv_heads;
+  const long long group_rows = static_cast<long long>(group_tokens) * p.group;
+  n.warps = group_units <= 64 ? 8 : group_units <= 256 ? 4 : group_units <= 1024 ? 2 : 1;
+  const int few_rows = p.row_limit > 0 ? static_cast<int>(std::min<long long>(group_rows, kRowUnit)) : 0;
+  n.few_blocks = (few_rows * n.warps + kCombineWarps - 1) / kCombineWarps;
+  n.group_tiles = group_rows > p.row_limit ? (group_tokens + p.tile_tokens - 1) / p.tile_tokens : 0;
+  n.group_subs = static_cast<int>((static_cast<long long>(std::min(group_tokens, p.tile_tokens)) * p.group + 15) / 16) * (D / 64);
+  const long long few = static_cast<long long>(group_units) * n.few_blocks;
+  n.few = static_cast<int>(std::min<long long>(few, 0x7fffffff));
+  const long long blocks = n.tiles + n.rows + few + static_cast<long long>(group_units) * n.group_tiles * n.group_subs;
   if (blocks > 0x7fffffff) return SV_ERR_UNSUPPORTED;
   cudaLaunchConfig_t cfg = cudaLaunchConfig_t{};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
@@ -364,11 +570,19 @@ sv_status sv_prefix_attention(const sv_prefix_params* params, sv_stream_t stream
   p.whole_o = reinterpret_cast<float*>(base + w.whole_o);
   p.whole_lse = reinterpret_cast<float*>(base + w.whole_lse);
   p.tile_rec = reinterpret_cast<int2*>(base + w.tile_rec);
+  p.entries = reinterpret_cast<int4*>(base + w.entries);
+  p.starts = reinterpret_cast<longlong2*>(base + w.starts);
+  p.work = reinterpret_cast<chunk::Work*>(base + 64);  // (in the header)
+  p.alone = p.err + 4;
   l.k_cache = params->k_cache;
   l.v_cache = params->v_cache;
   l.head_dim = params->head_dim;
   l.fp16 = params->dtype == SV_FP16;
   l.stream = reinterpret_cast<cudaStream_t>(stream);
+  {
+    const sv_status r = chunk::launch_entries(l);
+    if (r != SV_OK) return r;
+  }
   if (p.tile_ctas > 0) {
     const sv_status r = chunk::launch_tiles(l);
     if (r != SV_OK) return r;
