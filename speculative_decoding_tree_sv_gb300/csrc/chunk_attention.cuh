@@ -133,11 +133,18 @@ struct Group {
   bool ok, shared;
 };
 
-__device__ __forceinline__ Group load_group(const PrefixParams& p, int g) {
-  Group x{p.cu_groups[g], p.cu_groups[g + 1], 0, 0, p.prefix_lens[g], false, false};
+// The index arrays that say so, in global or shared memory.
+struct GroupArrays {
+  const int* cu_groups;
+  const int* prefix_lens;
+  const int* cu_tokens;
+};
+
+__device__ __forceinline__ Group load_group(const PrefixParams& p, const GroupArrays& at, int g) {
+  Group x{at.cu_groups[g], at.cu_groups[g + 1], 0, 0, at.prefix_lens[g], false, false};
   if (x.first < 0 || x.last < x.first || x.last > p.num_seqs) return x;
-  x.n0 = p.cu_tokens[x.first];
-  const int n1 = p.cu_tokens[x.last];
+  x.n0 = at.cu_tokens[x.first];
+  const int n1 = at.cu_tokens[x.last];
   x.n = n1 - x.n0;
   x.ok = x.n0 >= 0 && n1 >= x.n0 && n1 <= p.total_tokens && x.n <= p.max_group_tokens && x.prefix >= 0 &&
          x.prefix % kPage == 0 && x.prefix / kPage <= p.max_pages_per_seq;
@@ -164,12 +171,12 @@ __device__ __forceinline__ int part_row(const PrefixParams& p, const Group& x, i
 }
 
 // Sequence b of group x.
-__device__ __forceinline__ PrefixSeq own_part(const PrefixParams& p, const Group& x, int b, bool report) {
+__device__ __forceinline__ PrefixSeq own_part(const PrefixParams& p, const Group& x, int b, int n0, int n1, int ctx,
+                                              bool report) {
   PrefixSeq s;
-  s.n0 = p.cu_tokens[b];
-  const int n1 = p.cu_tokens[b + 1];
-  s.ctx = p.ctx_lens[b];
-  s.n = n1 - s.n0;
+  s.n0 = n0;
+  s.ctx = ctx;
+  s.n = n1 - n0;
   s.row = b;
   const bool ok = x.ok && b >= x.first && b < x.last && s.n0 >= x.n0 && n1 >= s.n0 && n1 <= x.n0 + x.n &&
                   s.n <= p.max_tokens && s.ctx >= x.prefix &&
@@ -331,6 +338,12 @@ __device__ __forceinline__ TileSeq<P> tile_seq(const P& p, int b, bool report) {
   if (t.units > 0) t.weight = full_weight(p, t.s, t.units - 1) + last_weight(p, t.s, t.units);
   return t;
 }
+
+// What a unit counts in the row kernel's ranges beside its pages: its queries and its
+// rows' way out.  A prefix call has many short units (16 samples a few pages behind
+// four prefixes of 1000 pages: see prefix_attention.cu).
+template <class P>
+constexpr int kUnitPages = P::kPrefix ? 3 : 0;
 
 // A sequence's pages in the row kernel (of one KV head).
 template <class P>

@@ -102,7 +102,7 @@ __device__ __forceinline__ bool next_piece(const P& p, RowCursor<P>& c, long lon
     out.seq = c.seq;
     out.j0 = a < c.seq.pages ? static_cast<int>(a) : c.seq.pages;
     out.j1 = e < c.seq.pages ? static_cast<int>(e) : c.seq.pages;
-    c.pos += c.seq.pages;
+    c.pos += c.seq.pages + kUnitPages<P>;
     ++c.kh;
     if (out.j0 < out.j1) return true;
   }
@@ -277,8 +277,9 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
     start.kh = 0;
     start.pos = base;
     if (bsel < batch && hi > lo) {
-      start.kh = static_cast<int>(Share::divide(lo - base, start.seq.pages));
-      start.pos = base + static_cast<long long>(start.kh) * start.seq.pages;
+      const int length = start.seq.pages + kUnitPages<P>;
+      start.kh = static_cast<int>(Share::divide(lo - base, length));
+      start.pos = base + static_cast<long long>(start.kh) * length;
     }
   }
   // ---- the loads, a ring ahead of the products, running on across pieces

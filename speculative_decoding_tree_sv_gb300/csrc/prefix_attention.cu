@@ -25,13 +25,13 @@ namespace sv {
 namespace chunk {
 
 constexpr int kEntryThreads = 1024;
-constexpr int kStagedGroups = 2048;
+constexpr int kStaged = 1024;  // sequences whose index arrays fit in shared memory
 
 // The list's entries, where each starts and their sums, in one CTA: the kernels that
 // follow read an entry with one load (made by every warp of theirs from the lengths,
 // over 80 entries, this took 20 us).
 __global__ void __launch_bounds__(kEntryThreads) prefix_entries_kernel(const __grid_constant__ PrefixParams p) {
-  __shared__ int s_groups[kStagedGroups + 1];
+  __shared__ int s_groups[kStaged + 1], s_prefix[kStaged], s_tokens[kStaged + 1];
   __shared__ long long s_pages[32], s_weight[32];
   __shared__ Work s_work[32];
   __shared__ int s_alone;
@@ -40,9 +40,16 @@ __global__ void __launch_bounds__(kEntryThreads) prefix_entries_kernel(const __g
   griddep_wait();
   griddep_launch_dependents();  // (they wait for this grid's end)
   const int threads = blockDim.x, warps = threads / 32;
-  const bool staged = p.num_groups <= kStagedGroups;
-  if (staged)
-    for (int i = tid; i <= p.num_groups; i += threads) s_groups[i] = p.cu_groups[i];
+  GroupArrays at{p.cu_groups, p.prefix_lens, p.cu_tokens};
+  if (p.num_seqs <= kStaged) {
+    for (int i = tid; i <= p.num_seqs; i += threads) {
+      s_tokens[i] = p.cu_tokens[i];
+      if (i <= p.num_groups) s_groups[i] = p.cu_groups[i];
+      if (i < p.num_groups) s_prefix[i] = p.prefix_lens[i];
+    }
+    at = {s_groups, s_prefix, s_tokens};
+  }
+  int ctx = tid >= p.num_groups && tid < p.batch ? p.ctx_lens[tid - p.num_groups] : 0;
   __syncthreads();
   Work sum{};
   sum.lightest = 1ll << 60;
@@ -53,13 +60,15 @@ __global__ void __launch_bounds__(kEntryThreads) prefix_entries_kernel(const __g
     TileSeq<PrefixParams> t{};
     long long pages = 0;
     if (v < p.batch) {
-      const int g = v < p.num_groups ? v : group_of(staged ? s_groups : p.cu_groups, p.num_groups, v - p.num_groups);
-      const Group x = load_group(p, g);
-      if (v < p.num_groups) {
+      const int b = v - p.num_groups;
+      const int g = b < 0 ? v : group_of(at.cu_groups, p.num_groups, b);
+      const Group x = load_group(p, at, g);
+      if (v0 > 0 && b >= 0) ctx = p.ctx_lens[b];
+      if (b < 0) {
         if (!x.ok) report_error(p.err, SV_DEVERR_BAD_LENGTH);
         s = {x.n0, x.shared ? x.n : 0, x.prefix, x.first, 0, kShared, part_row(p, x, x.n0)};
       } else {
-        s = own_part(p, x, v - p.num_groups, true);
+        s = own_part(p, x, b, at.cu_tokens[b], at.cu_tokens[b + 1], ctx, true);
         if (s.part == kAlone && s.n > 0) s_alone = 1;
       }
       p.entries[2 * v] = make_int4(s.n0, s.n, s.ctx, s.row);
@@ -67,7 +76,7 @@ __global__ void __launch_bounds__(kEntryThreads) prefix_entries_kernel(const __g
       t.s = s;
       if (s.n > 0 && in_rows(p, s.n)) {
         const Keys k = unit_keys(p, s, 0, s.n);
-        pages = (k.end + kPage - 1) / kPage - k.first_page;
+        pages = (k.end + kPage - 1) / kPage - k.first_page + kUnitPages<PrefixParams>;
       } else if (s.n > 0) {
         t.units = (s.n + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens);
         t.weight = full_weight(p, s, t.units - 1) + last_weight(p, s, t.units);
