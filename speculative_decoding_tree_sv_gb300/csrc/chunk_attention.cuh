@@ -270,6 +270,9 @@ constexpr long long kMinWeight = 8 * kBlockN;  // a CTA's least share
 // 100 after 1500 tokens 29.9 / 31.8 / 31.9 us, one of 300 after 1300 25.0 / 25.1 / 31.1,
 // two of 256 among 130 sequences 276 / 276 / 263).
 constexpr long long kCutWeight = 7 * 8 * kBlockN;
+// In a prefix call every row goes through the combine, cut or whole.
+template <class P>
+constexpr long long kCut = P::kPrefix ? 4 * 8 * kBlockN : kCutWeight;
 // A page of the row kernel (about 0.1 us on an SM) beside a tile's 1024 (1.5 us):
 // 40 / 50 / 60 / 80 measured 98.5 / 96.3 / 100 / 110 us for two chunks of 1024 among 100
 // sequences, 107 / 98.6 / 90.3 / 91.2 for one of 2048 among 32, 191 / 162 / 154 / 156 for
@@ -423,7 +426,8 @@ __device__ __forceinline__ bool side_by_side(const Params& p) {
 // 124 (88 since whole units go by ticket), a chunk of 100 and 60 tokens over 8000
 // 318 / 335.  Tile units that one per SM leaves whole are cut only when that costs
 // less in both kernels (the first case: 65 us).
-__device__ __forceinline__ int row_sms(const Params& p, const Work& w) {
+template <class P>
+__device__ __forceinline__ int row_sms(const P& p, const Work& w) {
   const int sms = p.row_workers / kRowWarps;
   if (w.pages == 0) return 0;
   if (w.weight == 0) return sms;
@@ -432,7 +436,7 @@ __device__ __forceinline__ int row_sms(const Params& p, const Work& w) {
   const int units = static_cast<int>(min(static_cast<long long>(w.units) * p.num_kv_heads, static_cast<long long>(sms)));
   const float even = (rows + tiles) * __fdividef(1.f, static_cast<float>(sms));
   if (units < sms && fmaxf(static_cast<float>(w.heaviest), __fdividef(rows, static_cast<float>(sms - units))) <=
-                         even + static_cast<float>(kCutWeight))
+                         even + static_cast<float>(kCut<P>))
     return sms - units;
   const int x = static_cast<int>(__fdividef(rows, even) + 0.5f);
   const int use = static_cast<int>(fminf(tiles * (1.f / kMinWeight), static_cast<float>(sms)));

@@ -340,7 +340,7 @@ __device__ void deal_pieces(const P& p, int cta, Publish&& publish, NearEnd&& ne
     long long longest = even.each + sum.lightest / 2;
     if (rounds * sum.heaviest < longest) longest = rounds * sum.heaviest;
     if (longest < sum.heaviest) longest = sum.heaviest;
-    whole = p.whole_tiles || (longest <= even.each + kCutWeight && units < (1 << 30));
+    whole = p.whole_tiles || (longest <= even.each + kCut<P> && units < (1 << 30));
     if (whole) {
       all = static_cast<int>(units);
       if (P::kPrefix && lane < p.batch) mine = tile_seq(p, lane, false);
