@@ -197,20 +197,31 @@ __device__ __forceinline__ PrefixSeq load_seq(const PrefixParams& p, int v, bool
 }
 
 // The last entry that starts at or before `pos` of the row kernel's pages (PAGES) or the
-// tile kernel's weights, 32 probes at a time; every lane returns it.
+// tile kernel's weights, and its start, 128 probes at a time; every lane returns them.
 template <bool PAGES>
-__device__ __forceinline__ int entry_at(const PrefixParams& p, long long pos) {
+__device__ __forceinline__ int entry_at(const PrefixParams& p, long long pos, long long& start) {
   const int lane = threadIdx.x & 31;
   int lo = 0, hi = p.batch;  // starts[lo] <= pos
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 31) / 32;
-    const int k = lo + lane * step;
-    bool le = false;
-    if (k < hi) le = (PAGES ? __ldcg(&p.starts[k].x) : __ldcg(&p.starts[k].y)) <= pos;
-    const int last = 31 - __clz(__ballot_sync(0xffffffffu, le) | 1u);
-    lo += last * step;
+  do {
+    const int step = (hi - lo + 127) / 128;
+    long long v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int k = lo + (lane * 4 + i) * step;
+      v[i] = 1ll << 62;
+      if (k < hi) v[i] = PAGES ? __ldcg(&p.starts[k].x) : __ldcg(&p.starts[k].y);
+    }
+    int n = 0;  // the lane's probes at or before pos
+    start = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (v[i] <= pos) n = i + 1, start = v[i];
+    const int last = 31 - __clz(__ballot_sync(0xffffffffu, n > 0) | 1u);
+    n = __shfl_sync(0xffffffffu, n, last);
+    start = __shfl_sync(0xffffffffu, start, last);
+    lo += (last * 4 + max(n - 1, 0)) * step;
     hi = min(hi, lo + step);
-  }
+  } while (hi - lo > 1);
   return lo;
 }
 

@@ -237,8 +237,8 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
     int bsel = batch;
     if constexpr (P::kPrefix) {
       if (hi > lo) {
-        bsel = entry_at<true>(p, Share::divide(lo, p.num_kv_heads));
-        base = __ldcg(&p.starts[bsel].x) * p.num_kv_heads;
+        bsel = entry_at<true>(p, Share::divide(lo, p.num_kv_heads), base);
+        base *= p.num_kv_heads;
         start.seq = row_seq(p, bsel, SHIFT, false);
       }
     }

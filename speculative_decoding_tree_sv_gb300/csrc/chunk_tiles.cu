@@ -195,8 +195,8 @@ __device__ __forceinline__ bool deal_range(const P& p, const Share& share, int c
   long long base = 0;
   int bsel = p.batch == 1 ? 0 : p.batch;
   if constexpr (P::kPrefix) {
-    bsel = entry_at<false>(p, Share::divide(lo, p.num_kv_heads));
-    base = __ldcg(&p.starts[bsel].y) * p.num_kv_heads;
+    bsel = entry_at<false>(p, Share::divide(lo, p.num_kv_heads), base);
+    base *= p.num_kv_heads;
     mine = tile_seq(p, bsel, false);
   }
   for (int b0 = 0; !P::kPrefix && b0 < p.batch && bsel == p.batch; b0 += 32) {
@@ -270,6 +270,7 @@ __device__ __forceinline__ bool deal_range(const P& p, const Share& share, int c
         p.tile_lse[static_cast<size_t>(cta) * 2 * kGroupRows + r] = -INFINITY;
     }
     pos += w;
+    if (P::kPrefix && pos >= hi) break;  // (not past the sequences, one by one, that are not tiled)
     if (++m == t.units) {
       m = 0;
       if (++kh == p.num_kv_heads) {
