@@ -89,7 +89,7 @@ struct PrefixParams : Params {
   // written by the call's first kernel (prefix_attention.cu)
   int4* entries;      // [batch][2] the entries (PrefixSeq)
   longlong2* starts;  // [batch] pages of the row kernel and weight of the tile kernel before the entry, per KV head
-  struct Work* work;  // their sums
+  struct Split* split;  // how the work is shared out
   int* alone;         // whether an entry shares nothing
 };
 
@@ -423,6 +423,17 @@ __device__ __forceinline__ void add_round(Work& sum, Work w) {
   sum.heaviest = max(sum.heaviest, w.heaviest);
   sum.lightest = min(sum.lightest, w.lightest);
 }
+
+// How a prefix call's work is shared out, by its first kernel.
+struct Split {
+  long long pages;     // of the row kernel, all heads
+  long long weight;    // of the tile kernel, all heads
+  int units;           // of the tile kernel, all heads
+  int row_sms;         // as row_sms; 0: all
+  int tile_ctas;       // the tile kernel's CTAs that take units or ranges
+  int whole;           // units stay whole
+  int per_unit;        // all units are alike: a range is one such part of a unit (0: equal shares of the list)
+};
 
 // Whether the two kernels share the SMs.
 __device__ __forceinline__ bool side_by_side(const Params& p) {

@@ -168,6 +168,8 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
   // the SMs that the tile kernel leaves free and waits for it at its end.  (Should
   // the two kernels' row_sms ever differ, a CTA only starts later.)
   if (p.tile_ctas == 0) griddep_wait();
+  // (the combine of a prefix call takes SMs as they come free, and waits there)
+  if constexpr (P::kPrefix) griddep_launch_dependents();
 
   // ---- this worker's range of the page list
   // consecutive ranges go to different CTAs, so few workers spread over the SMs
@@ -185,10 +187,8 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
     const int batch = p.batch << SHIFT;
     if constexpr (P::kPrefix) {
       mine = RowSeq<P>{};
-      const Work sum = *p.work;
-      total = sum.pages;
-      const int own = side_by_side(p) ? row_sms(p, sum) : 0;
-      if (own > 0) blocks = own;
+      total = p.split->pages;
+      if (p.split->row_sms > 0) blocks = p.split->row_sms;
       worker = warp * blocks + blockIdx.x;
     } else if (side_by_side(p)) {
       Work sum{};
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
         total += w;
       }
     }
-    total *= p.num_kv_heads;
+    if constexpr (!P::kPrefix) total *= p.num_kv_heads;
     const long long most = (total + min_pages(total) - 1) / min_pages(total);
     const int all = blocks * kRowWarps;
     workers = static_cast<int>(most < all ? (most > 0 ? most : 1) : all);

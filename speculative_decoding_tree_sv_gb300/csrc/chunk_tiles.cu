@@ -188,8 +188,9 @@ __device__ void deal_units(const P& p, int cta, int ctas, int all, TileSeq<P> mi
 
 // The pieces of the range [lo, hi) of the weights of all units; `record` becomes
 // the cut unit that starts in it.  False when the dealer gave up.
-template <class P, class Publish>
-__device__ __forceinline__ bool deal_range(const P& p, const Share& share, int cta, long long lo, long long hi,
+// (`holder`: the CTA whose range holds a position.)
+template <class P, class Holder, class Publish>
+__device__ __forceinline__ bool deal_range(const P& p, Holder&& holder, int cta, long long lo, long long hi,
                                            TileSeq<P> mine, int4& record, Publish&& publish) {
   const int lane = threadIdx.x & 31;
   long long base = 0;
@@ -259,10 +260,10 @@ __device__ __forceinline__ bool deal_range(const P& p, const Share& share, int c
       bool alone = true;  // (the rows of a shared group are merged by a rule of their own)
       if constexpr (P::kPrefix) {
         alone = pc.part == kAlone;
-        if (!alone && pc.ja == 0) note_unit(p, pc, whole ? -1 : cta, whole ? -1 : share.holder(pos + w - 1));
+        if (!alone && pc.ja == 0) note_unit(p, pc, whole ? -1 : cta, whole ? -1 : holder(pos + w - 1));
       }
       if (pc.slot == 1 && alone)
-        record = make_int4(pc.n0 + pc.tok0, min(pc.n - pc.tok0, 2 * p.tile_tokens), kh, share.holder(pos + w - 1));
+        record = make_int4(pc.n0 + pc.tok0, min(pc.n - pc.tok0, 2 * p.tile_tokens), kh, holder(pos + w - 1));
       if (!publish(pc)) return false;
     } else if (pc.ja > 0) {
       // less than a tile of a unit that others share: this CTA's piece is empty
@@ -308,9 +309,7 @@ __device__ void deal_pieces(const P& p, int cta, Publish&& publish, NearEnd&& ne
     // the call's work, and this kernel's CTAs
     Work sum{};
     sum.lightest = 1ll << 60;
-    if constexpr (P::kPrefix) {
-      sum = *p.work;
-    } else if (p.batch == 1) {  // (a prompt alone: no sums)
+    if (p.batch == 1) {  // (a prompt alone: no sums)
       mine = tile_seq(p, 0, report);
       sum = work_of(p, mine, 0);
     } else {
@@ -344,7 +343,6 @@ __device__ void deal_pieces(const P& p, int cta, Publish&& publish, NearEnd&& ne
     whole = p.whole_tiles || (longest <= even.each + kCut<P> && units < (1 << 30));
     if (whole) {
       all = static_cast<int>(units);
-      if (P::kPrefix && lane < p.batch) mine = tile_seq(p, lane, false);
       if (p.batch == 1 && lane > 0) mine.units = 0;
     } else {
       const long long most = total / kMinWeight;
@@ -352,12 +350,45 @@ __device__ void deal_pieces(const P& p, int cta, Publish&& publish, NearEnd&& ne
       const Share share = ctas == avail ? even : share_of(total, ctas);
       const long long lo = cta < ctas ? share.start(cta) : 0;
       const long long hi = cta < ctas ? share.start(cta + 1) : 0;
-      if (hi > lo && !deal_range(p, share, cta, lo, hi, mine, record, publish)) return;
+      if (hi > lo && !deal_range(p, [&](long long x) { return share.holder(x); }, cta, lo, hi, mine, record, publish))
+        return;
     }
   }
   if (whole) deal_units(p, cta, avail, all, mine, publish, near_end);
   if (lane == 0) p.tile_units[cta] = record;
   PieceOf<P> end{};
+  end.je = 0;
+  publish(end);
+}
+
+// The same for a prefix call, whose first kernel has made the split.
+template <class Publish, class NearEnd>
+__device__ void deal_pieces(const PrefixParams& p, int cta, Publish&& publish, NearEnd&& near_end) {
+  const int lane = threadIdx.x & 31;
+  const Split x = *p.split;
+  int4 record = make_int4(0, 0, 0, 0);
+  if (x.whole) {
+    TileSeq<PrefixParams> mine{};
+    if (lane < p.batch) mine = tile_seq(p, lane, false);
+    deal_units(p, cta, x.tile_ctas, x.units, mine, publish, near_end);
+  } else if (cta < x.tile_ctas) {
+    bool ok;
+    if (x.per_unit > 0) {
+      const long long w = Share::divide(x.weight, x.units);
+      const int u = cta / x.per_unit, i = cta - u * x.per_unit;
+      const long long lo = u * w + Share::divide(w * i, x.per_unit), hi = u * w + Share::divide(w * (i + 1), x.per_unit);
+      ok = deal_range(p, [&](long long) { return (u + 1) * x.per_unit - 1; }, cta, lo, hi, TileSeq<PrefixParams>{}, record,
+                      publish);
+    } else {
+      const Share share = share_of(x.weight, x.tile_ctas);
+      const long long lo = share.start(cta), hi = share.start(cta + 1);
+      ok = hi <= lo || deal_range(p, [&](long long y) { return share.holder(y); }, cta, lo, hi, TileSeq<PrefixParams>{},
+                                  record, publish);
+    }
+    if (!ok) return;
+  }
+  if (lane == 0) p.tile_units[cta] = record;
+  PrefixPiece end{};
   end.je = 0;
   publish(end);
 }
@@ -440,7 +471,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   griddep_wait();  // everything read below may come from the preceding grid
-  if (p.row_workers > 0) griddep_launch_dependents();  // the row kernel takes the SMs that are free
+  // the row kernel takes the SMs that are free (the combine of a prefix call too)
+  if (p.row_workers > 0 || P::kPrefix) griddep_launch_dependents();
 
   // Warp-uniform outcome of a bounded wait, by every lane.
   auto wait_all = [&](uint64_t* bar, uint32_t parity) {
@@ -919,7 +951,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (p.row_workers == 0) griddep_launch_dependents();  // the partials are written: the combine may run
+  if (p.row_workers == 0 && !P::kPrefix) griddep_launch_dependents();  // the partials are written: the combine may run
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);

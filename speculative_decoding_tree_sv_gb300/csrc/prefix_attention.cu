@@ -27,6 +27,37 @@ namespace chunk {
 constexpr int kEntryThreads = 1024;
 constexpr int kStaged = 1024;  // sequences whose index arrays fit in shared memory
 
+// Shares the work out: the SMs between the two kernels, the tile units whole or in
+// ranges (the rules of deal_pieces).  Units that are all alike, one prefix for all heads
+// for instance, are cut into equal parts where that idles an eighth of the CTAs at
+// most: a range with the end of one unit and the start of the next takes 6 us more (64
+// samples over 60000 tokens: 131 CTAs of equal shares 77 us but seven of them up to 86).
+__device__ Split split_of(const PrefixParams& p, const Work& sum) {
+  Split x{};
+  const long long heads = p.num_kv_heads;
+  x.pages = sum.pages * heads;
+  x.weight = sum.weight * heads;
+  x.units = static_cast<int>(sum.units * heads);
+  x.row_sms = side_by_side(p) ? row_sms(p, sum) : 0;
+  int avail = p.tile_ctas;
+  if (side_by_side(p)) avail = max(1, min(avail, p.row_workers / kRowWarps - x.row_sms));
+  x.tile_ctas = avail;
+  if (p.tile_ctas == 0 || x.units == 0) return x;
+  const long long rounds = share_of(static_cast<long long>(x.units) + avail - 1, avail).each;
+  const Share even = share_of(x.weight, avail);
+  const long long longest = max(min(even.each + sum.lightest / 2, rounds * sum.heaviest), sum.heaviest);
+  x.whole = longest <= even.each + kCut<PrefixParams>;
+  if (x.whole) return x;
+  const long long most = x.weight / kMinWeight;
+  x.tile_ctas = static_cast<int>(most < avail ? max(most, 1ll) : avail);
+  const int per_unit = x.tile_ctas / x.units, idle = x.tile_ctas - per_unit * x.units;
+  if (sum.heaviest == sum.lightest && per_unit > 0 && idle * 8 <= x.tile_ctas) {
+    x.per_unit = per_unit;
+    x.tile_ctas -= idle;
+  }
+  return x;
+}
+
 // The list's entries, where each starts and their sums, in one CTA: the kernels that
 // follow read an entry with one load (made by every warp of theirs from the lengths,
 // over 80 entries, this took 20 us).
@@ -120,7 +151,7 @@ __global__ void __launch_bounds__(kEntryThreads) prefix_entries_kernel(const __g
     __syncthreads();
   }
   if (tid == 0) {
-    *p.work = sum;
+    *p.split = split_of(p, sum);
     *p.alone = s_alone;
   }
 }
@@ -453,6 +484,8 @@ static sv_status check(const sv_prefix_params* c) {
   if (!c->cu_groups || !c->prefix_lens || c->num_groups < 1 || c->num_groups > c->batch || c->max_group_tokens < 0)
     return SV_ERR_INVALID_ARG;
   if (static_cast<long long>(c->batch) * c->num_kv_heads > (1 << 29)) return SV_ERR_UNSUPPORTED;
+  // (tile units of all heads count in 32 bits)
+  if (static_cast<long long>(c->total_tokens) * c->num_q_heads > (1ll << 36)) return SV_ERR_UNSUPPORTED;
   return SV_OK;
 }
 
@@ -581,7 +614,7 @@ sv_status sv_prefix_attention(const sv_prefix_params* params, sv_stream_t stream
   p.tile_rec = reinterpret_cast<int2*>(base + w.tile_rec);
   p.entries = reinterpret_cast<int4*>(base + w.entries);
   p.starts = reinterpret_cast<longlong2*>(base + w.starts);
-  p.work = reinterpret_cast<chunk::Work*>(base + 64);  // (in the header)
+  p.split = reinterpret_cast<chunk::Split*>(base + 64);  // (in the header)
   p.alone = p.err + 4;
   l.k_cache = params->k_cache;
   l.v_cache = params->v_cache;
