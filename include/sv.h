@@ -745,10 +745,12 @@ sv_status sv_prefix_attention(const sv_prefix_params* params, sv_stream_t stream
  * token -1 (and logprob and probs NaN), and the error word records
  * SV_DEVERR_BAD_VALUE.
  *
- * Weights have an absolute error below 2^-36 (below 2^-34 of a weight under
- * 2^-13) and are summed as 64-bit integers, so that neither the order of sums
- * nor the size of the vocabulary shows in the tokens; entries below 2^-46 of
- * the largest are never drawn.
+ * Every weight (the largest is 1) is off by less than 2^-36.  Sums are 64-bit
+ * integers, the same on every run; weights below 2^-13 are summed as fp32 over
+ * runs of up to 64 entries first, which adds 2^-20 of a run's sum at most and
+ * 2^-30 of the row's as a rule.  Only a uniform or a top_p within that of a border
+ * may see it; the number of rows, which decides how a row is divided, can move
+ * such a border by as much.  Entries below 2^-46 of the largest are not drawn.
  * ---------------------------------------------------------------------- */
 typedef struct sv_sample_params {
   int rows;                 /* R                                             */

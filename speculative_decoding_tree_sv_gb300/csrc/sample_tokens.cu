@@ -7,28 +7,36 @@
 // and one least weight; the token is the first index, in index order, whose running
 // sum passes u times the sum.  A token is a comparison of sums of up to 2^18 terms
 // with borders that may lie 2^-20 apart, so weights are 64-bit integers in units
-// of 2^-45: sums are exact, the same in any order, and only the weights' own error
-// (2^-36 of the largest, see weights4) can move a border.
+// of 2^-45, off by 2^-36 of the largest at most, and sums are integers, the same in any
+// order.  A weight below 2^-13 needs no more than fp32 for that: those of 64 consecutive
+// entries are summed in fp32 first, which is what most of a large vocabulary costs.
 //
-// A cluster of CTAs takes a row, each holds its slice in shared memory as fp32; all
+// A cluster of CTAs takes a row, each holds its slice in shared memory as it came; all
 // further passes read that.  No filter sorts the row:
 //   * a top-k of up to kFew: the entries that every thread saw largest on loading its
 //     part are 512 per CTA; with b the least over the CTAs of their (k / CTAs)-th
 //     largest, at least k entries are >= b, and seldom many more.  Those are listed
 //     and sorted by the first CTA, which has the kept ones whole and draws from them;
+//   * top-p: the entries above 2^-13 are listed while all weights are summed.  Mostly
+//     they reach the target, and the first CTA sorts and draws as above;
 //   * otherwise a histogram of 2048 bins over the distance from the maximum (1/32 of a
 //     power of two each) in numbers and, for top-p, weights, summed over the cluster,
 //     finds the threshold's bin; the entries down to it, or where they are many the
 //     bin's alone, are listed and sorted (a bin of more than kMost is first split by
 //     the bits of the logits and then of the indices).  Entries below a V-th of 1 -
 //     top_p together weigh less than what top-p leaves out, so they stay out of the
-//     bins;
+//     bins, and so do those below a top-k's b;
 //   * where the kept entries are many, or for min-p alone, a thread sums a run of
 //     consecutive entries, so that one scan of the threads' sums finds the run of the
 //     token.
 //
-// Bound by HBM for large batches in principle (the logits are read once), in fact
-// by the weights' arithmetic and the passes over shared memory.
+// The logits are read once, but HBM bounds none of the measured calls: 20 to 40 steps
+// of a row (barriers of the cluster, scans, a sort) follow one another, each some 500 to
+// 2000 cycles, and a pass of the weights is about 15 instructions per entry.  One row of
+// 32000 with top-k 50 and top-p takes 12 us; 32 rows of 128256 without a filter 16; 64
+// with top-p 0.9 40 us; 60 with top-k 64 and their distributions 38; 256 of 151936, each
+// with its own settings, 143 (0.54 TB/s).  Flat rows whose nucleus is thousands of entries
+// cost most: 256 of them 490 us.
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -43,10 +51,13 @@ namespace sample {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kSlice = 16384;      // entries per CTA while a cluster is no larger than kMaxCluster
+constexpr int kHalf = 109 * 1024;  // shared memory of a CTA beside another one
+constexpr int kRunEntries = 64;    // of a thread's run that are summed in fp32, a bit each
 constexpr int kBins = 2048;
 constexpr int kBinBits = 11;
 constexpr int kBinsPerOctave = 32;
+constexpr int kNear = 13;          // weights above 2^-kNear are near (see weight_near), the others far
+constexpr int kNearBins = kNear * kBinsPerOctave + 1;  // the bins from here on hold far weights alone
 constexpr int kMost = 2048;        // entries that are sorted
 static_assert(3 * kBins * 4 <= 2 * kMost * 8, "the bins lie where the lists do");
 constexpr int kWhole = 512;        // kept ones that are listed whole: more are quicker summed in place
@@ -162,47 +173,53 @@ __device__ __forceinline__ u64 weight_near(const Row& row, float l, const Power*
   return s == 0 ? w : static_cast<u64>(w + (1ll << (s - 1))) >> s;
 }
 
-// The sum of far weights, those below 2^-15: by a polynomial of degree six for 2^f (2^-26;
-// 2^-23 of a weight with its 24 bits and the exponent's rounding), two at a time, added
-// in fp32 over a thread's run.  A far weight is worth no more than 2^-15 of the row's
-// sum and a run's no more than 2^-9, so this is off by 2^-39 a weight and 2^-33 a run at
-// most.  What is to stay out, and any exponent below -100, is below `least_logit`.
+// The sum of far weights: by a polynomial of degree six for 2^f (2^-26; 2^-23 of a
+// weight with its 24 bits and the exponent's rounding, so 2^-36 at most as the near
+// ones), two at a time, added in fp32 over kRunEntries of a thread's run in two sums of
+// 32: each addition is off by 2^-24 of a sum of at most 2^-8, 2^-27 a run at the very
+// worst.  What is to stay out, and any exponent below -100, is below `least_logit`.
 // EXACT: l - m is a float (16-bit logits: but for entries of 2^-16 of the maximum or
 // less, where the difference's own rounding is as small).
+template <bool EXACT>
+__device__ __forceinline__ void far_two(const Row& r, uint64_t l, uint64_t& e, uint64_t& power) {
+  constexpr float kMagic = 12582912.f;  // 1.5 * 2^23
+  auto two = [](float x) { return f2_pack(x, x); };
+  const uint64_t minus1 = two(-1.f), nm = two(-r.m), nc = two(-r.chi), chi = two(r.chi), clo = two(r.clo);
+  const uint64_t dh = f2_add(l, nm);
+  const uint64_t y = f2_mul(dh, nc);  // minus the exponent
+  uint64_t yl = f2_fma(dh, chi, y);
+  if constexpr (!EXACT) {
+    const uint64_t b = f2_fma(l, minus1, dh), t = f2_fma(b, minus1, dh);
+    yl = f2_fma(f2_add(f2_fma(t, minus1, l), f2_fma(b, minus1, nm)), chi, yl);
+  }
+  yl = f2_fma(dh, clo, yl);
+  const uint64_t k = f2_add(y, two(kMagic));
+  const uint64_t kf = f2_add(k, two(-kMagic));
+  const uint64_t f = f2_fma(f2_fma(kf, minus1, y), minus1, yl);
+  e = f2_fma(f, two(0x1.444004p-13f), two(0x1.5f0896p-10f));
+  e = f2_fma(f, e, two(0x1.3b2a1cp-7f));
+  e = f2_fma(f, e, two(0x1.c6af6cp-5f));
+  e = f2_fma(f, e, two(0x1.ebfbe0p-3f));
+  e = f2_fma(f, e, two(0x1.62e430p-1f));
+  e = f2_fma(f, e, two(1.f));
+  // 2^-k: the exponent field from the whole number at the bottom of k
+  constexpr int kOne = (127 << 23) + static_cast<int>(0x4b400000u << 23);
+  const int p0 = kOne - (__float_as_int(f2_lo(k)) << 23), p1 = kOne - (__float_as_int(f2_hi(k)) << 23);
+  power = f2_pack(__int_as_float(p0), __int_as_float(p1));
+}
+
 struct Far {
   uint64_t sum;
   float least_logit;
 };
 template <bool EXACT>
 __device__ __forceinline__ void add_far(const Row& r, const float4& v, Far& far) {
-  constexpr float kMagic = 12582912.f;  // 1.5 * 2^23
-  auto two = [](float x) { return f2_pack(x, x); };
-  const uint64_t minus1 = two(-1.f), nm = two(-r.m), nc = two(-r.chi), chi = two(r.chi), clo = two(r.clo);
   const float c = far.least_logit;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const uint64_t l = h ? f2_pack(fmaxf(v.z, c), fmaxf(v.w, c)) : f2_pack(fmaxf(v.x, c), fmaxf(v.y, c));
-    const uint64_t dh = f2_add(l, nm);
-    const uint64_t y = f2_mul(dh, nc);  // minus the exponent
-    uint64_t yl = f2_fma(dh, chi, y);
-    if constexpr (!EXACT) {
-      const uint64_t b = f2_fma(l, minus1, dh), t = f2_fma(b, minus1, dh);
-      yl = f2_fma(f2_add(f2_fma(t, minus1, l), f2_fma(b, minus1, nm)), chi, yl);
-    }
-    yl = f2_fma(dh, clo, yl);
-    const uint64_t k = f2_add(y, two(kMagic));
-    const uint64_t kf = f2_add(k, two(-kMagic));
-    const uint64_t f = f2_fma(f2_fma(kf, minus1, y), minus1, yl);
-    uint64_t e = f2_fma(f, two(0x1.444004p-13f), two(0x1.5f0896p-10f));
-    e = f2_fma(f, e, two(0x1.3b2a1cp-7f));
-    e = f2_fma(f, e, two(0x1.c6af6cp-5f));
-    e = f2_fma(f, e, two(0x1.ebfbe0p-3f));
-    e = f2_fma(f, e, two(0x1.62e430p-1f));
-    e = f2_fma(f, e, two(1.f));
-    // 2^-k: the exponent field from the whole number at the bottom of k
-    constexpr int kOne = (127 << 23) + static_cast<int>(0x4b400000u << 23);
-    const int p0 = kOne - (__float_as_int(f2_lo(k)) << 23), p1 = kOne - (__float_as_int(f2_hi(k)) << 23);
-    far.sum = f2_fma(e, f2_pack(__int_as_float(p0), __int_as_float(p1)), far.sum);
+    uint64_t e, power;
+    far_two<EXACT>(r, h ? f2_pack(fmaxf(v.z, c), fmaxf(v.w, c)) : f2_pack(fmaxf(v.x, c), fmaxf(v.y, c)), e, power);
+    far.sum = f2_fma(e, power, far.sum);
   }
 }
 
@@ -210,10 +227,10 @@ __device__ __forceinline__ void add_far(const Row& r, const float4& v, Far& far)
 __device__ __noinline__ u64 weight_of(Row row, float l, const Power* powers) {
   const float2 y = exponent_of(row, l);
   if (!(y.x > -47.f)) return 0;
-  if (y.x > -15.f) return weight_near(row, l, powers);
-  Far far{0, -INFINITY};
-  add_far<false>(row, make_float4(l, -INFINITY, l, -INFINITY), far);  // (the others: NaN)
-  return __float2uint_rn(f2_lo(far.sum) * 0x1p44f);  // (twice: entries 0 and 2)
+  if (y.x > -kNear) return weight_near(row, l, powers);
+  uint64_t e, power;
+  far_two<false>(row, f2_pack(l, l), e, power);
+  return __float2uint_rn(f2_lo(e) * f2_lo(power) * 0x1p45f);
 }
 
 // A weight as fp32, however small.
@@ -322,6 +339,7 @@ struct Shared {
   Power powers[32];
   Barrier barrier;
   u64 scan[kWarps];
+  ulonglong2 sums[kWarps];
   uint32_t best[kWarps];
   // read by the other CTAs of the cluster
   uint32_t top;         // key of the slice's largest
@@ -358,6 +376,28 @@ __device__ __noinline__ u64 block_scan(u64 v, u64* slots) {
 #pragma unroll
   for (int o = kWarps / 2; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
   return __shfl_sync(0xffffffffu, before, 0) + v;
+}
+// The sums of two values over the block's threads.
+__device__ __noinline__ ulonglong2 block_sums(u64 a, u64 b, ulonglong2* slots) {
+  __syncwarp();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+    b += __shfl_xor_sync(0xffffffffu, b, o);
+  }
+  __syncthreads();  // the slots' last readers are done
+  if (lane == 0) slots[warp] = make_ulonglong2(a, b);
+  __syncthreads();
+  const ulonglong2 v = slots[lane & (kWarps - 1)];
+  a = v.x;
+  b = v.y;
+#pragma unroll
+  for (int o = kWarps / 2; o > 0; o >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+    b += __shfl_xor_sync(0xffffffffu, b, o);
+  }
+  return make_ulonglong2(a, b);
 }
 // ... over all of them, by the slots that block_scan left (before the next one).
 __device__ __forceinline__ u64 block_all(const u64* slots) {
@@ -420,9 +460,45 @@ __device__ __noinline__ void sort(u64* a, int size) {
   __syncthreads();
 }
 
+// n - 1 where a < b: the difference's borrow.
+__device__ __forceinline__ int minus_less(int n, u64 a, u64 b) {
+  asm("{\n\t.reg .u32 t;\n\t"
+      "sub.cc.u32 t, %1, %3;\n\tsubc.cc.u32 t, %2, %4;\n\tsubc.u32 %0, %0, 0;\n\t}"
+      : "+r"(n)
+      : "r"(static_cast<uint32_t>(a)), "r"(static_cast<uint32_t>(a >> 32)), "r"(static_cast<uint32_t>(b)),
+        "r"(static_cast<uint32_t>(b >> 32)));
+  return n;
+}
+
+// The same for few entries, zeros left out (what lies behind the others then is not
+// said): an entry's place is the number of those above it, counted by several threads
+// (117 entries 2.6 -> 1.2 us; 361 in steps 7, counted 11).
+constexpr int kCounted = 256;
+__device__ __noinline__ void sort_few(u64* a, int size) {
+  const int tid = threadIdx.x;
+  int parts = 1;
+  while (parts < 32 && 2 * parts * size <= kThreads) parts *= 2;
+  const int e = tid / parts, pairs = size / 2;
+  __syncwarp();
+  __syncthreads();
+  const u64 own = e < size ? a[e] : 0;
+  int above = 0;
+  const ulonglong2* two = reinterpret_cast<const ulonglong2*>(a);
+#pragma unroll 4
+  for (int j = tid & (parts - 1); j < pairs; j += parts) {
+    const ulonglong2 x = two[j];
+    above = minus_less(minus_less(above, own, x.x), own, x.y);
+  }
+  for (int o = 1; o < parts; o *= 2) above += __shfl_xor_sync(0xffffffffu, above, o);
+  __syncthreads();
+  if (own != 0) a[-above] = own;
+  __syncthreads();
+}
+
 __device__ __forceinline__ void sort(u64* a, int size) {
   static_assert(kMost <= 4 * kThreads, "entries per thread");
-  if (size <= kThreads) sort<1>(a, size);
+  if (size <= kCounted) sort_few(a, size);
+  else if (size <= kThreads) sort<1>(a, size);
   else if (size <= 2 * kThreads) sort<2>(a, size);
   else sort<4>(a, size);
 }
@@ -509,6 +585,29 @@ __device__ __noinline__ Added add_run(const uint4* run, int vecs, int x, Row r, 
   }
   const float sum = f2_lo(far.sum) + f2_hi(far.sum);
   return {c.gone == -INFINITY ? 0 : static_cast<u64>(__float2ull_rn(sum * 0x1p45f)), large};
+}
+
+// A bit for every entry of up to kRunEntries in [lo, hi].  (Few are wanted: looked at
+// one by one where they come, they took ten times as long, each branch at a warp's pace.)
+template <int TYPE>
+__device__ __noinline__ u64 between(const uint4* run, int vecs, float lo, float hi) {
+  constexpr int V = TYPE == SV_FP32 ? 4 : 8;
+  u64 bits = 0;
+#pragma unroll 2
+  for (int j = 0; j < vecs; ++j) {
+    const uint4 raw = run[j];
+    uint32_t b = 0;
+#pragma unroll
+    for (int h = 0; h < V / 4; ++h) {
+      const float4 v = four<TYPE>(raw, h);
+      b |= v.x >= lo && v.x <= hi ? 1u << (4 * h) : 0;
+      b |= v.y >= lo && v.y <= hi ? 2u << (4 * h) : 0;
+      b |= v.z >= lo && v.z <= hi ? 4u << (4 * h) : 0;
+      b |= v.w >= lo && v.w <= hi ? 8u << (4 * h) : 0;
+    }
+    bits |= static_cast<u64>(b) << (j * V);
+  }
+  return bits;
 }
 
 template <int TYPE>
@@ -625,9 +724,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     s.run = -1;
     s.first = 0x7fffffff;
   }
-  const bool few = top_k > 1 && top_k <= kFew && top_k < p.vocab;
-  if (few) {  // the upper bits of the part's (top_k / CTAs)-th largest of the threads' best
-    const int want = (top_k + cs - 1) / cs;
+  const int want = (top_k + cs - 1) / cs;
+  const bool bounded = top_k > 1 && top_k < p.vocab && want <= kThreads / 2, few = bounded && top_k <= kFew;
+  if (bounded) {  // the upper bits of the part's (top_k / CTAs)-th largest of the threads' best
     uint32_t low = 0;
     for (uint32_t bit = 0x80000000u; bit >= 0x1000u; bit >>= 1) {
       const int have = __syncthreads_count(best_key >= (low | bit));
@@ -700,12 +799,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     r.clo = c < 1e37f && temperature < 1e30f ? (fmaf(-c, temperature, kLog2eHi) + kLog2eLo) / temperature : 0.f;
   }
   const float bin_scale = r.chi * kBinsPerOctave;
-  // Above near_logit weights are near (2^-15 or nearly), below gone_logit nothing.  (The
+  // Above near_logit weights are near or nearly, below gone_logit nothing.  (The
   // margin keeps both below the maximum.)  All are near at temperatures past 10^35, and
   // below a millionth of the maximum, where floats next to it are whole powers apart.
   const float margin = fabsf(r.m) * 0x1p-22f;
   const bool all_near = !(100.f / r.chi < 1e37f && margin * r.chi < 1.f);
-  const float near_logit = all_near ? -INFINITY : r.m - 15.f / r.chi - margin;
+  const float near_logit = all_near ? -INFINITY : r.m - kNear / r.chi - margin;
   const float gone_logit = all_near ? -INFINITY : r.m - 100.f / r.chi - margin;
   const u64 least = min_p > 0.f ? times<true>(1ull << kUnit, min_p) : 0;
   const bool by_k = top_k > 0 && top_k < p.vocab, by_p = top_p < 1.f;
@@ -715,7 +814,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     return static_cast<int>(__float_as_uint(fminf((r.m - l) * bin_scale, kBins - 1.f) + 8388608.f) & (kBins - 1));
   };
   auto scalar_at = [&](int x) { return E::get(scalars[place_in(x / V) * V + x % V]); };
-  auto entry = [](const float4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; };
+  // (a little beyond) the least and the largest logit of a bin
+  auto lowest_of = [&](int bin) { return bin >= kBins - 1 ? -INFINITY : r.m - (bin + 0.51f) / bin_scale - margin; };
+  auto highest_of = [&](int bin) { return r.m - (bin - 0.51f) / bin_scale + margin; };
   // Sum over the cluster of a value per CTA, and over the ranks before this one.
   auto over_cluster = [&](const u64* slot, u64& before) {
     const u64 x = lane < cs ? (cs > 1 ? peer(slot, lane) : *slot) : 0;
@@ -728,31 +829,37 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     before = __shfl_sync(0xffffffffu, to - x, rank);
     return __shfl_sync(0xffffffffu, to, kMaxCluster - 1);
   };
-  // Lists the entries that `take` wants, chunks above whose largest entry `skip` says
-  // there are none left out; the cluster's number of them (more than kMost: not all
+  int have = 0;  // of lane's CTA in its list
+  constexpr int kRunVecs = kRunEntries / V;
+  // Calls f(logit, index) for the entries of the thread's run in [lo, hi], in order.
+  auto each_between = [&](float lo, float hi, auto&& f) {
+#pragma unroll 1
+    for (int j = 0; j < run_vecs; j += kRunVecs) {
+      const int at = run_at + j * V;
+      for (u64 bits = between<TYPE>(run + j, min(run_vecs - j, kRunVecs), lo, hi); bits != 0; bits &= bits - 1) {
+        const int x = at + __ffsll(bits) - 1;
+        f(scalar_at(x), first + x);
+      }
+    }
+  };
+  // Lists the entries in [lo, hi] that `take` wants; the cluster's number of them (more than kMost: not all
   // are there).  (The count of the list before is read by now.)
-  auto gather = [&](auto&& skip, auto&& take) {
+  auto gather = [&](float lo, float hi, auto&& take) {
     if (tid == 0) s.listed = 0;
     __syncthreads();
-    each([&](const float4& v, int x) {
-      if (skip(most_of(v))) return;
-#pragma unroll 1
-      for (int i = 0; i < 4; ++i) {
-        const float l = entry(v, i);
-        if (!(l > -INFINITY) || !take(l, x + i)) continue;
-        const int at = atomicAdd(&s.listed, 1);
-        if (at < kMost) list[at] = place_of(l, x + i);
-      }
+    each_between(lo, hi, [&](float l, int index) {
+      if (!(l > -INFINITY) || !take(l, index)) return;
+      const int at = atomicAdd(&s.listed, 1);
+      if (at < kMost) list[at] = place_of(l, index);
     });
     if (!meet()) return -1;
-    const int have = lane < cs ? (cs > 1 ? peer(&s.listed, lane) : s.listed) : 0;
+    have = lane < cs ? (cs > 1 ? peer(&s.listed, lane) : s.listed) : 0;
     return static_cast<int>(__reduce_add_sync(0xffffffffu, have));
   };
   // The cluster's listed entries, m <= kMost, in `sorted` (one CTA); its size.
   auto pull = [&](int m) {
     int size = 4;
     while (size < m) size *= 2;
-    const int have = lane < cs ? (cs > 1 ? peer(&s.listed, lane) : s.listed) : 0;
     int to = have;
 #pragma unroll
     for (int o = 1; o < kMaxCluster; o <<= 1) {
@@ -770,6 +877,19 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       sorted[i] = i >= m ? 0 : cs > 1 ? peer(list + (i - from), rank_of) : list[i];
     }
     return size;
+  };
+  // Sums the thread's run: far weights, and f(place in the slice) for every entry to be
+  // weighed by itself.
+  auto sum_run = [&](const Limits& c, auto&& f) {
+    u64 sum = 0;
+#pragma unroll 1
+    for (int j = 0; j < run_vecs; j += kRunVecs) {
+      const int at = run_at + j * V;
+      const Added part = add_run<TYPE>(run + j, min(run_vecs - j, kRunVecs), first + at, r, c);
+      sum += part.far;
+      for (u64 large = part.large; large != 0; large &= large - 1) f(at + __ffsll(large) - 1);
+    }
+    return sum;
   };
   auto logit_at = [&](int i) { return logit_of(static_cast<uint32_t>(sorted[i] >> kIndexBits)); };
   constexpr int kPer = kMost / kThreads;  // sorted entries of a thread
@@ -828,10 +948,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         const int x = tid * run + i;
         const bool keep = i < run && x < cut && w[i] >= least;
         place[i] = keep ? (static_cast<u64>(kIndexMask - index_of(sorted[x])) << (kUnit + 1)) | w[i] : 0;
-        kept += keep;
+        if (i < run) kept += __syncthreads_count(keep);
       }
-      kept = static_cast<int>(block_scan(kept, s.scan));
-      kept = static_cast<int>(block_all(s.scan));
       size = 4;
       while (size < cut) size *= 2;
 #pragma unroll
@@ -870,11 +988,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     if (rank > 0 || !prow) wait();  // no CTA leaves while another reads its list
   };
 
-  if (few) {
+  float bound = -INFINITY;  // top-k keeps none below
+  if (bounded) {
     uint32_t low = lane < cs ? (cs > 1 ? peer(&s.low, lane) : s.low) : 0xffffffffu;
     low = __reduce_min_sync(0xffffffffu, low);
-    const float bound = low <= key_of(-INFINITY) ? -INFINITY : logit_of(low);
-    const int m = gather([&](float l) { return l < bound; }, [&](float l, int) { return l >= bound; });
+    if (low > key_of(-INFINITY)) bound = logit_of(low);
+  }
+  if (few) {
+    const int m = gather(bound, INFINITY, [&](float, int) { return true; });
     if (m < 0) return;
     if (m <= kMost) {
       draw_from_list(m, min(top_k, m), by_p, 0);
@@ -899,34 +1020,36 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       // the near entries listed, with all weights' sum: mostly they weigh enough
       if (tid == 0) s.listed = 0;
       __syncthreads();
-      const Added run_sum = add_run<TYPE>(run, run_vecs, first + run_at, r,
-                                          Limits{-INFINITY, 0x7fffffff, near_logit, gone_logit, false, false});
       u64 near = 0;
-      for (u64 large = run_sum.large; large != 0; large &= large - 1) {
-        const int x = run_at + __ffsll(large) - 1;
+      const u64 far = sum_run(Limits{-INFINITY, 0x7fffffff, near_logit, gone_logit, false, target != 0}, [&](int x) {
         const float l = scalar_at(x);
         near += weight_of(r, l, s.powers);
         const int at = atomicAdd(&s.listed, 1);
         if (at < kMost) list[at] = place_of(l, first + x);
-      }
-      block_scan(near, s.scan);
-      const u64 near_sum = block_all(s.scan);
-      block_scan(near + run_sum.far, s.scan);
-      const u64 sum = block_all(s.scan);
+      });
+      const ulonglong2 sum = block_sums(near, near + far, s.sums);
       if (tid == 0) {
-        s.mass = near_sum;
-        s.all = sum;
+        s.mass = sum.x;
+        s.all = sum.y;
       }
       if (!meet()) return gone();
-      u64 unused;
-      if (target == 0) target = max(1ull, times<true>(over_cluster(&s.all, unused), top_p));
-      const bool enough = over_cluster(&s.mass, unused) >= target;
-      const int have = lane < cs ? (cs > 1 ? peer(&s.listed, lane) : s.listed) : 0;
+      u64 x_all = lane < cs ? (cs > 1 ? peer(&s.all, lane) : s.all) : 0;
+      u64 x_near = lane < cs ? (cs > 1 ? peer(&s.mass, lane) : s.mass) : 0;
+      have = lane < cs ? (cs > 1 ? peer(&s.listed, lane) : s.listed) : 0;
+#pragma unroll
+      for (int o = kMaxCluster / 2; o > 0; o >>= 1) {
+        x_all += __shfl_xor_sync(0xffffffffu, x_all, o);
+        x_near += __shfl_xor_sync(0xffffffffu, x_near, o);
+      }
+      if (target == 0) target = max(1ull, times<true>(__shfl_sync(0xffffffffu, x_all, 0), top_p));
+      const bool enough = __shfl_sync(0xffffffffu, x_near, 0) >= target;
       const int listed = static_cast<int>(__reduce_add_sync(0xffffffffu, have));
       if (enough && listed <= kMost) {
         draw_from_list(listed, listed, true, target);
         return gone();
       }
+      // where min-p keeps near entries alone and those do not reach the target, it decides
+      if (!enough && least >= 1ull << (kUnit - kNear)) return threshold;
       if (!meet()) return gone();  // the numbers listed are read
     }
     // what weighs less than `light` is never kept (see above; 1 - top_p rounded down), and
@@ -936,7 +1059,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       const u64 light = times<false>(1ull << kUnit, (1.f - top_p) * (1.f - 0x1p-20f)) / static_cast<u64>(p.vocab);
       reach = static_cast<float>(kUnit - 63 + __clzll(max(light, 1ull))) + 0.5f;
     }
-    auto counts = [&](float l) { return by_mass ? (r.m - l) * r.chi < reach : l > -INFINITY; };
+    auto counts = [&](float l) { return l >= bound && (by_mass ? (r.m - l) * r.chi < reach : l > -INFINITY); };
+    const float least_logit = by_mass ? fmaxf(bound, r.m - (reach + 0.01f) / r.chi - margin) : bound;  // (or below)
     const u64 given = target;
     bool whole = false;
     for (int round = 0;; ++round) {
@@ -963,14 +1087,36 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           if (hi) atomicAdd(bin_hi + d, hi);
         }
       };
-      each([&](const float4& v, int x) {
-        if (!counts(most_of(v))) return;
-#pragma unroll 1
-        for (int i = 0; i < 4; ++i) {
-          const float l = entry(v, i);
-          put(l, x + i, by_mass && counts(l) ? weight_of(r, l, s.powers) : 0);
-        }
-      });
+      const bool by_twos = by_mass && round == 0;
+      each_between(round > 0 ? lowest_of(bin) : by_twos ? fmaxf(least_logit, lowest_of(kNearBins)) : least_logit,
+                   round > 0 ? highest_of(bin) : INFINITY, [&](float l, int index) {
+                     if (by_twos && bin_of(l) >= kNearBins) return;
+                     put(l, index, by_mass && counts(l) ? weight_of(r, l, s.powers) : 0);
+                   });
+      if (by_twos) {
+        // far weights by twos; below 2^32, their lower 16 bits and the others are added
+        // apart: no carry (a slice's entries' sums stay below 2^32)
+        each([&](const float4& v, int) {
+          if (most_of(v) < least_logit) return;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float l0 = h ? v.z : v.x, l1 = h ? v.w : v.y;
+            uint64_t e, power;
+            far_two<false>(r, f2_pack(l0, l1), e, power);
+            const uint64_t w2 = f2_mul(f2_mul(e, power), f2_pack(0x1p45f, 0x1p45f));
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float l = i ? l1 : l0;
+              const int d = bin_of(l);
+              if (d < kNearBins || !counts(l)) continue;
+              const uint32_t w = __float2uint_rn(i ? f2_hi(w2) : f2_lo(w2));
+              atomicAdd(bin_count + d, 1u);
+              atomicAdd(bin_lo + d, w & 0xffffu);
+              atomicAdd(bin_hi + d, w >> 16);
+            }
+          }
+        });
+      }
       if (!meet()) return gone();
       // this CTA's part of the bins, over the cluster
       const int part = kBins / cs, each_bins = max(1, part / kThreads);
@@ -989,7 +1135,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 #pragma unroll
         for (int k = 0; k < kMaxCluster; ++k) {
           c += x[k];
-          w += (static_cast<u64>(hi[k]) << 32) + lo[k];
+          w += (static_cast<u64>(hi[k]) << (round == 0 && b >= kNearBins ? 16 : 32)) + lo[k];
         }
       };
       u64 c = 0, ms = 0;
@@ -1058,7 +1204,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     // the bin's entries, or all down to it (of the bin, those in the histogram and, for
     // top-p, maybe lighter ones, which come behind them)
     if (whole) {
-      m = gather([&](float l) { return bin_of(l) > bin; }, [&](float l, int) { return bin_of(l) <= bin; });
+      m = gather(lowest_of(bin), INFINITY, [&](float l, int) { return bin_of(l) <= bin; });
       if (m < 0) return gone();
       if (m <= kMost) {
         draw_from_list(m, by_mass ? m : static_cast<int>(given), by_p, by_mass ? target : 0);
@@ -1066,12 +1212,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       }
       if (!meet()) return gone();  // the numbers listed are read
     }
-    m = gather([&](float l) { return bin_of(l) > bin; },
-               [&](float l, int index) {
-                 if (bin_of(l) != bin || !counts(l)) return false;
-                 if (shift < 32 + kIndexBits && (place_of(l, index) >> shift) != prefix) return false;
-                 return true;
-               });
+    m = gather(lowest_of(bin), highest_of(bin), [&](float l, int index) {
+      if (bin_of(l) != bin || !counts(l)) return false;
+      return shift >= 32 + kIndexBits || (place_of(l, index) >> shift) == prefix;
+    });
     if (m < 0) return gone();
     if (whole) target -= by_mass ? above_mass : above;
     if (rank == 0) {
@@ -1105,13 +1249,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     // with min-p the entries that may pass are weighed one by one, the others left out
     const bool least_too = floor_weight != 0;
     const float one_by_one = least_too ? r.m - (log2f(1.f / min_p) + 1.f) / r.chi - margin : near_logit;
-    const Added run_sum = add_run<TYPE>(run, run_vecs, first + run_at, r,
-                                        Limits{floor_logit, floor_index, one_by_one, gone_logit, place != 0, least_too});
-    mine = least_too ? 0 : run_sum.far;
-    for (u64 large = run_sum.large; large != 0; large &= large - 1) {
-      const u64 w = weight_of(r, scalar_at(run_at + __ffsll(large) - 1), s.powers);
-      if (w >= floor_weight) mine += w;
-    }
+    u64 by_one = 0;
+    const u64 far = sum_run(Limits{floor_logit, floor_index, one_by_one, gone_logit, place != 0, least_too}, [&](int x) {
+      const u64 w = weight_of(r, scalar_at(x), s.powers);
+      if (w >= floor_weight) by_one += w;
+    });
+    mine = by_one + (least_too ? 0 : far);
     end = block_scan(mine, s.scan);
     const u64 sum = block_all(s.scan);
     if (tid == 0) s.sum = sum;
@@ -1255,18 +1398,29 @@ extern "C" sv_status sv_sample_tokens(const sv_sample_params* c, sv_stream_t str
   p.probs = c->probs;
   p.err = static_cast<int*>(c->workspace);
   p.vocab = c->vocab;
-  // A CTA per kSlice entries; while SMs are free, more and smaller slices.
-  p.cluster = 1;
-  while (p.cluster < sample::kMaxCluster && p.cluster * sample::kSlice < c->vocab) p.cluster *= 2;
-  while (p.cluster < sample::kMaxCluster && static_cast<long long>(c->rows) * p.cluster * 2 <= sms &&
-         c->vocab >= 2048 * p.cluster)
-    p.cluster *= 2;
-  p.slice = ((c->vocab + p.cluster - 1) / p.cluster + 7) / 8 * 8;
-  const int vecs = p.slice / (c->dtype == SV_FP32 ? 4 : 8);
-  p.per = (vecs + sample::kThreads - 1) / sample::kThreads;
-  p.per_inverse = ((1u << 18) + p.per - 1) / p.per;
-  p.val_bytes = static_cast<uint32_t>((vecs + (p.per & 1 ? 0 : vecs / p.per) + 1) * 16);
-  const size_t smem = p.val_bytes + 2 * sample::kMost * 8;
+  // As few CTAs as hold a row with two of them on an SM; more and smaller slices as
+  // long as all rows are on the SMs at once.  Most of a row's time is steps that take as
+  // long for a small slice as for a large one (256 rows of 151936 16-bit logits, top-k 50:
+  // clusters of eight 111 us, of four 78).
+  int smem = 0;
+  auto lay_out = [&](int cluster) {
+    p.cluster = cluster;
+    p.slice = ((c->vocab + cluster - 1) / cluster + 7) / 8 * 8;
+    const int vecs = p.slice / (c->dtype == SV_FP32 ? 4 : 8);
+    p.per = (vecs + sample::kThreads - 1) / sample::kThreads;
+    // runs of an even number of vectors lie a vector apart; where that takes too much
+    // room, runs of one more (in fewer threads)
+    auto bytes = [&] { return (vecs + (p.per & 1 ? 0 : vecs / p.per) + 1) * 16 + 2 * sample::kMost * 8; };
+    if (bytes() > sample::kHalf) p.per |= 1;
+    p.per_inverse = ((1u << 18) + p.per - 1) / p.per;
+    smem = bytes();
+    p.val_bytes = static_cast<uint32_t>(smem - 2 * sample::kMost * 8);
+  };
+  for (int n = 1; n <= sample::kMaxCluster; n *= 2) {
+    lay_out(n);
+    if (smem <= sample::kHalf && static_cast<long long>(c->rows) * n > sms) break;
+    if (c->vocab < 2048 * n) break;
+  }
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (c->dtype == SV_FP32) return sample::launch<SV_FP32>(p, c->rows, smem, s);
   return c->dtype == SV_FP16 ? sample::launch<SV_FP16>(p, c->rows, smem, s) : sample::launch<SV_BF16>(p, c->rows, smem, s);

@@ -1,10 +1,11 @@
 """Token sampling on the GPU against the oracle: tokens are equal, kept sets are
 equal, logprobs and probabilities within fp32.
 
-The kernel's weights are off by 2^-36 of the largest, so a token may differ from
-float64's only where the uniform (or a filter's limit) lies within that of a border
-of sums: a draw nearer than 1e-9 to one (a uniform of one half over a symmetric row)
-may take the entry on either side.
+The kernel's weights are off by 2^-36 of the largest, and its sums of weights below
+2^-13 by what fp32 rounds over 64 entries (in practice below 2^-30 of the row), so a
+token may differ from float64's only where the uniform (or a filter's limit) lies
+within that of a border of sums: a draw nearer than 1e-9 to one (a uniform of one half
+over a symmetric row) may take the entry on either side.
 Logprobs: the logarithm's argument is off by 2^-23 at most, and so are the
 exponent's product and its sum, each at most 2^-23 of |logprob| more.
 Probabilities: the hardware's power 2^-22, a quotient and two products 2^-23 each."""
@@ -133,6 +134,30 @@ def test_masked_entries_and_extreme_values():
     u = torch.tensor([0.9, 0.6, 0.2, 0.1, 0.5, 0.25], device="cuda")
     for settings in (dict(), dict(top_k=2), dict(top_p=0.5001), dict(min_p=0.3), dict(temperature=0.0), dict(top_k=1500)):
         check(x, u, **settings)
+
+
+@pytest.mark.parametrize("settings", [dict(), dict(top_p=0.95, temperature=1.3), dict(top_p=0.98, min_p=0.02, temperature=1.2),
+                                      dict(top_k=700), dict(top_k=1000, top_p=0.9), dict(top_p=0.995, temperature=1.2)])
+def test_batches_that_give_a_cta_a_whole_row(settings):
+    """More rows than SMs: runs of more entries than are summed in fp32, and flat rows whose nucleus is thousands of
+    entries; a few rows against the oracle."""
+    x, u = random_logits(160, 38000, torch.bfloat16, seed=21, sigma=2.0)
+    some = [0, 77, 159]
+    tokens, logprobs, probs, err = sample(x, u, probs=True, **settings)
+    assert err == 0
+    few = sample(x[some].contiguous(), u[some].contiguous(), probs=True, **settings)  # three rows: eight CTAs each
+    for i, r in enumerate(some):
+        args = [float(np.float32(settings.get(k, d))) for k, d in (("top_p", 1.0), ("min_p", 0.0))]
+        token, logprob, want, gap = oracle.sample_token(x[r].double().cpu().numpy(), float(u[r]),
+                                                        float(np.float32(settings.get("temperature", 1.0))),
+                                                        settings.get("top_k", 0), *args)
+        assert gap > 1e-9   # (these uniforms lie at no border)
+        for t, lp, p in ((tokens[r], logprobs[r], probs[r]), (few[0][i], few[1][i], few[2][i])):
+            assert int(t) == token
+            assert abs(float(lp) - logprob) <= 2.0 ** -23 * (2 + 2 * abs(logprob))
+            got = p.double().cpu().numpy()
+            assert ((got > 0) == (want > 0)).all()
+            np.testing.assert_allclose(got, want, rtol=2.0 ** -22 * 3, atol=1e-44)
 
 
 def test_uniform_at_the_ends():
