@@ -16,7 +16,8 @@
 // sums) and angles while they are on their way, and keeps cos and sin in shared
 // memory for all heads.  The next grid starts at this one's end, not before: it may
 // be a tree attention that reads context ahead of its wait
-// (SV_ATTN_EARLY_CONTEXT).
+// (SV_ATTN_EARLY_CONTEXT).  32 tokens of 32 and 8 heads of 128 take 3.5 us, 7620 tokens
+// 38.7 (4.8 TB/s; start and tail of 2.5 waves of CTAs).
 #include <math.h>
 
 #include <algorithm>
@@ -273,6 +274,9 @@ static sv_status launch(const Params& p, cudaStream_t stream) {
   return launch<FP16, NEXT, TOKENS, 0>(p, stream);
 }
 
+// Four tokens per CTA share its start, with fewer CTAs than SMs at once that costs more
+// than it saves (with the events around them: 32 tokens by ones 8.2 us, by fours 12.3;
+// 1024 tokens 16.4 and 14.4, 7620 tokens 47 and 43; by eights 45).
 template <bool FP16, bool NEXT>
 static sv_status launch(const Params& p, cudaStream_t stream) {
   return p.total_tokens > 1024 ? launch<FP16, NEXT, 4>(p, stream) : launch<FP16, NEXT, 1>(p, stream);
