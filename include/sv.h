@@ -737,7 +737,7 @@ sv_status sv_prefix_attention(const sv_prefix_params* params, sv_stream_t stream
  * first of the order.  logprobs[r] is the natural logarithm of the token's
  * share of the kept weights; probs[r, :] are all shares, 0 for the others: the
  * draft distributions of sv_sample_accept, and their tokens, from a draft
- * model's logits.
+ * model's logits.  Outputs overlap no input.
  *
  * Logits of -inf are entries that do not exist.  A row without any other
  * entry, with +inf or NaN among its logits, or with a setting that is NaN, a

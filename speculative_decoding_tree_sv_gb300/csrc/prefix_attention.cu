@@ -319,12 +319,11 @@ __device__ __forceinline__ void combine_few(const PrefixParams& p, int g, int kh
 // 16 rows of an M tile's worth of a larger group's rows and 16 of its D / 4 columns of
 // four: half a warp per 16 rows, eight pieces in flight.
 template <int D, bool FP16>
-__device__ __forceinline__ void combine_shared(const PrefixParams& p, int g, int kh, int tile, int sub) {
+__device__ __forceinline__ void combine_shared(const PrefixParams& p, const PrefixSeq& x, int g, int kh, int tile, int sub) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const PrefixSeq x = load_seq(p, g, false);
   const int col = (sub % (D / 64)) * 16 + warp * 2 + (lane >> 4);
   const int r = sub / (D / 64) * 16 + (lane & 15), i = tile * p.tile_tokens + r / p.group, hg = r % p.group;
-  if (r >= p.tile_tokens * p.group || i >= x.n || in_rows(p, x.n)) return;
+  if (r >= p.tile_tokens * p.group || i >= x.n) return;
   const int t = x.n0 + i;
   int b;
   PrefixSeq s;
@@ -404,7 +403,12 @@ __global__ void __launch_bounds__(kCombineThreads, 4) prefix_combine_kernel(cons
   block /= n.group_subs;
   const int tile = block % n.group_tiles;
   block /= n.group_tiles;
-  combine_shared<D, FP16>(p, block / p.num_kv_heads, block % p.num_kv_heads, tile, sub);
+  const int g = block / p.num_kv_heads;
+  const PrefixSeq x = load_seq(p, g, false);
+  if (in_rows(p, x.n)) return;
+#pragma unroll 1
+  for (int i = tile; static_cast<long long>(i) * p.tile_tokens < x.n; i += n.group_tiles)
+    combine_shared<D, FP16>(p, x, g, block % p.num_kv_heads, i, sub);
 }
 
 struct PrefixPlan {
@@ -488,7 +492,7 @@ static sv_status check(const sv_prefix_params* c) {
   if (st != SV_OK) return st;
   if (!c->cu_groups || !c->prefix_lens || c->num_groups < 1 || c->num_groups > c->batch || c->max_group_tokens < 0)
     return SV_ERR_INVALID_ARG;
-  if (static_cast<long long>(c->batch) * c->num_kv_heads > (1 << 29)) return SV_ERR_UNSUPPORTED;
+  if (static_cast<long long>(c->batch) * c->num_kv_heads > (1 << 22)) return SV_ERR_UNSUPPORTED;  // (the combine's grid)
   // (tile units of all heads count in 32 bits)
   if (static_cast<long long>(c->total_tokens) * c->num_q_heads > (1ll << 36)) return SV_ERR_UNSUPPORTED;
   return SV_OK;
@@ -522,12 +526,18 @@ static sv_status launch_combine(const PrefixLaunch& l, int group_tokens) {
   n.warps = group_units <= 64 ? 8 : group_units <= 256 ? 4 : group_units <= 1024 ? 2 : 1;
   const int few_rows = p.row_limit > 0 ? static_cast<int>(std::min<long long>(group_rows, kRowUnit)) : 0;
   n.few_blocks = (few_rows * n.warps + kCombineWarps - 1) / kCombineWarps;
-  n.group_tiles = group_rows > p.row_limit ? (group_tokens + p.tile_tokens - 1) / p.tile_tokens : 0;
   n.group_subs = static_cast<int>((static_cast<long long>(std::min(group_tokens, p.tile_tokens)) * p.group + 15) / 16) * (D / 64);
-  const long long few = static_cast<long long>(group_units) * n.few_blocks;
-  n.few = static_cast<int>(std::min<long long>(few, 0x7fffffff));
-  const long long blocks = n.tiles + n.rows + few + static_cast<long long>(group_units) * n.group_tiles * n.group_subs;
-  if (blocks > 0x7fffffff) return SV_ERR_UNSUPPORTED;
+  // M tiles of a group: no more than the call's tokens have on average (the bound on a
+  // group's may be any; a block takes more of them in turn), nor blocks than start soon
+  n.group_tiles = 0;
+  if (group_rows > p.row_limit) {
+    const long long need = (group_tokens + p.tile_tokens - 1) / p.tile_tokens;
+    const long long mean = p.total_tokens / (static_cast<long long>(p.tile_tokens) * p.num_groups) + 1;
+    const long long soon = std::max(1ll, (1ll << 20) / (static_cast<long long>(group_units) * n.group_subs));
+    n.group_tiles = static_cast<int>(std::min(std::min(need, mean), soon));
+  }
+  n.few = group_units * n.few_blocks;
+  const long long blocks = n.tiles + n.rows + n.few + static_cast<long long>(group_units) * n.group_tiles * n.group_subs;
   cudaLaunchConfig_t cfg = cudaLaunchConfig_t{};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
   cfg.blockDim = dim3(kCombineThreads, 1, 1);

@@ -1371,6 +1371,7 @@ extern "C" sv_status sv_sample_tokens(const sv_sample_params* c, sv_stream_t str
   if (c == nullptr) return SV_ERR_INVALID_ARG;
   if (c->rows < 0 || c->vocab < 1 || c->flags != 0) return SV_ERR_INVALID_ARG;
   if (c->rows > 0 && (!c->logits || !c->uniforms || !c->tokens)) return SV_ERR_INVALID_ARG;  // (an empty tensor has no address)
+  if (c->probs != nullptr && c->probs == c->logits) return SV_ERR_INVALID_ARG;  // (read again after the first are written)
   if (c->dtype != SV_BF16 && c->dtype != SV_FP16 && c->dtype != SV_FP32) return SV_ERR_UNSUPPORTED;
   if (c->vocab > (1 << sample::kIndexBits) || c->rows > (1 << 24)) return SV_ERR_UNSUPPORTED;
   for (const long long stride : {c->logits_stride, c->probs_stride})

@@ -92,6 +92,7 @@ def sample(**over):
     (dict(logits_stride=(1 << 38) + 1), 1), (dict(logits=A + 2), 1), (dict(dtype=0, logits=A + 1), 1),
     (dict(uniforms=A + 2), 1), (dict(temperature=A + 2), 1), (dict(top_k=A + 1), 1), (dict(top_p=A + 2), 1),
     (dict(min_p=A + 3), 1), (dict(tokens=A + 2), 1), (dict(logprobs=A + 2), 1), (dict(probs=A + 2), 1),
+    (dict(probs=A), 1),                              # in place
     (dict(workspace=A + 2, workspace_bytes=256), 1), (dict(workspace=A, workspace_bytes=255), 4),
 ])
 def test_sample_tokens_refuses(lib, over, status):

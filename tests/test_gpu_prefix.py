@@ -162,6 +162,14 @@ def test_without_lse_and_larger_host_bounds():
     c.check()
 
 
+def test_groups_of_very_different_sizes():
+    """One group of several M tiles among many small ones, its bound and a far larger one."""
+    for most in (50, 66, 1 << 20):
+        c = Case([64] * 9, [[(i, 1) for i in range(50)]] + [[(3, 1), (20, 1)]] * 8, 32, 8, 128, seed=12)
+        assert c.run(max_group_tokens=most) == 0
+        c.check()
+
+
 def test_equals_chunk_attention():
     """Each of the two is off by eps / 2 (A + |out|) + 2e-4 A at most, A the mean of |v| under the weights (itself
     computed to 1 %), so they differ by twice that."""
