@@ -25,6 +25,7 @@
 #include <algorithm>
 
 #include "chunk_combine.cuh"
+#include "prefix_kernels.h"
 
 namespace sv {
 namespace chunk {
@@ -428,10 +429,10 @@ static PrefixPlan make_plan(const sv_prefix_params* c, int sms) {
   PrefixPlan w{};
   // a shared group has fewer tokens than an M tile per sequence
   w.group_tokens = static_cast<int>(std::min<long long>(c->max_group_tokens, c->batch * tile_tokens));
-  const long long most = static_cast<long long>(std::max(w.group_tokens, c->max_tokens)) * G;
-  const long long least = c->total_tokens - (c->batch - 1ll) * c->max_tokens;  // tokens of the shortest sequence
-  w.row_workers = G <= kRowUnit && least * G <= kRowUnit ? sms * kRowWarps : 0;
-  w.tile_ctas = most > kRowUnit ? sms : 0;
+  const PrefixKernels kernels =
+      prefix_kernels(c->total_tokens, c->batch, c->max_tokens, w.group_tokens, G, kRowUnit);
+  w.row_workers = kernels.rows ? sms * kRowWarps : 0;
+  w.tile_ctas = kernels.tiles ? sms : 0;
   w.compact = c->total_tokens > c->batch * tile_tokens;
   w.rows = w.compact ? c->batch * tile_tokens : c->total_tokens;
   size_t at = kWorkspaceHeader;

@@ -3,6 +3,8 @@ shared prefix, token sampling) without a GPU: the library's host checks (fake
 device addresses, no CUDA call on these paths) and the binding's checks of tensors."""
 
 import ctypes
+import random
+import subprocess
 
 import pytest
 import torch
@@ -204,3 +206,35 @@ def test_the_append_with_rotation_signals_nothing_early():
     with open(f"{build.CSRC}/rope_append.cu") as f:
         source = f.read()
     assert "griddep_wait();" in source and "launch_dependents" not in source
+
+
+KERNELS = r"""
+#include "prefix_kernels.h"
+extern "C" int kernels(long long total, long long batch, long long most, long long group, long long heads) {
+  const sv::PrefixKernels k = sv::prefix_kernels(total, batch, most, group, heads, 16);
+  return (k.rows ? 1 : 0) | (k.tiles ? 2 : 0);
+}
+"""
+
+
+def test_every_entry_of_a_prefix_call_has_a_kernel(tmp_path):
+    """Whatever the token rows behind the last sequence and the host's bounds: an entry of n tokens goes to the row kernel
+    up to 16 rows per KV head where that is in the call, else to the tile kernel, which then is."""
+    source, module = tmp_path / "kernels.cpp", tmp_path / "kernels.so"
+    source.write_text(KERNELS)
+    subprocess.run(["g++", "-std=c++17", "-shared", "-fPIC", "-I", build.CSRC, "-o", module, source], check=True)
+    kernels = ctypes.CDLL(str(module)).kernels
+    kernels.argtypes = [ctypes.c_longlong] * 5
+    rng = random.Random(1)
+    for lens in [[1], [1] * 4, [1] * 64, [0, 1], [2, 9], [5, 1, 1], [17], [40, 30]] + [
+            [rng.randint(0, 30) for _ in range(rng.randint(1, 12))] for _ in range(60)]:
+        for heads in (1, 2, 4, 5, 8, 16, 17, 32, 128):
+            for padding in (0, 1, 2, 3, 4, 7, 8, 40, 900, 1 << 29):
+                for loose in (0, 1, 50):
+                    for group in (max(lens), sum(lens)):
+                        taken = kernels(sum(lens) + padding, len(lens), max(1, max(lens)) + loose, max(1, group) + loose, heads)
+                        for n in lens + [group]:
+                            by_rows = taken & 1 and n * heads <= 16
+                            assert n == 0 or by_rows or taken & 2, (lens, heads, padding, loose, group)
+    # a padded step of single tokens stays in the row kernel
+    assert kernels(128, 64, 1, 4, 4) == 1 and kernels(128, 64, 1, 64, 4) == 3

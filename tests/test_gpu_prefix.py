@@ -275,3 +275,24 @@ def test_captured_replayed_and_two_streams():
     torch.cuda.synchronize()
     assert torch.equal(first, c.out)
     d.check()
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(2, 2, 128), (8, 2, 64), (16, 2, 128), (32, 2, 64), (20, 1, 64)])
+@pytest.mark.parametrize("each", [1, 2, 4])
+def test_padded_decode_steps(each, Hq, Hkv, D):
+    """One token per sequence and token rows behind them, as of a step captured for more sequences; the workspace held
+    other calls' rows (here NaN, and indices of -1) behind its header."""
+    for extra in (0, 1, 2, 4, 12, 40):
+        c = Case([48, 0, 1600], [[(5 * i + 1, 1) for i in range(each)]] * 3, Hq, Hkv, D, seed=each + extra, extra_rows=extra)
+        p = c.params()
+        c.ws[256:] = 255
+        sv.sv_prefix_attention(p)
+        torch.cuda.synchronize()
+        assert sv.sv_get_device_error(c.ws) == 0
+        c.check()
+    c = Case([320], [[(3, 1), (0, 0), (9, 1)]], Hq, Hkv, D, seed=each, extra_rows=70)  # and one that brings nothing
+    p = c.params()
+    c.ws[256:] = 255
+    sv.sv_prefix_attention(p)
+    torch.cuda.synchronize()
+    c.check()
