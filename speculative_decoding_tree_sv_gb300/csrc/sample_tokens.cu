@@ -295,10 +295,10 @@ struct Pick {
 };
 
 // The cluster's barrier: an mbarrier in every CTA that one thread of each CTA arrives
-// on, between __syncthreads.  (The hardware's wants every warp together, which the
-// compiler does not promise inline assembly behind loops that threads leave one by
-// one, and its wait has no limit.)  Where a wait gives up, `dead` is set and
-// sv_get_device_error tells.
+// on, between __syncthreads.  (The hardware's barrier, which the kernel passes once at
+// its start, hung behind loops that threads leave one by one, and its wait has no limit.)
+// Where a wait gives up, `dead` is set and sv_get_device_error tells; the CTA then stays
+// as long again, so that the others have given up too before its memory goes.
 struct Barrier {
   uint64_t arrived;
   uint32_t phase;
@@ -316,7 +316,7 @@ __device__ __noinline__ void cluster_arrive(Barrier* b, int cluster) {
 __device__ __noinline__ void cluster_wait(Barrier* b, int* err) {
   if (threadIdx.x == 0) {
     const uint32_t parity = b->phase++ & 1;
-    const uint64_t t0 = globaltimer_ns();
+    uint64_t t0 = globaltimer_ns();
     for (uint32_t i = 1;; ++i) {
       uint32_t ok;
       asm volatile(
@@ -330,6 +330,8 @@ __device__ __noinline__ void cluster_wait(Barrier* b, int* err) {
       if ((i & 63u) == 0 && globaltimer_ns() - t0 > kWaitTimeoutNs) {
         b->dead = 1;
         report_error(err, SV_DEVERR_TIMEOUT);
+        t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 <= kWaitTimeoutNs) __nanosleep(1000);
         break;
       }
     }
@@ -649,9 +651,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     s.barrier.dead = 0;
     fence_mbar_init();
   }
-  // Every CTA has started and its barrier is ready when this one is waited for below.
+  // Every CTA has started and its barrier is ready behind this.  (The hardware's barrier,
+  // which no loop or branch of a thread's own precedes.)
   __syncthreads();
-  if (cs > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  if (cs > 1)
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
   auto arrive = [&] {
     if (cs > 1) cluster_arrive(&s.barrier, cs);
   };
@@ -743,8 +747,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     const uint32_t k = __reduce_max_sync(0xffffffffu, lane < kWarps ? s.best[lane] : 0);
     if (lane == 0) s.top = k;
   }
-  __syncthreads();
-  if (cs > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   if (!meet()) return;
   const uint32_t top = __reduce_max_sync(0xffffffffu, lane < cs ? (cs > 1 ? peer(&s.top, lane) : s.top) : 0);
   const float most = logit_of(top);

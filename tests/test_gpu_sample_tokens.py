@@ -251,3 +251,22 @@ def test_draft_tokens_and_distributions_feed_stochastic_acceptance():
                         bonus, ws)
     assert sv.sv_get_device_error(ws) == 0
     assert length.item() == 1 and nodes.tolist() == [[0, 1]]
+
+
+@pytest.mark.parametrize("R", [3, 20, 50, 100, 170])
+@pytest.mark.parametrize("V", [2049, 16395, 20011])
+def test_clusters_whose_threads_have_unequal_parts(R, V):
+    """Clusters of eight, four, two and one CTAs whose threads leave the loops over their parts one by one, before the
+    barriers that follow; three rows against the oracle, and the same bits again."""
+    base, u = random_logits(R, V + 3, torch.bfloat16, seed=R + V)
+    x = base[:, 3:]
+    for settings in (dict(), dict(top_k=40, top_p=0.9), dict(top_p=0.95), dict(top_k=900)):
+        tokens, logprobs, probs, err = sample(x, u, probs=True, **settings)
+        again = sample(x, u, probs=True, **settings)
+        assert err == 0 and again[3] == 0
+        assert torch.equal(tokens, again[0]) and torch.equal(logprobs, again[1]) and torch.equal(probs, again[2])
+        for r in (0, R // 2, R - 1):
+            token, logprob, want, gap = oracle.sample_token(x[r].double().cpu().numpy(), float(u[r]), 1.0,
+                                                            settings.get("top_k", 0), float(np.float32(settings.get("top_p", 1.0))))
+            assert gap > 1e-9 and int(tokens[r]) == token
+            assert ((probs[r] > 0).cpu().numpy() == (want > 0)).all()
