@@ -4,9 +4,10 @@
 // Mathematics: pair j of a head turns by the angle x f_j, x the token's position
 // and f_j = inv_freq[j].  At position 10^6 an angle held in fp32 is off by up to
 // 0.06, so angles are counted in turns as 64-bit fixed-point fractions: f_j / 2 pi
-// becomes an integer once (exact to 2^-64 of a turn), its product with x wraps at
+// becomes an integer once (exact to 2^-64 of a turn up to f_j = 128, to 2^-62 up to
+// 1024, so to 2^-30 of half a turn at any 32-bit x), its product with x wraps at
 // whole turns by itself, and the top 32 bits give cos and sin in fp32 (off by at
-// most 2^-25 of half a turn).  The rotated values are fp32, rounded once to the 16
+// most 2^-25 of half a turn more).  The rotated values are fp32, rounded once to the 16
 // bits of the tensors.
 //
 // Bound by HBM: q, k and v are read and written once.  A unit of work is 16
@@ -52,12 +53,15 @@ struct Params {
   int num_q_heads, num_kv_heads, units_per_head, rotary_units;
 };
 
-// f / 2 pi in units of 2^-64 turns.  f = m 2^e with a 24-bit m; m times the 64 bits
-// of 2 / pi has 88, of which a shift keeps what lies below a whole turn.  `ok` is
+// f / 2 pi in units of 2^-64 turns.  f = m 2^e with a 24-bit m; m times 2 / pi rounded
+// to 64 bits (which is off by 2^-70, a 64th of a unit) has 88, of which a shift by s keeps what
+// lies below a whole turn: off by a unit for the bits dropped and 2^(18 - s), four where
+// f is near 1024.  (2 / pi cut off after 64 bits is off by a unit: 2^(24 - s) here, 2^-24 of
+// half a turn at x = 2^31.)  `ok` is
 // false for f beyond 1024 (more than 160 turns from a token to the next), infinite
 // or NaN.
 __device__ __forceinline__ uint64_t turns_of(float f, bool& ok) {
-  constexpr uint64_t kTwoOverPi = 0xa2f9836e4e441529ull;  // 2^64 * 2 / pi
+  constexpr uint64_t kTwoOverPi = 0xa2f9836e4e44152aull;  // 2^64 * 2 / pi, to nearest
   const uint32_t bits = __float_as_uint(f);
   const int exponent = (bits >> 23) & 0xff;
   const uint64_t m = (bits & 0x7fffffu) | (exponent ? 0x800000u : 0u);

@@ -5,6 +5,8 @@ eps / 2 of it; below the smallest normal fp16 2^-25), from fp32 products of an
 angle that is off by pi 2^-25 at most, cos and sin by two units in the last place
 more: 5e-7 of |a| + |c| times the amplitude.  v and what does not turn are bit copies."""
 
+from fractions import Fraction
+
 import numpy as np
 import pytest
 import torch
@@ -14,6 +16,7 @@ from speculative_decoding_tree_sv_gb300 import binding as sv
 from tests.gpu_support import ensure_lib
 
 pytestmark = pytest.mark.gpu
+PI = Fraction(31415926535897932384626433832795028841971693993751, 10 ** 49)
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -221,3 +224,28 @@ def test_captured_and_replayed_on_another_stream():
     call(out, kc, vc)
     torch.cuda.synchronize()
     assert torch.equal(out, out2)
+
+
+@pytest.mark.parametrize("f", [float(np.nextafter(np.float32(1024), np.float32(0))), 700.1, 1.0, 0.7654321])
+def test_angles_at_the_ends_of_both_ranges(f):
+    """Angles within 2^-24 of half a turn at positions next to 2^31, where they show: next to a quarter turn the cosine
+    (the pair (1, 0) turned) is small, so its 16 bits hold the angle's error.  Beside that the cosine is off by
+    fp32's rounding of it and half a step of bf16, relative."""
+    exact = Fraction(float(np.float32(f))) / (2 * PI)                # turns per position
+    step = np.uint64(int(exact * 2 ** 64) % 2 ** 64)                 # 2^-33 of a turn off at most at 2^31
+    x = np.arange(2 ** 31 - 2 ** 22, 2 ** 31, dtype=np.uint64)
+    half_turns = (x * step).view(np.int64).astype(np.float64) / 2 ** 63
+    x = x[np.argsort(np.abs(np.abs(half_turns) - 0.5))[:24]].astype(np.int64)
+    x = np.concatenate([x, -x])
+    T = len(x)
+    q = torch.zeros((T, 1, 16), dtype=torch.bfloat16, device="cuda")
+    q[:, :, :8] = 1.0
+    out, cache = torch.empty_like(q), torch.zeros((T, 1, 1, 16), dtype=torch.bfloat16, device="cuda")
+    ints = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    sv.sv_rope_append(q, q, q, out, cache, cache.clone(), ints(list(range(T)))[None], ints([0]), ints([0, T]),
+                      torch.full((8,), f, device="cuda"), positions=ints(x))
+    for t in range(T):
+        turns = exact * int(x[t]) % 1
+        want = float(np.sin(float(2 * PI * (Fraction(1, 4) - turns if turns < Fraction(1, 2) else turns - Fraction(3, 4)))))
+        assert abs(want) < 1e-4
+        assert (out[t, 0, :8].double() - want).abs().max() <= np.pi * 2.0 ** -24 + 1.01 * 2.0 ** -8 * abs(want), int(x[t])
