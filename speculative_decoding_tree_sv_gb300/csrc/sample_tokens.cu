@@ -475,7 +475,7 @@ __device__ __forceinline__ int minus_less(int n, u64 a, u64 b) {
   return n;
 }
 
-// The same for few entries, zeros left out (what lies behind the others then is not
+// The same for few entries, of the zeros only the first (what lies behind it then is not
 // said): an entry's place is the number of those above it, counted by several threads
 // (117 entries 2.6 -> 1.2 us; 361 in steps 7, counted 11).
 constexpr int kCounted = 256;
@@ -496,7 +496,7 @@ __device__ __noinline__ void sort_few(u64* a, int size) {
   }
   for (int o = 1; o < parts; o *= 2) above += __shfl_xor_sync(0xffffffffu, above, o);
   __syncthreads();
-  if (own != 0) a[-above] = own;
+  if (e < size) a[-above] = own;
   __syncthreads();
 }
 
@@ -946,7 +946,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       }
       __syncthreads();
       const int cut = s.cut;
-      // (least is at most the first weight)
+      // (least is at most the first weight; a place is 0 for the last of 2^18 entries without weight
+      // alone, and then the last of the places)
       u64 place[kPer];
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {

@@ -270,3 +270,17 @@ def test_clusters_whose_threads_have_unequal_parts(R, V):
                                                             settings.get("top_k", 0), float(np.float32(settings.get("top_p", 1.0))))
             assert gap > 1e-9 and int(tokens[r]) == token
             assert ((probs[r] > 0).cpu().numpy() == (want > 0)).all()
+
+
+
+def last_entry_rows():
+    x = torch.full((2, 1 << 18), -1000.0, device="cuda")
+    x[:, 0], x[:, 1], x[:, -1], x[:, 7] = 0.0, -0.5, -40.0, -41.0
+    x[1, 3:260] = -2.0
+    return x, torch.tensor([0.7, 0.999], device="cuda")
+
+
+def test_the_last_entry_of_the_largest_vocabulary():
+    """It may be kept with a weight below the last bit of the sums, in front of another such entry."""
+    for settings in (dict(top_k=3), dict(top_k=4), dict(top_k=262)):
+        check(*last_entry_rows(), **settings)
