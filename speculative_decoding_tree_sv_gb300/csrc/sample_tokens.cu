@@ -813,6 +813,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   const float gone_logit = all_near ? -INFINITY : r.m - 100.f / r.chi - margin;
   const u64 least = min_p > 0.f ? times<true>(1ull << kUnit, min_p) : 0;
   const bool by_k = top_k > 0 && top_k < p.vocab, by_p = top_p < 1.f;
+  // Whether min-p keeps an entry of weight w: one without weight (never drawn, it may have a
+  // share) by its weight in fp32.
+  auto passes = [&](u64 w, float l) { return w >= least || (w == 0 && least == 1 && weight32(r, l) >= min_p); };
 
   // Rounded to a whole number by the sum with 2^23; -inf lies in the last bin.
   auto bin_of = [&](float l) {
@@ -952,7 +955,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         const int x = tid * run + i;
-        const bool keep = i < run && x < cut && w[i] >= least;
+        const bool keep = i < run && x < cut && passes(w[i], logit_at(x));
         place[i] = keep ? (static_cast<u64>(kIndexMask - index_of(sorted[x])) << (kUnit + 1)) | w[i] : 0;
         if (i < run) kept += __syncthreads_count(keep);
       }
@@ -1332,7 +1335,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     for (int x = tid; x < n; x += kThreads) {
       const float l = scalar_at(x);
       float v = 0.f;
-      if (keeps(l, first + x) && (least == 0 || weight_of(r, l, s.powers) >= least)) v = weight32(r, l) * inv;
+      if (keeps(l, first + x) && (least == 0 || passes(weight_of(r, l, s.powers), l))) v = weight32(r, l) * inv;
       prow[x] = v;
     }
   }

@@ -284,3 +284,15 @@ def test_the_last_entry_of_the_largest_vocabulary():
     """It may be kept with a weight below the last bit of the sums, in front of another such entry."""
     for settings in (dict(top_k=3), dict(top_k=4), dict(top_k=262)):
         check(*last_entry_rows(), **settings)
+
+
+def test_min_p_below_the_last_bit_of_the_sums():
+    """Entries that weigh as much are kept, and have their share, though no uniform draws them."""
+    for settings in (dict(min_p=1e-30), dict(min_p=1e-30, top_k=262), dict(min_p=3e-18, top_k=500), dict(min_p=3e-18),
+                     dict(min_p=1e-30, top_k=2000, temperature=0.7), dict(min_p=1e-30, top_p=0.9999)):
+        check(*last_entry_rows(), **settings)
+    x, u = random_logits(3, 3001, torch.float32, seed=17)
+    x[:, 500:] -= 30.0
+    for min_p in (1e-17, 1e-20, 1e-37):
+        check(x, u, min_p=min_p)
+        check(x, u, min_p=min_p, top_k=3000)
