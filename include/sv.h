@@ -746,11 +746,11 @@ sv_status sv_prefix_attention(const sv_prefix_params* params, sv_stream_t stream
  * SV_DEVERR_BAD_VALUE.
  *
  * Every weight (the largest is 1) is off by less than 2^-36.  Sums are 64-bit
- * integers, the same on every run; weights below 2^-13 are summed as fp32 over
- * runs of up to 64 entries first, which adds 2^-20 of a run's sum at most and
- * 2^-30 of the row's as a rule.  Only a uniform or a top_p within that of a border
- * may see it; the number of rows, which decides how a row is divided, can move
- * such a border by as much.  Entries below 2^-46 of the largest are not drawn.
+ * integers in units of 2^-45, the same on every run, whatever the other rows and
+ * their number: neither the batch nor the order of sums shows in a row's outputs.
+ * A border of sums is off by 2^-30 of the row's as a rule; only a uniform or a
+ * top_p within that of one may see it.  Entries below 2^-46 of the largest are not
+ * drawn.
  * ---------------------------------------------------------------------- */
 typedef struct sv_sample_params {
   int rows;                 /* R                                             */

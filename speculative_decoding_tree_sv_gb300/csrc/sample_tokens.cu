@@ -8,8 +8,11 @@
 // sum passes u times the sum.  A token is a comparison of sums of up to 2^18 terms
 // with borders that may lie 2^-20 apart, so weights are 64-bit integers in units
 // of 2^-45, off by 2^-36 of the largest at most, and sums are integers, the same in any
-// order.  A weight below 2^-13 needs no more than fp32 for that: those of 64 consecutive
-// entries are summed in fp32 first, which is what most of a large vocabulary costs.
+// order and however a row is divided.  A weight below 2^-13 needs no more than fp32 for
+// that, two at a time, each rounded to a whole unit, which is what most of a large
+// vocabulary costs.  (Summed in fp32 over 64 entries they cost up to 2 % less of a large
+// batch's time, but their rounding let masked entries through at borders, and the batch
+// show in a row's token.)
 //
 // A cluster of CTAs takes a row, each holds its slice in shared memory as it came; all
 // further passes read that.  No filter sorts the row:
@@ -52,11 +55,11 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kHalf = 109 * 1024;  // shared memory of a CTA beside another one
-constexpr int kRunEntries = 64;    // of a thread's run that are summed in fp32, a bit each
+constexpr int kRunEntries = 64;    // of a thread's run that are looked at together, a bit each
 constexpr int kBins = 2048;
 constexpr int kBinBits = 11;
 constexpr int kBinsPerOctave = 32;
-constexpr int kNear = 13;          // weights above 2^-kNear are near (see weight_near), the others far
+constexpr int kNear = 13;          // weights above 2^-kNear are near (see weight_near), lighter ones far (far_two)
 constexpr int kNearBins = kNear * kBinsPerOctave + 1;  // the bins from here on hold far weights alone
 constexpr int kMost = 2048;        // entries that are sorted
 static_assert(3 * kBins * 4 <= 2 * kMost * 8, "the bins lie where the lists do");
@@ -147,7 +150,8 @@ __device__ __forceinline__ float2 exponent_of(const Row& r, float l) {
 
 // A weight of 2^-16 or more in units of 2^-45: 2^(j/32) from the table and 2^r - 1, |r|
 // <= 1/64, from its series, each product with its rounding error beside it: off by
-// 2^-37 of the weight.
+// 2^-35.8 of the weight and the rounding to a unit, so by 2^-36.3 of the largest weight
+// at most (12 million weights at four temperatures against 64 bits).
 __device__ __forceinline__ u64 weight_near(const Row& row, float l, const Power* powers) {
   const float2 y = exponent_of(row, l);
   const float j32 = rintf(y.x * 32.f);
@@ -176,15 +180,13 @@ __device__ __forceinline__ u64 weight_near(const Row& row, float l, const Power*
   return s == 0 ? w : static_cast<u64>(w + (1ll << (s - 1))) >> s;
 }
 
-// The sum of far weights: by a polynomial of degree six for 2^f (2^-26; 2^-23 of a
-// weight with its 24 bits and the exponent's rounding, so 2^-36 at most as the near
-// ones), two at a time, added in fp32 over kRunEntries of a thread's run in two sums of
-// 32: each addition is off by 2^-24 of a sum of at most 2^-8, 2^-27 a run at the very
-// worst.  What is to stay out, and any exponent below -100, is below `least_logit`.
-// EXACT: l - m is a float (16-bit logits: but for entries of 2^-16 of the maximum or
-// less, where the difference's own rounding is as small).
+// Two far weights, as floats in units of 2^-45 (the caller rounds them to whole ones, below
+// 2^32): by a polynomial of degree six for 2^f (2^-26; 2^-23 of a weight with its 24 bits
+// and the exponent's rounding, so 2^-36 at most as the near ones).  Exponents down to
+// -100.  EXACT: l - m is a float (16-bit logits: but for entries of 2^-16 of the maximum
+// or less, where the difference's own rounding is as small).
 template <bool EXACT>
-__device__ __forceinline__ void far_two(const Row& r, uint64_t l, uint64_t& e, uint64_t& power) {
+__device__ __forceinline__ uint64_t far_two(const Row& r, uint64_t l) {
   constexpr float kMagic = 12582912.f;  // 1.5 * 2^23
   auto two = [](float x) { return f2_pack(x, x); };
   const uint64_t minus1 = two(-1.f), nm = two(-r.m), nc = two(-r.chi), chi = two(r.chi), clo = two(r.clo);
@@ -199,41 +201,36 @@ __device__ __forceinline__ void far_two(const Row& r, uint64_t l, uint64_t& e, u
   const uint64_t k = f2_add(y, two(kMagic));
   const uint64_t kf = f2_add(k, two(-kMagic));
   const uint64_t f = f2_fma(f2_fma(kf, minus1, y), minus1, yl);
-  e = f2_fma(f, two(0x1.444004p-13f), two(0x1.5f0896p-10f));
+  uint64_t e = f2_fma(f, two(0x1.444004p-13f), two(0x1.5f0896p-10f));
   e = f2_fma(f, e, two(0x1.3b2a1cp-7f));
   e = f2_fma(f, e, two(0x1.c6af6cp-5f));
   e = f2_fma(f, e, two(0x1.ebfbe0p-3f));
   e = f2_fma(f, e, two(0x1.62e430p-1f));
   e = f2_fma(f, e, two(1.f));
-  // 2^-k: the exponent field from the whole number at the bottom of k
-  constexpr int kOne = (127 << 23) + static_cast<int>(0x4b400000u << 23);
+  // 2^(45 - k): the exponent field from the whole number at the bottom of k
+  constexpr int kOne = ((127 + kUnit) << 23) + static_cast<int>(0x4b400000u << 23);
   const int p0 = kOne - (__float_as_int(f2_lo(k)) << 23), p1 = kOne - (__float_as_int(f2_hi(k)) << 23);
-  power = f2_pack(__int_as_float(p0), __int_as_float(p1));
+  return f2_mul(e, f2_pack(__int_as_float(p0), __int_as_float(p1)));
 }
 
-struct Far {
-  uint64_t sum;
-  float least_logit;
-};
+// The sum of four far weights; what is to stay out is below `least_logit`, where weights
+// are 0.
 template <bool EXACT>
-__device__ __forceinline__ void add_far(const Row& r, const float4& v, Far& far) {
-  const float c = far.least_logit;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint64_t e, power;
-    far_two<EXACT>(r, h ? f2_pack(fmaxf(v.z, c), fmaxf(v.w, c)) : f2_pack(fmaxf(v.x, c), fmaxf(v.y, c)), e, power);
-    far.sum = f2_fma(e, power, far.sum);
-  }
+__device__ __forceinline__ u64 far_four(const Row& r, const float4& v, float least_logit) {
+  const float c = least_logit;
+  const uint64_t a = far_two<EXACT>(r, f2_pack(fmaxf(v.x, c), fmaxf(v.y, c)));
+  const uint64_t b = far_two<EXACT>(r, f2_pack(fmaxf(v.z, c), fmaxf(v.w, c)));
+  return (static_cast<u64>(__float2uint_rn(f2_lo(a))) + __float2uint_rn(f2_hi(a))) +
+         (static_cast<u64>(__float2uint_rn(f2_lo(b))) + __float2uint_rn(f2_hi(b)));
 }
 
-// One weight, far or near, in units of 2^-45.
+// One weight, far or near, in units of 2^-45: the same integer as in every sum.
+template <bool EXACT>
 __device__ __noinline__ u64 weight_of(Row row, float l, const Power* powers) {
   const float2 y = exponent_of(row, l);
   if (!(y.x > -47.f)) return 0;
   if (y.x > -kNear) return weight_near(row, l, powers);
-  uint64_t e, power;
-  far_two<false>(row, f2_pack(l, l), e, power);
-  return __float2uint_rn(f2_lo(e) * f2_lo(power) * 0x1p45f);
+  return __float2uint_rn(f2_lo(far_two<EXACT>(row, f2_pack(l, l))));
 }
 
 // A weight as fp32, however small.
@@ -561,8 +558,7 @@ struct Added {
 };
 template <int TYPE>
 __device__ __noinline__ Added add_run(const uint4* run, int vecs, int x, Row r, Limits c) {
-  Far far{0, c.gone};
-  u64 large = 0;
+  u64 far = 0, large = 0;
   int at = 0;
   for (int j = 0; j < vecs; ++j) {
     const uint4 raw = run[j];
@@ -585,11 +581,10 @@ __device__ __noinline__ Added add_run(const uint4* run, int vecs, int x, Row r, 
         look(v.w, 3);
         large |= static_cast<u64>(bits) << at;
       }
-      add_far<TYPE != SV_FP32>(r, v, far);
+      far += far_four<TYPE != SV_FP32>(r, v, c.gone);
     }
   }
-  const float sum = f2_lo(far.sum) + f2_hi(far.sum);
-  return {c.gone == -INFINITY ? 0 : static_cast<u64>(__float2ull_rn(sum * 0x1p45f)), large};
+  return {c.gone == -INFINITY ? 0 : far, large};
 }
 
 // A bit for every entry of up to kRunEntries in [lo, hi].  (Few are wanted: looked at
@@ -794,6 +789,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     wait();
     return;
   }
+  constexpr bool kExact = TYPE != SV_FP32;
   Row r;
   r.m = most;
   {
@@ -804,12 +800,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     r.clo = c < 1e37f && temperature < 1e30f ? (fmaf(-c, temperature, kLog2eHi) + kLog2eLo) / temperature : 0.f;
   }
   const float bin_scale = r.chi * kBinsPerOctave;
-  // Above near_logit weights are near or nearly, below gone_logit nothing.  (The
+  // Up to near_logit every weight is far (its exponent below -kNear whatever is rounded, so
+  // that it is the same integer here and in weight_of), below gone_logit it is 0.  (The
   // margin keeps both below the maximum.)  All are near at temperatures past 10^35, and
   // below a millionth of the maximum, where floats next to it are whole powers apart.
   const float margin = fabsf(r.m) * 0x1p-22f;
   const bool all_near = !(100.f / r.chi < 1e37f && margin * r.chi < 1.f);
-  const float near_logit = all_near ? -INFINITY : r.m - kNear / r.chi - margin;
+  const float near_logit = all_near ? -INFINITY : r.m - (kNear + 0x1p-10f) / r.chi - margin;
   const float gone_logit = all_near ? -INFINITY : r.m - 100.f / r.chi - margin;
   const u64 least = min_p > 0.f ? times<true>(1ull << kUnit, min_p) : 0;
   const bool by_k = top_k > 0 && top_k < p.vocab, by_p = top_p < 1.f;
@@ -934,7 +931,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       for (int i = 0; i < kPer; ++i) {
         const int x = tid * run + i;
         w[i] = 0;
-        if (i < run) w[i] = weight_of(r, x < count ? logit_at(x) : -INFINITY, s.powers);
+        if (i < run) w[i] = weight_of<kExact>(r, x < count ? logit_at(x) : -INFINITY, s.powers);
         own += w[i];
       }
       u64 at = block_scan(own, s.scan) - own;
@@ -1032,7 +1029,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       u64 near = 0;
       const u64 far = sum_run(Limits{-INFINITY, 0x7fffffff, near_logit, gone_logit, false, target != 0}, [&](int x) {
         const float l = scalar_at(x);
-        near += weight_of(r, l, s.powers);
+        near += weight_of<kExact>(r, l, s.powers);
         const int at = atomicAdd(&s.listed, 1);
         if (at < kMost) list[at] = place_of(l, first + x);
       });
@@ -1100,7 +1097,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       each_between(round > 0 ? lowest_of(bin) : by_twos ? fmaxf(least_logit, lowest_of(kNearBins)) : least_logit,
                    round > 0 ? highest_of(bin) : INFINITY, [&](float l, int index) {
                      if (by_twos && bin_of(l) >= kNearBins) return;
-                     put(l, index, by_mass && counts(l) ? weight_of(r, l, s.powers) : 0);
+                     put(l, index, by_mass && counts(l) ? weight_of<kExact>(r, l, s.powers) : 0);
                    });
       if (by_twos) {
         // far weights by twos; below 2^32, their lower 16 bits and the others are added
@@ -1110,9 +1107,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const float l0 = h ? v.z : v.x, l1 = h ? v.w : v.y;
-            uint64_t e, power;
-            far_two<false>(r, f2_pack(l0, l1), e, power);
-            const uint64_t w2 = f2_mul(f2_mul(e, power), f2_pack(0x1p45f, 0x1p45f));
+            const uint64_t w2 = far_two<kExact>(r, f2_pack(l0, l1));
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const float l = i ? l1 : l0;
@@ -1144,7 +1139,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 #pragma unroll
         for (int k = 0; k < kMaxCluster; ++k) {
           c += x[k];
-          w += (static_cast<u64>(hi[k]) << (round == 0 && b >= kNearBins ? 16 : 32)) + lo[k];
+          w += (static_cast<u64>(hi[k]) << (by_twos && b >= kNearBins ? 16 : 32)) + lo[k];
         }
       };
       u64 c = 0, ms = 0;
@@ -1173,7 +1168,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         if (lane >= o) to_c += uc, to_m += um;
       }
       const unsigned owners = __ballot_sync(0xffffffffu, lane < cs && (by_mass ? to_m : to_c) >= target);
-      if (owners == 0) return 0;  // (round 0 alone)
+      if (owners == 0) return threshold;  // (round 0 alone; fewer entries than top-k)
       const int owner = __ffs(owners) - 1;
       if (rank == owner) {
         at_c += __shfl_sync(0xffffffffu, to_c - pc, rank);
@@ -1237,7 +1232,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
           const int x = tid * kPer + i;
-          w[i] = x < m ? weight_of(r, logit_at(x), s.powers) : 0;
+          w[i] = x < m ? weight_of<kExact>(r, logit_at(x), s.powers) : 0;
           own += w[i];
         }
         u64 at = block_scan(own, s.scan) - own;
@@ -1260,7 +1255,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     const float one_by_one = least_too ? r.m - (log2f(1.f / min_p) + 1.f) / r.chi - margin : near_logit;
     u64 by_one = 0;
     const u64 far = sum_run(Limits{floor_logit, floor_index, one_by_one, gone_logit, place != 0, least_too}, [&](int x) {
-      const u64 w = weight_of(r, scalar_at(x), s.powers);
+      const u64 w = weight_of<kExact>(r, scalar_at(x), s.powers);
       if (w >= floor_weight) by_one += w;
     });
     mine = by_one + (least_too ? 0 : far);
@@ -1303,39 +1298,34 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   }
   __syncthreads();
   if (s.run >= 0 && warp == 0) {
-    // (the weights one by one may sum to a little less than the run's sum: the last then)
-    u64 at = s.before, w_last = 0;
-    int x_last = -1;
+    u64 at = s.before;
     const int x1 = min((s.run + 1) * per * V, n);
     for (int x0 = s.run * per * V; x0 < x1; x0 += 32) {
       const int x = x0 + lane;
       const float l = x < x1 ? scalar_at(x) : -INFINITY;
-      bool kept = keeps(l, first + x);
-      u64 w = weight_of(r, kept ? l : -INFINITY, s.powers);
-      if (w < least) kept = false, w = 0;
+      u64 w = weight_of<kExact>(r, keeps(l, first + x) ? l : -INFINITY, s.powers);
+      if (w < least) w = 0;
       u64 sum = w;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const u64 v = __shfl_up_sync(0xffffffffu, sum, o);
         if (lane >= o) sum += v;
       }
-      const unsigned hit = __ballot_sync(0xffffffffu, at + sum > target), some = __ballot_sync(0xffffffffu, kept);
-      const int pick = hit ? __ffs(hit) - 1 : 31 - __clz(some);
-      if (hit || some) {
-        x_last = x0 + pick;
-        w_last = __shfl_sync(0xffffffffu, w, pick);
+      const unsigned hit = __ballot_sync(0xffffffffu, at + sum > target);
+      if (hit) {  // (the run's weights are those of its sum)
+        const int pick = __ffs(hit) - 1;
+        if (lane == pick) answer(first + x, w, total);
+        break;
       }
-      if (hit) break;
       at += __shfl_sync(0xffffffffu, sum, 31);
     }
-    if (lane == 0 && x_last >= 0) answer(first + x_last, w_last, total);
   }
   if (prow) {
     const float inv = 1.f / (static_cast<float>(total) * 0x1p-45f);
     for (int x = tid; x < n; x += kThreads) {
       const float l = scalar_at(x);
       float v = 0.f;
-      if (keeps(l, first + x) && (least == 0 || passes(weight_of(r, l, s.powers), l))) v = weight32(r, l) * inv;
+      if (keeps(l, first + x) && (least == 0 || passes(weight_of<kExact>(r, l, s.powers), l))) v = weight32(r, l) * inv;
       prow[x] = v;
     }
   }

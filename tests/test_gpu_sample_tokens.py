@@ -1,8 +1,8 @@
 """Token sampling on the GPU against the oracle: tokens are equal, kept sets are
 equal, logprobs and probabilities within fp32.
 
-The kernel's weights are off by 2^-36 of the largest, and its sums of weights below
-2^-13 by what fp32 rounds over 64 entries (in practice below 2^-30 of the row), so a
+The kernel's weights are off by 2^-36 of the largest, its sums of them are exact (in
+practice off by less than 2^-30 of the row), so a
 token may differ from float64's only where the uniform (or a filter's limit) lies
 within that of a border of sums: a draw nearer than 1e-9 to one (a uniform of one half
 over a symmetric row) may take the entry on either side.
@@ -296,3 +296,69 @@ def test_min_p_below_the_last_bit_of_the_sums():
     for min_p in (1e-17, 1e-20, 1e-37):
         check(x, u, min_p=min_p)
         check(x, u, min_p=min_p, top_k=3000)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("V", [4096, 20000])
+def test_an_entry_without_weight_is_drawn_at_no_border(V, dtype):
+    """Every run of eight holds seven weights a little below 2^-13 and then a mask of finite value; uniforms at the borders
+    between them, within a few units of fp32 on either side."""
+    rng = np.random.default_rng(V)
+    R = 600
+    x = torch.from_numpy(rng.uniform(-12.0, -9.1, (R, V)).astype(np.float32))
+    x[:, 7::8] = -3.0e4
+    x[:, -1] = 0.0
+    x = x.to(dtype).cuda()
+    w = x.double().exp()
+    w[:, 7::8] = 0.0
+    w[:, -1] = 1.0
+    share = w.cumsum(1) / w.sum(1, keepdim=True)
+    r = torch.arange(R)
+    for run in (0, 3, 17):
+        border = share[r, 8 * run + 6].float()
+        for off in (-2, -1, 0, 1, 2):
+            u = (border.view(torch.int32) + off).view(torch.float32)
+            tokens, logprobs, _, err = sample(x, u)
+            assert err == 0
+            assert (x[r, tokens.long()] > -100).all() and (logprobs > -100).all()
+            assert ((tokens == 8 * run + 6) | (tokens == 8 * run + 8)).all()
+
+
+@pytest.mark.parametrize("settings", [dict(), dict(top_k=700), dict(top_k=300, top_p=0.9), dict(top_p=0.9), dict(min_p=1e-5)])
+def test_the_batch_does_not_show_in_a_row(settings):
+    """Flat rows with uniforms next to borders of their sums, alone and in batches of other sizes, which divide a row
+    otherwise: the same bits."""
+    g = torch.Generator(device="cuda").manual_seed(31)
+    R, V = 400, 20011
+    x = torch.rand((R, V), generator=g, device="cuda") - 10.5   # weights near 2^-14 of the largest
+    x[:, 9000] = 0.0
+    share = x.double().softmax(1).cumsum(1)
+    u = share.gather(1, torch.randint(V // 4, V, (R, 1), generator=g, device="cuda"))[:, 0].float().clamp(max=1 - 2.0 ** -24)
+    whole = sample(x, u, probs=True, **settings)
+    assert whole[3] == 0
+    for size in (1, 5, 40, 130):
+        for at in range(0, 130 if size == 1 else R - size + 1, size):
+            part = sample(x[at:at + size], u[at:at + size], probs=True, **settings)
+            for a, b in zip(whole, part[:3]):
+                assert torch.equal(a[at:at + size], b), (size, at)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_the_batch_does_not_show_in_rows_of_every_kind(dtype):
+    rng = np.random.default_rng(5)
+    R, V = 320, 20011
+    x, u = random_logits(R, V, dtype, seed=41, sigma=1.5)
+    x[::7] *= 0.1                                               # flat ones
+    x[3::11, ::2] = torch.finfo(dtype).min                      # masked by the type's lowest value
+    x[5::13, 1::2] = -torch.inf
+    settings = dict(temperature=rng.choice([0.0, 0.3, 1.0, 2.0], R).astype(np.float32),
+                    top_k=rng.choice([0, 0, 1, 60, 513, 900, 3000, 99999], R),
+                    top_p=rng.choice([0.0, 0.3, 0.9, 0.99999994, 1.0], R).astype(np.float32),
+                    min_p=rng.choice([0.0, 0.0, 1e-30, 1e-4, 0.1], R).astype(np.float32))
+    whole = sample(x, u, probs=True, **settings)
+    assert whole[3] == 0
+    for size in (1, 6, 45, 160):
+        for at in range(0, 160 if size == 1 else R - size + 1, size):
+            part = sample(x[at:at + size], u[at:at + size], probs=True, **{k: v[at:at + size] for k, v in settings.items()})
+            for a, b in zip(whole, part[:3]):
+                assert torch.equal(a[at:at + size], b), (size, at)
