@@ -107,7 +107,8 @@ struct PrefixSeq {
   int row;         // of the block table
   int first_page;
   int part;
-  int at;          // its first token's row in the part's arrays
+  int at;          // its first token's row in the part's arrays; kAlone: the group's first row of the block table
+  int head_pages;  // kAlone: the prefix's pages, which that row names; else 0 (`row` names all)
 };
 
 __device__ __forceinline__ Seq load_seq(const Params& p, int b, bool report) {
@@ -187,13 +188,14 @@ __device__ __forceinline__ PrefixSeq own_part(const PrefixParams& p, const Group
   }
   s.part = x.shared ? kOwn : kAlone;
   s.first_page = x.shared ? x.prefix / kPage : 0;
-  s.at = part_row(p, x, s.n0);
+  s.at = x.shared ? part_row(p, x, s.n0) : x.first;
+  s.head_pages = x.shared ? 0 : x.prefix / kPage;
   return s;
 }
 
 __device__ __forceinline__ PrefixSeq load_seq(const PrefixParams& p, int v, bool) {
   const int4 a = __ldcg(p.entries + 2 * v), b = __ldcg(p.entries + 2 * v + 1);
-  return {a.x, a.y, a.z, a.w, b.x, b.y, b.z};
+  return {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 }
 
 // The last entry that starts at or before `pos` of the row kernel's pages (PAGES) or the
@@ -225,9 +227,9 @@ __device__ __forceinline__ int entry_at(const PrefixParams& p, long long pos, lo
   return lo;
 }
 
-// An entry's row of the block table.
-__device__ __forceinline__ int table_row(const Seq&, int b) { return b; }
-__device__ __forceinline__ int table_row(const PrefixSeq& s, int) { return s.row; }
+// The row of the block table that names page `lp` of an entry.
+__device__ __forceinline__ int table_row(const Seq&, int b, int) { return b; }
+__device__ __forceinline__ int table_row(const PrefixSeq& s, int, int lp) { return lp < s.head_pages ? s.at : s.row; }
 
 // The lane's entry, on every lane.
 __device__ __forceinline__ Seq from_lane(const Seq& s, int lane) {
@@ -238,7 +240,7 @@ __device__ __forceinline__ PrefixSeq from_lane(const PrefixSeq& s, int lane) {
   return {__shfl_sync(0xffffffffu, s.n0, lane),  __shfl_sync(0xffffffffu, s.n, lane),
           __shfl_sync(0xffffffffu, s.ctx, lane), __shfl_sync(0xffffffffu, s.row, lane),
           __shfl_sync(0xffffffffu, s.first_page, lane), __shfl_sync(0xffffffffu, s.part, lane),
-          __shfl_sync(0xffffffffu, s.at, lane)};
+          __shfl_sync(0xffffffffu, s.at, lane), __shfl_sync(0xffffffffu, s.head_pages, lane)};
 }
 
 // Whether the row kernel takes a sequence of n > 0 new tokens.

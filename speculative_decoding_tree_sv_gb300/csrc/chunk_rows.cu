@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
       const int j = load_j + lane;
       if (j < lp.j1) {
         const int page = j < k.sink_pages ? j : k.first_page + (j - k.sink_pages);
-        ids = p.block_table[static_cast<size_t>(table_row(lp.seq.s, lp.b >> SHIFT)) * p.max_pages_per_seq + page];
+        ids = p.block_table[static_cast<size_t>(table_row(lp.seq.s, lp.b >> SHIFT, page)) * p.max_pages_per_seq + page];
         if (ids < 0 || ids >= p.num_pages) {
           report_error(p.err, SV_DEVERR_BAD_PAGE);
           ids = p.num_pages;  // outside the pool: the box arrives as zeros

@@ -77,15 +77,16 @@ struct Piece {
   int sink_pages, sink_tiles, first_page, end;
 };
 struct PrefixPiece : Piece {
-  int row, part, at;
+  int row, part, at, head_pages;
 };
 static_assert(sizeof(PrefixPiece) * kPieceRing <= 512, "piece ring");
 template <class P>
 using PieceOf = std::conditional_t<P::kPrefix, PrefixPiece, Piece>;
 
-// A piece's row of the block table, and one past its sequence's (or prefix's) last position.
-__device__ __forceinline__ int table_row(const Piece& pc) { return pc.b; }
-__device__ __forceinline__ int table_row(const PrefixPiece& pc) { return pc.row; }
+// The row of the block table that names page `lp` of a piece, and one past its
+// sequence's (or prefix's) last position.
+__device__ __forceinline__ int table_row(const Piece& pc, int) { return pc.b; }
+__device__ __forceinline__ int table_row(const PrefixPiece& pc, int lp) { return lp < pc.head_pages ? pc.at : pc.row; }
 __device__ __forceinline__ int all_keys(const Piece& pc) { return pc.ctx + pc.n; }
 __device__ __forceinline__ int all_keys(const PrefixPiece& pc) { return pc.part == kShared ? pc.ctx : pc.ctx + pc.n; }
 // The last position that token `tok` sees.
@@ -127,6 +128,7 @@ __device__ __forceinline__ PieceOf<P> unit_piece(const P& p, const typename P::E
     pc.row = s.row;
     pc.part = s.part;
     pc.at = s.at;
+    pc.head_pages = s.head_pages;
   }
   return pc;
 }
@@ -537,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane < kPagesPerTile) {
             const int lp = tile_page(pc, j, lane);
             if (lp >= 0) {
-              phys = p.block_table[static_cast<size_t>(table_row(pc)) * p.max_pages_per_seq + lp];
+              phys = p.block_table[static_cast<size_t>(table_row(pc, lp)) * p.max_pages_per_seq + lp];
               if (phys < 0 || phys >= p.num_pages) {
                 report_error(p.err, SV_DEVERR_BAD_PAGE);
                 phys = p.num_pages;

@@ -103,13 +103,13 @@ __global__ void __launch_bounds__(kEntryThreads) prefix_entries_kernel(const __g
       if (v0 > 0 && b >= 0) ctx = p.ctx_lens[b];
       if (b < 0) {
         if (!x.ok) report_error(p.err, SV_DEVERR_BAD_LENGTH);
-        s = {x.n0, x.shared ? x.n : 0, x.prefix, x.first, 0, kShared, part_row(p, x, x.n0)};
+        s = {x.n0, x.shared ? x.n : 0, x.prefix, x.first, 0, kShared, part_row(p, x, x.n0), 0};
       } else {
         s = own_part(p, x, b, at.cu_tokens[b], at.cu_tokens[b + 1], ctx, true);
         if (s.part == kAlone && s.n > 0) s_alone = 1;
       }
       p.entries[2 * v] = make_int4(s.n0, s.n, s.ctx, s.row);
-      p.entries[2 * v + 1] = make_int4(s.first_page, s.part, s.at, 0);
+      p.entries[2 * v + 1] = make_int4(s.first_page, s.part, s.at, s.head_pages);
       t.s = s;
       if (s.n > 0 && in_rows(p, s.n)) {
         const Keys k = unit_keys(p, s, 0, s.n);

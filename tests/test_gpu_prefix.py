@@ -296,3 +296,17 @@ def test_padded_decode_steps(each, Hq, Hkv, D):
     sv.sv_prefix_attention(p)
     torch.cuda.synchronize()
     c.check()
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 2, 64), (32, 8, 128), (16, 1, 128)])
+@pytest.mark.parametrize("groups", [[[(3, 1), (0, 1), (9, 1)]] * 3, [[(3, 150), (0, 170)], [(1, 1)], [(4, 70), (60, 1), (2, 2), (9, 300)]]])
+def test_shared_pages_are_named_by_the_first_row_alone(groups, Hq, Hkv, D):
+    """The entries of a group's other rows for them are not read, whether or not it is worth sharing: here they name no page,
+    or another one."""
+    for other in (-1, 1 << 30, 0):
+        c = Case([160, 64, 1600], groups, Hq, Hkv, D, seed=Hq)
+        ends = c.cu_groups.tolist()
+        for first, end, prefix in zip(ends, ends[1:], (160, 64, 1600)):
+            c.table[first + 1:end, :prefix // 16] = other
+        assert c.run() == 0
+        c.check()
