@@ -187,8 +187,10 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
     const int batch = p.batch << SHIFT;
     if constexpr (P::kPrefix) {
       mine = RowSeq<P>{};
-      total = p.split->pages;
-      if (p.split->row_sms > 0) blocks = p.split->row_sms;
+      // (from L2: beside the tile kernel this grid has no wait of its own behind the first one)
+      total = __ldcg(&p.split->pages);
+      const int own = __ldcg(&p.split->row_sms);
+      if (own > 0) blocks = own;
       worker = warp * blocks + blockIdx.x;
     } else if (side_by_side(p)) {
       Work sum{};

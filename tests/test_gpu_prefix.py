@@ -310,3 +310,25 @@ def test_shared_pages_are_named_by_the_first_row_alone(groups, Hq, Hkv, D):
             c.table[first + 1:end, :prefix // 16] = other
         assert c.run() == 0
         c.check()
+
+
+def test_calls_one_behind_the_other_on_one_workspace():
+    """Calls whose work is shared out differently, nothing between them: each sees its own entries and split."""
+    cases = [Case([1600, 320], [[(i, 1) for i in range(each)], [(900, 3), (i0, 40)]], 32, 8, 128, seed=each)
+             for each, i0 in ((40, 7), (9, 1500), (64, 30))]
+    params = [c.params() for c in cases]
+    ws = max((c.ws for c in cases), key=lambda t: t.numel())
+    first = []
+    for c, p in zip(cases, params):
+        p.workspace, p.workspace_bytes = ws.data_ptr(), ws.numel()
+        sv.sv_prefix_attention(p)
+        torch.cuda.synchronize()
+        c.check()
+        first.append((c.out.clone(), c.lse.clone()))
+    for i in range(30):
+        for c, p in zip(cases, params):
+            sv.sv_prefix_attention(p)
+    torch.cuda.synchronize()
+    for c, (out, lse) in zip(cases, first):
+        assert torch.equal(c.out, out) and torch.equal(c.lse, lse)
+    assert sv.sv_get_device_error(ws) == 0
