@@ -750,7 +750,8 @@ sv_status sv_prefix_attention(const sv_prefix_params* params, sv_stream_t stream
  * their number: neither the batch nor the order of sums shows in a row's outputs.
  * A border of sums is off by 2^-30 of the row's as a rule; only a uniform or a
  * top_p within that of one may see it.  Entries below 2^-46 of the largest are not
- * drawn.
+ * drawn.  Temperatures below 1.4427e-37 count as that; above 10^30, or between logits
+ * more than 3.4e38 apart, weights have fewer bits.
  * ---------------------------------------------------------------------- */
 typedef struct sv_sample_params {
   int rows;                 /* R                                             */

@@ -726,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     s.run = -1;
     s.first = 0x7fffffff;
   }
-  const int want = (top_k + cs - 1) / cs;
+  const int want = static_cast<int>((static_cast<unsigned>(top_k) + cs - 1) / cs);
   const bool bounded = top_k > 1 && top_k < p.vocab && want <= kThreads / 2, few = bounded && top_k <= kFew;
   if (bounded) {  // the upper bits of the part's (top_k / CTAs)-th largest of the threads' best
     uint32_t low = 0;

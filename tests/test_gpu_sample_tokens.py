@@ -362,3 +362,14 @@ def test_the_batch_does_not_show_in_rows_of_every_kind(dtype):
             part = sample(x[at:at + size], u[at:at + size], probs=True, **{k: v[at:at + size] for k, v in settings.items()})
             for a, b in zip(whole, part[:3]):
                 assert torch.equal(a[at:at + size], b), (size, at)
+
+
+def test_settings_at_the_ends_of_their_types():
+    x, u = random_logits(3, 5003, torch.float32, seed=51)
+    for top_k in (2 ** 31 - 1, -2 ** 31, 2 ** 31 - 8):
+        check(x, u, top_k=top_k)
+        check(x, u, top_k=top_k, top_p=0.7)
+    for temperature in (1e-45, 1e-38, 1e-30, 1e20, 1e30, 3.4e38):
+        check(x, u, temperature=temperature)
+        check(x, u, temperature=temperature, top_k=30, top_p=0.6)
+        check(x, u, temperature=temperature, top_p=0.5)
