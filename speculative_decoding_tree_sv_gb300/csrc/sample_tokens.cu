@@ -337,6 +337,23 @@ __device__ __noinline__ void cluster_wait(Barrier* b, int* err) {
   __syncthreads();
 }
 
+// What the CTAs of a cluster read of one another is safe by the order of their meetings (an
+// arrival and a wait).  A slot is written before a meeting, read behind it, and written
+// again only behind one more:
+//   top, low      the load; read behind the first meeting, never written again
+//   first         a greedy row's search and its meeting
+//   listed, list  gather, or find's listing of near entries, up to the meeting at its end; the
+//                 number is read behind that, the entries (pull) too, before the first CTA's
+//                 next arrival.  A list that was too long is not pulled, and a meeting follows
+//                 (or those of a histogram) before the next one begins
+//   mass, all     find's listing: with its number
+//   the bins      a histogram's round, up to its first meeting; read by the owners of their parts
+//                 up to its second.  They lie over the lists, which nobody pulls any more then
+//   count, mass   the owner's part, up to the second meeting; read up to the third
+//   pick          the owner of the target, up to the third; read before the next round's first
+//   found         the first CTA, up to find's last meeting
+//   sum           kept_sum and its meeting; find's lie between two of them
+// A CTA arrives once more when it reads no other's slots, and waits before it leaves.
 struct Shared {
   Power powers[32];
   Barrier barrier;
