@@ -737,7 +737,8 @@ sv_status sv_prefix_attention(const sv_prefix_params* params, sv_stream_t stream
  *   top_k[r]  entries (0 or less: all);
  *   top_p[r]: the fewest entries whose weights sum to top_p[r] or more of the
  *             weights of the top_k ones (1 or more: all; at least one entry);
- *   min_p[r]: entries of weight >= min_p[r] (the largest weight is 1).
+ *   min_p[r]: entries of weight >= min_p[r] (the largest weight is 1; weights
+ *             are off by 2^-36 here, below 2^-14 by 2^-22 of themselves).
  * tokens[r] is the smallest index x whose kept weights up to and including x
  * sum to more than uniforms[r] of all kept ones.  temperature[r] = 0 takes the
  * first of the order.  logprobs[r] is the natural logarithm of the token's

@@ -827,9 +827,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   const float gone_logit = all_near ? -INFINITY : r.m - 100.f / r.chi - margin;
   const u64 least = min_p > 0.f ? times<true>(1ull << kUnit, min_p) : 0;
   const bool by_k = top_k > 0 && top_k < p.vocab, by_p = top_p < 1.f;
-  // Whether min-p keeps an entry of weight w: one without weight (never drawn, it may have a
-  // share) by its weight in fp32.
-  auto passes = [&](u64 w, float l) { return w >= least || (w == 0 && least == 1 && weight32(r, l) >= min_p); };
+  // Whether min-p keeps an entry of weight w: below 2^-14 by its weight in fp32 (2^-22 of it off),
+  // which then says more than whole units.
+  auto passes = [&](u64 w, float l) {
+    return least >= 1ull << (kUnit - 14) || least == 0 ? w >= least : weight32(r, l) >= min_p;
+  };
 
   // Rounded to a whole number by the sum with 2^23; -inf lies in the last bin.
   auto bin_of = [&](float l) {
@@ -1264,16 +1266,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     return cs > 1 ? peer(&s.found, 0) : s.found;
   };
   // Sum over the cluster of the weights at or above a place.
-  auto kept_sum = [&](u64 place, u64 floor_weight, u64& end, u64& mine, u64& base) -> u64 {
+  auto kept_sum = [&](u64 place, bool least_too, u64& end, u64& mine, u64& base) -> u64 {
     const float floor_logit = place ? logit_of(static_cast<uint32_t>(place >> kIndexBits)) : -INFINITY;
     const int floor_index = place ? index_of(place) : 0x7fffffff;
     // with min-p the entries that may pass are weighed one by one, the others left out
-    const bool least_too = floor_weight != 0;
     const float one_by_one = least_too ? r.m - (log2f(1.f / min_p) + 1.f) / r.chi - margin : near_logit;
     u64 by_one = 0;
     const u64 far = sum_run(Limits{floor_logit, floor_index, one_by_one, gone_logit, place != 0, least_too}, [&](int x) {
-      const u64 w = weight_of<kExact>(r, scalar_at(x), s.powers);
-      if (w >= floor_weight) by_one += w;
+      const float l = scalar_at(x);
+      const u64 w = weight_of<kExact>(r, l, s.powers);
+      if (!least_too || passes(w, l)) by_one += w;
     });
     mine = by_one + (least_too ? 0 : far);
     end = block_scan(mine, s.scan);
@@ -1290,7 +1292,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   u64 goal = by_k ? static_cast<u64>(top_k) : 0;
   for (;;) {
     if (step == kShareOfKept || step == kDraw) {
-      total = kept_sum(threshold, step == kDraw ? least : 0, end, mine, base);
+      total = kept_sum(threshold, step == kDraw && least != 0, end, mine, base);
       if (over) return;
       if (step == kDraw) break;
       goal = max(1ull, times<true>(total, top_p));
@@ -1321,7 +1323,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       const int x = x0 + lane;
       const float l = x < x1 ? scalar_at(x) : -INFINITY;
       u64 w = weight_of<kExact>(r, keeps(l, first + x) ? l : -INFINITY, s.powers);
-      if (w < least) w = 0;
+      if (w != 0 && !passes(w, l)) w = 0;
       u64 sum = w;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {

@@ -373,3 +373,14 @@ def test_settings_at_the_ends_of_their_types():
         check(x, u, temperature=temperature)
         check(x, u, temperature=temperature, top_k=30, top_p=0.6)
         check(x, u, temperature=temperature, top_p=0.5)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_small_min_p_keeps_by_relative_weight(dtype):
+    """Weights next to a limit of a few units of the sums' last bit: what is kept is decided to 2^-22 of the weight (these
+    random weights lie further from the limit)."""
+    x, u = random_logits(4, 20011, dtype, seed=61, sigma=6.0)
+    x[2, 3000:] -= 25.0
+    for min_p in (2e-16, 1e-14, 1e-13, 1e-12, 3e-11, 1e-8, 1e-6, 5e-5, 7e-5):
+        for settings in (dict(), dict(top_k=300), dict(top_k=9000)):
+            check(x, u, min_p=min_p, **settings)
