@@ -759,6 +759,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     const uint32_t k = __reduce_max_sync(0xffffffffu, lane < kWarps ? s.best[lane] : 0);
     if (lane == 0) s.top = k;
   }
+  __syncthreads();  // (for the compiler: without it, in front of the meeting's own, it spills 800 bytes of loads more)
   if (!meet()) return;
   const uint32_t top = __reduce_max_sync(0xffffffffu, lane < cs ? (cs > 1 ? peer(&s.top, lane) : s.top) : 0);
   const float most = logit_of(top);
