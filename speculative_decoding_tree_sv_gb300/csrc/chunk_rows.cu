@@ -187,9 +187,11 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
     const int batch = p.batch << SHIFT;
     if constexpr (P::kPrefix) {
       mine = RowSeq<P>{};
-      // (from L2: beside the tile kernel this grid has no wait of its own behind the first one)
-      total = __ldcg(&p.split->pages);
-      const int own = __ldcg(&p.split->row_sms);
+      // (from L2 beside the tile kernel, where this grid has no wait of its own behind the first
+      // one; by every warp of a call without tiles that took 2 us)
+      const bool alone = p.tile_ctas == 0;
+      total = alone ? p.split->pages : __ldcg(&p.split->pages);
+      const int own = alone ? p.split->row_sms : __ldcg(&p.split->row_sms);
       if (own > 0) blocks = own;
       worker = warp * blocks + blockIdx.x;
     } else if (side_by_side(p)) {
