@@ -332,3 +332,36 @@ def test_calls_one_behind_the_other_on_one_workspace():
     for c, (out, lse) in zip(cases, first):
         assert torch.equal(c.out, out) and torch.equal(c.lse, lse)
     assert sv.sv_get_device_error(ws) == 0
+
+
+@pytest.mark.parametrize("B,Hq,Hkv", [(1023, 4, 2), (1024, 4, 2), (1025, 4, 1), (2500, 2, 2), (9000, 1, 1)])
+def test_more_sequences_than_the_entries_are_made_of_at_once(B, Hq, Hkv):
+    """Groups of one to seven sequences (and empty ones), more of them than a block has threads and than fit its staged
+    arrays; tokens of every kind among them."""
+    rng = np.random.default_rng(B)
+    groups, prefixes, left = [], [], B
+    while left > 0:
+        n = min(left, int(rng.integers(0, 8)))
+        if n == 0 and len(groups) % 9:
+            continue
+        groups.append([(int(rng.integers(0, 40)), int(rng.choice([0, 1, 1, 1, 1, 2, 30]))) for _ in range(n)])
+        prefixes.append(16 * int(rng.integers(0, 4)))
+        left -= n
+    c = Case(prefixes, groups, Hq, Hkv, 64, seed=B, extra_rows=int(rng.integers(0, 100)))
+    p = c.params(max_group_tokens=c.most_of_group + 5)
+    c.ws[256:] = 255
+    sv.sv_prefix_attention(p)
+    torch.cuda.synchronize()
+    assert sv.sv_get_device_error(c.ws) == 0
+    c.check()
+
+
+def test_cache_offsets_past_32_bits():
+    """The pages at the end of a pool of 2.3e9 elements."""
+    c = Case([160, 1600], [[(3, 1), (20, 2)], [(i, 1) for i in range(20)] + [(5, 40)]], 32, 8, 128, seed=14)
+    first = 140000 - c.pages
+    big = [torch.zeros((140000, 8, 16, 128), dtype=c.dtype, device="cuda") for _ in range(2)]
+    big[0][first:], big[1][first:] = c.k, c.v
+    c.table += first
+    assert c.run(k_cache=big[0], v_cache=big[1]) == 0
+    c.check()

@@ -249,3 +249,47 @@ def test_angles_at_the_ends_of_both_ranges(f):
         want = float(np.sin(float(2 * PI * (Fraction(1, 4) - turns if turns < Fraction(1, 2) else turns - Fraction(3, 4)))))
         assert abs(want) < 1e-4
         assert (out[t, 0, :8].double() - want).abs().max() <= np.pi * 2.0 ** -24 + 1.01 * 2.0 ** -8 * abs(want), int(x[t])
+
+
+def test_cache_offsets_past_32_bits():
+    """The last pages of a pool of 2.6e9 elements, from token rows whose offsets pass 2^31 too."""
+    pages, T = 40000, 3
+    kc, vc = (torch.zeros((pages, 8, 64, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    wide = torch.empty((T, 1 << 30), dtype=torch.bfloat16, device="cuda")
+    k = wide[:, :1024].view(T, 8, 128)
+    k.copy_(torch.randn((T, 8, 128), device="cuda"))
+    out = torch.empty_like(k, memory_format=torch.contiguous_format)
+    ints = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    sv.sv_rope_append(k, k, k, out, kc, vc, ints([[0, pages - 1], [pages - 2, 1]]), ints([63, 10]), ints([0, 2, 3]), frequencies(64),
+                      workspace=ws)
+    assert sv.sv_get_device_error(ws) == 0
+    assert torch.equal(vc[0, :, 63], k[0]) and torch.equal(vc[pages - 1, :, 0], k[1]) and torch.equal(vc[pages - 2, :, 10], k[2])
+    want = oracle.rotate(f64(k), [63, 64, 10], frequencies(64).cpu().numpy())
+    close(f64(out), want, f64(k), 64, False, 1.0, torch.bfloat16)
+    for t, at in enumerate([(0, 63), (pages - 1, 0), (pages - 2, 10)]):
+        assert torch.equal(kc[at[0], :, at[1]], out[t])
+    assert int(kc.any(dim=3).any(dim=1).sum()) == 3
+
+
+def test_many_sequences():
+    """More sequences than a search takes in three rounds, and than the grid has threads, most without a token."""
+    B = 70000
+    new = torch.zeros(B, dtype=torch.int64)
+    new[torch.tensor([0, 5, 6, 40000, 65536, B - 1])] = torch.tensor([2, 1, 3, 1, 2, 4])
+    T = int(new.sum())
+    cu = torch.cat([torch.zeros(1, dtype=torch.int64), new.cumsum(0)]).int().cuda()
+    ctx = (torch.arange(B, dtype=torch.int32) % 29).cuda()
+    table = torch.arange(2 * B, dtype=torch.int32).view(B, 2).cuda()
+    k = torch.randn((T, 1, 16), device="cuda").half()
+    kc, vc = (torch.zeros((2 * B, 1, 16, 16), dtype=torch.float16, device="cuda") for _ in range(2))
+    after = torch.full((B,), -7, dtype=torch.int32, device="cuda")
+    sv.sv_rope_append(None, k, k, None, kc, vc, table, ctx, cu, frequencies(16), new_ctx_lens=after)
+    assert torch.equal(after, ctx + new.int().cuda())
+    seen = 0
+    for b in new.nonzero().flatten().tolist():
+        for i in range(int(new[b])):
+            slot = int(ctx[b]) + i
+            assert torch.equal(vc[2 * b + slot // 16, :, slot % 16], k[seen])
+            seen += 1
+    assert int(vc.any(dim=3).sum()) == T

@@ -384,3 +384,32 @@ def test_small_min_p_keeps_by_relative_weight(dtype):
     for min_p in (2e-16, 1e-14, 1e-13, 1e-12, 3e-11, 1e-8, 1e-6, 5e-5, 7e-5):
         for settings in (dict(), dict(top_k=300), dict(top_k=9000)):
             check(x, u, min_p=min_p, **settings)
+
+
+def test_offsets_past_32_bits():
+    """The last rows of 2.2e9 logits, and of as many probabilities."""
+    R, V = 17000, 131072
+    x = torch.zeros((R, V), dtype=torch.bfloat16, device="cuda")
+    last, u = random_logits(3, V, torch.bfloat16, seed=71)
+    x[-3:] = last
+    every = torch.full((R,), 0.25, device="cuda")
+    every[-3:] = u
+    tokens, logprobs, probs, err = sample(x, every, probs=True, top_k=40)
+    assert err == 0
+    for a, b in zip((tokens, logprobs, probs), sample(last, u, probs=True, top_k=40)):
+        assert torch.equal(a[-3:], b)
+    assert tokens[:-3].eq(10).all() and probs[-4, :40].eq(0.025).all() and not probs[-4, 40:].any()
+
+
+def test_many_small_rows():
+    R, V = 100000, 33
+    x, u = random_logits(R, V, torch.float32, seed=72)
+    tokens, logprobs, _, err = sample(x, u)
+    assert err == 0
+    share = x.double().softmax(1)
+    running = share.cumsum(1)
+    gap = (running - u.double()[:, None]).abs().min(1).values
+    want = (running <= u.double()[:, None]).sum(1)
+    assert ((tokens == want) | (gap < 1e-9)).all() and (gap < 1e-9).sum() < 10
+    got = share.log().gather(1, tokens.long()[:, None])[:, 0]
+    assert ((logprobs - got).abs() <= 2.0 ** -23 * (2 + 2 * got.abs())).all()
