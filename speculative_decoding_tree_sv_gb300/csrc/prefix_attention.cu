@@ -18,7 +18,7 @@
 //
 // The first kernel takes 2.4 us, the combine 5 to 11.  64 samples over 60000 tokens, 32
 // and 8 heads of 128: 88 us (chunk attention, which reads them 64 times, 1194; the bytes
-// alone 52); 16 prompts of 1000 to 1600 with four samples each 45 (52; 23).  Two samples
+// alone 52); 16 prompts of 1000 to 1600 with four samples each 46 (52; 23).  Two samples
 // over 2000 tokens 15.5 (10.3: three launches cost more there than the reads they save).
 #include <math.h>
 

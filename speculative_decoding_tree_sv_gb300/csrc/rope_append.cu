@@ -18,7 +18,7 @@
 // memory for all heads.  The next grid starts at this one's end, not before: it may
 // be a tree attention that reads context ahead of its wait
 // (SV_ATTN_EARLY_CONTEXT).  32 tokens of 32 and 8 heads of 128 take 3.5 us, 7620 tokens
-// 38.7 (4.8 TB/s; start and tail of 2.5 waves of CTAs).
+// 38.6 (4.8 TB/s; start and tail of 2.5 waves of CTAs).
 #include <math.h>
 
 #include <algorithm>

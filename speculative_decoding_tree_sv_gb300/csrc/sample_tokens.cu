@@ -36,10 +36,10 @@
 // The logits are read once, but HBM bounds none of the measured calls: 20 to 40 steps
 // of a row (barriers of the cluster, scans, a sort) follow one another, each some 500 to
 // 2000 cycles, and a pass of the weights is about 15 instructions per entry.  One row of
-// 32000 with top-k 50 and top-p takes 12 us; 32 rows of 128256 without a filter 16; 64
-// with top-p 0.9 40 us; 60 with top-k 64 and their distributions 38; 256 of 151936, each
-// with its own settings, 143 (0.54 TB/s).  Flat rows whose nucleus is thousands of entries
-// cost most: 256 of them 490 us.
+// 32000 with top-k 50 and top-p takes 12.5 us; 32 rows of 128256 without a filter 16.5; 64
+// with top-p 0.9 42.5; 60 with top-k 64 and their distributions 40; 256 of 151936, each
+// with its own settings, 145 to 160 (0.5 TB/s).  Flat rows whose nucleus is thousands of
+// entries cost most: 256 of them, a top-p of 0.9 at temperatures of 1.5 to 8, 820 to 1210.
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 #include <math.h>
