@@ -829,9 +829,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   const u64 least = min_p > 0.f ? times<true>(1ull << kUnit, min_p) : 0;
   const bool by_k = top_k > 0 && top_k < p.vocab, by_p = top_p < 1.f;
   // Whether min-p keeps an entry of weight w: below 2^-14 by its weight in fp32 (2^-22 of it off),
-  // which then says more than whole units.
+  // which next to the limit says more than whole units.
+  const u64 beside = least >= 1ull << (kUnit - 14) || least == 0 ? 0 : 2 + (least >> 20);
   auto passes = [&](u64 w, float l) {
-    return least >= 1ull << (kUnit - 14) || least == 0 ? w >= least : weight32(r, l) >= min_p;
+    return beside == 0 || w > least + beside || w + beside < least ? w >= least : weight32(r, l) >= min_p;
   };
 
   // Rounded to a whole number by the sum with 2^23; -inf lies in the last bin.
