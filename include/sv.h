@@ -677,9 +677,9 @@ sv_status sv_chunk_attention(const sv_chunk_params* params, sv_stream_t stream);
  * sequences cu_groups[g] .. cu_groups[g+1] - 1 form group g (consecutive rows of
  * block_table; a group may hold one sequence, or none), and the first
  * prefix_lens[g] tokens of each lie in the same pages (as sv_pages_fork and
- * sv_pages_reserve leave them: the whole pages of the parent).  Those pages, as the group's first row names them, are
- * read once for all new tokens of the group; the entries of its other rows for
- * them are not read.  Every sequence's own tokens from prefix_lens[g] on are
+ * sv_pages_reserve leave them: the whole pages of the parent).  Those pages, as
+ * the group's first row names them, are read once for all new tokens of the
+ * group; the entries of its other rows for them are not read.  Every sequence's own tokens from prefix_lens[g] on are
  * read as always.  prefix_lens[g] is a multiple of page_size and at most the
  * ctx_lens of each of the group's sequences; 0 shares nothing.
  *
